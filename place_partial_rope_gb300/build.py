@@ -24,8 +24,11 @@ LIB = os.path.join(PKG, "librope_partial.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 CU_SOURCES = ["rope_kernels_bf16.cu", "rope_kernels_fp16.cu", "rope_kernels_fp32.cu",
-              "rope_launch.cu"]
-CPP_SOURCES = ["rope_host.cpp"]
+              "rope_launch.cu", "rope_axes_bf16.cu", "rope_axes_fp16.cu", "rope_axes_fp32.cu",
+              "rope_axes_launch.cu", "rope_cache_bf16.cu", "rope_cache_fp16.cu",
+              "rope_cache_fp32.cu", "rope_cache_launch.cu", "rope_tree_bf16.cu",
+              "rope_tree_fp16.cu", "rope_tree_fp8.cu", "rope_tree_int8.cu", "rope_tree_launch.cu"]
+CPP_SOURCES = ["rope_host.cpp", "rope_serving_host.cpp"]
 
 
 def _nvcc() -> str:
@@ -37,7 +40,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "rope_partial.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -13,12 +13,15 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include "rope_axes.h"
+#include "rope_error.h"
 #include "rope_internal.h"
 
 namespace rope {
-namespace {
 
-thread_local char g_msg[512] = "";
+static thread_local char g_msg[512] = "";
+
+void clear_error() { g_msg[0] = '\0'; }
 
 rope_status_t fail(rope_status_t st, const char* fmt, ...) {
     va_list ap;
@@ -27,6 +30,13 @@ rope_status_t fail(rope_status_t st, const char* fmt, ...) {
     va_end(ap);
     return st;
 }
+
+bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && pa < pb + uint64_t(nb) && pb < pa + uint64_t(na);
+}
+
+namespace {
 
 // Prefix the current message (copied first: vsnprintf must not read the
 // buffer it writes).
@@ -417,12 +427,6 @@ int64_t r_extent(const Resolved& R, int r, const int64_t* shape) {
     return far + R.L * R.e;
 }
 
-// Byte ranges [a, a + na) and [b, b + nb) share a byte.
-bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && pa < pb + uint64_t(nb) && pb < pa + uint64_t(na);
-}
-
 // x (or a gradient) is written in place while r1 and r2 are read: they must
 // not share bytes (a tensor's bytes: x whole, cos/sin from their first to
 // the end of their farthest row).
@@ -604,6 +608,112 @@ rope_status_t run_pos(int dir, void* x, const int32_t* positions, int dtype, int
     }
     const Seg seg{x, N, D, start};
     return launch_all(dir, mode, dtype, &seg, 1, nullptr, nullptr, R, B, S, stream, &pc);
+}
+
+// The positions call with several axes: the table of each pair's axis and
+// frequency is made here, the rest is the positions call's.
+rope_status_t run_axes(int dir, void* x, const int32_t* positions, int dtype, int64_t B, int64_t S,
+                       int64_t N, int64_t D, int32_t axes, const int32_t* sections,
+                       const int64_t* pos_shape, const int64_t* pos_stride, int order,
+                       int spectrum, double base, int64_t start, int64_t end, int mode,
+                       rope_stream_t stream) {
+    g_msg[0] = '\0';
+    if (mode != kInterleave && mode != kHalf)
+        return fail(ROPE_ERR_INVALID, "rotary mode %d is not interleave (1) or half (2)", mode);
+    if (order != ROPE_AXES_BLOCKED && order != ROPE_AXES_INTERLEAVED)
+        return fail(ROPE_ERR_INVALID, "axes order %d is not blocked (0) or interleaved (1)", order);
+    if (spectrum != ROPE_SPECTRUM_SHARED && spectrum != ROPE_SPECTRUM_OWN)
+        return fail(ROPE_ERR_INVALID, "spectrum %d is not shared (0) or own (1)", spectrum);
+    if (!(base > 0.0) || !isfinite(base))
+        return fail(ROPE_ERR_INVALID, "base %g must be a finite number > 0", base);
+    if (axes < 1 || axes > ROPE_MAX_AXES)
+        return fail(ROPE_ERR_INVALID, "%d axes; there must be 1 to %d", int(axes), ROPE_MAX_AXES);
+    const int64_t L = end - start;
+    const int64_t ones[4] = {1, 1, 1, L >= 0 ? L : 0};
+    const int64_t unit[4] = {0, 0, 0, 1};
+    Resolved R;
+    // a stand-in table lets check() apply the rules for x, as in run_pos()
+    rope_status_t st = check(x, x, x, dtype, B, S, N, D, ones, unit, ones, unit, start, end, &R);
+    if (st != ROPE_OK) return st;
+    if (!sections) {
+        if (R.empty) return ROPE_OK;
+        return fail(ROPE_ERR_NULLPTR, "sections is null");
+    }
+    int64_t sum = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 0)
+            return fail(ROPE_ERR_INVALID, "section %d is negative (%d)", a, int(sections[a]));
+        sum += sections[a];
+    }
+    if (sum != L / 2)
+        return fail(ROPE_ERR_INVALID, "the sections hold %lld pairs; the slice has %lld",
+                    (long long)sum, (long long)(L / 2));
+    if (R.empty) return ROPE_OK;
+    if (!positions) return fail(ROPE_ERR_NULLPTR, "positions is null");
+    if (!pos_shape || !pos_stride) return fail(ROPE_ERR_NULLPTR, "pos_shape or pos_stride is null");
+    if (pos_shape[0] != axes)
+        return fail(ROPE_ERR_INVALID, "positions dim 0 is %lld; it must be the %d axes",
+                    (long long)pos_shape[0], int(axes));
+    const int64_t dims[3] = {axes, B, S};
+    int64_t ps[3], reach = 0;
+    for (int k = 0; k < 3; ++k) {
+        if (!(pos_shape[k] == 1 || pos_shape[k] == dims[k]))
+            return fail(ROPE_ERR_INVALID, "positions dim %d is %lld; it must be 1 or %lld", k,
+                        (long long)pos_shape[k], (long long)dims[k]);
+        if (pos_shape[k] != 1 && pos_stride[k] < 0)
+            return fail(ROPE_ERR_INVALID, "positions stride %d is negative", k);
+        ps[k] = pos_shape[k] == 1 ? 0 : pos_stride[k];
+        if (mul_overflows(pos_shape[k] * 4, ps[k]))
+            return fail(ROPE_ERR_INVALID, "positions stride %d overflows", k);
+        reach += (pos_shape[k] - 1) * ps[k];
+    }
+    if (reinterpret_cast<uintptr_t>(positions) % 4)
+        return fail(ROPE_ERR_INVALID, "positions must be 4-byte aligned int32");
+    if (overlaps(x, B * S * N * D * R.e, positions, (reach + 1) * 4))
+        return fail(ROPE_ERR_INVALID, "positions overlap x, which is written in place");
+
+    AxisTable table;
+    table.pos_a = ps[0];
+    table.axes = axes;
+    int32_t dealt[ROPE_MAX_AXES] = {0, 0, 0, 0};
+    int a = 0;
+    const int64_t pairs = L / 2;
+    for (int64_t k = 0; k < pairs; ++k) {
+        // blocked: stay on an axis until it is full; interleaved: the next
+        // axis that still has pairs left
+        while (dealt[a] == sections[a]) a = a + 1 == axes ? 0 : a + 1;
+        const int32_t j = dealt[a]++;
+        table.axis[k] = static_cast<uint8_t>(a);
+        const double part = spectrum == ROPE_SPECTRUM_SHARED ? double(k) / double(pairs)
+                                                             : double(j) / double(sections[a]);
+        const double w = pow(base, -part);
+        table.hi[k] = static_cast<float>(w);
+        table.lo[k] = static_cast<float>(w - static_cast<double>(table.hi[k]));
+        if (order == ROPE_AXES_INTERLEAVED) a = a + 1 == axes ? 0 : a + 1;
+    }
+
+    const Seg seg{x, N, D, start};
+    Plan P;
+    st = make_plan(dir, mode, dtype, &seg, 1, nullptr, nullptr, R, &P, false, true);
+    if (st != ROPE_OK) return st;
+    KernelArgs whole = base_args(P, &seg, 1, nullptr, nullptr, R);
+    whole.pos = positions;
+    whole.pos_b = ps[1];
+    whole.pos_s = ps[2];
+    whole.pairs = static_cast<int32_t>(pairs);
+    const int64_t per_tok = int64_t(P.H) * P.C;
+    return for_each_piece(B, S, per_tok, [&](const Piece& pc) -> rope_status_t {
+        KernelArgs k = whole;
+        k.x += (pc.b0 * S + pc.s0) * whole.tok_bytes;
+        k.pos += pc.b0 * whole.pos_b + pc.s0 * whole.pos_s;
+        k.tasks = static_cast<uint32_t>(pc.count * per_tok);
+        k.divS = FastDiv::make(static_cast<uint32_t>(pc.sp));
+        const uint32_t blocks = static_cast<uint32_t>((int64_t(k.tasks) + kThreads - 1) / kThreads);
+        const char* err = nullptr;
+        if (launch_axes_piece(P, k, table, blocks, stream, &err) != ROPE_OK)
+            return fail(ROPE_ERR_CUDA, "%s", err);
+        return ROPE_OK;
+    });
 }
 
 }  // namespace
@@ -820,6 +930,31 @@ rope_status_t rope_partial_plan(const void* x, const void* r1, const void* r2,
                                 rope_plan_t* plan) {
     return rope_partial_plan_mode(x, r1, r2, dtype, B, S, N, D, r1_shape, r1_stride, r2_shape,
                                   r2_stride, start, end, ROPE_MODE_INTERLEAVE, sm_count, plan);
+}
+
+rope_status_t rope_partial_inplace_fwd_axes(void* x, const int32_t* positions, rope_dtype_t dtype,
+                                            int64_t B, int64_t S, int64_t N, int64_t D,
+                                            int32_t axes, const int32_t* sections,
+                                            const int64_t pos_shape[3], const int64_t pos_stride[3],
+                                            rope_axes_order_t order, rope_spectrum_t spectrum,
+                                            double base, int64_t start, int64_t end,
+                                            rope_mode_t mode, rope_stream_t stream) {
+    return rope::run_axes(rope::kFwd, x, positions, dtype, B, S, N, D, axes, sections, pos_shape,
+                          pos_stride, static_cast<int>(order), static_cast<int>(spectrum), base,
+                          start, end, static_cast<int>(mode), stream);
+}
+
+rope_status_t rope_partial_inplace_bwd_axes(void* grad, const int32_t* positions,
+                                            rope_dtype_t dtype, int64_t B, int64_t S, int64_t N,
+                                            int64_t D, int32_t axes, const int32_t* sections,
+                                            const int64_t pos_shape[3], const int64_t pos_stride[3],
+                                            rope_axes_order_t order, rope_spectrum_t spectrum,
+                                            double base, int64_t start, int64_t end,
+                                            rope_mode_t mode, rope_stream_t stream) {
+    return rope::run_axes(rope::kBwd, grad, positions, dtype, B, S, N, D, axes, sections,
+                          pos_shape, pos_stride, static_cast<int>(order),
+                          static_cast<int>(spectrum), base, start, end, static_cast<int>(mode),
+                          stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,127 @@
+// rope_tree_launch.cu -- kernel choice, grid, workspace and launches of the
+// attention over the cache.
+#include <mutex>
+#include <unordered_map>
+
+#include "rope_tree_kernels.cuh"
+
+namespace rope {
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int kBlocksPerSm = 8;  // no kernel here has more resident blocks an SM
+
+struct Resident {
+    int sms, per_sm;
+};
+
+std::mutex g_mu;
+std::unordered_map<const void*, Resident> g_resident[kMaxDevices];
+
+TreeKernel kernel_of(const TreePlan& p) {
+    switch (p.store) {
+        case ROPE_CACHE_BF16: return tree_kernel_bf16(p);
+        case ROPE_CACHE_FP16: return tree_kernel_fp16(p);
+        case ROPE_CACHE_FP8: return tree_kernel_fp8(p);
+        default: return tree_kernel_int8(p);
+    }
+}
+
+rope_status_t cuda_fail(cudaError_t e, const char** err) {
+    *err = cudaGetErrorString(e);
+    (void)cudaGetLastError();
+    return ROPE_ERR_CUDA;
+}
+
+// The kernel's resident blocks on the current device; the first call for a
+// device and kernel also allows its shared memory.
+rope_status_t resident(const TreeKernel& k, Resident* out, const char** err) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, err);
+    if (dev < 0 || dev >= kMaxDevices) {
+        *err = "device number out of range";
+        return ROPE_ERR_CUDA;
+    }
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto it = g_resident[dev].find(k.main);
+    if (it != g_resident[dev].end()) {
+        *out = it->second;
+        return ROPE_OK;
+    }
+    Resident r{};
+    e = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r.per_sm, k.main, kTreeThreads, k.smem);
+    if (e != cudaSuccess) return cuda_fail(e, err);
+    if (r.per_sm < 1) {
+        *err = "the attention kernel does not fit this device";
+        return ROPE_ERR_CUDA;
+    }
+    if (r.per_sm > kBlocksPerSm) r.per_sm = kBlocksPerSm;
+    g_resident[dev][k.main] = r;
+    *out = r;
+    return ROPE_OK;
+}
+
+rope_status_t launch(const void* f, dim3 grid, int threads, int smem, void** params,
+                     rope_stream_t stream, const char** err) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, f, params);
+    return e == cudaSuccess ? ROPE_OK : cuda_fail(e, err);
+}
+
+}  // namespace
+
+void choose_tree(int Dk, int Dv, int64_t rows, TreePlan* p) {
+    if (Dk <= 64) p->dk = 64, p->dv = 64;
+    else if (Dk <= 128) p->dk = 128, p->dv = 128;
+    else if (Dk <= 192 && Dv <= 128) p->dk = 192, p->dv = 128;
+    else p->dk = 256, p->dv = 256;
+    p->rows = p->dk == 256 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+rope_status_t tree_blocks(const TreePlan& p, int sm_count, int* blocks, const char** err) {
+    if (sm_count > 0) {
+        *blocks = sm_count * kBlocksPerSm;
+        return ROPE_OK;
+    }
+    Resident r;
+    const rope_status_t st = resident(kernel_of(p), &r, err);
+    if (st == ROPE_OK) *blocks = r.sms * r.per_sm;
+    return st;
+}
+
+int64_t tree_workspace(const TreePlan& p, int blocks) {
+    const int64_t rows = int64_t(2) * blocks * p.rows;
+    return rows * p.dv * int64_t(sizeof(float)) + rows * int64_t(sizeof(float2)) +
+           int64_t(blocks) * int64_t(sizeof(TreeMeta));
+}
+
+rope_status_t launch_tree(const TreePlan& p, const TreeArgs& args, void* workspace, int blocks,
+                          rope_stream_t stream, const char** err) {
+    const TreeKernel k = kernel_of(p);
+    TreeArgs a = args;
+    const int64_t rows = int64_t(2) * blocks * p.rows;
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part + rows * p.dv);
+    a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
+    void* params[] = {&a};
+    rope_status_t st = launch(k.main, dim3(blocks), kTreeThreads, k.smem, params, stream, err);
+    if (st != ROPE_OK || blocks < 2) return st;
+    float bias = k.bias;
+    void* join[] = {&a, &bias};
+    return launch(k.join, dim3(blocks - 1, p.rows / 16), kJoinThreads, 0, join, stream, err);
+}
+
+}  // namespace rope

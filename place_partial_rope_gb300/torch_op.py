@@ -26,6 +26,13 @@ inplace_partial_rotary_mul" (sections å‡½æ•°åŽŸåž‹ä¸Žå‚æ•°è¯´æ˜Ž, è‡ªåŠ¨å¾®åˆ†è
 * The backward writes into its own contiguous copy of the incoming gradient,
   so a gradient that autograd also hands to someone else (``retain_grad``,
   an expanded gradient of a sum) is never changed.
+
+Rotary positions with several axes, with the same rules (in place, Meta kernel,
+autograd; the positions get no gradient):
+
+    inplace_axes_rotary_mul(x, positions, sections, *, rotary_mode="interleave",
+                            partial_slice=None, base=10000.0, order="blocked",
+                            spectrum="shared") -> None
 """
 from __future__ import annotations
 
@@ -38,6 +45,8 @@ from . import binding
 NAMESPACE = "place_partial_rope"
 _FWD = "inplace_partial_rotary_mul"
 _BWD = "inplace_partial_rotary_mul_backward"
+_AXES_FWD = "inplace_axes_rotary_mul"
+_AXES_BWD = "inplace_axes_rotary_mul_backward"
 _MODES = ("interleave", "half")
 
 _lib = None
@@ -72,8 +81,39 @@ def _meta(x, r1, r2, rotary_mode="interleave", partial_slice=(0, 0)):
     return None
 
 
+def _check_axes(x, positions, sections, rotary_mode, partial_slice, order, spectrum) -> None:
+    if x.dim() != 4:
+        raise ValueError(f"inplace_axes_rotary_mul: x must be 4-D (B, S, N, D), got {x.dim()}-D")
+    if positions.dim() != 3 or positions.shape[0] != len(sections):
+        raise ValueError("inplace_axes_rotary_mul: positions must be 3-D (axes, B|1, S|1) with one "
+                         "section per axis")
+    if rotary_mode not in _MODES:
+        raise ValueError(f"inplace_axes_rotary_mul: rotary_mode must be 'interleave' or 'half', "
+                         f"got {rotary_mode!r}")
+    if len(partial_slice) != 2:
+        raise ValueError(f"inplace_axes_rotary_mul: partial_slice must hold 2 integers, "
+                         f"got {len(partial_slice)}")
+    if order not in binding.ORDER_CODE or spectrum not in binding.SPECTRUM_CODE:
+        raise ValueError(f"inplace_axes_rotary_mul: order {order!r} or spectrum {spectrum!r} is unknown")
+
+
+def _axes_impl(fn):
+    def call(x, positions, sections, rotary_mode="interleave", partial_slice=(0, 0), base=10000.0,
+             order="blocked", spectrum="shared"):
+        _check_axes(x, positions, sections, rotary_mode, partial_slice, order, spectrum)
+        fn(x, positions, sections, int(partial_slice[0]), int(partial_slice[1]), base, rotary_mode, order,
+           spectrum)
+    return call
+
+
+def _axes_meta(x, positions, sections, rotary_mode="interleave", partial_slice=(0, 0), base=10000.0,
+               order="blocked", spectrum="shared"):
+    _check_axes(x, positions, sections, rotary_mode, partial_slice, order, spectrum)
+    return None
+
+
 def register() -> None:
-    """Define the two operators once per process (idempotent)."""
+    """Define the operators once per process (idempotent)."""
     global _lib
     if _lib is not None:
         return
@@ -86,6 +126,13 @@ def register() -> None:
     lib.impl(_BWD, _cuda_bwd, "CUDA")
     lib.impl(_FWD, _meta, "Meta")
     lib.impl(_BWD, _meta, "Meta")
+    for name, arg, fn in ((_AXES_FWD, "x", binding.rope_partial_inplace_fwd_axes),
+                          (_AXES_BWD, "grad", binding.rope_partial_inplace_bwd_axes)):
+        lib.define(f"{name}(Tensor(a!) {arg}, Tensor positions, int[] sections, *, "
+                   "str rotary_mode='interleave', int[2] partial_slice=[0, 0], float base=10000.0, "
+                   "str order='blocked', str spectrum='shared') -> ()")
+        lib.impl(name, _axes_impl(fn), "CUDA")
+        lib.impl(name, _axes_meta, "Meta")
     _lib = lib
 
 
@@ -124,4 +171,42 @@ def inplace_partial_rotary_mul(x: torch.Tensor, r1: torch.Tensor, r2: torch.Tens
     else:
         getattr(torch.ops, NAMESPACE).inplace_partial_rotary_mul(
             x, r1, r2, rotary_mode=rotary_mode, partial_slice=ps)
+    return None
+
+
+class InplaceAxesRotaryMulFn(torch.autograd.Function):
+    """Autograd for the rotation with several axes: the positions get no gradient."""
+
+    @staticmethod
+    def forward(ctx, x, positions, sections, kwargs):
+        getattr(torch.ops, NAMESPACE).inplace_axes_rotary_mul(x, positions, sections, **kwargs)
+        ctx.mark_dirty(x)
+        ctx.save_for_backward(positions)
+        ctx.sections, ctx.kwargs = sections, kwargs
+        return x
+
+    @staticmethod
+    def backward(ctx, grad):
+        (positions,) = ctx.saved_tensors
+        g = grad.clone(memory_format=torch.contiguous_format)
+        getattr(torch.ops, NAMESPACE).inplace_axes_rotary_mul_backward(g, positions, ctx.sections, **ctx.kwargs)
+        return g, None, None, None
+
+
+def inplace_axes_rotary_mul(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int], *,
+                            rotary_mode: str = "interleave",
+                            partial_slice: Optional[Sequence[int]] = None, base: float = 10000.0,
+                            order: str = "blocked", spectrum: str = "shared") -> None:
+    """Rotate ``x[..., start:end]`` in place by positions on several axes
+    (int32, (axes, B|1, S|1)), ``sections[a]`` of the slice's pairs each; see
+    ``binding.rope_partial_inplace_fwd_axes``.  Returns None; x holds the result."""
+    register()
+    ps = [0, 0] if partial_slice is None else [int(v) for v in partial_slice]
+    sections = [int(v) for v in sections]
+    _check_axes(x, positions, sections, rotary_mode, ps, order, spectrum)
+    kwargs = dict(rotary_mode=rotary_mode, partial_slice=ps, base=float(base), order=order, spectrum=spectrum)
+    if x.requires_grad and torch.is_grad_enabled():
+        InplaceAxesRotaryMulFn.apply(x, positions, sections, kwargs)
+    else:
+        getattr(torch.ops, NAMESPACE).inplace_axes_rotary_mul(x, positions, sections, **kwargs)
     return None
