@@ -27,7 +27,8 @@ CU_SOURCES = ["rope_kernels_bf16.cu", "rope_kernels_fp16.cu", "rope_kernels_fp32
               "rope_launch.cu", "rope_axes_bf16.cu", "rope_axes_fp16.cu", "rope_axes_fp32.cu",
               "rope_axes_launch.cu", "rope_cache_bf16.cu", "rope_cache_fp16.cu",
               "rope_cache_fp32.cu", "rope_cache_launch.cu", "rope_tree_bf16.cu",
-              "rope_tree_fp16.cu", "rope_tree_fp8.cu", "rope_tree_int8.cu", "rope_tree_launch.cu"]
+              "rope_tree_fp16.cu", "rope_tree_fp8.cu", "rope_tree_int8.cu", "rope_tile_bf16.cu",
+              "rope_tile_fp16.cu", "rope_tile_fp8.cu", "rope_tile_int8.cu", "rope_tree_launch.cu"]
 CPP_SOURCES = ["rope_host.cpp", "rope_serving_host.cpp"]
 
 

@@ -9,7 +9,8 @@
 
 namespace rope {
 
-constexpr int kTreeThreads = 128;
+constexpr int kNarrowThreads = 128;
+constexpr int kTileThreads = 512;
 constexpr int kJoinThreads = 256;
 
 struct TreeArgs {
@@ -51,7 +52,7 @@ struct TreePlan {
     int dtype;    // rope_dtype_t of q
     int store;    // rope_cache_dtype_t
     int dk, dv;   // row lengths the kernel is built for (>= the call's)
-    int rows;     // query rows of a tile
+    int rows;     // query rows of a tile: 16, 128 or 256
 };
 
 // The kernel for rows of Dk and Dv and `rows` query rows a key head.

@@ -1,0 +1,467 @@
+// rope_tree_common.cuh -- what the attention kernels share: the division of
+// the work, the visibility of cache rows, the joining of parts.
+//
+// Units of work are (request, key head, row tile, cache tile), in that order;
+// every block takes an equal, contiguous run of them (one block per resident
+// slot), so a long request is spread over many blocks and short ones share a
+// block.  A block that holds a whole (request, head, row tile) writes the
+// result; one that holds a part writes (O, m, l), and rope_tree_join_kernel
+// puts the parts together.  Lengths are known on the device only: each block
+// sums them itself (no plan pass, no host synchronisation).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <string.h>
+
+#include "rope_tree.h"
+
+namespace rope {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// 16 bytes from global to shared memory, zeros when !ok.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void lds128(uint32_t* r, uint32_t at) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+__device__ __forceinline__ void lds64(uint32_t* r, uint32_t at) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at) : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// 2^x in one instruction (relative error 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    uint32_t u;
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        memcpy(&u, &h, 4);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        memcpy(&u, &h, 4);
+    }
+    return u;
+}
+
+// The two codes in the low half (high half) of w as an fp16 pair, exactly.
+//   fp8: a conversion instruction.  int8: the byte b ^ 128 = b + 128 under the
+// exponent of 1024 is the fp16 number 1024 + 128 + b.
+template <int STORE, bool HIGH>
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
+    uint32_t r;
+    if constexpr (STORE == ROPE_CACHE_FP8) {
+        const uint16_t x = static_cast<uint16_t>(HIGH ? w >> 16 : w & 0xffffu);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+    } else {
+        const uint32_t m = __byte_perm(w ^ 0x80808080u, 0x64646464u, HIGH ? 0x4342 : 0x4140);
+        __half2 h;
+        memcpy(&h, &m, 4);
+        h = __hsub2(h, __half2half2(__ushort_as_half(0x6480)));  // 1152
+        memcpy(&r, &h, 4);
+    }
+    return r;
+}
+
+// 16-bit values (the storage type's) that are not finite, and as numbers.
+template <int STORE>
+__device__ __forceinline__ bool not_finite(uint32_t x) {
+    constexpr uint32_t e = STORE == ROPE_CACHE_BF16 ? 0x7f80u : 0x7c00u;
+    return (x & e) == e;
+}
+
+template <int STORE>
+__device__ __forceinline__ float value16(uint32_t x) {
+    if constexpr (STORE == ROPE_CACHE_BF16) return __uint_as_float(x << 16);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(x)));
+}
+
+// The power of two of a query row's largest |q| (its bit pattern `most`),
+// kept within [2^-100, 2^100]; a row that is not finite needs none.
+__device__ __forceinline__ float row_power(uint32_t most) {
+    const uint32_t e = most & 0x7f800000u;
+    return __uint_as_float(most >= 0x7f800000u
+                               ? 0x3f800000u
+                               : min(max(e, uint32_t(27) << 23), uint32_t(227) << 23));
+}
+
+__device__ __forceinline__ float one_over_power(float p) {  // of a power of two
+    return __uint_as_float(0x7f000000u - __float_as_uint(p));
+}
+
+// The power of two above x, within [2^-120, 2^120].
+__device__ __forceinline__ float power_above(float x) {
+    const uint32_t e = (__float_as_uint(x) & 0x7f800000u) + 0x00800000u;
+    return __uint_as_float(min(max(e, uint32_t(7) << 23), uint32_t(247) << 23));
+}
+
+constexpr float kLeastPower = 7.5231638452626401e-37f;  // 2^-120
+
+// Eight 16-bit values of q as fp32.
+__device__ __forceinline__ void widen8(const uint4& x, bool bf16, float* f) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (bf16) {
+            f[2 * j] = __uint_as_float(w[j] << 16);
+            f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        } else {
+            __half2 h;
+            memcpy(&h, &w[j], 4);
+            const float2 v = __half22float2(h);
+            f[2 * j] = v.x;
+            f[2 * j + 1] = v.y;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t most_of(const float* f) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+    return m;
+}
+
+__device__ __forceinline__ uint4 half8(const float* f, float by) {
+    return make_uint4(pack2<false>(f[0] * by, f[1] * by), pack2<false>(f[2] * by, f[3] * by),
+                      pack2<false>(f[4] * by, f[5] * by), pack2<false>(f[6] * by, f[7] * by));
+}
+
+// ------------------------------------------------------------------------
+// the division of the work
+// ------------------------------------------------------------------------
+
+// Units of request r: key heads x row tiles x cache tiles (a request with no
+// cache rows still has a tile, so that its results are written).
+struct Request {
+    int qs, n, len, mt, nt;
+    int64_t units;
+};
+
+template <int ROWS, int TN>
+__device__ __forceinline__ Request request(const TreeArgs& a, int r) {
+    Request q;
+    const int lo = min(max(__ldg(a.q_start + r), 0), a.Tq);
+    const int hi = min(max(__ldg(a.q_start + r + 1), lo), a.Tq);
+    q.qs = lo;
+    q.n = hi - lo;
+    q.len = min(max(__ldg(a.kv_len + r), 0), a.max_len);
+    q.mt = static_cast<int>((int64_t(q.n) * a.G + ROWS - 1) / ROWS);
+    q.nt = max(1, (q.len + TN - 1) / TN);
+    q.units = q.n == 0 ? 0 : int64_t(a.Hk) * q.mt * q.nt;
+    return q;
+}
+
+// A block's units, and the request that holds the first of them.
+struct Place {
+    int r;
+    int64_t base, start, end, chunk;  // base: units before request r
+};
+
+// Sum the requests' units, cut them into equal runs, and find this block's.
+// All THREADS threads of the block take part; `scratch` holds THREADS / 32 + 2
+// numbers of shared memory.
+template <int ROWS, int TN, int THREADS>
+__device__ __forceinline__ Place find_place(const TreeArgs& a, int64_t* scratch) {
+    constexpr int WARPS = THREADS / 32;
+    int64_t* warp_sum = scratch;
+    int64_t* found = scratch + WARPS;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    int64_t mine = 0;
+    for (int r = tid; r < a.R; r += THREADS) mine += request<ROWS, TN>(a, r).units;
+#pragma unroll
+    for (int d = 16; d; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    if (lane == 0) warp_sum[warp] = mine;
+    if (tid == 0) found[0] = a.R;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < WARPS; ++w) total += warp_sum[w];
+    Place p;
+    p.chunk = (total + gridDim.x - 1) / gridDim.x;
+    if (p.chunk < 1) p.chunk = 1;
+    p.start = int64_t(blockIdx.x) * p.chunk;
+    p.end = min(p.start + p.chunk, total);
+    p.r = a.R;
+    p.base = 0;
+    if (p.start >= total) return p;  // the same for the whole block
+    int64_t before = 0;
+    for (int r0 = 0; r0 < a.R; r0 += THREADS) {
+        const int r = r0 + tid;
+        const int64_t u = r < a.R ? request<ROWS, TN>(a, r).units : 0;
+        int64_t sum = u;  // inclusive over the warp
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += x;
+        }
+        __syncthreads();  // warp_sum has been read
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        int64_t base = before + sum - u;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) base += warp_sum[w];
+            before += warp_sum[w];
+        }
+        if (u > 0 && p.start >= base && p.start < base + u) {
+            found[0] = r;
+            found[1] = base;
+        }
+        if (before > p.start) break;  // the same for the whole block
+    }
+    __syncthreads();
+    p.r = static_cast<int>(found[0]);
+    p.base = found[1];
+    return p;
+}
+
+// One run of a block: cache tiles [t0, t0 + count) of (request, head, row tile).
+struct RunAt {
+    Request rq;
+    int r, h, m, t0, count;
+    int64_t slot;  // where a part goes; -1: the run is whole
+};
+
+// A block's runs, one after the other; several warps may each walk them.
+template <int ROWS, int TN>
+struct Walk {
+    const TreeArgs& a;
+    int64_t u, base, end;
+    int r;
+    bool first;
+
+    __device__ __forceinline__ Walk(const TreeArgs& args, const Place& p)
+        : a(args), u(p.start), base(p.base), end(p.end), r(p.r), first(true) {}
+
+    __device__ __forceinline__ bool next(RunAt& x) {
+        while (u < end && r < a.R) {
+            const Request q = request<ROWS, TN>(a, r);
+            if (u >= base + q.units) {
+                base += q.units;
+                ++r;
+                continue;
+            }
+            const int64_t per = int64_t(q.mt) * q.nt, at = u - base;
+            x.rq = q;
+            x.r = r;
+            x.h = static_cast<int>(at / per);
+            const int rest = static_cast<int>(at - x.h * per);
+            x.m = rest / q.nt;
+            x.t0 = rest - x.m * q.nt;
+            x.count = static_cast<int>(min(int64_t(q.nt - x.t0), end - u));
+            x.slot = x.count == q.nt ? int64_t(-1) : int64_t(blockIdx.x) * 2 + (first ? 0 : 1);
+            first = false;
+            u += x.count;
+            return true;
+        }
+        return false;
+    }
+};
+
+// What the join kernel needs to know of a block: the group that its first run
+// belongs to, when that began in an earlier block.
+__device__ __forceinline__ TreeMeta meta_of(const Place& p, const RunAt& x) {
+    if (x.t0 == 0) return TreeMeta{0, p.chunk, 0, 0, 0, 0};
+    return TreeMeta{p.start - x.t0, p.chunk, x.r, x.h, x.m, x.rq.nt};
+}
+
+// Which of the 32 rows from j drafted token i of a request sees.
+__device__ __forceinline__ uint32_t sees32(const TreeArgs& a, int qs, int i, int prefix, int len, int j) {
+    const int cols = len - j;
+    if (cols <= 0) return 0u;
+    const uint32_t in = cols >= 32 ? 0xffffffffu : (1u << cols) - 1u;
+    const int jj = j - prefix;
+    if (jj <= -32) return in;
+    if (!a.tree) {
+        const int c = i - jj + 1;
+        return c <= 0 ? 0u : c >= 32 ? in : in & ((1u << c) - 1u);
+    }
+    const int from = max(jj, 0), w = from >> 6, sh = from & 63;
+    const unsigned long long* t =
+        reinterpret_cast<const unsigned long long*>(a.tree) + int64_t(qs + i) * a.words;
+    unsigned long long b = w < a.words ? __ldg(t + w) >> sh : 0ull;
+    if (sh > 32 && w + 1 < a.words) b |= __ldg(t + w + 1) << (64 - sh);
+    const uint32_t bits = static_cast<uint32_t>(b);
+    return in & (jj < 0 ? (bits << -jj) | ((1u << -jj) - 1u) : bits);
+}
+
+// A drafted row's 16-bit values that are not finite are taken out of the
+// product (a weight of 0 times infinity would reach the tokens that do not
+// see the row) and added here to the tokens that do see it, which end up not
+// finite in those columns whatever the weight: N columns from c of query row
+// `at`, over the drafted rows of the run's tiles.
+template <int STORE, int TN, int N>
+__device__ __noinline__ void add_not_finite(const TreeArgs& a, const RunAt x, int at, int c, float* o) {
+    const int i = static_cast<int>(a.div_group.div(uint32_t(at)));
+    const int prefix = x.rq.len - x.rq.n;
+    const int to = static_cast<int>(min(int64_t(x.rq.len), int64_t(x.t0 + x.count) * TN));
+    for (int j = max(max(prefix, 0), x.t0 * TN); j < to; ++j) {
+        if (!(sees32(a, x.rq.qs, i, prefix, x.rq.len, j) & 1u)) continue;
+        uint32_t p, off;
+        a.div_page.divmod(uint32_t(j), p, off);
+        const int page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
+        if (page < 0 || page >= a.pages) continue;
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v + page * a.v_st[0] + int64_t(off) * a.v_st[1] +
+                                                              int64_t(x.h) * a.v_st[2]);
+        for (int k = 0; k < N && c + k < a.Dv; ++k) {
+            const uint32_t y = __ldg(v + c + k);
+            if (not_finite<STORE>(y)) o[k] += value16<STORE>(y);
+        }
+    }
+}
+
+__device__ __forceinline__ void after_predecessor() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A result's place: row `at` of the request's n * G query rows of a key head.
+struct OutAt {
+    char* out;
+    float* lse;  // null: not wanted
+};
+
+__device__ __forceinline__ OutAt out_at(const TreeArgs& a, int qs, int h, int at) {
+    uint32_t tok, g;
+    a.div_group.divmod(uint32_t(at), tok, g);
+    const int64_t q = qs + int(tok), hq = h * a.G + int(g);
+    return OutAt{a.out + q * a.o_st[0] + hq * a.o_st[1], a.lse ? a.lse + q * a.Hq + hq : nullptr};
+}
+
+__device__ __forceinline__ float lse_of(float top, float l, float bias) {
+    return l == 0.0f ? -INFINITY : (top - bias + log2f(l)) * 0.69314718055994531f;
+}
+
+// Puts the parts of each split (request, head, row tile) together: out =
+// sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).  A group cut by s block
+// borders has s blocks here (the ones whose run begins inside it) that share
+// out its rows, so every block reads about as much as one of the main
+// kernel's blocks wrote; blockIdx.y cuts that further.  Groups of few parts
+// take a warp a row; of many, the whole block a row.  Bound by latency: the
+// parts were written just before and come from L2.
+template <int ROWS, int DV>
+__global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __grid_constant__ TreeArgs a,
+                                                                      float bias) {
+    constexpr int WARPS = kJoinThreads / 32, V = DV / 32;  // columns of a lane
+    __shared__ float sums[WARPS][DV];
+    __shared__ float sum_l[WARPS];
+    after_predecessor();
+    const int64_t b = int64_t(blockIdx.x) + 1;
+    const TreeMeta w = a.meta[b];
+    if (w.nt == 0) return;
+    const int64_t from = w.u0 / w.chunk, to = (w.u0 + w.nt - 1) / w.chunk;
+    const int parts = static_cast<int>(to - from + 1), cuts = parts - 1;
+    const int own = static_cast<int>(b - from - 1);
+    const int qs = min(max(__ldg(a.q_start + w.r), 0), a.Tq);
+    const int n = min(max(__ldg(a.q_start + w.r + 1), qs), a.Tq) - qs;
+    const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(w.m) * ROWS));
+    const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
+    const bool alone = parts <= WARPS;  // a warp a row
+
+    for (int k = int(blockIdx.y) + (alone ? warp * int(gridDim.y) : 0);; k += int(gridDim.y) * (alone ? WARPS : 1)) {
+        const int row = own + cuts * k;
+        if (row >= left) break;
+        // part p of the group: block `from` holds it second unless the group
+        // begins with the block's run; the others hold it first
+        auto slot = [&](int p) { return (from + p) * 2 + (p == 0 && from * w.chunk != w.u0 ? 1 : 0); };
+        float top = -INFINITY;
+        for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[slot(p) * ROWS + row].x);
+#pragma unroll
+        for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float base = top == -INFINITY ? 0.0f : top;
+        float o[V], l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = 0.0f;
+#pragma unroll 4
+        for (int p = alone ? 0 : warp; p < parts; p += alone ? 1 : WARPS) {
+            const int64_t s = slot(p) * ROWS + row;
+            const float2 x = a.part_ml[s];
+            const float f = pow2(x.x - base);
+            l += x.y * f;
+            const float2* src = reinterpret_cast<const float2*>(a.part + s * DV + lane * V);
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 y = src[i / 2];
+                o[i] += y.x * f;
+                o[i + 1] += y.y * f;
+            }
+        }
+        if (!alone) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) sums[warp][lane * V + i] = o[i];
+            if (lane == 0) sum_l[warp] = l;
+            __syncthreads();
+            l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = 0.0f;
+            if (warp == 0) {
+                for (int x = 0; x < WARPS; ++x) {
+                    l += sum_l[x];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[i] += sums[x][lane * V + i];
+                }
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+        }
+        const OutAt to_ = out_at(a, qs, w.h, w.m * ROWS + row);
+        if (lane == 0 && to_.lse) *to_.lse = lse_of(top, l, bias);
+        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        if (lane * V < a.Dv) {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(to_.out) + lane * V / 2;
+#pragma unroll
+            for (int i = 0; i < V; i += 2)
+                dst[i / 2] = a.bf16 ? pack2<true>(o[i] * f, o[i + 1] * f) : pack2<false>(o[i] * f, o[i + 1] * f);
+        }
+    }
+}
+
+struct TreeKernel {
+    const void* main;
+    const void* join;
+    int smem, threads;
+    float bias;
+};
+
+// defined in rope_tree_*.cu (up to 16 query rows) and rope_tile_*.cu
+TreeKernel narrow_kernel_bf16(const TreePlan& p);
+TreeKernel narrow_kernel_fp16(const TreePlan& p);
+TreeKernel narrow_kernel_fp8(const TreePlan& p);
+TreeKernel narrow_kernel_int8(const TreePlan& p);
+TreeKernel tile_kernel_bf16(const TreePlan& p);
+TreeKernel tile_kernel_fp16(const TreePlan& p);
+TreeKernel tile_kernel_fp8(const TreePlan& p);
+TreeKernel tile_kernel_int8(const TreePlan& p);
+
+}  // namespace rope

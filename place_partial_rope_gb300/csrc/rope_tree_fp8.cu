@@ -1,8 +1,14 @@
-// rope_tree_fp8.cu -- the attention kernels over fp8 caches.
-#include "rope_tree_kernels.cuh"
+// rope_tree_fp8.cu -- the attention kernels over fp8 caches, for up to 16 query
+// rows a key head (and rows of 256 lanes).
+#include "rope_tree_narrow.cuh"
 
 namespace rope {
 
-TreeKernel tree_kernel_fp8(const TreePlan& p) { return pick_tree<ROPE_CACHE_FP8>(p); }
+TreeKernel narrow_kernel_fp8(const TreePlan& p) {
+    if (p.dk == 64) return narrow_kernel<ROPE_CACHE_FP8, 64, 64>();
+    if (p.dk == 128) return narrow_kernel<ROPE_CACHE_FP8, 128, 128>();
+    if (p.dk == 192) return narrow_kernel<ROPE_CACHE_FP8, 192, 128>();
+    return narrow_kernel<ROPE_CACHE_FP8, 256, 256>();
+}
 
 }  // namespace rope

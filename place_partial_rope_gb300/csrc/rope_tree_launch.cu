@@ -3,7 +3,7 @@
 #include <mutex>
 #include <unordered_map>
 
-#include "rope_tree_kernels.cuh"
+#include "rope_tree_common.cuh"
 
 namespace rope {
 namespace {
@@ -19,11 +19,12 @@ std::mutex g_mu;
 std::unordered_map<const void*, Resident> g_resident[kMaxDevices];
 
 TreeKernel kernel_of(const TreePlan& p) {
+    const bool narrow = p.rows == 16;
     switch (p.store) {
-        case ROPE_CACHE_BF16: return tree_kernel_bf16(p);
-        case ROPE_CACHE_FP16: return tree_kernel_fp16(p);
-        case ROPE_CACHE_FP8: return tree_kernel_fp8(p);
-        default: return tree_kernel_int8(p);
+        case ROPE_CACHE_BF16: return narrow ? narrow_kernel_bf16(p) : tile_kernel_bf16(p);
+        case ROPE_CACHE_FP16: return narrow ? narrow_kernel_fp16(p) : tile_kernel_fp16(p);
+        case ROPE_CACHE_FP8: return narrow ? narrow_kernel_fp8(p) : tile_kernel_fp8(p);
+        default: return narrow ? narrow_kernel_int8(p) : tile_kernel_int8(p);
     }
 }
 
@@ -53,7 +54,7 @@ rope_status_t resident(const TreeKernel& k, Resident* out, const char** err) {
     e = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r.per_sm, k.main, kTreeThreads, k.smem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r.per_sm, k.main, k.threads, k.smem);
     if (e != cudaSuccess) return cuda_fail(e, err);
     if (r.per_sm < 1) {
         *err = "the attention kernel does not fit this device";
@@ -88,7 +89,7 @@ void choose_tree(int Dk, int Dv, int64_t rows, TreePlan* p) {
     else if (Dk <= 128) p->dk = 128, p->dv = 128;
     else if (Dk <= 192 && Dv <= 128) p->dk = 192, p->dv = 128;
     else p->dk = 256, p->dv = 256;
-    p->rows = p->dk == 256 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p->rows = p->dk == 256 || rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
 }
 
 rope_status_t tree_blocks(const TreePlan& p, int sm_count, int* blocks, const char** err) {
@@ -117,7 +118,7 @@ rope_status_t launch_tree(const TreePlan& p, const TreeArgs& args, void* workspa
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * p.dv);
     a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
     void* params[] = {&a};
-    rope_status_t st = launch(k.main, dim3(blocks), kTreeThreads, k.smem, params, stream, err);
+    rope_status_t st = launch(k.main, dim3(blocks), k.threads, k.smem, params, stream, err);
     if (st != ROPE_OK || blocks < 2) return st;
     float bias = k.bias;
     void* join[] = {&a, &bias};
