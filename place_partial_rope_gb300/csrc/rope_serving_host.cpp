@@ -332,7 +332,8 @@ rope_status_t tree_plan(const rope_kv_cache_t* c, int dtype, int64_t Hq, int64_t
         return fail(ROPE_ERR_INVALID, "max_q=%lld must be positive", (long long)max_q);
     p->dtype = dtype;
     p->store = c->dtype;
-    choose_tree(static_cast<int>(c->k_dim), static_cast<int>(c->v_dim), max_q * (Hq / c->heads), p);
+    choose_tree(static_cast<int>(c->k_dim), static_cast<int>(c->v_dim), max_q * (Hq / c->heads),
+                c->page_size, p);
     return ROPE_OK;
 }
 

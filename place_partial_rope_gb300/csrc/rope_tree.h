@@ -35,6 +35,7 @@ struct TreeArgs {
     int32_t words;
     int32_t R, Tq, Hk, G, Hq, Dk, Dv;
     int32_t pages, page_size, max_len;
+    int32_t box;                 // tile kernels: rows of a fetch, a power of two that divides page_size
     FastDiv div_page, div_group;
     float scale_log2;            // scale * log2(e)
     bool bf16;                   // type of q and out (the cache's own for 16 bits)
@@ -52,11 +53,12 @@ struct TreePlan {
     int dtype;    // rope_dtype_t of q
     int store;    // rope_cache_dtype_t
     int dk, dv;   // row lengths the kernel is built for (>= the call's)
-    int rows;     // query rows of a tile: 16, 128 or 256
+    int rows;     // query rows of a tile: 16 (narrow kernel), 128 or 256 (tile kernel)
 };
 
-// The kernel for rows of Dk and Dv and `rows` query rows a key head.
-void choose_tree(int Dk, int Dv, int64_t rows, TreePlan* p);
+// The kernel for rows of Dk and Dv, `rows` query rows a key head and pages of
+// `page_size` rows.
+void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, TreePlan* p);
 
 // The grid of a plan: the blocks that are resident on the device (sm_count
 // 0), or an upper bound of that for a device of sm_count SMs.

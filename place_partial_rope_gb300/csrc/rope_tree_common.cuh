@@ -316,8 +316,8 @@ __device__ __forceinline__ uint32_t sees32(const TreeArgs& a, int qs, int i, int
     return in & (jj < 0 ? (bits << -jj) | ((1u << -jj) - 1u) : bits);
 }
 
-// A drafted row's 16-bit values that are not finite are taken out of the
-// product (a weight of 0 times infinity would reach the tokens that do not
+// A drafted row's values that are not finite (8-bit: whose scale is not) are
+// taken out of the product (a weight of 0 times infinity would reach the tokens that do not
 // see the row) and added here to the tokens that do see it, which end up not
 // finite in those columns whatever the weight: N columns from c of query row
 // `at`, over the drafted rows of the run's tiles.
@@ -332,11 +332,18 @@ __device__ __noinline__ void add_not_finite(const TreeArgs& a, const RunAt x, in
         a.div_page.divmod(uint32_t(j), p, off);
         const int page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
         if (page < 0 || page >= a.pages) continue;
-        const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v + page * a.v_st[0] + int64_t(off) * a.v_st[1] +
-                                                              int64_t(x.h) * a.v_st[2]);
-        for (int k = 0; k < N && c + k < a.Dv; ++k) {
-            const uint32_t y = __ldg(v + c + k);
-            if (not_finite<STORE>(y)) o[k] += value16<STORE>(y);
+        if constexpr (STORE == ROPE_CACHE_BF16 || STORE == ROPE_CACHE_FP16) {
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v + page * a.v_st[0] + int64_t(off) * a.v_st[1] +
+                                                                  int64_t(x.h) * a.v_st[2]);
+            for (int k = 0; k < N && c + k < a.Dv; ++k) {
+                const uint32_t y = __ldg(v + c + k);
+                if (not_finite<STORE>(y)) o[k] += value16<STORE>(y);
+            }
+        } else {
+            // a scale that is not finite makes the whole row so
+            const float y = __ldg(a.vs + page * a.vs_st[0] + int64_t(off) * a.vs_st[1] + int64_t(x.h) * a.vs_st[2]);
+            if (!(fabsf(y) <= 3.4028234663852886e38f))
+                for (int k = 0; k < N; ++k) o[k] = NAN;
         }
     }
 }
@@ -451,6 +458,7 @@ struct TreeKernel {
     const void* main;
     const void* join;
     int smem, threads;
+    int tile;  // cache rows of a tile
     float bias;
 };
 

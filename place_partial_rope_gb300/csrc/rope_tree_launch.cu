@@ -3,6 +3,8 @@
 #include <mutex>
 #include <unordered_map>
 
+#include <cuda.h>
+
 #include "rope_tree_common.cuh"
 
 namespace rope {
@@ -66,6 +68,48 @@ rope_status_t resident(const TreeKernel& k, Resident* out, const char** err) {
     return ROPE_OK;
 }
 
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                            CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder() {
+    static const Encode f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<Encode>(p);
+    }();
+    return f;
+}
+
+// The map of a cache tensor: (lane, head, token of the page, page).  `lanes`
+// are those of a fetch: 64 of a 16-bit row, in the 128-byte swizzle, or a whole
+// row of codes.
+rope_status_t map_of(CUtensorMap* map, const void* base, int dim, const TreeArgs& a, const int64_t* st, bool wide,
+                     int lanes, const char** err) {
+    const Encode encode = encoder();
+    if (!encode) {
+        *err = "the driver has no cuTensorMapEncodeTiled";
+        return ROPE_ERR_CUDA;
+    }
+    // the stride of a dim of one is not looked at by the call: any valid one does
+    const cuuint64_t sizes[4] = {cuuint64_t(dim), cuuint64_t(a.Hk), cuuint64_t(a.page_size), cuuint64_t(a.pages)};
+    const cuuint64_t strides[3] = {a.Hk > 1 ? cuuint64_t(st[2]) : 16, a.page_size > 1 ? cuuint64_t(st[1]) : 16,
+                                   a.pages > 1 ? cuuint64_t(st[0]) : 16};
+    const cuuint32_t box[4] = {cuuint32_t(lanes), 1, cuuint32_t(a.box), 1}, steps[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+                              const_cast<void*>(base), sizes, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        *err = "the cache's sizes or strides do not fit a tensor map";
+        return ROPE_ERR_CUDA;
+    }
+    return ROPE_OK;
+}
+
 rope_status_t launch(const void* f, dim3 grid, int threads, int smem, void** params,
                      rope_stream_t stream, const char** err) {
     cudaLaunchAttribute attr[1];
@@ -84,12 +128,18 @@ rope_status_t launch(const void* f, dim3 grid, int threads, int smem, void** par
 
 }  // namespace
 
-void choose_tree(int Dk, int Dv, int64_t rows, TreePlan* p) {
+// Up to 16 query rows, the narrow kernel's matrix instructions waste less than
+// 128-row ones would: TODO measured.  Beyond that the tile kernel, with both
+// row tiles of a pair from 129 rows on, so that each cache row is fetched once
+// for 256 query rows.  It fetches boxes of at least 8 rows of a page; pages
+// that those do not divide, and rows of more than 192 lanes (whose O does not
+// fit tensor memory twice), stay with the narrow kernel.
+void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, TreePlan* p) {
     if (Dk <= 64) p->dk = 64, p->dv = 64;
     else if (Dk <= 128) p->dk = 128, p->dv = 128;
     else if (Dk <= 192 && Dv <= 128) p->dk = 192, p->dv = 128;
     else p->dk = 256, p->dv = 256;
-    p->rows = p->dk == 256 || rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+    p->rows = p->dk == 256 || rows <= 16 || page_size % 8 ? 16 : rows <= 128 ? 128 : 256;
 }
 
 rope_status_t tree_blocks(const TreePlan& p, int sm_count, int* blocks, const char** err) {
@@ -117,7 +167,16 @@ rope_status_t launch_tree(const TreePlan& p, const TreeArgs& args, void* workspa
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * p.dv);
     a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
-    void* params[] = {&a};
+    CUtensorMap km, vm;
+    if (p.rows != 16) {
+        const bool wide = p.store == ROPE_CACHE_BF16 || p.store == ROPE_CACHE_FP16;
+        a.box = 8;
+        while (a.page_size % (2 * a.box) == 0 && 2 * a.box <= k.tile) a.box *= 2;
+        rope_status_t st = map_of(&km, a.k, a.Dk, a, a.k_st, wide, wide ? 64 : p.dk, err);
+        if (st == ROPE_OK) st = map_of(&vm, a.v, a.Dv, a, a.v_st, wide, wide ? 64 : p.dv, err);
+        if (st != ROPE_OK) return st;
+    }
+    void* params[] = {&a, &km, &vm};  // the narrow kernel takes the first
     rope_status_t st = launch(k.main, dim3(blocks), k.threads, k.smem, params, stream, err);
     if (st != ROPE_OK || blocks < 2) return st;
     float bias = k.bias;

@@ -18,12 +18,14 @@
 //   0-3, 4-7  two softmax groups.  A thread owns a query row (a lane of tensor
 //             memory): it reads its row of s, makes p, writes p back over s as
 //             16-bit pairs, and keeps m and l.
-//   8-11      loads.  16-bit rows go from global to shared memory by cp.async;
-//             8-bit rows to a ring of each thread's own and from there, as
-//             fp16, to the tile.  Both put 128-byte lines of 64 lanes in the
-//             128-byte swizzle, the layout that the tensor pipe takes for keys
-//             (lanes contiguous along the sum) and values (along the columns)
-//             alike.  Gathered by page, so pages of any size do.
+//   13        fetches tiles by tensor copies, boxes of rows of one page, keys
+//             and values in rings of their own.
+//   8-11, 14, 15  helpers.  16-bit rows land in the layout that the tensor
+//             pipe takes (lines of 64 lanes in the 128-byte swizzle; the same
+//             for keys, whose lanes run along the sum, and values, whose lanes
+//             run along the columns), and helpers touch only the last tiles of a
+//             request.  8-bit rows land as codes, and helpers write them to
+//             such tiles as fp16.
 //   12        the one thread that issues tcgen05.mma: s = q k into tensor
 //             memory, O += p v with p from tensor memory.
 // Each softmax group has its own s (128 columns) and O (128 columns), all 512
@@ -34,7 +36,10 @@
 // then is read once for 256 rows.
 //   Every wait is bounded: a wait that gives up sets `dead`, later waits
 // return at once, and the run's rows come out as NaN.
+//   Page sizes that are no multiple of 8 are left to rope_tree_narrow.cuh.
 #pragma once
+#include <cuda.h>
+
 #include "rope_tree_common.cuh"
 
 namespace rope {
@@ -45,35 +50,47 @@ struct TileCfg {
     static constexpr bool PAIR = PAIR_;
     static constexpr bool kWide = STORE == ROPE_CACHE_BF16 || STORE == ROPE_CACHE_FP16;  // 16-bit codes
     static constexpr bool BF16 = STORE == ROPE_CACHE_BF16;
-    static constexpr int TN = (kWide && DK <= 128) || DK == 64 ? 128 : 64;  // cache rows of a tile
+    // cache rows of a tile: 128 where shared memory holds two tiles of that
+    // (a product of 64 columns takes three quarters of the time of 128)
+    static constexpr int TN = DK == 64 || (!PAIR && (kWide || DK == 128)) || (kWide && DK == 128) ? 128 : 64;
     static constexpr int ROWS = PAIR ? 256 : 128;
     static constexpr int QTILE = 128 * DK * 2, Q_BYTES = QTILE * (PAIR ? 2 : 1);
-    static constexpr int K_BYTES = TN * DK * 2, TILE = K_BYTES + TN * DV * 2;
-    // 8-bit: what the load warps hold as codes (and two scales a thread), and
-    // the scales of a tile with the largest value's scale of each load warp
-    static constexpr int RAW = kWide ? 0 : TN * (DK + DV) + 1024;
-    static constexpr int RAWS = kWide ? 0 : (PAIR && DK == 192 ? 1 : 3);
-    static constexpr int SC = kWide ? 0 : TN * 8 + 16;
-    static constexpr int MISC = 3072;
+    // keys and values have rings of their own: a tile's keys are done with when
+    // s is there, its values only after the softmax
+    static constexpr int K_SLOT = TN * DK * 2, V_SLOT = TN * DV * 2;
+    // 8-bit: the codes of a tile's keys or values, before they become fp16
+    static constexpr int RAW = kWide ? 0 : TN * DK;
+    static constexpr int RAWS = kWide ? 0 : (TN == 128 && DK == 128) || (PAIR && DK == 192) ? 3 : 4;
+    static constexpr int MISC = PAIR ? 512 : 2560;
     static constexpr int kSmemMax = 232448;
-    static constexpr int FIT = (kSmemMax - MISC - Q_BYTES - RAW * RAWS) / (TILE + SC);
-    static constexpr int STAGES = FIT > 4 ? 4 : FIT;
-    static constexpr int TILES_AT = Q_BYTES;
-    static constexpr int RAW_AT = TILES_AT + STAGES * TILE;
+    static constexpr int fit(int slots) {
+        return Q_BYTES + slots * (K_SLOT + V_SLOT) + RAWS * RAW + (kWide ? 0 : (slots + 2) * (TN * 8 + 16)) + MISC <=
+               kSmemMax;
+    }
+    static constexpr int SLOTS = fit(4) ? 4 : fit(3) ? 3 : 2;
+    // scales: a tile's outlive its keys' slot until the softmax, at most two
+    // tiles on
+    static constexpr int SCS = SLOTS + 2, SC = kWide ? 0 : TN * 8 + 16;
+    static constexpr int K_AT = Q_BYTES, V_AT = K_AT + SLOTS * K_SLOT;
+    static constexpr int RAW_AT = V_AT + SLOTS * V_SLOT;
     static constexpr int SC_AT = RAW_AT + RAWS * RAW;
-    static constexpr int MISC_AT = SC_AT + STAGES * SC;
-    // in MISC: (m, l) of both groups, then TileSync
-    static constexpr int ML_AT = MISC_AT, SYNC_AT = MISC_AT + 2048;
+    static constexpr int MISC_AT = SC_AT + SCS * SC;
+    // in MISC: (m, l) of both groups (split rows only), then TileSync
+    static constexpr int ML_AT = MISC_AT, SYNC_AT = MISC_AT + (PAIR ? 0 : 2048);
     static constexpr int SMEM = MISC_AT + MISC;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f;
     static constexpr float kLag = 8.0f;
-    static_assert(STAGES >= 2, "a tile in use and one on its way");
+    static_assert(fit(SLOTS), "two tiles fit");
 };
 
 constexpr uint32_t kSpins = 1u << 20;  // tries of one wait before it gives up
+constexpr uint32_t kPolls = 1u << 26;  // looks of the issuing thread, which does not pause
 
 struct TileSync {
-    unsigned long long full[4], empty[4], s_full[2], p_full[2], o_full[2], q_full, done;
+    unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
+    unsigned long long fix_full[4];                // 16-bit: values that the helpers see to first
+    unsigned long long raw_full[4], raw_empty[4];  // 8-bit: codes
+    unsigned long long s_full[2], p_full[2], o_full[2], q_full, done;
     uint32_t tmem;
     volatile uint32_t dead;
     volatile uint32_t patch[8];  // of run r at r % 8: values were taken out
@@ -96,6 +113,16 @@ __device__ __forceinline__ bool bar_test(unsigned long long* b, uint32_t parity)
     return ok != 0;
 }
 
+// Without the pause that try_wait may take: for a thread that looks at several.
+__device__ __forceinline__ bool bar_poll(unsigned long long* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(smem_addr(b)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity, TileSync* s) {
     for (uint32_t i = 0; i < kSpins; ++i) {
         if (bar_test(b, parity)) return;
@@ -106,6 +133,10 @@ __device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity,
 
 // The 256 threads of the softmax groups.
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The 192 threads that see to tiles between the fetch and the products.
+constexpr int kHelpers = 192;
+__device__ __forceinline__ void helpers_sync() { asm volatile("bar.sync 2, 192;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -181,6 +212,44 @@ __device__ __forceinline__ void mma_commit(unsigned long long* b) {
                  : "memory");
 }
 
+// Two fp32 operations in one instruction, each rounded as the single one.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long x, y, z, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    memcpy(&z, &c, 8);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    float2 r;
+    memcpy(&r, &d, 8);
+    return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long x, y, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    float2 r;
+    memcpy(&r, &d, 8);
+    return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long x, y, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    float2 r;
+    memcpy(&r, &d, 8);
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Column of tensor memory of group w's s (and p) and O.
 __host__ __device__ constexpr uint32_t s_col(int w) { return uint32_t(w) * 128; }
 __host__ __device__ constexpr uint32_t o_col(int w) { return 256 + uint32_t(w) * 128; }
@@ -194,31 +263,108 @@ struct Tile {
 
     // ---------------------------------------------------------- loads
 
-    // Rows of this warp: [rows0, rows0 + PER) of a tile; lane l looks up row
-    // rows0 + l.  `at` is -1 for a row that is not there.
-    struct Found {
-        int64_t k, v;  // bytes from the cache's start, -1: none
-        int64_t ks, vs;
+    // A tile's cache rows lie in boxes of a.box rows of one page (a power of
+    // two, 8 or more).  A lane asks for its box's page a tile ahead.
+    struct Look {
+        int page;  // as the table says; -1: no such rows
+        uint32_t off;
     };
-    static constexpr int PER = C::TN / 4;
 
-    __device__ __forceinline__ Found find(const RunAt& x, int tile, int rows0, int lane) const {
-        Found f{-1, -1, -1, -1};
-        const int j = tile * C::TN + rows0 + lane;
-        if (lane < PER && j < x.rq.len) {
-            uint32_t p, off;
-            a.div_page.divmod(uint32_t(j), p, off);
-            const int page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
-            if (page >= 0 && page < a.pages) {
-                f.k = page * a.k_st[0] + int64_t(off) * a.k_st[1] + int64_t(x.h) * a.k_st[2];
-                f.v = page * a.v_st[0] + int64_t(off) * a.v_st[1] + int64_t(x.h) * a.v_st[2];
-                if constexpr (!C::kWide) {
-                    f.ks = page * a.ks_st[0] + int64_t(off) * a.ks_st[1] + int64_t(x.h) * a.ks_st[2];
-                    f.vs = page * a.vs_st[0] + int64_t(off) * a.vs_st[1] + int64_t(x.h) * a.vs_st[2];
-                }
-            }
+    __device__ __forceinline__ Look look(const RunAt& x, int j) const {
+        Look f{-1, 0};
+        if (j < x.rq.len) {
+            uint32_t p;
+            a.div_page.divmod(uint32_t(j), p, f.off);
+            f.page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
         }
         return f;
+    }
+
+    // The keys or values of a tile (16-bit: 64 lanes of a row to a line, in
+    // planes; 8-bit: rows of codes) into shared memory.
+    template <int D>
+    __device__ __forceinline__ void fetch(const CUtensorMap* map, const Look& f, int h, uint32_t to, int lane,
+                                          unsigned long long* bar) const {
+        constexpr int BYTES = C::TN * D * (C::kWide ? 2 : 1);
+        if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(BYTES)
+                         : "memory");
+        __syncwarp();
+        if (lane < C::TN / a.box) {
+            constexpr int PLANES = C::kWide ? D / 64 : 1, LINE = C::kWide ? 128 : D;
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p)
+                asm volatile(
+                    "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                    "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + p * (C::TN * 128) + lane * a.box * LINE),
+                    "l"(map), "r"(p * 64), "r"(h), "r"(int(f.off)), "r"(f.page), "r"(smem_addr(bar))
+                    : "memory");
+        }
+    }
+
+    // The warp that fetches tiles, keys and values in turn, across runs, as far
+    // ahead as the rings allow.  Rows of pages that are not there (no such row,
+    // or a number outside the cache) are filled with zeros by the fetch.
+    __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* km, const CUtensorMap* vm) const {
+        const int lane = int(threadIdx.x) & 31;
+        constexpr uint32_t SLOTS = C::SLOTS, RAWS = C::RAWS > 0 ? C::RAWS : 1;
+        Walk<C::ROWS, C::TN> walk(a, place);
+        RunAt x;
+        bool more = walk.next(x);
+        Look now{-1, 0};
+        if (more) now = look(x, x.t0 * C::TN + lane * a.box);
+        int it = 0;
+        uint32_t n = 0, fix_par = 0, fixed = 0;  // a bit for each slot: fix_full's parity, and whether it was used last
+        for (; more && !sync->dead; ++n) {
+            const uint32_t slot = n % SLOTS;
+            const int tile = x.t0 + it, h = x.h;
+            const bool part = (tile + 1) * C::TN > x.rq.len - x.rq.n;  // more than context rows
+            if (it + 1 == x.count) {
+                more = walk.next(x);
+                it = 0;
+            } else {
+                ++it;
+            }
+            Look next{-1, 0};
+            if (more) next = look(x, (x.t0 + it) * C::TN + lane * a.box);
+#pragma unroll
+            for (int values = 0; values < 2; ++values) {
+                if constexpr (C::kWide) {
+                    if (n >= SLOTS)
+                        bar_wait(values ? &sync->v_empty[slot] : &sync->k_empty[slot], (n / SLOTS - 1) & 1, sync);
+                    if (values) {
+                        fixed = (fixed & ~(1u << slot)) | uint32_t(part) << slot;
+                        fix_par ^= uint32_t(part) << slot;
+                        fetch<C::DV>(vm, now, h, smem_addr(smem + C::V_AT) + slot * C::V_SLOT, lane,
+                                     part ? &sync->fix_full[slot] : &sync->v_full[slot]);
+                    } else {
+                        fetch<C::DK>(km, now, h, smem_addr(smem + C::K_AT) + slot * C::K_SLOT, lane, &sync->k_full[slot]);
+                    }
+                } else {
+                    const uint32_t item = 2 * n + values, r = item % RAWS;
+                    if (item >= RAWS) bar_wait(&sync->raw_empty[r], (item / RAWS - 1) & 1, sync);
+                    const uint32_t to = smem_addr(smem + C::RAW_AT) + r * C::RAW;
+                    if (values) fetch<C::DV>(vm, now, h, to, lane, &sync->raw_full[r]);
+                    else fetch<C::DK>(km, now, h, to, lane, &sync->raw_full[r]);
+                }
+            }
+            now = next;
+        }
+        if (!sync->dead) return;
+        // a wait gave up: the block may not end before its copies have
+        for (uint32_t k = n > SLOTS ? n - SLOTS : 0; C::kWide && k < n; ++k) {
+            const uint32_t slot = k % SLOTS, par = (k / SLOTS) & 1;
+            const bool f = fixed >> slot & 1;
+            landed(&sync->k_full[slot], par);
+            landed(f ? &sync->fix_full[slot] : &sync->v_full[slot], f ? ~(fix_par >> slot) & 1 : par);
+        }
+        for (uint32_t k = 2 * n > RAWS ? 2 * n - RAWS : 0; !C::kWide && k < 2 * n; ++k)
+            landed(&sync->raw_full[k % RAWS], (k / RAWS) & 1);
+    }
+
+    static __device__ __forceinline__ void landed(unsigned long long* b, uint32_t parity) {
+        for (uint32_t i = 0; i < kSpins && !bar_test(b, parity); ++i) {
+        }
     }
 
     // Where 16 bytes (8 lanes from 8 ch) of row `row` lie in a 16-bit tile.
@@ -226,171 +372,143 @@ struct Tile {
         return uint32_t(ch >> 3) * (C::TN * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
     }
 
-    // One side (keys or values) of a 16-bit tile.
+    // Codes to fp16, in a tile's layout; rows from `valid` on become zeros.
+    // Eight threads take 16 codes each of two successive rows: 64 of either row,
+    // in an order that meets all banks both reading rows of codes and writing
+    // lines (128 lanes: the second row's other half).
     template <int D>
-    __device__ __forceinline__ void copy_side(const char* base, int64_t mine, uint32_t to, int rows0, int lane,
-                                              int dim) const {
-        constexpr int CH = D / 8;  // chunks of a row
+    __device__ __forceinline__ void widen(uint32_t raw, uint32_t to, int id, int valid) const {
+        constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kHelpers / 8, N = (UNITS + STEP - 1) / STEP, B = 3;
+        const int odd = (id >> 2) & 1, c = id & 3;
 #pragma unroll
-        for (int i = 0; i < PER * CH / 32; ++i) {
-            const int idx = lane + 32 * i, row = idx / CH, ch = idx % CH;
-            const int64_t at = __shfl_sync(0xffffffffu, mine, row);
-            const bool ok = at >= 0 && ch * 8 < dim;
-            copy16(to + line_at(rows0 + row, ch), ok ? base + at + ch * 16 : base, ok);
-        }
-    }
-
-    // The same for 8-bit codes: the thread's own 16 bytes of `raw` (chunk i of
-    // thread t at 16 (128 i + t)).
-    template <int D>
-    __device__ __forceinline__ void copy_codes(const char* base, int64_t mine, uint32_t raw, int lane, int dim) const {
-        constexpr int CH = D / 16;
+        for (int i0 = 0; i0 < N; i0 += B) {
+            // a few loads, then their conversions: the loads do not wait for each other
+            uint32_t w[B][4];
 #pragma unroll
-        for (int i = 0; i < PER * CH / 32; ++i) {
-            const int idx = lane + 32 * i, row = idx / CH, ch = idx % CH;
-            const int64_t at = __shfl_sync(0xffffffffu, mine, row);
-            const bool ok = at >= 0 && ch * 16 < dim;
-            copy16(raw + i * 2048, ok ? base + at + ch * 16 : base, ok);
-        }
-    }
-
-    template <int D>
-    __device__ __forceinline__ void widen_codes(uint32_t raw, uint32_t to, int rows0, int lane) const {
-        constexpr int CH = D / 16;
-#pragma unroll
-        for (int i = 0; i < PER * CH / 32; ++i) {
-            const int idx = lane + 32 * i, row = rows0 + idx / CH, ch = idx % CH;
-            uint32_t w[4], h[8];
-            lds128(w, raw + i * 2048);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[2 * j] = codes_to_half2<C::STORE, false>(w[j]);
-                h[2 * j + 1] = codes_to_half2<C::STORE, true>(w[j]);
+            for (int i = 0; i < B; ++i) {
+                const int u = (id >> 3) + (i0 + i) * STEP, row = u / G * 2 + odd;
+                const int ch = ((G == 2 && odd ? u % G ^ 1 : u % G) << 2) + c;
+                if (i0 + i < N && u < UNITS) lds128(w[i], raw + row * D + ch * 16);
             }
-            sts128(to + line_at(row, 2 * ch), h[0], h[1], h[2], h[3]);
-            sts128(to + line_at(row, 2 * ch + 1), h[4], h[5], h[6], h[7]);
-        }
-    }
-
-    // 16-bit values of drafted rows that are not finite become zeros (see
-    // add_not_finite); the thread looks at what it copied itself.
-    static __device__ __noinline__ void take_out_not_finite(TileSync* sync, uint32_t to, int rows0, int lane,
-                                                            int from, uint32_t run) {
-        constexpr int CH = C::DV / 8;
-        for (int i = 0; i < PER * CH / 32; ++i) {
-            const int idx = lane + 32 * i, row = rows0 + idx / CH, ch = idx % CH;
-            if (row < from) continue;
-            uint32_t w[4];
-            lds128(w, to + line_at(row, ch));
-            bool found = false;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool lo = not_finite<C::STORE>(w[j] & 0xffffu), hi = not_finite<C::STORE>(w[j] >> 16);
-                if (lo || hi) {
-                    found = true;
-                    w[j] = (lo ? 0u : w[j] & 0xffffu) | (hi ? 0u : w[j] & 0xffff0000u);
+            for (int i = 0; i < B; ++i) {
+                const int u = (id >> 3) + (i0 + i) * STEP, row = u / G * 2 + odd;
+                const int ch = ((G == 2 && odd ? u % G ^ 1 : u % G) << 2) + c;
+                if (i0 + i >= N || u >= UNITS) continue;
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[2 * j] = codes_to_half2<C::STORE, false>(w[i][j]);
+                    h[2 * j + 1] = codes_to_half2<C::STORE, true>(w[i][j]);
                 }
-            }
-            if (found) {
-                sts128(to + line_at(row, ch), w[0], w[1], w[2], w[3]);
-                sync->patch[run] = 1;
+                if (row >= valid) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[j] = 0u;
+                }
+                sts128(to + line_at(row, 2 * ch), h[0], h[1], h[2], h[3]);
+                sts128(to + line_at(row, 2 * ch + 1), h[4], h[5], h[6], h[7]);
             }
         }
     }
 
-    static __device__ __forceinline__ void wait_all_but(uint32_t newer) {
-        if (newer == 0) copies_wait<0>();
-        else if (newer == 1) copies_wait<1>();
-        else if (newer == 2) copies_wait<2>();
-        else copies_wait<3>();
-    }
-
-    // The load warps.  Tiles are issued as far ahead as the ring allows, across
-    // runs, and arrive in order: a thread's copies are complete, its fence lets
-    // the tensor pipe see them, its arrival is one of 128.
-    __device__ __forceinline__ void loads(const Place& place) const {
-        const int lane = int(threadIdx.x) & 31, warp = (int(threadIdx.x) >> 5) & 3;
-        const int rows0 = warp * PER;
-        constexpr uint32_t AHEAD = C::kWide ? C::STAGES : C::RAWS;
+    // 8-bit: the helpers turn codes into fp16 tiles and bring the scales.
+    __device__ __forceinline__ void widen_tiles(const Place& place, int id) const {
+        constexpr uint32_t SLOTS = C::SLOTS, RAWS = C::RAWS > 0 ? C::RAWS : 1;
         Walk<C::ROWS, C::TN> walk(a, place);
         RunAt x;
-        bool more = walk.next(x);
-        uint32_t run = 0, issued = 0, arrived = 0;
-        int it = 0;
-        // of each tile on its way: the first row that is a drafted token's own
-        // (8 bits) and its run modulo 8
-        unsigned long long fifo = 0;
-        Found next{-1, -1, -1, -1};
-        if (more) next = find(x, x.t0, rows0, lane);
-
-        while (true) {
-            while (more && issued - arrived < AHEAD) {
-                if (C::kWide && issued >= uint32_t(C::STAGES)) {
-                    // the tile's place must be free; while others are on their
-                    // way, they come first
-                    const uint32_t st = issued % C::STAGES, par = (issued / C::STAGES - 1) & 1;
-                    if (issued == arrived) bar_wait(&sync->empty[st], par, sync);
-                    else if (!__all_sync(0xffffffffu, bar_test(&sync->empty[st], par) || sync->dead)) break;
+        uint32_t n = 0, run = 0;
+        while (walk.next(x)) {
+            Look now{-1, 0};
+            if (id < C::TN) now = look(x, x.t0 * C::TN + id);
+            for (int it = 0; it < x.count; ++it, ++n) {
+                const uint32_t slot = n % SLOTS;
+                const int j0 = (x.t0 + it) * C::TN;
+                float* sc = reinterpret_cast<float*>(smem + C::SC_AT + n % C::SCS * C::SC);
+                const bool there = now.page >= 0 && now.page < a.pages;
+                float scale[2] = {0.0f, 0.0f};
+                if (there) {
+                    scale[0] = __ldg(a.ks + now.page * a.ks_st[0] + int64_t(now.off) * a.ks_st[1] + int64_t(x.h) * a.ks_st[2]);
+                    scale[1] = __ldg(a.vs + now.page * a.vs_st[0] + int64_t(now.off) * a.vs_st[1] + int64_t(x.h) * a.vs_st[2]);
                 }
-                if constexpr (C::kWide) {
-                    const uint32_t to = smem_addr(smem + C::TILES_AT + issued % C::STAGES * C::TILE);
-                    copy_side<C::DK>(a.k, next.k, to, rows0, lane, a.Dk);
-                    copy_side<C::DV>(a.v, next.v, to + C::K_BYTES, rows0, lane, a.Dv);
-                    const int from = x.rq.len - x.rq.n - (x.t0 + it) * C::TN;
-                    fifo |= (unsigned long long)(min(max(from, 0), 255) | (run & 7) << 8) << (16 * (issued - arrived));
-                } else {
-                    const uint32_t raw = smem_addr(smem + C::RAW_AT + issued % AHEAD * C::RAW);
-                    const uint32_t mine = raw + (int(threadIdx.x) & 127) * 16;
-                    copy_codes<C::DK>(a.k, next.k, mine, lane, a.Dk);
-                    copy_codes<C::DV>(a.v, next.v, mine + C::TN * C::DK, lane, a.Dv);
-                    if (lane < PER) {
-                        const uint32_t sc = raw + C::TN * (C::DK + C::DV) + (int(threadIdx.x) & 127) * 8;
-                        copy4(sc, next.ks >= 0 ? a.ks + next.ks : a.ks, next.ks >= 0);
-                        copy4(sc + 4, next.vs >= 0 ? a.vs + next.vs : a.vs, next.vs >= 0);
+                if (id < C::TN && it + 1 < x.count) now = look(x, j0 + C::TN + id);
+                else now.page = -1;
+#pragma unroll
+                for (int values = 0; values < 2; ++values) {
+                    const uint32_t item = 2 * n + values, r = item % RAWS;
+                    bar_wait(&sync->raw_full[r], (item / RAWS) & 1, sync);
+                    if (n >= SLOTS)
+                        bar_wait(values ? &sync->v_empty[slot] : &sync->k_empty[slot], (n / SLOTS - 1) & 1, sync);
+                    const uint32_t raw = smem_addr(smem + C::RAW_AT) + r * C::RAW;
+                    if (values) widen<C::DV>(raw, smem_addr(smem + C::V_AT) + slot * C::V_SLOT, id, x.rq.len - j0);
+                    else widen<C::DK>(raw, smem_addr(smem + C::K_AT) + slot * C::K_SLOT, id, x.rq.len - j0);
+                    float v = scale[values];
+                    if (values) {
+                        // a drafted row's scale that is not finite is taken out (see add_not_finite)
+                        if (j0 + id >= x.rq.len - x.rq.n && !(fabsf(v) <= 3.4028234663852886e38f)) {
+                            v = 0.0f;
+                            sync->patch[run & 7] = 1;
+                        }
+                        if (id < C::TN) sc[C::TN + id] = v;
+#pragma unroll
+                        for (int d = 16; d; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                        if ((id & 31) == 0 && id < 128) sc[2 * C::TN + (id >> 5)] = v;
+                    } else if (id < C::TN) {
+                        sc[id] = v;
+                    }
+                    to_async_proxy();
+                    bar_arrive(&sync->raw_empty[r]);
+                    bar_arrive(values ? &sync->v_full[slot] : &sync->k_full[slot]);
+                }
+            }
+            ++run;
+        }
+    }
+
+    // 16-bit: in tiles with more than context rows, rows past the request's
+    // become zeros (what the page holds there may be anything), and so do
+    // drafted rows' values that are not finite (see add_not_finite).
+    __device__ __forceinline__ void mend_tiles(const Place& place, int id) const {
+        constexpr uint32_t SLOTS = C::SLOTS;
+        Walk<C::ROWS, C::TN> walk(a, place);
+        RunAt x;
+        uint32_t n = 0, run = 0, par = 0;  // a parity bit for each slot
+        while (walk.next(x)) {
+            const int prefix = x.rq.len - x.rq.n;
+            for (int it = 0; it < x.count; ++it, ++n) {
+                const int j0 = (x.t0 + it) * C::TN;
+                if (j0 + C::TN <= prefix) continue;
+                const uint32_t slot = n % SLOTS;
+                bar_wait(&sync->fix_full[slot], (par >> slot) & 1, sync);
+                par ^= 1u << slot;
+                const uint32_t to = smem_addr(smem + C::V_AT) + slot * C::V_SLOT;
+                const int from = max(prefix - j0, 0), valid = x.rq.len - j0;
+                constexpr int CH = C::DV / 8;
+                for (int i = from * CH + id; i < C::TN * CH; i += kHelpers) {
+                    const int row = i / CH;
+                    const uint32_t at = to + line_at(row, i % CH);
+                    if (row >= valid) {
+                        sts128(at, 0u, 0u, 0u, 0u);
+                        continue;
+                    }
+                    uint32_t w[4];
+                    lds128(w, at);
+                    bool found = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool lo = not_finite<C::STORE>(w[j] & 0xffffu), hi = not_finite<C::STORE>(w[j] >> 16);
+                        found = found || lo || hi;
+                        w[j] = (lo ? 0u : w[j] & 0xffffu) | (hi ? 0u : w[j] & 0xffff0000u);
+                    }
+                    if (found) {
+                        sts128(at, w[0], w[1], w[2], w[3]);
+                        sync->patch[run & 7] = 1;
                     }
                 }
-                copies_commit();
-                ++issued;
-                if (++it == x.count) {
-                    more = walk.next(x);
-                    ++run;
-                    it = 0;
-                }
-                if (more) next = find(x, x.t0 + it, rows0, lane);
+                to_async_proxy();
+                helpers_sync();
+                if (id == 0) bar_arrive(&sync->v_full[slot]);
             }
-            if (issued == arrived) break;
-            wait_all_but(issued - arrived - 1);
-            const uint32_t st = arrived % C::STAGES;
-            const uint32_t to = smem_addr(smem + C::TILES_AT + st * C::TILE);
-            if constexpr (C::kWide) {
-                const int from = int(fifo & 255);
-                if (from < C::TN) 
-                    take_out_not_finite(sync, to + C::K_BYTES, rows0, lane, from, uint32_t(fifo >> 8) & 7);
-                fifo >>= 16;
-            } else {
-                if (arrived >= uint32_t(C::STAGES))
-                    bar_wait(&sync->empty[st], (arrived / C::STAGES - 1) & 1, sync);
-                const uint32_t raw = smem_addr(smem + C::RAW_AT + arrived % AHEAD * C::RAW);
-                const uint32_t mine = raw + (int(threadIdx.x) & 127) * 16;
-                widen_codes<C::DK>(mine, to, rows0, lane);
-                widen_codes<C::DV>(mine + C::TN * C::DK, to + C::K_BYTES, rows0, lane);
-                float* sc = reinterpret_cast<float*>(smem + C::SC_AT + st * C::SC);
-                float v = 0.0f;
-                if (lane < PER) {
-                    const float2 y = *reinterpret_cast<const float2*>(
-                        smem + C::RAW_AT + arrived % AHEAD * C::RAW + C::TN * (C::DK + C::DV) +
-                        (int(threadIdx.x) & 127) * 8);
-                    sc[rows0 + lane] = y.x;
-                    sc[C::TN + rows0 + lane] = y.y;
-                    v = y.y;
-                }
-#pragma unroll
-                for (int d = 16; d; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                if (lane == 0) sc[2 * C::TN + warp] = v;
-            }
-            to_async_proxy();
-            bar_arrive(&sync->full[st]);
-            ++arrived;
+            ++run;
         }
     }
 
@@ -404,7 +522,8 @@ struct Tile {
         Walk<C::ROWS, C::TN> walk(a, place);
         RunAt x;
         uint32_t before = 0, q_par = 0, p_par[2] = {0, 0};
-        const uint32_t q_at = smem_addr(smem), tiles = smem_addr(smem + C::TILES_AT);
+        constexpr uint32_t SLOTS = C::SLOTS;
+        const uint32_t q_at = smem_addr(smem);
         while (walk.next(x)) {
             bar_wait(&sync->q_full, q_par, sync);
             q_par ^= 1;
@@ -416,40 +535,45 @@ struct Tile {
                 bool moved = false;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    if (s_next[w] > p_next[w] && bar_test(&sync->p_full[w], p_par[w])) {
-                        tmem_after();
+                    if (s_next[w] > p_next[w]) {
                         const int v = p_next[w], t = C::PAIR ? v >> 1 : v;
-                        const uint32_t st = (before + t) % C::STAGES;
-                        const uint32_t vs = tiles + st * C::TILE + C::K_BYTES;
+                        const uint32_t n = before + t, slot = n % SLOTS;
+                        if (bar_poll(&sync->p_full[w], p_par[w]) && bar_poll(&sync->v_full[slot], (n / SLOTS) & 1)) {
+                            tmem_after();
+                            const uint32_t vs = smem_addr(smem + C::V_AT) + slot * C::V_SLOT;
 #pragma unroll
-                        for (int k = 0; k < C::TN / 16; ++k)
-                            mma_ts(tmem + o_col(w), tmem + s_col(w) + 8 * k, smem_matrix(vs + k * 2048, C::TN * 128),
-                                   PV, v > 1 || k > 0);
-                        p_par[w] ^= 1;
-                        p_next[w] += 2;
-                        if (!C::PAIR || (p_next[1 - w] >> 1) > t) mma_commit(&sync->empty[st]);
-                        if (p_next[w] >= nv) mma_commit(&sync->o_full[w]);
-                        --left;
-                        moved = true;
+                            for (int k = 0; k < C::TN / 16; ++k)
+                                mma_ts(tmem + o_col(w), tmem + s_col(w) + 8 * k,
+                                       smem_matrix(vs + k * 2048, C::TN * 128), PV, v > 1 || k > 0);
+                            p_par[w] ^= 1;
+                            p_next[w] += 2;
+                            // a pair's slot is free when both have been there
+                            if (!C::PAIR || (p_next[1 - w] >> 1) > t) mma_commit(&sync->v_empty[slot]);
+                            if (p_next[w] >= nv) mma_commit(&sync->o_full[w]);
+                            --left;
+                            moved = true;
+                        }
                     }
                     if (s_next[w] == p_next[w] && s_next[w] < nv) {
                         const int t = C::PAIR ? s_next[w] >> 1 : s_next[w];
-                        const uint32_t n = before + t, st = n % C::STAGES;
-                        if (bar_test(&sync->full[st], (n / C::STAGES) & 1)) {
+                        const uint32_t n = before + t, slot = n % SLOTS;
+                        if (bar_poll(&sync->k_full[slot], (n / SLOTS) & 1)) {
                             tmem_after();
-                            const uint32_t ks = tiles + st * C::TILE, q = q_at + (C::PAIR ? w * C::QTILE : 0);
+                            const uint32_t ks = smem_addr(smem + C::K_AT) + slot * C::K_SLOT;
+                            const uint32_t q = q_at + (C::PAIR ? w * C::QTILE : 0);
 #pragma unroll
                             for (int k = 0; k < C::DK / 16; ++k)
                                 mma_ss(tmem + s_col(w), smem_matrix(q + (k >> 2) * 16384 + (k & 3) * 32, 16),
                                        smem_matrix(ks + (k >> 2) * (C::TN * 128) + (k & 3) * 32, 16), QK, k > 0);
                             mma_commit(&sync->s_full[w]);
                             s_next[w] += 2;
+                            if (!C::PAIR || (s_next[1 - w] >> 1) > t) mma_commit(&sync->k_empty[slot]);
                             moved = true;
                         }
                     }
                 }
                 if (moved) spins = 0;
-                else if (sync->dead || ++spins > kSpins) {
+                else if (sync->dead || ++spins > kPolls) {
                     sync->dead = 1;
                     break;
                 }
@@ -504,13 +628,16 @@ struct Tile {
         return factor;
     }
 
-    // Four sums or maxima side by side.
     template <int N>
     static __device__ __forceinline__ float max_of(const float* s) {
-        float m[4] = {s[0], s[1], s[2], s[3]};
+        float m[4] = {s[0], s[1], s[2], s[3]};  // four chains
 #pragma unroll
-        for (int j = 4; j < N; ++j) m[j & 3] = fmaxf(m[j & 3], s[j]);
-        return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        for (int j = 4; j + 8 <= N; j += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[j + 2 * i], s[j + 2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], s[N - 4 + i]);
+        return fmaxf(max3(m[0], m[1], m[2]), m[3]);
     }
 
     __device__ __forceinline__ void softmax(const Place& place, int w) const {
@@ -537,8 +664,8 @@ struct Tile {
 #pragma unroll 1
             for (int v = w; v < nv; v += 2) {
                 const int t = C::PAIR ? v >> 1 : v, j0 = (x.t0 + t) * C::TN;
-                const uint32_t n = before + t, st = n % C::STAGES;
-                const float* sc = reinterpret_cast<const float*>(smem + C::SC_AT + st * C::SC);
+                const uint32_t n = before + t;
+                const float* sc = reinterpret_cast<const float*>(smem + C::SC_AT + n % C::SCS * C::SC);
                 bar_wait(&sync->s_full[w], s_par, sync);
                 s_par ^= 1;
                 tmem_after();
@@ -548,14 +675,17 @@ struct Tile {
                     for (int c = 0; c < C::TN; c += 32) tmem_ld32(s + c, lanes + s_col(w) + c);
                     tmem_wait_ld();
                     if constexpr (!C::kWide) {
-                        bar_wait(&sync->full[st], (n / C::STAGES) & 1, sync);  // long since: the scales
+                        // the scales came with the keys and the values
+                        bar_wait(&sync->v_full[n % C::SLOTS], (n / C::SLOTS) & 1, sync);
 #pragma unroll
                         for (int j = 0; j < C::TN; j += 4) {
                             const float4 y = *reinterpret_cast<const float4*>(sc + j);
-                            s[j] *= y.x;
-                            s[j + 1] *= y.y;
-                            s[j + 2] *= y.z;
-                            s[j + 3] *= y.w;
+                            const float2 lo = mul2(make_float2(s[j], s[j + 1]), make_float2(y.x, y.y));
+                            const float2 hi = mul2(make_float2(s[j + 2], s[j + 3]), make_float2(y.z, y.w));
+                            s[j] = lo.x;
+                            s[j + 1] = lo.y;
+                            s[j + 2] = hi.x;
+                            s[j + 3] = hi.y;
                         }
                     }
                     if (j0 + C::TN > prefix) {
@@ -596,34 +726,34 @@ struct Tile {
                         }
                     }
                     const float base = C::kBias - (m == -INFINITY ? 0.0f : m);
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    const float back = C::kWide ? 1.0f : one_over_power(vref);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    const float2 fac = make_float2(factor, factor), off = make_float2(base, base);
+                    const float b1 = C::kWide ? 1.0f : one_over_power(vref);
+                    const float2 back = make_float2(b1, b1);
 #pragma unroll
                     for (int c = 0; c < C::TN; c += 32) {
                         uint32_t p[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
-                            float4 u = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-                            if constexpr (!C::kWide) u = *reinterpret_cast<const float4*>(sc + C::TN + c + j);
-                            float e[4];
+                            float2 e[2];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                e[i] = pow2(fmaf(s[c + j + i], factor, base));
-                                sum[i] += e[i];
+                            for (int i = 0; i < 2; ++i) {
+                                e[i] = fma2(make_float2(s[c + j + 2 * i], s[c + j + 2 * i + 1]), fac, off);
+                                e[i].x = pow2(e[i].x);
+                                e[i].y = pow2(e[i].y);
+                                sum[i] = add2(sum[i], e[i]);
                             }
                             if constexpr (!C::kWide) {
-                                // a row that is not seen adds nothing, whatever its scale
-                                e[0] = e[0] == 0.0f ? 0.0f : e[0] * (u.x * back);
-                                e[1] = e[1] == 0.0f ? 0.0f : e[1] * (u.y * back);
-                                e[2] = e[2] == 0.0f ? 0.0f : e[2] * (u.z * back);
-                                e[3] = e[3] == 0.0f ? 0.0f : e[3] * (u.w * back);
+                                const float4 u = *reinterpret_cast<const float4*>(sc + C::TN + c + j);
+                                e[0] = mul2(e[0], mul2(make_float2(u.x, u.y), back));
+                                e[1] = mul2(e[1], mul2(make_float2(u.z, u.w), back));
                             }
-                            p[j / 2] = pack2<C::BF16>(e[0], e[1]);
-                            p[j / 2 + 1] = pack2<C::BF16>(e[2], e[3]);
+                            p[j / 2] = pack2<C::BF16>(e[0].x, e[0].y);
+                            p[j / 2 + 1] = pack2<C::BF16>(e[1].x, e[1].y);
                         }
                         tmem_st16(lanes + s_col(w) + c / 2, p);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                 }
                 tmem_before();
@@ -700,9 +830,7 @@ struct Tile {
     // 32 columns from c of one row: the result, or the part.
     __device__ __forceinline__ void put(const RunAt& x, int row, int at, int c, float* o, float top, float l,
                                         bool patch) const {
-        if constexpr (C::kWide) {
-            if (patch) add_not_finite<C::STORE, C::TN, 32>(a, x, at, c, o);
-        }
+        if (patch) add_not_finite<C::STORE, C::TN, 32>(a, x, at, c, o);
         if (sync->dead) l = NAN;
         if (x.slot >= 0) {
             float4* to = reinterpret_cast<float4*>(a.part + (x.slot * C::ROWS + row) * C::DV + c);
@@ -730,14 +858,22 @@ struct Tile {
 };
 
 template <class C>
-__global__ void __launch_bounds__(kTileThreads, 1) rope_tree_tile_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kTileThreads, 1)
+rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap km,
+                      const __grid_constant__ CUtensorMap vm) {
     extern __shared__ __align__(1024) char smem[];
     TileSync* sync = reinterpret_cast<TileSync*>(smem + C::SYNC_AT);
     const int warp = int(threadIdx.x) >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
-            bar_init(&sync->full[i], 128);
-            bar_init(&sync->empty[i], 1);
+            // 16-bit: the fetch itself, or one helper for all; 8-bit: every helper
+            bar_init(&sync->k_full[i], C::kWide ? 1 : kHelpers);
+            bar_init(&sync->k_empty[i], 1);
+            bar_init(&sync->v_full[i], C::kWide ? 1 : kHelpers);
+            bar_init(&sync->v_empty[i], 1);
+            bar_init(&sync->fix_full[i], 1);
+            bar_init(&sync->raw_full[i], 1);
+            bar_init(&sync->raw_empty[i], kHelpers);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&sync->s_full[i], 1);
@@ -756,24 +892,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) rope_tree_tile_kernel(const _
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     after_predecessor();
-    const Place place = find_place<C::ROWS, C::TN, kTileThreads>(a, reinterpret_cast<int64_t*>(smem + C::ML_AT));
+    const Place place = find_place<C::ROWS, C::TN, kTileThreads>(a, reinterpret_cast<int64_t*>(smem));
     tmem_before();
     __syncthreads();
     tmem_after();
     const Tile<C> tile{a, smem, sync, sync->tmem};
 
-    // registers: 128 a thread at launch; 256 x 192 + 128 x 80 + 128 x 48 of
-    // the same 65536
+    // registers: 128 a thread at launch; 256 x 192 + 256 x 64 of the same 65536
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         tile.softmax(place, warp >> 2);
-    } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        tile.loads(place);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (threadIdx.x == 12 * 32) tile.products(place);
-        __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 12) {
+            if (threadIdx.x == 12 * 32) tile.products(place);
+            __syncwarp();
+        } else if (warp == 13) {
+            tile.fetches(place, &km, &vm);
+        } else {
+            const int id = int(threadIdx.x) - (warp < 12 ? 256 : 320);
+            if constexpr (C::kWide) tile.mend_tiles(place, id);
+            else tile.widen_tiles(place, id);
+        }
     }
     tmem_before();
     __syncthreads();
@@ -788,7 +928,7 @@ TreeKernel tile_kernel() {
     using C = TileCfg<STORE, DK, DV, PAIR>;
     return TreeKernel{reinterpret_cast<const void*>(&rope_tree_tile_kernel<C>),
                       reinterpret_cast<const void*>(&rope_tree_join_kernel<C::ROWS, DV>), C::SMEM, kTileThreads,
-                      C::kBias};
+                      C::TN, C::kBias};
 }
 
 }  // namespace rope
