@@ -6,7 +6,10 @@
 // and l shrink) only when the row's maximum has passed it by more than 2^8,
 // so p reaches 2^8 at most and the sums stay exact in fp32; O lives in tensor
 // memory, where rescaling it costs a read and a write of the whole
-// accumulator.  And the fp16 bias is 2^7, which leaves p below 2^15.
+// accumulator.  And the fp16 bias is 2^7, which leaves p below 2^15.  8-bit: O
+// and l are both kept in units of 1 / w (w the power of two above the values'
+// scales), so that a weight is 2^(s - m - log2 w) u, one product; w starts at
+// 2^-80.
 //
 // What bounds it.  128 x TN x (Dk + Dv) multiply-adds a tile against TN (Dk +
 // Dv) cache elements: 128 query rows take 1024 cycles of tensor pipe a tile
@@ -146,6 +149,8 @@ __device__ __forceinline__ void to_async_proxy() { asm volatile("fence.proxy.asy
 
 #define ROPE_R8(r, i) "=f"(r[i]), "=f"(r[i + 1]), "=f"(r[i + 2]), "=f"(r[i + 3]), "=f"(r[i + 4]), "=f"(r[i + 5]), \
                       "=f"(r[i + 6]), "=f"(r[i + 7])
+#define ROPE_B8(r, i) "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]), \
+                      "+f"(r[i + 6]), "+f"(r[i + 7])
 #define ROPE_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
                       "r"(r[i + 6]), "r"(r[i + 7])
 
@@ -157,6 +162,11 @@ __device__ __forceinline__ void tmem_ld32(float* r, uint32_t at) {
         : ROPE_R8(r, 0), ROPE_R8(r, 8), ROPE_R8(r, 16), ROPE_R8(r, 24)
         : "r"(at)
         : "memory");
+}
+
+// After tmem_wait_ld: what was loaded is not touched before this.
+__device__ __forceinline__ void tmem_here32(float* r) {
+    asm volatile("" : ROPE_B8(r, 0), ROPE_B8(r, 8), ROPE_B8(r, 16), ROPE_B8(r, 24));
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
@@ -377,12 +387,14 @@ struct Tile {
     // in an order that meets all banks both reading rows of codes and writing
     // lines (128 lanes: the second row's other half).
     template <int D>
-    __device__ __forceinline__ void widen(uint32_t raw, uint32_t to, int id, int valid) const {
+    static __device__ __noinline__ void widen(uint32_t raw, uint32_t to, int id, int valid) {
         constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kHelpers / 8, N = (UNITS + STEP - 1) / STEP, B = 3;
         const int odd = (id >> 2) & 1, c = id & 3;
-#pragma unroll
+#pragma unroll 1
         for (int i0 = 0; i0 < N; i0 += B) {
-            // a few loads, then their conversions: the loads do not wait for each other
+            // a few loads, then their conversions: the loads do not wait for each
+            // other (and the loop stays small: the kernel's roles share the
+            // instruction cache)
             uint32_t w[B][4];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
@@ -432,16 +444,17 @@ struct Tile {
                 }
                 if (id < C::TN && it + 1 < x.count) now = look(x, j0 + C::TN + id);
                 else now.page = -1;
-#pragma unroll
+#pragma unroll 1
                 for (int values = 0; values < 2; ++values) {
                     const uint32_t item = 2 * n + values, r = item % RAWS;
                     bar_wait(&sync->raw_full[r], (item / RAWS) & 1, sync);
                     if (n >= SLOTS)
                         bar_wait(values ? &sync->v_empty[slot] : &sync->k_empty[slot], (n / SLOTS - 1) & 1, sync);
                     const uint32_t raw = smem_addr(smem + C::RAW_AT) + r * C::RAW;
-                    if (values) widen<C::DV>(raw, smem_addr(smem + C::V_AT) + slot * C::V_SLOT, id, x.rq.len - j0);
-                    else widen<C::DK>(raw, smem_addr(smem + C::K_AT) + slot * C::K_SLOT, id, x.rq.len - j0);
-                    float v = scale[values];
+                    const uint32_t to = smem_addr(smem) + (values ? C::V_AT + slot * C::V_SLOT : C::K_AT + slot * C::K_SLOT);
+                    if (C::DV == C::DK || !values) widen<C::DK>(raw, to, id, x.rq.len - j0);
+                    else widen<C::DV>(raw, to, id, x.rq.len - j0);
+                    float v = values ? scale[1] : scale[0];
                     if (values) {
                         // a drafted row's scale that is not finite is taken out (see add_not_finite)
                         if (j0 + id >= x.rq.len - x.rq.n && !(fabsf(v) <= 3.4028234663852886e38f)) {
@@ -596,48 +609,116 @@ struct Tile {
         if (there) a.div_group.divmod(uint32_t(at), tok, g);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] +
                                                           int64_t(x.h * a.G + int(g)) * a.q_st[1]);
+        // the whole row in flight at once
+        constexpr int CH = C::DK / 8;
         const int chunks = there ? a.Dk / 8 : 0;
+        uint4 y[CH];
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) y[ch] = ch < chunks ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
         float factor = a.scale_log2, down = 1.0f;
         if constexpr (!C::kWide) {
             uint32_t most = 0;
-#pragma unroll 4
-            for (int ch = 0; ch < chunks; ++ch) {
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
                 float f[8];
-                widen8(__ldg(src + ch), a.bf16, f);
+                widen8(y[ch], a.bf16, f);
                 most = max(most, most_of(f));
             }
             const float p = row_power(most);
             down = one_over_power(p);
             factor *= p;
         }
-        // up to 128 rows, both groups' threads of a row take half of it each
-        constexpr int CH = C::DK / 8, N = C::PAIR ? CH : CH / 2;
-        const int first = C::PAIR ? 0 : w * N;
+        // up to 128 rows, both groups' threads of a row store half of it each
         const uint32_t to = smem_addr(smem) + (C::PAIR ? w * C::QTILE : 0) + row * 128;
-#pragma unroll 4
-        for (int i = 0; i < N; ++i) {
-            const int ch = first + i;
-            uint4 y = ch < chunks ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+            if (!C::PAIR && (ch & 1) != w) continue;
             if constexpr (!C::kWide) {
                 float f[8];
-                widen8(y, a.bf16, f);
-                y = half8(f, down);
+                widen8(y[ch], a.bf16, f);
+                y[ch] = half8(f, down);
             }
-            sts128(to + (ch >> 3) * 16384 + (((ch & 7) ^ (row & 7)) << 4), y.x, y.y, y.z, y.w);
+            sts128(to + (ch >> 3) * 16384 + (((ch & 7) ^ (row & 7)) << 4), y[ch].x, y[ch].y, y[ch].z, y[ch].w);
         }
         return factor;
     }
 
-    template <int N>
-    static __device__ __forceinline__ float max_of(const float* s) {
+    // 32 scores of a row: times the keys' scales (8-bit), and -inf where the
+    // token does not see the row.
+    static __device__ __forceinline__ void scores32(float* s, const float* scale, uint32_t bits) {
+        if constexpr (!C::kWide) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(scale + j);
+                const float2 lo = mul2(make_float2(s[j], s[j + 1]), make_float2(y.x, y.y));
+                const float2 hi = mul2(make_float2(s[j + 2], s[j + 3]), make_float2(y.z, y.w));
+                s[j] = lo.x;
+                s[j + 1] = lo.y;
+                s[j + 2] = hi.x;
+                s[j + 3] = hi.y;
+            }
+        }
+        if (bits != 0xffffffffu) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1u)) s[j] = -INFINITY;
+        }
+    }
+
+    static __device__ __forceinline__ float max_of32(const float* s) {
         float m[4] = {s[0], s[1], s[2], s[3]};  // four chains
 #pragma unroll
-        for (int j = 4; j + 8 <= N; j += 8)
+        for (int j = 4; j + 8 <= 32; j += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[j + 2 * i], s[j + 2 * i + 1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], s[N - 4 + i]);
+        for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], s[28 + i]);
         return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+    }
+
+    // The weights of 32 scores: their sum, and the 16-bit pairs at `to`.
+    static __device__ __forceinline__ void weights32(const float* s, const float* scale, float factor, float base,
+                                                     float2* sum, uint32_t to) {
+        const float2 fac = make_float2(factor, factor), off = make_float2(base, base);
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            float2 e[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                e[i] = fma2(make_float2(s[j + 2 * i], s[j + 2 * i + 1]), fac, off);
+                e[i].x = pow2(e[i].x);
+                e[i].y = pow2(e[i].y);
+                sum[i] = add2(sum[i], e[i]);
+            }
+            if constexpr (!C::kWide) {
+                const float4 u = *reinterpret_cast<const float4*>(scale + j);
+                e[0] = mul2(e[0], make_float2(u.x, u.y));
+                e[1] = mul2(e[1], make_float2(u.z, u.w));
+            }
+            p[j / 2] = pack2<C::BF16>(e[0].x, e[0].y);
+            p[j / 2 + 1] = pack2<C::BF16>(e[1].x, e[1].y);
+        }
+        tmem_st16(to, p);
+    }
+
+    // O of the thread's row times f.  The group's product before is complete: s
+    // of this tile came after it.
+    static __device__ __forceinline__ void rescale(uint32_t at, float f) {
+#pragma unroll 1
+        for (int c = 0; c < C::DV; c += 32) {
+            float o[32];
+            tmem_ld32(o, at + c);
+            tmem_wait_ld();
+            tmem_here32(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= f;
+            tmem_st32(at + c, reinterpret_cast<const uint32_t*>(o));
+        }
+    }
+
+    static __device__ __forceinline__ float exponent(float power) {  // of a power of two
+        return float(int(__float_as_uint(power) >> 23) - 127);
     }
 
     __device__ __forceinline__ void softmax(const Place& place, int w) const {
@@ -659,7 +740,7 @@ struct Tile {
             const bool active = at - (row & 31) < rows;  // the warp has a row
             const int tok = min(int(a.div_group.div(uint32_t(at))), x.rq.n - 1);
             const int prefix = x.rq.len - x.rq.n, nv = C::PAIR ? 2 * x.count : x.count;
-            float m = -INFINITY, l = 0.0f, vref = kLeastPower;
+            float m = -INFINITY, l = 0.0f, vref = 8.2718061255302767e-25f;  // 2^-80
 
 #pragma unroll 1
             for (int v = w; v < nv; v += 2) {
@@ -670,89 +751,42 @@ struct Tile {
                 s_par ^= 1;
                 tmem_after();
                 if (active) {
+                    const bool part = j0 + C::TN > prefix;  // more than context rows
+                    if constexpr (!C::kWide) {
+                        // the scales came with the keys and the values
+                        bar_wait(&sync->v_full[n % C::SLOTS], (n / C::SLOTS) & 1, sync);
+                        const float4 y = *reinterpret_cast<const float4*>(sc + 2 * C::TN);
+                        const float u = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+                        if (u > vref) {
+                            const float p = power_above(u), f = vref / p;
+                            vref = p;
+                            l *= f;
+                            if (v > 1) rescale(lanes + o_col(w), f);
+                        }
+                    }
                     float s[C::TN];
 #pragma unroll
                     for (int c = 0; c < C::TN; c += 32) tmem_ld32(s + c, lanes + s_col(w) + c);
                     tmem_wait_ld();
-                    if constexpr (!C::kWide) {
-                        // the scales came with the keys and the values
-                        bar_wait(&sync->v_full[n % C::SLOTS], (n / C::SLOTS) & 1, sync);
-#pragma unroll
-                        for (int j = 0; j < C::TN; j += 4) {
-                            const float4 y = *reinterpret_cast<const float4*>(sc + j);
-                            const float2 lo = mul2(make_float2(s[j], s[j + 1]), make_float2(y.x, y.y));
-                            const float2 hi = mul2(make_float2(s[j + 2], s[j + 3]), make_float2(y.z, y.w));
-                            s[j] = lo.x;
-                            s[j + 1] = lo.y;
-                            s[j + 2] = hi.x;
-                            s[j + 3] = hi.y;
-                        }
-                    }
-                    if (j0 + C::TN > prefix) {
-#pragma unroll
-                        for (int c = 0; c < C::TN; c += 32) {
-                            const uint32_t bits = sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!(bits >> j & 1u)) s[c + j] = -INFINITY;
-                        }
-                    }
-                    const float top = max_of<C::TN>(s) * factor;
-                    const bool up = top > m + C::kLag || (m == -INFINITY && top > m);
-                    float shrink = 1.0f;
-                    if (up) {
-                        shrink = pow2(m - top);
-                        m = top;
-                        l *= shrink;
-                    }
-                    if constexpr (!C::kWide) {
-                        const float4 y = *reinterpret_cast<const float4*>(sc + 2 * C::TN);
-                        const float u = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-                        if (u > vref) {
-                            const float p = power_above(u);
-                            shrink *= vref / p;
-                            vref = p;
-                        }
-                    }
-                    if (v > 1 && __any_sync(0xffffffffu, shrink != 1.0f)) {
-#pragma unroll 1
-                        for (int c = 0; c < C::DV; c += 32) {
-                            float o[32];
-                            tmem_ld32(o, lanes + o_col(w) + c);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= shrink;
-                            tmem_st32(lanes + o_col(w) + c, reinterpret_cast<const uint32_t*>(o));
-                        }
-                    }
-                    const float base = C::kBias - (m == -INFINITY ? 0.0f : m);
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    const float2 fac = make_float2(factor, factor), off = make_float2(base, base);
-                    const float b1 = C::kWide ? 1.0f : one_over_power(vref);
-                    const float2 back = make_float2(b1, b1);
+                    float top = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < C::TN; c += 32) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            float2 e[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                e[i] = fma2(make_float2(s[c + j + 2 * i], s[c + j + 2 * i + 1]), fac, off);
-                                e[i].x = pow2(e[i].x);
-                                e[i].y = pow2(e[i].y);
-                                sum[i] = add2(sum[i], e[i]);
-                            }
-                            if constexpr (!C::kWide) {
-                                const float4 u = *reinterpret_cast<const float4*>(sc + C::TN + c + j);
-                                e[0] = mul2(e[0], mul2(make_float2(u.x, u.y), back));
-                                e[1] = mul2(e[1], mul2(make_float2(u.z, u.w), back));
-                            }
-                            p[j / 2] = pack2<C::BF16>(e[0].x, e[0].y);
-                            p[j / 2 + 1] = pack2<C::BF16>(e[1].x, e[1].y);
-                        }
-                        tmem_st16(lanes + s_col(w) + c / 2, p);
+                        tmem_here32(s + c);
+                        scores32(s + c, sc + c, part ? sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c) : 0xffffffffu);
+                        top = fmaxf(top, max_of32(s + c));
                     }
+                    top *= factor;
+                    const bool up = top > m + C::kLag || (m == -INFINITY && top > m);
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float f = up ? pow2(m - top) : 1.0f;
+                        if (up) m = top;
+                        l *= f;
+                        if (v > 1) rescale(lanes + o_col(w), f);
+                    }
+                    const float base = C::kBias - (m == -INFINITY ? 0.0f : m) - (C::kWide ? 0.0f : exponent(vref));
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int c = 0; c < C::TN; c += 32) weights32(s + c, sc + C::TN + c, factor, base, sum, lanes + s_col(w) + c / 2);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                 }
@@ -764,6 +798,7 @@ struct Tile {
                 o_par ^= 1;
                 tmem_after();
             }
+            if constexpr (!C::kWide) l *= vref;
             finish(x, w, row, at, at < rows, active, nv, m, l, vref, sync->patch[run & 7] != 0, ml, lanes);
             tmem_before();
             groups_sync();  // queries, O and ml are done with
@@ -774,86 +809,105 @@ struct Tile {
         if (tid == 0) a.meta[blockIdx.x] = meta;
     }
 
-    // The results of a run.
+    // The results of a run.  A thread holds a row, which it would write 16 bytes
+    // at a time, 32 rows an instruction; rows go through shared memory (the
+    // queries' place; 32 words of 32 rows a warp, words swizzled by the row), so
+    // that a warp writes 128 bytes of a row at once.
     __device__ __forceinline__ void finish(const RunAt& x, int w, int row, int at, bool there, bool active, int nv,
                                            float m, float l, float vref, bool patch, float2* ml,
                                            uint32_t lanes) const {
         float f = C::kWide ? 1.0f : vref;
-        if (C::PAIR || nv == 1) {
-            // one group has the row to itself
-            if ((C::PAIR || w == 0) && active) {
-#pragma unroll 1
-                for (int c = 0; c < C::DV; c += 32) {
-                    float o[32];
-                    tmem_ld32(o, lanes + o_col(w) + c);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] *= f;
-                    if (there) put(x, (C::PAIR ? 128 * w : 0) + row, at, c, o, m, l, patch);
-                }
-            }
-            return;
+        const bool alone = C::PAIR || nv == 1;  // one group has the row to itself
+        const int lane = row & 31;
+        float top = m;
+        if (!alone) {
+            // the groups took turns at the tiles
+            ml[w * 128 + row] = make_float2(m, l);
+            groups_sync();
+            const float2 other = ml[(1 - w) * 128 + row];
+            top = fmaxf(m, other.x);
+            const float base = top == -INFINITY ? 0.0f : top, own = pow2(m - base);
+            f *= own;
+            l = l * own + other.y * pow2(other.x - base);
         }
-        // the groups took turns at the tiles: group 1's sums go through shared
-        // memory (the queries' place, a column of rows at a time) to group 0
-        ml[w * 128 + row] = make_float2(m, l);
-        groups_sync();
-        const float2 other = ml[(1 - w) * 128 + row];
-        const float top = fmaxf(m, other.x), base = top == -INFINITY ? 0.0f : top;
-        const float own = pow2(m - base);
-        f *= own;
-        l = l * own + other.y * pow2(other.x - base);
-        float* give = reinterpret_cast<float*>(smem);
+        if (sync->dead) l = NAN;
+        const bool whole = x.slot < 0, mine = alone ? (C::PAIR || w == 0) : w == 0;
+        OutAt to{nullptr, nullptr};
+        float norm = 1.0f;
+        if (mine && there) {
+            if (whole) {
+                to = out_at(a, x.rq.qs, x.h, at);
+                if (to.lse) *to.lse = lse_of(top, l, C::kBias);
+                norm = l == 0.0f ? 0.0f : 1.0f / l;  // a token that has seen no row gives zeros
+            } else {
+                const int64_t r = x.slot * C::ROWS + (C::PAIR ? 128 * w : 0) + row;
+                to.out = reinterpret_cast<char*>(a.part + r * C::DV);
+                a.part_ml[r] = make_float2(top, l);
+            }
+        }
+        float* words = reinterpret_cast<float*>(smem + (C::PAIR ? w * C::QTILE : 0)) + (row >> 5) * 1024;
 #pragma unroll 1
         for (int c = 0; c < C::DV; c += 32) {
             float o[32];
-            if (active) {
+            if (active && (mine || !alone)) {
                 tmem_ld32(o, lanes + o_col(w) + c);
                 tmem_wait_ld();
+                tmem_here32(o);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] *= f;
-                if (w == 1) {
+            }
+            if (!alone) {
+                if (active && w == 1) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) give[j * 128 + row] = o[j];
+                    for (int j = 0; j < 32; ++j) words[lane * 32 + (j ^ lane)] = o[j];
+                }
+                groups_sync();
+                if (active && w == 0) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] += words[lane * 32 + (j ^ lane)];
                 }
             }
-            groups_sync();
-            if (active && w == 0) {
+            if (active && mine) {
+                if (patch && there) add_not_finite<C::STORE, C::TN, 32>(a, x, at, c, o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] += give[j * 128 + row];
-                if (there) put(x, row, at, c, o, top, l, patch);
+                for (int j = 0; j < 32; ++j) o[j] *= norm;
+                write32(words, o, to.out, c, whole, lane);
             }
-            groups_sync();
+            if (!alone) groups_sync();
         }
     }
 
-    // 32 columns from c of one row: the result, or the part.
-    __device__ __forceinline__ void put(const RunAt& x, int row, int at, int c, float* o, float top, float l,
-                                        bool patch) const {
-        if (patch) add_not_finite<C::STORE, C::TN, 32>(a, x, at, c, o);
-        if (sync->dead) l = NAN;
-        if (x.slot >= 0) {
-            float4* to = reinterpret_cast<float4*>(a.part + (x.slot * C::ROWS + row) * C::DV + c);
+    // 32 columns from c of the warp's rows; `mine` is the thread's own row's
+    // place (null: none).
+    __device__ __forceinline__ void write32(float* words, const float* o, char* mine, int c, bool whole,
+                                            int lane) const {
+        __syncwarp();
+        if (whole) {
+            // 16 words a row: two rows an instruction
+            uint32_t* u = reinterpret_cast<uint32_t*>(words);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) to[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            if (c == 0) a.part_ml[x.slot * C::ROWS + row] = make_float2(top, l);
-            return;
-        }
-        const OutAt to = out_at(a, x.rq.qs, x.h, at);
-        if (c == 0 && to.lse) *to.lse = lse_of(top, l, C::kBias);
-        const float f = l == 0.0f ? 0.0f : 1.0f / l;  // a token that has seen no row gives zeros
+            for (int j = 0; j < 16; ++j)
+                u[lane * 32 + (j ^ lane)] = a.bf16 ? pack2<true>(o[2 * j], o[2 * j + 1]) : pack2<false>(o[2 * j], o[2 * j + 1]);
+            __syncwarp();
+            const int k = lane & 15;
+#pragma unroll 4
+            for (int r = lane >> 4; r < 32; r += 2) {
+                char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+                const uint32_t y = u[r * 32 + (k ^ r)];
+                if (to && c + 2 * k < a.Dv) *reinterpret_cast<uint32_t*>(to + (c + 2 * k) * 2) = y;
+            }
+        } else {
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            if (c + j >= a.Dv) break;
-            uint4 y;
-            if (a.bf16)
-                y = make_uint4(pack2<true>(o[j] * f, o[j + 1] * f), pack2<true>(o[j + 2] * f, o[j + 3] * f),
-                               pack2<true>(o[j + 4] * f, o[j + 5] * f), pack2<true>(o[j + 6] * f, o[j + 7] * f));
-            else
-                y = make_uint4(pack2<false>(o[j] * f, o[j + 1] * f), pack2<false>(o[j + 2] * f, o[j + 3] * f),
-                               pack2<false>(o[j + 4] * f, o[j + 5] * f), pack2<false>(o[j + 6] * f, o[j + 7] * f));
-            *reinterpret_cast<uint4*>(to.out + (c + j) * 2) = y;
+            for (int j = 0; j < 32; ++j) words[lane * 32 + (j ^ lane)] = o[j];
+            __syncwarp();
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r) {
+                char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+                const float y = words[r * 32 + (lane ^ r)];
+                if (to) reinterpret_cast<float*>(to)[c + lane] = y;
+            }
         }
+        __syncwarp();
     }
 };
 
