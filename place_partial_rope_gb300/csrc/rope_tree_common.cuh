@@ -254,40 +254,40 @@ struct RunAt {
 };
 
 // A block's runs, one after the other; several warps may each walk them.
-template <int ROWS, int TN>
 struct Walk {
-    const TreeArgs& a;
     int64_t u, base, end;
     int r;
     bool first;
 
-    __device__ __forceinline__ Walk(const TreeArgs& args, const Place& p)
-        : a(args), u(p.start), base(p.base), end(p.end), r(p.r), first(true) {}
-
-    __device__ __forceinline__ bool next(RunAt& x) {
-        while (u < end && r < a.R) {
-            const Request q = request<ROWS, TN>(a, r);
-            if (u >= base + q.units) {
-                base += q.units;
-                ++r;
-                continue;
-            }
-            const int64_t per = int64_t(q.mt) * q.nt, at = u - base;
-            x.rq = q;
-            x.r = r;
-            x.h = static_cast<int>(at / per);
-            const int rest = static_cast<int>(at - x.h * per);
-            x.m = rest / q.nt;
-            x.t0 = rest - x.m * q.nt;
-            x.count = static_cast<int>(min(int64_t(q.nt - x.t0), end - u));
-            x.slot = x.count == q.nt ? int64_t(-1) : int64_t(blockIdx.x) * 2 + (first ? 0 : 1);
-            first = false;
-            u += x.count;
-            return true;
-        }
-        return false;
-    }
+    __device__ __forceinline__ explicit Walk(const Place& p) : u(p.start), base(p.base), end(p.end), r(p.r), first(true) {}
 };
+
+template <int ROWS, int TN>
+__device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out) {
+    while (w.u < w.end && w.r < a.R) {
+        const Request q = request<ROWS, TN>(a, w.r);
+        if (w.u >= w.base + q.units) {
+            w.base += q.units;
+            ++w.r;
+            continue;
+        }
+        const int64_t per = int64_t(q.mt) * q.nt, at = w.u - w.base;
+        RunAt x;
+        x.rq = q;
+        x.r = w.r;
+        x.h = static_cast<int>(at / per);
+        const int rest = static_cast<int>(at - x.h * per);
+        x.m = rest / q.nt;
+        x.t0 = rest - x.m * q.nt;
+        x.count = static_cast<int>(min(int64_t(q.nt - x.t0), w.end - w.u));
+        x.slot = x.count == q.nt ? int64_t(-1) : int64_t(blockIdx.x) * 2 + (w.first ? 0 : 1);
+        w.first = false;
+        w.u += x.count;
+        out = x;
+        return true;
+    }
+    return false;
+}
 
 // What the join kernel needs to know of a block: the group that its first run
 // belongs to, when that began in an earlier block.
@@ -370,87 +370,125 @@ __device__ __forceinline__ float lse_of(float top, float l, float bias) {
     return l == 0.0f ? -INFINITY : (top - bias + log2f(l)) * 0.69314718055994531f;
 }
 
+// Parts lie in blocks of RB rows (32, or the 16 of a narrow tile), columns one
+// after the other with their rows side by side, so that a warp whose lanes are
+// rows writes and reads 128 bytes at a time.
+template <int ROWS, int DV>
+struct PartAt {
+    static constexpr int RB = ROWS < 32 ? ROWS : 32, BLOCKS = ROWS / RB;
+    static __device__ __forceinline__ int64_t block(int64_t slot, int rb) { return (slot * BLOCKS + rb) * (DV * RB); }
+};
+
 // Puts the parts of each split (request, head, row tile) together: out =
 // sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).  A group cut by s block
-// borders has s blocks here (the ones whose run begins inside it) that share
-// out its rows, so every block reads about as much as one of the main
-// kernel's blocks wrote; blockIdx.y cuts that further.  Groups of few parts
-// take a warp a row; of many, the whole block a row.  Bound by latency: the
+// borders has s blocks here (times gridDim.y), those whose run begins inside
+// it, that share out its pieces: 32 columns of a block of rows each.  A warp's
+// lanes are rows (of two columns, when there are 16).  Few parts: the warps
+// share out the columns; many: the parts, joined through shared memory.  The
 // parts were written just before and come from L2.
 template <int ROWS, int DV>
 __global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __grid_constant__ TreeArgs a,
                                                                       float bias) {
-    constexpr int WARPS = kJoinThreads / 32, V = DV / 32;  // columns of a lane
-    __shared__ float sums[WARPS][DV];
-    __shared__ float sum_l[WARPS];
+    using P = PartAt<ROWS, DV>;
+    constexpr int WARPS = kJoinThreads / 32, RB = P::RB;
+    constexpr int E = RB;          // words of a lane in a piece: 32 columns of RB rows
+    constexpr int FEW = WARPS / 2;
+    __shared__ float sums[32][33];
+    __shared__ float2 warp_ml[WARPS][32];
     after_predecessor();
     const int64_t b = int64_t(blockIdx.x) + 1;
     const TreeMeta w = a.meta[b];
     if (w.nt == 0) return;
     const int64_t from = w.u0 / w.chunk, to = (w.u0 + w.nt - 1) / w.chunk;
-    const int parts = static_cast<int>(to - from + 1), cuts = parts - 1;
-    const int own = static_cast<int>(b - from - 1);
+    const int parts = static_cast<int>(to - from + 1);
     const int qs = min(max(__ldg(a.q_start + w.r), 0), a.Tq);
     const int n = min(max(__ldg(a.q_start + w.r + 1), qs), a.Tq) - qs;
     const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(w.m) * ROWS));
     const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
-    const bool alone = parts <= WARPS;  // a warp a row
+    const bool few = parts <= FEW;
+    // part p of the group: block `from` holds it second unless the group
+    // begins with the block's run; the others hold it first
+    auto slot = [&](int p) { return (from + p) * 2 + (p == 0 && from * w.chunk != w.u0 ? 1 : 0); };
 
-    for (int k = int(blockIdx.y) + (alone ? warp * int(gridDim.y) : 0);; k += int(gridDim.y) * (alone ? WARPS : 1)) {
-        const int row = own + cuts * k;
-        if (row >= left) break;
-        // part p of the group: block `from` holds it second unless the group
-        // begins with the block's run; the others hold it first
-        auto slot = [&](int p) { return (from + p) * 2 + (p == 0 && from * w.chunk != w.u0 ? 1 : 0); };
-        float top = -INFINITY;
-        for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[slot(p) * ROWS + row].x);
-#pragma unroll
-        for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float base = top == -INFINITY ? 0.0f : top;
-        float o[V], l = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = 0.0f;
+    const int pieces = (left + RB - 1) / RB * (DV / 32), step = (parts - 1) * int(gridDim.y);
+    for (int piece = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y); piece < pieces; piece += step) {
+        const int rb = piece / (DV / 32), c0 = piece % (DV / 32) * 32;
+        const int row = lane % RB;
+        // few parts: every warp takes all of them for its columns; many: a
+        // warp takes each eighth part for all 32 columns
+        const int first = few ? 0 : warp, every = few ? 1 : WARPS;
+        const float2* ml = a.part_ml + rb * RB + row;
+        float top = -INFINITY, l = 0.0f;
 #pragma unroll 4
-        for (int p = alone ? 0 : warp; p < parts; p += alone ? 1 : WARPS) {
-            const int64_t s = slot(p) * ROWS + row;
-            const float2 x = a.part_ml[s];
-            const float f = pow2(x.x - base);
-            l += x.y * f;
-            const float2* src = reinterpret_cast<const float2*>(a.part + s * DV + lane * V);
+        for (int p = first; p < parts; p += every) top = fmaxf(top, ml[slot(p) * ROWS].x);
+        float base = top == -INFINITY ? 0.0f : top;
+        if (few) {
+            constexpr int MINE = E / WARPS;  // words of a lane: the warp's columns
+            float o[MINE];
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 y = src[i / 2];
-                o[i] += y.x * f;
-                o[i + 1] += y.y * f;
+            for (int e = 0; e < MINE; ++e) o[e] = 0.0f;
+#pragma unroll 2
+            for (int p = 0; p < parts; ++p) {
+                const float2 x = ml[slot(p) * ROWS];
+                const float f = pow2(x.x - base);
+                l += x.y * f;
+                const float* src = a.part + P::block(slot(p), rb) + c0 * RB + warp * (MINE * 32) + lane;
+#pragma unroll
+                for (int e = 0; e < MINE; ++e) o[e] += src[e * 32] * f;
             }
-        }
-        if (!alone) {
+            const float norm = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sums[warp][lane * V + i] = o[i];
-            if (lane == 0) sum_l[warp] = l;
+            for (int e = 0; e < MINE; ++e) sums[((warp * MINE + e) * 32 + lane) / RB][row] = o[e] * norm;
+        } else {
+            float o[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 2
+            for (int p = warp; p < parts; p += WARPS) {
+                const float2 x = ml[slot(p) * ROWS];
+                const float f = pow2(x.x - base);
+                l += x.y * f;
+                const float* src = a.part + P::block(slot(p), rb) + c0 * RB + lane;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] += src[e * 32] * f;
+            }
+            warp_ml[warp][lane] = make_float2(top, l);
+            for (int i = int(threadIdx.x); i < 32 * 33; i += kJoinThreads) (&sums[0][0])[i] = 0.0f;
             __syncthreads();
+            float all = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < WARPS; ++x) all = fmaxf(all, warp_ml[x][lane].x);
+            base = all == -INFINITY ? 0.0f : all;
             l = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = 0.0f;
-            if (warp == 0) {
-                for (int x = 0; x < WARPS; ++x) {
-                    l += sum_l[x];
+            for (int x = 0; x < WARPS; ++x) l += warp_ml[x][lane].y * pow2(warp_ml[x][lane].x - base);
+            const float f = pow2(top - base) * (l == 0.0f ? 0.0f : 1.0f / l);
+            top = all;
+            // one warp after the other: the same order every time
+            for (int x = 0; x < WARPS; ++x) {
+                if (x == warp) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] += sums[x][lane * V + i];
+                    for (int e = 0; e < E; ++e) sums[(e * 32 + lane) / RB][row] += o[e] * f;
                 }
+                __syncthreads();
             }
-            __syncthreads();
-            if (warp != 0) continue;
         }
-        const OutAt to_ = out_at(a, qs, w.h, w.m * ROWS + row);
-        if (lane == 0 && to_.lse) *to_.lse = lse_of(top, l, bias);
-        const float f = l == 0.0f ? 0.0f : 1.0f / l;
-        if (lane * V < a.Dv) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(to_.out) + lane * V / 2;
-#pragma unroll
-            for (int i = 0; i < V; i += 2)
-                dst[i / 2] = a.bf16 ? pack2<true>(o[i] * f, o[i + 1] * f) : pack2<false>(o[i] * f, o[i + 1] * f);
+        __syncthreads();
+        // sums[column][row]: rows leave two columns a lane
+        const int k = (lane & 15) * 2;
+        for (int r = warp * 2 + (lane >> 4); r < RB; r += 2 * WARPS) {
+            const int at = rb * RB + r;
+            if (at < left && c0 + k < a.Dv) {
+                const OutAt y = out_at(a, qs, w.h, w.m * ROWS + at);
+                reinterpret_cast<uint32_t*>(y.out)[(c0 + k) / 2] =
+                    a.bf16 ? pack2<true>(sums[k][r], sums[k + 1][r]) : pack2<false>(sums[k][r], sums[k + 1][r]);
+            }
         }
+        if (c0 == 0 && warp == 0 && lane < RB && rb * RB + lane < left) {
+            const OutAt y = out_at(a, qs, w.h, w.m * ROWS + rb * RB + lane);
+            if (y.lse) *y.lse = lse_of(top, l, bias);
+        }
+        __syncthreads();
     }
 }
 

@@ -181,7 +181,7 @@ rope_status_t launch_tree(const TreePlan& p, const TreeArgs& args, void* workspa
     if (st != ROPE_OK || blocks < 2) return st;
     float bias = k.bias;
     void* join[] = {&a, &bias};
-    return launch(k.join, dim3(blocks - 1, p.rows / 16), kJoinThreads, 0, join, stream, err);
+    return launch(k.join, dim3(blocks - 1, p.rows > 16 ? 4 : 1), kJoinThreads, 0, join, stream, err);
 }
 
 }  // namespace rope

@@ -539,17 +539,17 @@ struct Narrow {
             for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, ml[w * C::ROWS + row].x);
             float f = pow2(mrow[b] - (top == -INFINITY ? 0.0f : top));
             if constexpr (!C::kWide) f *= vref;
-            float* to = part + (warp * C::ROWS + row) * C::DV;
+            float* to = part + warp * (C::ROWS * C::DV) + row;
 #pragma unroll
             for (int d = 0; d < C::ND; ++d)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) to[column(d, e, t)] = O[d][2 * b + e] * f;
+                for (int e = 0; e < 2; ++e) to[column(d, e, t) * C::ROWS] = O[d][2 * b + e] * f;
         }
         __syncthreads();
-        constexpr int V = C::DV / 4;  // float4s of a row
-        for (int i = tid; i < C::ROWS * V; i += kNarrowThreads) {
-            const int row = i / V, c = i % V * 4, at = x.m * C::ROWS + row;
-            if (at >= x.rq.n * a.G) break;  // rows only grow with i
+        // four columns of a row a thread, rows side by side
+        for (int i = tid; i < C::ROWS * (C::DV / 4); i += kNarrowThreads) {
+            const int row = i % C::ROWS, c = i / C::ROWS * 4, at = x.m * C::ROWS + row;
+            if (at >= x.rq.n * a.G) continue;
             float top = -INFINITY, l = 0.0f;
 #pragma unroll
             for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, ml[w * C::ROWS + row].x);
@@ -561,19 +561,16 @@ struct Narrow {
             }
             float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) {
-                const float4 y = *reinterpret_cast<const float4*>(part + (w * C::ROWS + row) * C::DV + c);
-                o[0] += y.x;
-                o[1] += y.y;
-                o[2] += y.z;
-                o[3] += y.w;
-            }
+            for (int w = 0; w < C::WARPS; ++w)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] += part[w * (C::ROWS * C::DV) + (c + k) * C::ROWS + row];
             if constexpr (C::kWide) {
                 if (patch) add_not_finite<C::STORE, C::TN, 4>(a, x, at, c, o);
             }
             if (x.slot >= 0) {
-                *reinterpret_cast<float4*>(a.part + (x.slot * C::ROWS + row) * C::DV + c) =
-                    make_float4(o[0], o[1], o[2], o[3]);
+                float* to = a.part + PartAt<C::ROWS, C::DV>::block(x.slot, 0) + c * C::ROWS + row;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) to[k * C::ROWS] = o[k];
                 if (c == 0) a.part_ml[x.slot * C::ROWS + row] = make_float2(top, l);
             } else {
                 const OutAt to = out_at(a, x.rq.qs, x.h, at);
@@ -597,12 +594,13 @@ __global__ void __launch_bounds__(kNarrowThreads) rope_tree_narrow_kernel(const 
     extern __shared__ __align__(128) char smem[];
     after_predecessor();
     const Place p = find_place<C::ROWS, C::TN, kNarrowThreads>(a, reinterpret_cast<int64_t*>(smem));
-    Walk<C::ROWS, C::TN> walk(a, p);
+    Walk walk(p);
     TreeMeta meta{0, p.chunk, 0, 0, 0, 0};
-    RunAt x;
+    RunAt step;
     bool first = true;
     __syncthreads();  // the place's scratch is done with
-    while (walk.next(x)) {
+    while (next_run<C::ROWS, C::TN>(a, walk, step)) {
+        const RunAt x = step;
         if (first) meta = meta_of(p, x);
         first = false;
         Narrow<C>{a, smem, x}.go();

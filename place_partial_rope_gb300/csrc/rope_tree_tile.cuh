@@ -292,22 +292,21 @@ struct Tile {
 
     // The keys or values of a tile (16-bit: 64 lanes of a row to a line, in
     // planes; 8-bit: rows of codes) into shared memory.
-    template <int D>
-    __device__ __forceinline__ void fetch(const CUtensorMap* map, const Look& f, int h, uint32_t to, int lane,
+    __device__ __forceinline__ void fetch(const CUtensorMap* map, int dim, const Look& f, int h, uint32_t to, int lane,
                                           unsigned long long* bar) const {
-        constexpr int BYTES = C::TN * D * (C::kWide ? 2 : 1);
         if (lane == 0)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(BYTES)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+                         "r"(C::TN * dim * (C::kWide ? 2 : 1))
                          : "memory");
         __syncwarp();
         if (lane < C::TN / a.box) {
-            constexpr int PLANES = C::kWide ? D / 64 : 1, LINE = C::kWide ? 128 : D;
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p)
+            const int line = C::kWide ? 128 : dim;
+#pragma unroll 1
+            for (int p = 0; p < (C::kWide ? dim : 64); p += 64)
                 asm volatile(
                     "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-                    "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + p * (C::TN * 128) + lane * a.box * LINE),
-                    "l"(map), "r"(p * 64), "r"(h), "r"(int(f.off)), "r"(f.page), "r"(smem_addr(bar))
+                    "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + p * (C::TN * 2) + lane * a.box * line),
+                    "l"(map), "r"(p), "r"(h), "r"(int(f.off)), "r"(f.page), "r"(smem_addr(bar))
                     : "memory");
         }
     }
@@ -318,9 +317,10 @@ struct Tile {
     __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* km, const CUtensorMap* vm) const {
         const int lane = int(threadIdx.x) & 31;
         constexpr uint32_t SLOTS = C::SLOTS, RAWS = C::RAWS > 0 ? C::RAWS : 1;
-        Walk<C::ROWS, C::TN> walk(a, place);
-        RunAt x;
-        bool more = walk.next(x);
+        Walk walk(place);
+        RunAt step;
+        bool more = next_run<C::ROWS, C::TN>(a, walk, step);
+        RunAt x = step;
         Look now{-1, 0};
         if (more) now = look(x, x.t0 * C::TN + lane * a.box);
         int it = 0;
@@ -330,33 +330,33 @@ struct Tile {
             const int tile = x.t0 + it, h = x.h;
             const bool part = (tile + 1) * C::TN > x.rq.len - x.rq.n;  // more than context rows
             if (it + 1 == x.count) {
-                more = walk.next(x);
+                more = next_run<C::ROWS, C::TN>(a, walk, step);
+                x = step;
                 it = 0;
             } else {
                 ++it;
             }
             Look next{-1, 0};
             if (more) next = look(x, (x.t0 + it) * C::TN + lane * a.box);
-#pragma unroll
+#pragma unroll 1
             for (int values = 0; values < 2; ++values) {
+                const uint32_t item = 2 * n + values, r = item % RAWS;
+                unsigned long long* bar = &sync->raw_full[r];
+                uint32_t to = smem_addr(smem + C::RAW_AT) + r * C::RAW;
                 if constexpr (C::kWide) {
                     if (n >= SLOTS)
                         bar_wait(values ? &sync->v_empty[slot] : &sync->k_empty[slot], (n / SLOTS - 1) & 1, sync);
+                    to = smem_addr(smem) + (values ? C::V_AT + slot * C::V_SLOT : C::K_AT + slot * C::K_SLOT);
+                    bar = values ? &sync->v_full[slot] : &sync->k_full[slot];
                     if (values) {
                         fixed = (fixed & ~(1u << slot)) | uint32_t(part) << slot;
                         fix_par ^= uint32_t(part) << slot;
-                        fetch<C::DV>(vm, now, h, smem_addr(smem + C::V_AT) + slot * C::V_SLOT, lane,
-                                     part ? &sync->fix_full[slot] : &sync->v_full[slot]);
-                    } else {
-                        fetch<C::DK>(km, now, h, smem_addr(smem + C::K_AT) + slot * C::K_SLOT, lane, &sync->k_full[slot]);
+                        if (part) bar = &sync->fix_full[slot];
                     }
                 } else {
-                    const uint32_t item = 2 * n + values, r = item % RAWS;
                     if (item >= RAWS) bar_wait(&sync->raw_empty[r], (item / RAWS - 1) & 1, sync);
-                    const uint32_t to = smem_addr(smem + C::RAW_AT) + r * C::RAW;
-                    if (values) fetch<C::DV>(vm, now, h, to, lane, &sync->raw_full[r]);
-                    else fetch<C::DK>(km, now, h, to, lane, &sync->raw_full[r]);
                 }
+                fetch(values ? vm : km, values ? C::DV : C::DK, now, h, to, lane, bar);
             }
             now = next;
         }
@@ -426,10 +426,11 @@ struct Tile {
     // 8-bit: the helpers turn codes into fp16 tiles and bring the scales.
     __device__ __forceinline__ void widen_tiles(const Place& place, int id) const {
         constexpr uint32_t SLOTS = C::SLOTS, RAWS = C::RAWS > 0 ? C::RAWS : 1;
-        Walk<C::ROWS, C::TN> walk(a, place);
-        RunAt x;
+        Walk walk(place);
+        RunAt step;
         uint32_t n = 0, run = 0;
-        while (walk.next(x)) {
+        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
+            const RunAt x = step;
             Look now{-1, 0};
             if (id < C::TN) now = look(x, x.t0 * C::TN + id);
             for (int it = 0; it < x.count; ++it, ++n) {
@@ -482,10 +483,11 @@ struct Tile {
     // drafted rows' values that are not finite (see add_not_finite).
     __device__ __forceinline__ void mend_tiles(const Place& place, int id) const {
         constexpr uint32_t SLOTS = C::SLOTS;
-        Walk<C::ROWS, C::TN> walk(a, place);
-        RunAt x;
+        Walk walk(place);
+        RunAt step;
         uint32_t n = 0, run = 0, par = 0;  // a parity bit for each slot
-        while (walk.next(x)) {
+        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
+            const RunAt x = step;
             const int prefix = x.rq.len - x.rq.n;
             for (int it = 0; it < x.count; ++it, ++n) {
                 const int j0 = (x.t0 + it) * C::TN;
@@ -532,66 +534,71 @@ struct Tile {
     __device__ __forceinline__ void products(const Place& place) const {
         constexpr uint32_t QK = mma_shape<C::BF16, C::TN, false>();
         constexpr uint32_t PV = mma_shape<C::BF16, C::DV, true>();
-        Walk<C::ROWS, C::TN> walk(a, place);
-        RunAt x;
-        uint32_t before = 0, q_par = 0, p_par[2] = {0, 0};
+        Walk walk(place);
+        RunAt step;
         constexpr uint32_t SLOTS = C::SLOTS;
-        const uint32_t q_at = smem_addr(smem);
-        while (walk.next(x)) {
+        const uint32_t q_at = smem_addr(smem), k_at = smem_addr(smem + C::K_AT), v_at = smem_addr(smem + C::V_AT);
+        uint32_t before = 0, q_par = 0, p_par = 0;  // p_par: a bit for each group
+        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
+            const int count = step.count;
             bar_wait(&sync->q_full, q_par, sync);
             q_par ^= 1;
             tmem_after();
-            const int nv = C::PAIR ? 2 * x.count : x.count;  // steps; step v is group v & 1's
-            int s_next[2] = {0, 1}, p_next[2] = {0, 1}, left = nv;
+            const int nv = C::PAIR ? 2 * count : count;  // steps; step v is group v & 1's
+            // next steps of group w and of the other one
+            int s_mine = 0, s_other = 1, p_mine = 0, p_other = 1, left = nv, w = 0;
             uint32_t spins = 0;
             while (left > 0) {
-                bool moved = false;
+                if (s_mine > p_mine) {
+                    const int t = C::PAIR ? p_mine >> 1 : p_mine;
+                    const uint32_t n = before + t, slot = n % SLOTS;
+                    if (bar_poll(&sync->p_full[w], (p_par >> w) & 1) && bar_poll(&sync->v_full[slot], (n / SLOTS) & 1)) {
+                        tmem_after();
+                        const uint64_t vs = smem_matrix(v_at + slot * C::V_SLOT, C::TN * 128);
+                        const uint32_t d = tmem + o_col(w), p = tmem + s_col(w);
+                        const bool add = p_mine > 1;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (s_next[w] > p_next[w]) {
-                        const int v = p_next[w], t = C::PAIR ? v >> 1 : v;
-                        const uint32_t n = before + t, slot = n % SLOTS;
-                        if (bar_poll(&sync->p_full[w], p_par[w]) && bar_poll(&sync->v_full[slot], (n / SLOTS) & 1)) {
-                            tmem_after();
-                            const uint32_t vs = smem_addr(smem + C::V_AT) + slot * C::V_SLOT;
-#pragma unroll
-                            for (int k = 0; k < C::TN / 16; ++k)
-                                mma_ts(tmem + o_col(w), tmem + s_col(w) + 8 * k,
-                                       smem_matrix(vs + k * 2048, C::TN * 128), PV, v > 1 || k > 0);
-                            p_par[w] ^= 1;
-                            p_next[w] += 2;
-                            // a pair's slot is free when both have been there
-                            if (!C::PAIR || (p_next[1 - w] >> 1) > t) mma_commit(&sync->v_empty[slot]);
-                            if (p_next[w] >= nv) mma_commit(&sync->o_full[w]);
-                            --left;
-                            moved = true;
-                        }
-                    }
-                    if (s_next[w] == p_next[w] && s_next[w] < nv) {
-                        const int t = C::PAIR ? s_next[w] >> 1 : s_next[w];
-                        const uint32_t n = before + t, slot = n % SLOTS;
-                        if (bar_poll(&sync->k_full[slot], (n / SLOTS) & 1)) {
-                            tmem_after();
-                            const uint32_t ks = smem_addr(smem + C::K_AT) + slot * C::K_SLOT;
-                            const uint32_t q = q_at + (C::PAIR ? w * C::QTILE : 0);
-#pragma unroll
-                            for (int k = 0; k < C::DK / 16; ++k)
-                                mma_ss(tmem + s_col(w), smem_matrix(q + (k >> 2) * 16384 + (k & 3) * 32, 16),
-                                       smem_matrix(ks + (k >> 2) * (C::TN * 128) + (k & 3) * 32, 16), QK, k > 0);
-                            mma_commit(&sync->s_full[w]);
-                            s_next[w] += 2;
-                            if (!C::PAIR || (s_next[1 - w] >> 1) > t) mma_commit(&sync->k_empty[slot]);
-                            moved = true;
-                        }
+                        for (int k = 0; k < C::TN / 16; ++k) mma_ts(d, p + 8 * k, vs + k * (2048 >> 4), PV, add || k > 0);
+                        p_par ^= 1u << w;
+                        p_mine += 2;
+                        // a pair's slot is free when both have been there
+                        if (!C::PAIR || (p_other >> 1) > t) mma_commit(&sync->v_empty[slot]);
+                        if (p_mine >= nv) mma_commit(&sync->o_full[w]);
+                        --left;
+                        spins = 0;
                     }
                 }
-                if (moved) spins = 0;
-                else if (sync->dead || ++spins > kPolls) {
+                if (s_mine == p_mine && s_mine < nv) {
+                    const int t = C::PAIR ? s_mine >> 1 : s_mine;
+                    const uint32_t n = before + t, slot = n % SLOTS;
+                    if (bar_poll(&sync->k_full[slot], (n / SLOTS) & 1)) {
+                        tmem_after();
+                        const uint64_t ks = smem_matrix(k_at + slot * C::K_SLOT, 16);
+                        const uint64_t q = smem_matrix(q_at + (C::PAIR ? w * C::QTILE : 0), 16);
+                        const uint32_t d = tmem + s_col(w);
+#pragma unroll
+                        for (int k = 0; k < C::DK / 16; ++k)
+                            mma_ss(d, q + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                                   ks + (((k >> 2) * (C::TN * 128) + (k & 3) * 32) >> 4), QK, k > 0);
+                        mma_commit(&sync->s_full[w]);
+                        s_mine += 2;
+                        if (!C::PAIR || (s_other >> 1) > t) mma_commit(&sync->k_empty[slot]);
+                        spins = 0;
+                    }
+                }
+                if (++spins > kPolls || sync->dead) {
                     sync->dead = 1;
                     break;
                 }
+                // the other group's turn
+                w ^= 1;
+                const int s_ = s_mine, p_ = p_mine;
+                s_mine = s_other;
+                p_mine = p_other;
+                s_other = s_;
+                p_other = p_;
             }
-            before += x.count;
+            before += count;
         }
         mma_commit(&sync->done);
         for (uint32_t i = 0; i < kSpins && !bar_test(&sync->done, 0); ++i) {
@@ -609,60 +616,75 @@ struct Tile {
         if (there) a.div_group.divmod(uint32_t(at), tok, g);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] +
                                                           int64_t(x.h * a.G + int(g)) * a.q_st[1]);
-        // the whole row in flight at once
         constexpr int CH = C::DK / 8;
         const int chunks = there ? a.Dk / 8 : 0;
-        uint4 y[CH];
-#pragma unroll
-        for (int ch = 0; ch < CH; ++ch) y[ch] = ch < chunks ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
         float factor = a.scale_log2, down = 1.0f;
         if constexpr (!C::kWide) {
             uint32_t most = 0;
+#pragma unroll 1
+            for (int c = 0; c < CH; c += 8) {
+                uint4 y[8];  // in flight together
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                float f[8];
-                widen8(y[ch], a.bf16, f);
-                most = max(most, most_of(f));
+                for (int i = 0; i < 8; ++i) y[i] = c + i < chunks ? __ldg(src + c + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    // the largest |q| of bit patterns: bf16 and fp16 order alike
+                    most = max(most, max(max(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
+                                         max(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)) >> 16);
+                    most = max(most, max(max(y[i].x & 0x7fffu, y[i].y & 0x7fffu), max(y[i].z & 0x7fffu, y[i].w & 0x7fffu)));
+                }
             }
-            const float p = row_power(most);
+            const float big = a.bf16 ? __uint_as_float(most << 16)
+                                     : __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+            const float p = row_power(__float_as_uint(big));
             down = one_over_power(p);
             factor *= p;
         }
-        // up to 128 rows, both groups' threads of a row store half of it each
+        // up to 128 rows, both groups' threads of a row store a part of it each
         const uint32_t to = smem_addr(smem) + (C::PAIR ? w * C::QTILE : 0) + row * 128;
+#pragma unroll 1
+        for (int c = C::PAIR ? 0 : 8 * w; c < CH; c += C::PAIR ? 8 : 16) {
+            uint4 y[8];
 #pragma unroll
-        for (int ch = 0; ch < CH; ++ch) {
-            if (!C::PAIR && (ch & 1) != w) continue;
-            if constexpr (!C::kWide) {
-                float f[8];
-                widen8(y[ch], a.bf16, f);
-                y[ch] = half8(f, down);
+            for (int i = 0; i < 8; ++i) y[i] = c + i < chunks ? __ldg(src + c + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (!C::kWide) {
+                    float f[8];
+                    widen8(y[i], a.bf16, f);
+                    y[i] = half8(f, down);
+                }
+                sts128(to + (c >> 3) * 16384 + ((i ^ (row & 7)) << 4), y[i].x, y[i].y, y[i].z, y[i].w);
             }
-            sts128(to + (ch >> 3) * 16384 + (((ch & 7) ^ (row & 7)) << 4), y[ch].x, y[ch].y, y[ch].z, y[ch].w);
         }
         return factor;
     }
 
-    // 32 scores of a row: times the keys' scales (8-bit), and -inf where the
-    // token does not see the row.
-    static __device__ __forceinline__ void scores32(float* s, const float* scale, uint32_t bits) {
-        if constexpr (!C::kWide) {
+    // 32 scores of a row times the keys' scales.
+    static __device__ __forceinline__ void scale32(float* s, const float* scale) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(scale + j);
-                const float2 lo = mul2(make_float2(s[j], s[j + 1]), make_float2(y.x, y.y));
-                const float2 hi = mul2(make_float2(s[j + 2], s[j + 3]), make_float2(y.z, y.w));
-                s[j] = lo.x;
-                s[j + 1] = lo.y;
-                s[j + 2] = hi.x;
-                s[j + 3] = hi.y;
-            }
+        for (int j = 0; j < 32; j += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(scale + j);
+            const float2 lo = mul2(make_float2(s[j], s[j + 1]), make_float2(y.x, y.y));
+            const float2 hi = mul2(make_float2(s[j + 2], s[j + 3]), make_float2(y.z, y.w));
+            s[j] = lo.x;
+            s[j + 1] = lo.y;
+            s[j + 2] = hi.x;
+            s[j + 3] = hi.y;
         }
-        if (bits != 0xffffffffu) {
+    }
+
+    // 32 scores in tensor memory: scaled (8-bit), and -inf where the bit is not set.
+    static __device__ __forceinline__ void mask32(uint32_t at, const float* scale, uint32_t bits) {
+        float s[32];
+        tmem_ld32(s, at);
+        tmem_wait_ld();
+        tmem_here32(s);
+        if constexpr (!C::kWide) scale32(s, scale);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (!(bits >> j & 1u)) s[j] = -INFINITY;
-        }
+        for (int j = 0; j < 32; ++j)
+            if (!(bits >> j & 1u)) s[j] = -INFINITY;
+        tmem_st32(at, reinterpret_cast<const uint32_t*>(s));
     }
 
     static __device__ __forceinline__ float max_of32(const float* s) {
@@ -725,11 +747,12 @@ struct Tile {
         const int tid = int(threadIdx.x), row = tid & 127;
         const uint32_t lanes = tmem + (uint32_t(row & 96) << 16);  // this warp's lanes
         float2* ml = reinterpret_cast<float2*>(smem + C::ML_AT);
-        Walk<C::ROWS, C::TN> walk(a, place);
-        RunAt x;
+        Walk walk(place);
+        RunAt step;
         uint32_t before = 0, run = 0, s_par = 0, o_par = 0;
         TreeMeta meta{0, place.chunk, 0, 0, 0, 0};
-        while (walk.next(x)) {
+        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
+            const RunAt x = step;
             if (run == 0) meta = meta_of(place, x);
             const float factor = stage_queries(x, w, row);
             to_async_proxy();
@@ -764,6 +787,12 @@ struct Tile {
                             if (v > 1) rescale(lanes + o_col(w), f);
                         }
                     }
+                    if (part) {
+#pragma unroll 1
+                        for (int c = 0; c < C::TN; c += 32)
+                            mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c));
+                        tmem_wait_st();
+                    }
                     float s[C::TN];
 #pragma unroll
                     for (int c = 0; c < C::TN; c += 32) tmem_ld32(s + c, lanes + s_col(w) + c);
@@ -772,7 +801,7 @@ struct Tile {
 #pragma unroll
                     for (int c = 0; c < C::TN; c += 32) {
                         tmem_here32(s + c);
-                        scores32(s + c, sc + c, part ? sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c) : 0xffffffffu);
+                        if (!C::kWide && !part) scale32(s + c, sc + c);
                         top = fmaxf(top, max_of32(s + c));
                     }
                     top *= factor;
@@ -840,9 +869,7 @@ struct Tile {
                 if (to.lse) *to.lse = lse_of(top, l, C::kBias);
                 norm = l == 0.0f ? 0.0f : 1.0f / l;  // a token that has seen no row gives zeros
             } else {
-                const int64_t r = x.slot * C::ROWS + (C::PAIR ? 128 * w : 0) + row;
-                to.out = reinterpret_cast<char*>(a.part + r * C::DV);
-                a.part_ml[r] = make_float2(top, l);
+                a.part_ml[x.slot * C::ROWS + (C::PAIR ? 128 * w : 0) + row] = make_float2(top, l);
             }
         }
         float* words = reinterpret_cast<float*>(smem + (C::PAIR ? w * C::QTILE : 0)) + (row >> 5) * 1024;
@@ -869,9 +896,17 @@ struct Tile {
             }
             if (active && mine) {
                 if (patch && there) add_not_finite<C::STORE, C::TN, 32>(a, x, at, c, o);
+                if (whole) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] *= norm;
-                write32(words, o, to.out, c, whole, lane);
+                    for (int j = 0; j < 32; ++j) o[j] *= norm;
+                    write32(words, o, to.out, c, lane);
+                } else {
+                    // (rows that are not there have a place too)
+                    using P = PartAt<C::ROWS, C::DV>;
+                    float* part = a.part + P::block(x.slot, (C::PAIR ? 4 * w : 0) + (row >> 5)) + c * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) part[j * 32] = o[j];
+                }
             }
             if (!alone) groups_sync();
         }
@@ -879,33 +914,30 @@ struct Tile {
 
     // 32 columns from c of the warp's rows; `mine` is the thread's own row's
     // place (null: none).
-    __device__ __forceinline__ void write32(float* words, const float* o, char* mine, int c, bool whole,
-                                            int lane) const {
+    __device__ __forceinline__ void write32(float* words, const float* o, char* mine, int c, int lane) const {
+        const uint32_t at = smem_addr(words);
         __syncwarp();
-        if (whole) {
-            // 16 words a row: two rows an instruction
-            uint32_t* u = reinterpret_cast<uint32_t*>(words);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                u[lane * 32 + (j ^ lane)] = a.bf16 ? pack2<true>(o[2 * j], o[2 * j + 1]) : pack2<false>(o[2 * j], o[2 * j + 1]);
-            __syncwarp();
-            const int k = lane & 15;
-#pragma unroll 4
-            for (int r = lane >> 4; r < 32; r += 2) {
-                char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
-                const uint32_t y = u[r * 32 + (k ^ r)];
-                if (to && c + 2 * k < a.Dv) *reinterpret_cast<uint32_t*>(to + (c + 2 * k) * 2) = y;
-            }
-        } else {
+        for (int j = 0; j < 32; ++j) words[lane * 32 + (j ^ lane)] = o[j];
+        __syncwarp();
+        // two columns a lane, two rows an instruction, four of them at a time
+        const int k = (lane & 15) * 2;
+#pragma unroll 1
+        for (int r0 = lane >> 4; r0 < 32; r0 += 8) {
+            unsigned long long to[4];
+            float y[4], z[4];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) words[lane * 32 + (j ^ lane)] = o[j];
-            __syncwarp();
-#pragma unroll 4
-            for (int r = 0; r < 32; ++r) {
-                char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
-                const float y = words[r * 32 + (lane ^ r)];
-                if (to) reinterpret_cast<float*>(to)[c + lane] = y;
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + 2 * i;
+                to[i] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r);
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y[i]) : "r"(at + (r * 32 + (k ^ r)) * 4));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z[i]) : "r"(at + (r * 32 + ((k + 1) ^ r)) * 4));
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (to[i] && c + k < a.Dv)
+                    *reinterpret_cast<uint32_t*>(to[i] + (c + k) * 2) =
+                        a.bf16 ? pack2<true>(y[i], z[i]) : pack2<false>(y[i], z[i]);
         }
         __syncwarp();
     }
