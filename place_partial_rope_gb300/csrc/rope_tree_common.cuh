@@ -382,19 +382,20 @@ struct PartAt {
 // Puts the parts of each split (request, head, row tile) together: out =
 // sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).  A group cut by s block
 // borders has s blocks here (times gridDim.y), those whose run begins inside
-// it, that share out its pieces: 32 columns of a block of rows each.  A warp's
-// lanes are rows (of two columns, when there are 16).  Few parts: the warps
-// share out the columns; many: the parts, joined through shared memory.  The
-// parts were written just before and come from L2.
+// it, that share out its pieces.  The parts were written just before and come
+// from L2, so what counts is the chain of latencies and how many run side by
+// side.  Few parts: a warp takes a piece of 32 columns of a block of rows,
+// alone, its lanes being rows (of two columns, when there are 16).  Many: a
+// block takes a piece of 8 columns, its warps the parts in turn, joined
+// through shared memory in the same order every time.
 template <int ROWS, int DV>
 __global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __grid_constant__ TreeArgs a,
                                                                       float bias) {
     using P = PartAt<ROWS, DV>;
-    constexpr int WARPS = kJoinThreads / 32, RB = P::RB;
-    constexpr int E = RB;          // words of a lane in a piece: 32 columns of RB rows
-    constexpr int FEW = WARPS / 2;
-    __shared__ float sums[32][33];
-    __shared__ float2 warp_ml[WARPS][32];
+    constexpr int WARPS = kJoinThreads / 32, RB = P::RB, CW = 8, WORDS = CW * RB;
+    __shared__ float mine[WARPS][32][RB + 1];  // few: a warp's piece, a column after the other
+    __shared__ float part[WARPS][WORDS];       // many: the warps' sums of a piece
+    __shared__ float2 warp_ml[WARPS][RB];
     after_predecessor();
     const int64_t b = int64_t(blockIdx.x) + 1;
     const TreeMeta w = a.meta[b];
@@ -404,47 +405,26 @@ __global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __gr
     const int qs = min(max(__ldg(a.q_start + w.r), 0), a.Tq);
     const int n = min(max(__ldg(a.q_start + w.r + 1), qs), a.Tq) - qs;
     const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(w.m) * ROWS));
-    const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
-    const bool few = parts <= FEW;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, row = lane % RB;
+    const int rbs = (left + RB - 1) / RB;
+    const int own = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y), all = (parts - 1) * int(gridDim.y);
     // part p of the group: block `from` holds it second unless the group
     // begins with the block's run; the others hold it first
     auto slot = [&](int p) { return (from + p) * 2 + (p == 0 && from * w.chunk != w.u0 ? 1 : 0); };
 
-    const int pieces = (left + RB - 1) / RB * (DV / 32), step = (parts - 1) * int(gridDim.y);
-    for (int piece = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y); piece < pieces; piece += step) {
-        const int rb = piece / (DV / 32), c0 = piece % (DV / 32) * 32;
-        const int row = lane % RB;
-        // few parts: every warp takes all of them for its columns; many: a
-        // warp takes each eighth part for all 32 columns
-        const int first = few ? 0 : warp, every = few ? 1 : WARPS;
-        const float2* ml = a.part_ml + rb * RB + row;
-        float top = -INFINITY, l = 0.0f;
+    if (parts <= WARPS) {
+        constexpr int E = RB;  // words of a lane
+        for (int piece = own * WARPS + warp; piece < rbs * (DV / 32); piece += all * WARPS) {
+            const int rb = piece / (DV / 32), c0 = piece % (DV / 32) * 32;
+            const float2* ml = a.part_ml + rb * RB + row;
+            float top = -INFINITY, l = 0.0f, o[E];
 #pragma unroll 4
-        for (int p = first; p < parts; p += every) top = fmaxf(top, ml[slot(p) * ROWS].x);
-        float base = top == -INFINITY ? 0.0f : top;
-        if (few) {
-            constexpr int MINE = E / WARPS;  // words of a lane: the warp's columns
-            float o[MINE];
-#pragma unroll
-            for (int e = 0; e < MINE; ++e) o[e] = 0.0f;
-#pragma unroll 2
-            for (int p = 0; p < parts; ++p) {
-                const float2 x = ml[slot(p) * ROWS];
-                const float f = pow2(x.x - base);
-                l += x.y * f;
-                const float* src = a.part + P::block(slot(p), rb) + c0 * RB + warp * (MINE * 32) + lane;
-#pragma unroll
-                for (int e = 0; e < MINE; ++e) o[e] += src[e * 32] * f;
-            }
-            const float norm = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-            for (int e = 0; e < MINE; ++e) sums[((warp * MINE + e) * 32 + lane) / RB][row] = o[e] * norm;
-        } else {
-            float o[E];
+            for (int p = 0; p < parts; ++p) top = fmaxf(top, ml[slot(p) * ROWS].x);
+            const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = 0.0f;
 #pragma unroll 2
-            for (int p = warp; p < parts; p += WARPS) {
+            for (int p = 0; p < parts; ++p) {
                 const float2 x = ml[slot(p) * ROWS];
                 const float f = pow2(x.x - base);
                 l += x.y * f;
@@ -452,41 +432,76 @@ __global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __gr
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[e] += src[e * 32] * f;
             }
-            warp_ml[warp][lane] = make_float2(top, l);
-            for (int i = int(threadIdx.x); i < 32 * 33; i += kJoinThreads) (&sums[0][0])[i] = 0.0f;
-            __syncthreads();
-            float all = -INFINITY;
+            const float norm = l == 0.0f ? 0.0f : 1.0f / l;
+            __syncwarp();
 #pragma unroll
-            for (int x = 0; x < WARPS; ++x) all = fmaxf(all, warp_ml[x][lane].x);
-            base = all == -INFINITY ? 0.0f : all;
-            l = 0.0f;
-#pragma unroll
-            for (int x = 0; x < WARPS; ++x) l += warp_ml[x][lane].y * pow2(warp_ml[x][lane].x - base);
-            const float f = pow2(top - base) * (l == 0.0f ? 0.0f : 1.0f / l);
-            top = all;
-            // one warp after the other: the same order every time
-            for (int x = 0; x < WARPS; ++x) {
-                if (x == warp) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) sums[(e * 32 + lane) / RB][row] += o[e] * f;
+            for (int e = 0; e < E; ++e) mine[warp][(e * 32 + lane) / RB][row] = o[e] * norm;
+            if (c0 == 0 && lane < RB && rb * RB + lane < left) {
+                const OutAt y = out_at(a, qs, w.h, w.m * ROWS + rb * RB + lane);
+                if (y.lse) *y.lse = lse_of(top, l, bias);
+            }
+            __syncwarp();
+            // rows leave two columns a lane
+            const int k = (lane & 15) * 2;
+#pragma unroll 4
+            for (int r = lane >> 4; r < RB; r += 2) {
+                const int at = rb * RB + r;
+                if (at < left && c0 + k < a.Dv) {
+                    const float y = mine[warp][k][r], z = mine[warp][k + 1][r];
+                    reinterpret_cast<uint32_t*>(out_at(a, qs, w.h, w.m * ROWS + at).out)[(c0 + k) / 2] =
+                        a.bf16 ? pack2<true>(y, z) : pack2<false>(y, z);
                 }
-                __syncthreads();
             }
         }
+        return;
+    }
+    for (int piece = own; piece < rbs * (DV / CW); piece += all) {
+        constexpr int E = WORDS / 32;
+        const int rb = piece / (DV / CW), c0 = piece % (DV / CW) * CW;
+        const float2* ml = a.part_ml + rb * RB + row;
+        float top = -INFINITY, l = 0.0f, o[E];
+#pragma unroll 4
+        for (int p = warp; p < parts; p += WARPS) top = fmaxf(top, ml[slot(p) * ROWS].x);
+        float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 4
+        for (int p = warp; p < parts; p += WARPS) {
+            const float2 x = ml[slot(p) * ROWS];
+            const float f = pow2(x.x - base);
+            l += x.y * f;
+            const float* src = a.part + P::block(slot(p), rb) + c0 * RB + lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += src[e * 32] * f;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = o[e];
+        if (lane < RB) warp_ml[warp][lane] = make_float2(top, l);
         __syncthreads();
-        // sums[column][row]: rows leave two columns a lane
-        const int k = (lane & 15) * 2;
-        for (int r = warp * 2 + (lane >> 4); r < RB; r += 2 * WARPS) {
-            const int at = rb * RB + r;
-            if (at < left && c0 + k < a.Dv) {
-                const OutAt y = out_at(a, qs, w.h, w.m * ROWS + at);
-                reinterpret_cast<uint32_t*>(y.out)[(c0 + k) / 2] =
-                    a.bf16 ? pack2<true>(sums[k][r], sums[k + 1][r]) : pack2<false>(sums[k][r], sums[k + 1][r]);
+        // a thread's word has the thread's row
+        const int r = tid % RB;
+        top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < WARPS; ++x) top = fmaxf(top, warp_ml[x][r].x);
+        base = top == -INFINITY ? 0.0f : top;
+        float y = 0.0f;
+        l = 0.0f;
+        if (tid < WORDS) {
+#pragma unroll
+            for (int x = 0; x < WARPS; ++x) {
+                const float f = pow2(warp_ml[x][r].x - base);
+                l += warp_ml[x][r].y * f;
+                y += part[x][tid] * f;
             }
         }
-        if (c0 == 0 && warp == 0 && lane < RB && rb * RB + lane < left) {
-            const OutAt y = out_at(a, qs, w.h, w.m * ROWS + rb * RB + lane);
-            if (y.lse) *y.lse = lse_of(top, l, bias);
+        const int c = tid / RB, at = rb * RB + r;
+        if (tid < WORDS && at < left) {
+            const OutAt z = out_at(a, qs, w.h, w.m * ROWS + at);
+            y *= l == 0.0f ? 0.0f : 1.0f / l;
+            if (c0 + c < a.Dv)
+                reinterpret_cast<uint16_t*>(z.out)[c0 + c] =
+                    static_cast<uint16_t>(a.bf16 ? pack2<true>(y, 0.0f) : pack2<false>(y, 0.0f));
+            if (c0 + c == 0 && z.lse) *z.lse = lse_of(top, l, bias);
         }
         __syncthreads();
     }

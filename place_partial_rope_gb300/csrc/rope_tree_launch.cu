@@ -181,6 +181,7 @@ rope_status_t launch_tree(const TreePlan& p, const TreeArgs& args, void* workspa
     if (st != ROPE_OK || blocks < 2) return st;
     float bias = k.bias;
     void* join[] = {&a, &bias};
+    // tile kernels: few borders cut a group, which has pieces for many blocks
     return launch(k.join, dim3(blocks - 1, p.rows > 16 ? 4 : 1), kJoinThreads, 0, join, stream, err);
 }
 
