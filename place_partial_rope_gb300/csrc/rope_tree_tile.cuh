@@ -385,40 +385,40 @@ struct Tile {
     // Codes to fp16, in a tile's layout; rows from `valid` on become zeros.
     // Eight threads take 16 codes each of two successive rows: 64 of either row,
     // in an order that meets all banks both reading rows of codes and writing
-    // lines (128 lanes: the second row's other half).
+    // lines (128 lanes: the second row's other half).  The helpers' step from
+    // one such unit to the next is a multiple of eight rows, so a thread's
+    // addresses differ by constants and a unit costs a load, twelve conversion
+    // instructions and two stores: a helper is one warp in turn with few
+    // others, so that its instructions count at their latency.
     template <int D>
-    static __device__ __noinline__ void widen(uint32_t raw, uint32_t to, int id, int valid) {
-        constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kHelpers / 8, N = (UNITS + STEP - 1) / STEP, B = 3;
-        const int odd = (id >> 2) & 1, c = id & 3;
-#pragma unroll 1
+    static __device__ __forceinline__ void widen(uint32_t raw, uint32_t to, int id, int valid) {
+        constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kHelpers / 8, N = (UNITS + STEP - 1) / STEP;
+        constexpr int ROWS = STEP / G * 2;  // from a unit to the thread's next
+        static_assert(STEP % G == 0 && ROWS % 8 == 0, "the same place in the swizzle");
+        const int u = id >> 3, odd = (id >> 2) & 1;
+        const int row = u / G * 2 + odd, ch = ((G == 2 && odd ? u % G ^ 1 : u % G) << 2) + (id & 3);
+        raw += row * D + ch * 16;
+        const uint32_t lo = to + line_at(row, 2 * ch), hi = to + line_at(row, 2 * ch + 1);
+        constexpr int B = (N + 1) / 2;
+#pragma unroll
         for (int i0 = 0; i0 < N; i0 += B) {
-            // a few loads, then their conversions: the loads do not wait for each
-            // other (and the loop stays small: the kernel's roles share the
-            // instruction cache)
             uint32_t w[B][4];
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const int u = (id >> 3) + (i0 + i) * STEP, row = u / G * 2 + odd;
-                const int ch = ((G == 2 && odd ? u % G ^ 1 : u % G) << 2) + c;
-                if (i0 + i < N && u < UNITS) lds128(w[i], raw + row * D + ch * 16);
-            }
+            for (int i = 0; i < B; ++i)
+                if (i0 + i < N && (UNITS % STEP == 0 || i0 + i < N - 1 || u + (N - 1) * STEP < UNITS))
+                    lds128(w[i], raw + (i0 + i) * (ROWS * D));
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                const int u = (id >> 3) + (i0 + i) * STEP, row = u / G * 2 + odd;
-                const int ch = ((G == 2 && odd ? u % G ^ 1 : u % G) << 2) + c;
-                if (i0 + i >= N || u >= UNITS) continue;
+                if (i0 + i >= N || !(UNITS % STEP == 0 || i0 + i < N - 1 || u + (N - 1) * STEP < UNITS)) continue;
+                if (row + (i0 + i) * ROWS >= valid) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // codes of 0
                 uint32_t h[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     h[2 * j] = codes_to_half2<C::STORE, false>(w[i][j]);
                     h[2 * j + 1] = codes_to_half2<C::STORE, true>(w[i][j]);
                 }
-                if (row >= valid) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) h[j] = 0u;
-                }
-                sts128(to + line_at(row, 2 * ch), h[0], h[1], h[2], h[3]);
-                sts128(to + line_at(row, 2 * ch + 1), h[4], h[5], h[6], h[7]);
+                sts128(lo + (i0 + i) * (ROWS * 128), h[0], h[1], h[2], h[3]);
+                sts128(hi + (i0 + i) * (ROWS * 128), h[4], h[5], h[6], h[7]);
             }
         }
     }
@@ -463,9 +463,9 @@ struct Tile {
                             sync->patch[run & 7] = 1;
                         }
                         if (id < C::TN) sc[C::TN + id] = v;
-#pragma unroll
-                        for (int d = 16; d; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                        if ((id & 31) == 0 && id < 128) sc[2 * C::TN + (id >> 5)] = v;
+                        // (scales are not negative: their bits order like them)
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.0f)));
+                        if ((id & 31) == 0 && id < 128) sc[2 * C::TN + (id >> 5)] = __uint_as_float(most);
                     } else if (id < C::TN) {
                         sc[id] = v;
                     }
@@ -793,16 +793,25 @@ struct Tile {
                             mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c));
                         tmem_wait_st();
                     }
-                    float s[C::TN];
+                    // 16-bit: s is held in registers.  8-bit: it is read twice, 32
+                    // columns at a time, in loops small enough to stay in the
+                    // instruction cache beside the helpers' (with s held, the
+                    // roles' code missed it and every role ran at a third of its
+                    // speed); the rows are bound by HBM, so the second read hides.
+                    constexpr int HELD = C::kWide ? C::TN : 32;
+                    float s[HELD], top = -INFINITY;
+                    const uint32_t from = lanes + s_col(w);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < C::TN; c0 += HELD) {
 #pragma unroll
-                    for (int c = 0; c < C::TN; c += 32) tmem_ld32(s + c, lanes + s_col(w) + c);
-                    tmem_wait_ld();
-                    float top = -INFINITY;
+                        for (int c = 0; c < HELD; c += 32) tmem_ld32(s + c, from + c0 + c);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < C::TN; c += 32) {
-                        tmem_here32(s + c);
-                        if (!C::kWide && !part) scale32(s + c, sc + c);
-                        top = fmaxf(top, max_of32(s + c));
+                        for (int c = 0; c < HELD; c += 32) {
+                            tmem_here32(s + c);
+                            if (!C::kWide && !part) scale32(s + c, sc + c0 + c);
+                            top = fmaxf(top, max_of32(s + c));
+                        }
                     }
                     top *= factor;
                     const bool up = top > m + C::kLag || (m == -INFINITY && top > m);
@@ -814,8 +823,19 @@ struct Tile {
                     }
                     const float base = C::kBias - (m == -INFINITY ? 0.0f : m) - (C::kWide ? 0.0f : exponent(vref));
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+                    for (int c0 = 0; c0 < C::TN; c0 += HELD) {
+                        if constexpr (!C::kWide) {
+                            // (p of the columns before lies over s of columns before those)
+                            tmem_ld32(s, from + c0);
+                            tmem_wait_ld();
+                            tmem_here32(s);
+                            if (!part) scale32(s, sc + c0);
+                        }
 #pragma unroll
-                    for (int c = 0; c < C::TN; c += 32) weights32(s + c, sc + C::TN + c, factor, base, sum, lanes + s_col(w) + c / 2);
+                        for (int c = 0; c < HELD; c += 32)
+                            weights32(s + c, sc + C::TN + c0 + c, factor, base, sum, from + (c0 + c) / 2);
+                    }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                 }
