@@ -15,13 +15,15 @@
 // the division would make the kernel issue-bound (about 10 instructions a
 // lane against 4).
 //
-// What bounds it: HBM, one pass over the rows.  A row is spread over the
-// `lanes` lanes of a warp that hold it in whole 8-element accesses (16 lanes
-// for 128), kept in registers between the maximum and the rounding, so the
-// row is read once.  Rows of a token's keys and values follow each other in
-// the work index: the cache rows of a slot are written by neighbouring
-// warps.  Rows that are not aligned for 8-element accesses go one element an
-// access (vec 1).
+// What bounds it: HBM, one pass over the rows.  A row is spread over 8 lanes
+// (32 for rows of more than 256) in whole 8-element accesses, kept in registers
+// between the maximum and the rounding, so it is read once.  Eight lanes, where
+// one access a lane would take 16 or 24: a lane then has 2 or 3 accesses of its
+// row in flight, idles in no row length that 64 divides, and the maximum takes 3
+// shuffles.  A group of lanes takes U successive heads of a token, whose loads
+// are issued together and whose slot is looked up once.  Rows of a token's keys
+// and values follow each other in the work index.  Rows that are not aligned
+// for 8-element accesses go one element an access (V 1).
 #pragma once
 #include <cuda_fp8.h>
 
@@ -157,7 +159,7 @@ __device__ __forceinline__ void store_row(char* p, const float* v) {
     }
 }
 
-// Where a work row lies.
+// Where U work rows (successive heads of a token, keys or values) lie.
 struct RowAt {
     const CacheSide* side;
     char* dense;
@@ -168,17 +170,19 @@ struct RowAt {
     bool there;  // the slot is one of the cache's
 };
 
-__device__ __forceinline__ RowAt locate(const CacheArgs& a, uint32_t row) {
+template <int U>
+__device__ __forceinline__ RowAt locate(const CacheArgs& a, uint32_t group) {
     RowAt r;
     uint32_t h;
-    a.div_rows.divmod(row, r.tok, h);
+    a.div_rows.divmod(group, r.tok, h);
+    h *= U;
     const bool second = h >= uint32_t(a.heads);
     if (second) h -= a.heads;
     const int which = second ? 1 : a.first;
     r.side = &a.side[which];
     r.keys = which == 0;
-    r.dense = r.side->rows + int64_t(r.tok) * r.side->row_tok + int64_t(h) * r.side->row_head;
     const uint64_t slot = static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(a.slots) + r.tok));
+    r.dense = r.side->rows + int64_t(r.tok) * r.side->row_tok + int64_t(h) * r.side->row_head;
     r.there = slot < a.total;  // a negative slot is a huge unsigned one
     uint64_t page = 0, off = 0;
     if (r.there) {
@@ -199,7 +203,7 @@ __device__ __forceinline__ RowAt locate(const CacheArgs& a, uint32_t row) {
 
 // Turn the V elements of a key row that start at lane j0 (forward rotation).
 template <typename T, int V, bool TURN>
-__device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, int j0, float* v) {
+__device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, const char* dense, int j0, float* v) {
     constexpr int e = int(sizeof(T));
     const char* cos = a.cos + int64_t(r.tok) * a.cos_tok;
     const char* sin = a.sin + int64_t(r.tok) * a.sin_tok;
@@ -214,7 +218,7 @@ __device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, int j0,
         if (a.half_mode) {
             const bool lower = j < a.half;
             float x[V];
-            load_row<T, V>(r.dense + (lower ? j0 + a.half : j0 - a.half) * e, x);
+            load_row<T, V>(dense + (lower ? j0 + a.half : j0 - a.half) * e, x);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float p = __fmul_rn(v[i], c[i]), q = __fmul_rn(x[i], s[i]);
@@ -237,7 +241,7 @@ __device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, int j0,
             const bool lower = a.half_mode ? j < a.half : (j & 1) == 0;
             const int partner = a.half_mode ? (lower ? j + a.half : j - a.half) : (j ^ 1);
             float x, c, s;
-            load_row<T, 1>(r.dense + (a.start + partner) * e, &x);
+            load_row<T, 1>(dense + (a.start + partner) * e, &x);
             load_row<T, 1>(cos + j * e, &c);
             load_row<T, 1>(sin + j * e, &s);
             const float p = __fmul_rn(v[i], c), q = __fmul_rn(x, s);
@@ -246,112 +250,151 @@ __device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, int j0,
     }
 }
 
-template <typename T, int STORE, int V, int LANES, int CHUNKS, bool TURN>
+template <typename T, int STORE, int V, int LANES, int CHUNKS, int U, bool TURN>
 __global__ void __launch_bounds__(kCacheThreads)
 rope_cache_write_kernel(const __grid_constant__ CacheArgs a) {
     using S = Store<STORE>;
     enter_after_predecessor();
     const uint64_t t = uint64_t(blockIdx.x) * kCacheThreads + threadIdx.x;
     const uint32_t lane = threadIdx.x % LANES;
-    const uint64_t row = t / LANES;
-    if (row >= a.rows) return;  // whole rows: the lanes of one leave together
-    const RowAt r = locate(a, uint32_t(row));
+    const uint64_t group = t / LANES;
+    if (group >= a.groups) return;  // whole rows: the lanes of one leave together
+    const RowAt r = locate<U>(a, uint32_t(group));
 
-    // the row is loaded and turned whether or not its slot is one of the
-    // cache's: its loads need not wait for the slot's
-    float v[CHUNKS][V];
-    uint32_t most = 0;
+    // the rows are loaded and turned whether or not their slot is one of the
+    // cache's: their loads need not wait for the slot's
+    float v[U][CHUNKS][V];
 #pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-        const int j = (i * LANES + int(lane)) * V;
-        if (j < r.side->dim) {
-            load_row<T, V>(r.dense + int64_t(j) * int(sizeof(T)), v[i]);
-            if (r.keys && a.half) turn<T, V, TURN>(a, r, j, v[i]);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int k = 0; k < V; ++k) most = max(most, __float_as_uint(v[i][k]) & 0x7fffffffu);
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int j = (i * LANES + int(lane)) * V;
+            if (j < r.side->dim)
+                load_row<T, V>(r.dense + u * r.side->row_head + int64_t(j) * int(sizeof(T)), v[u][i]);
         }
+    if (r.keys && a.half) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int j = (i * LANES + int(lane)) * V;
+                if (j < r.side->dim) turn<T, V, TURN>(a, r, r.dense + u * r.side->row_head, j, v[u][i]);
+            }
     }
-    if constexpr (S::kBytes == 1) {
-        const uint32_t mask = LANES == 32 ? 0xffffffffu
-                                          : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
 #pragma unroll
-        for (int d = LANES / 2; d; d /= 2) most = max(most, __shfl_xor_sync(mask, most, d));
-        const bool finite = most < 0x7f800000u;
-        const float m = fmaxf(__uint_as_float(most), 7.8886090522101181e-31f);  // 2^-100
-        const float inv = __fdiv_rn(S::kTop, m);
-        if (lane == 0 && r.there) *r.scale = finite ? __fdiv_rn(m, S::kTop) : __uint_as_float(0x7fffffffu);
+    for (int u = 0; u < U; ++u) {
+        float inv = 1.0f;
+        bool finite = true;
+        if constexpr (S::kBytes == 1) {
+            uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < CHUNKS; ++i)
+            for (int i = 0; i < CHUNKS; ++i)
+                if ((i * LANES + int(lane)) * V < r.side->dim) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) v[i][k] = finite ? __fmul_rn(v[i][k], inv) : 0.0f;
-    }
-    if (!r.there) return;
+                    for (int k = 0; k < V; ++k) most = max(most, __float_as_uint(v[u][i][k]) & 0x7fffffffu);
+                }
+            const uint32_t mask = LANES == 32 ? 0xffffffffu
+                                              : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
 #pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-        const int j = (i * LANES + int(lane)) * V;
-        if (j < r.side->dim) store_codes<STORE, V>(r.codes + int64_t(j) * S::kBytes, v[i]);
+            for (int d = LANES / 2; d; d /= 2) most = max(most, __shfl_xor_sync(mask, most, d));
+            finite = most < 0x7f800000u;
+            const float m = fmaxf(__uint_as_float(most), 7.8886090522101181e-31f);  // 2^-100
+            inv = __fdiv_rn(S::kTop, m);
+            if (lane == 0 && r.there)
+                r.scale[u * r.side->s_head] = finite ? __fdiv_rn(m, S::kTop) : __uint_as_float(0x7fffffffu);
+        }
+        if (!r.there) continue;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int j = (i * LANES + int(lane)) * V;
+            if (j >= r.side->dim) continue;
+            if constexpr (S::kBytes == 1) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[u][i][k] = finite ? __fmul_rn(v[u][i][k], inv) : 0.0f;
+            }
+            store_codes<STORE, V>(r.codes + u * r.side->head + int64_t(j) * S::kBytes, v[u][i]);
+        }
     }
 }
 
-template <typename T, int STORE, int V, int LANES, int CHUNKS>
+template <typename T, int STORE, int V, int LANES, int CHUNKS, int U>
 __global__ void __launch_bounds__(kCacheThreads)
 rope_cache_read_kernel(const __grid_constant__ CacheArgs a) {
     using S = Store<STORE>;
     enter_after_predecessor();
     const uint64_t t = uint64_t(blockIdx.x) * kCacheThreads + threadIdx.x;
     const uint32_t lane = threadIdx.x % LANES;
-    const uint64_t row = t / LANES;
-    if (row >= a.rows) return;
-    const RowAt r = locate(a, uint32_t(row));
-    float scale = 1.0f;
-    if constexpr (S::kBytes == 1) {
-        if (r.there) scale = __ldg(r.scale);
+    const uint64_t group = t / LANES;
+    if (group >= a.groups) return;
+    const RowAt r = locate<U>(a, uint32_t(group));
+    float v[U][CHUNKS][V], scale[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        scale[u] = 1.0f;
+        if constexpr (S::kBytes == 1) {
+            if (r.there) scale[u] = __ldg(r.scale + u * r.side->s_head);
+        }
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int j = (i * LANES + int(lane)) * V;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[u][i][k] = 0.0f;
+            if (r.there && j < r.side->dim)
+                load_codes<STORE, V>(r.codes + u * r.side->head + int64_t(j) * S::kBytes, v[u][i]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-        const int j = (i * LANES + int(lane)) * V;
-        if (j >= r.side->dim) continue;
-        float v[V];
-        if (r.there) {
-            load_codes<STORE, V>(r.codes + int64_t(j) * S::kBytes, v);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int j = (i * LANES + int(lane)) * V;
+            if (j >= r.side->dim) continue;
             if constexpr (S::kBytes == 1) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) v[k] = __fmul_rn(v[k], scale);
+                for (int k = 0; k < V; ++k) v[u][i][k] = r.there ? __fmul_rn(v[u][i][k], scale[u]) : 0.0f;
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = 0.0f;
+            store_row<T, V>(r.dense + u * r.side->row_head + int64_t(j) * int(sizeof(T)), v[u][i]);
         }
-        store_row<T, V>(r.dense + int64_t(j) * int(sizeof(T)), v);
-    }
 }
 
 // ------------------------------------------------------------------------
 // kernel selection (instantiated in one .cu per dense type)
 // ------------------------------------------------------------------------
 
-template <typename T, int STORE, bool WRITE, int V, int LANES, int CHUNKS>
+template <typename T, int STORE, bool WRITE, int V, int LANES, int CHUNKS, int U>
 const void* pick_cache_turn(const CachePlan& p) {
-    if constexpr (!WRITE) return reinterpret_cast<const void*>(&rope_cache_read_kernel<T, STORE, V, LANES, CHUNKS>);
+    if constexpr (!WRITE)
+        return reinterpret_cast<const void*>(&rope_cache_read_kernel<T, STORE, V, LANES, CHUNKS, U>);
     else if constexpr (V == 1)
-        return reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, false>);
+        return reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, U, false>);
     else
-        return p.turn ? reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, true>)
-                      : reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, false>);
+        return p.turn ? reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, U, true>)
+                      : reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, U, false>);
 }
 
-// Rows of up to 64 / 128 / 256 / 1024 elements in 8-element accesses, or of
-// up to 128 / 1024 in single elements.
+template <typename T, int STORE, bool WRITE, int CHUNKS>
+const void* pick_cache_heads(const CachePlan& p) {
+    if constexpr (sizeof(T) == 2 && Store<STORE>::kBytes == 1) {
+        if (p.heads == 2) return pick_cache_turn<T, STORE, WRITE, 8, 8, CHUNKS, 2>(p);
+    }
+    return pick_cache_turn<T, STORE, WRITE, 8, 8, CHUNKS, 1>(p);
+}
+
+// Rows of up to 64 / 128 / 192 / 256 / 1024 elements in 8-element accesses, or
+// of up to 128 / 1024 in single elements.
 template <typename T, int STORE, bool WRITE>
 const void* pick_cache_row(const CachePlan& p) {
     if (p.vec == 8) {
-        if (p.lanes == 8) return pick_cache_turn<T, STORE, WRITE, 8, 8, 1>(p);
-        if (p.lanes == 16) return pick_cache_turn<T, STORE, WRITE, 8, 16, 1>(p);
-        return p.chunks == 1 ? pick_cache_turn<T, STORE, WRITE, 8, 32, 1>(p)
-                             : pick_cache_turn<T, STORE, WRITE, 8, 32, 4>(p);
+        if (p.lanes == 32) return pick_cache_turn<T, STORE, WRITE, 8, 32, 4, 1>(p);
+        switch (p.chunks) {
+            case 1: return pick_cache_heads<T, STORE, WRITE, 1>(p);
+            case 2: return pick_cache_heads<T, STORE, WRITE, 2>(p);
+            case 3: return pick_cache_heads<T, STORE, WRITE, 3>(p);
+            default: return pick_cache_heads<T, STORE, WRITE, 4>(p);
+        }
     }
-    return p.chunks <= 4 ? pick_cache_turn<T, STORE, WRITE, 1, 32, 4>(p)
-                         : pick_cache_turn<T, STORE, WRITE, 1, 32, 32>(p);
+    return p.chunks <= 4 ? pick_cache_turn<T, STORE, WRITE, 1, 32, 4, 1>(p)
+                         : pick_cache_turn<T, STORE, WRITE, 1, 32, 32, 1>(p);
 }
 
 template <typename T, bool WRITE>
