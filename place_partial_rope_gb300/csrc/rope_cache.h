@@ -8,7 +8,7 @@
 
 namespace rope {
 
-constexpr int kCacheThreads = 256;
+constexpr int kCacheThreads = 128;
 
 // The keys or the values of a call: dense rows (token, head) on one side,
 // cache rows (page, token of the page, head) and their scales on the other.
@@ -30,9 +30,9 @@ struct CacheArgs {
     int64_t cos_tok, sin_tok;  // bytes
     int64_t page_size;
     uint64_t total;       // pages * page_size
-    FastDiv div_rows;     // groups of one token: heads, or 2 * heads with values, over plan.heads
+    FastDiv div_rows;     // rows of one token: heads, or 2 * heads with values
     FastDiv div_page;     // used when total < 2^32
-    uint32_t groups;      // groups of this launch: plan.heads rows each
+    uint32_t rows;        // rows of this launch
     int32_t heads;
     int32_t first;        // the side that the first `heads` rows of a token are
     int32_t start, half;  // slice start and half its length
@@ -45,7 +45,6 @@ struct CachePlan {
     int vec;        // elements per access: 8 (16-byte accesses of a 16-bit row) or 1
     int lanes;      // lanes per row, a power of two <= 32
     int chunks;     // accesses per lane
-    int heads;      // successive heads that a group of lanes takes: 1 or 2
     bool turn;      // the rotation's partner and cos/sin come as whole accesses
 };
 

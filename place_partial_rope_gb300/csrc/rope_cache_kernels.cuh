@@ -20,10 +20,12 @@
 // between the maximum and the rounding, so it is read once.  Eight lanes, where
 // one access a lane would take 16 or 24: a lane then has 2 or 3 accesses of its
 // row in flight, idles in no row length that 64 divides, and the maximum takes 3
-// shuffles.  A group of lanes takes U successive heads of a token, whose loads
-// are issued together and whose slot is looked up once.  Rows of a token's keys
-// and values follow each other in the work index.  Rows that are not aligned
-// for 8-element accesses go one element an access (V 1).
+// shuffles.  Rows of a token's keys and values follow each other in the work
+// index, so that a warp's accesses lie side by side.  (A group of lanes with two
+// or four heads of a token, their loads issued together and one slot looked up,
+// was slower: reading 65536 rows of 8 heads of 128 fp8 codes took 97 and 148 us
+// against 77 with one.)  Rows that are not aligned for 8-element accesses go one
+// element an access (V 1).
 #pragma once
 #include <cuda_fp8.h>
 
@@ -159,7 +161,7 @@ __device__ __forceinline__ void store_row(char* p, const float* v) {
     }
 }
 
-// Where U work rows (successive heads of a token, keys or values) lie.
+// Where a work row lies.
 struct RowAt {
     const CacheSide* side;
     char* dense;
@@ -170,12 +172,10 @@ struct RowAt {
     bool there;  // the slot is one of the cache's
 };
 
-template <int U>
-__device__ __forceinline__ RowAt locate(const CacheArgs& a, uint32_t group) {
+__device__ __forceinline__ RowAt locate(const CacheArgs& a, uint32_t row) {
     RowAt r;
     uint32_t h;
-    a.div_rows.divmod(group, r.tok, h);
-    h *= U;
+    a.div_rows.divmod(row, r.tok, h);
     const bool second = h >= uint32_t(a.heads);
     if (second) h -= a.heads;
     const int which = second ? 1 : a.first;
@@ -203,7 +203,7 @@ __device__ __forceinline__ RowAt locate(const CacheArgs& a, uint32_t group) {
 
 // Turn the V elements of a key row that start at lane j0 (forward rotation).
 template <typename T, int V, bool TURN>
-__device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, const char* dense, int j0, float* v) {
+__device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, int j0, float* v) {
     constexpr int e = int(sizeof(T));
     const char* cos = a.cos + int64_t(r.tok) * a.cos_tok;
     const char* sin = a.sin + int64_t(r.tok) * a.sin_tok;
@@ -218,7 +218,7 @@ __device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, const c
         if (a.half_mode) {
             const bool lower = j < a.half;
             float x[V];
-            load_row<T, V>(dense + (lower ? j0 + a.half : j0 - a.half) * e, x);
+            load_row<T, V>(r.dense + (lower ? j0 + a.half : j0 - a.half) * e, x);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float p = __fmul_rn(v[i], c[i]), q = __fmul_rn(x[i], s[i]);
@@ -241,7 +241,7 @@ __device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, const c
             const bool lower = a.half_mode ? j < a.half : (j & 1) == 0;
             const int partner = a.half_mode ? (lower ? j + a.half : j - a.half) : (j ^ 1);
             float x, c, s;
-            load_row<T, 1>(dense + (a.start + partner) * e, &x);
+            load_row<T, 1>(r.dense + (a.start + partner) * e, &x);
             load_row<T, 1>(cos + j * e, &c);
             load_row<T, 1>(sin + j * e, &s);
             const float p = __fmul_rn(v[i], c), q = __fmul_rn(x, s);
@@ -250,134 +250,109 @@ __device__ __forceinline__ void turn(const CacheArgs& a, const RowAt& r, const c
     }
 }
 
-template <typename T, int STORE, int V, int LANES, int CHUNKS, int U, bool TURN>
+template <typename T, int STORE, int V, int LANES, int CHUNKS, bool TURN>
 __global__ void __launch_bounds__(kCacheThreads)
 rope_cache_write_kernel(const __grid_constant__ CacheArgs a) {
     using S = Store<STORE>;
     enter_after_predecessor();
     const uint64_t t = uint64_t(blockIdx.x) * kCacheThreads + threadIdx.x;
     const uint32_t lane = threadIdx.x % LANES;
-    const uint64_t group = t / LANES;
-    if (group >= a.groups) return;  // whole rows: the lanes of one leave together
-    const RowAt r = locate<U>(a, uint32_t(group));
+    const uint64_t row = t / LANES;
+    if (row >= a.rows) return;  // whole rows: the lanes of one leave together
+    const RowAt r = locate(a, uint32_t(row));
 
-    // the rows are loaded and turned whether or not their slot is one of the
-    // cache's: their loads need not wait for the slot's
-    float v[U][CHUNKS][V];
+    // the row is loaded and turned whether or not its slot is one of the
+    // cache's: its loads need not wait for the slot's
+    float v[CHUNKS][V];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-            const int j = (i * LANES + int(lane)) * V;
-            if (j < r.side->dim)
-                load_row<T, V>(r.dense + u * r.side->row_head + int64_t(j) * int(sizeof(T)), v[u][i]);
-        }
+    for (int i = 0; i < CHUNKS; ++i) {
+        const int j = (i * LANES + int(lane)) * V;
+        if (j < r.side->dim) load_row<T, V>(r.dense + int64_t(j) * int(sizeof(T)), v[i]);
+    }
     if (r.keys && a.half) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < CHUNKS; ++i) {
-                const int j = (i * LANES + int(lane)) * V;
-                if (j < r.side->dim) turn<T, V, TURN>(a, r, r.dense + u * r.side->row_head, j, v[u][i]);
-            }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float inv = 1.0f;
-        bool finite = true;
-        if constexpr (S::kBytes == 1) {
-            uint32_t most = 0;
-#pragma unroll
-            for (int i = 0; i < CHUNKS; ++i)
-                if ((i * LANES + int(lane)) * V < r.side->dim) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) most = max(most, __float_as_uint(v[u][i][k]) & 0x7fffffffu);
-                }
-            const uint32_t mask = LANES == 32 ? 0xffffffffu
-                                              : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
-#pragma unroll
-            for (int d = LANES / 2; d; d /= 2) most = max(most, __shfl_xor_sync(mask, most, d));
-            finite = most < 0x7f800000u;
-            const float m = fmaxf(__uint_as_float(most), 7.8886090522101181e-31f);  // 2^-100
-            inv = __fdiv_rn(S::kTop, m);
-            if (lane == 0 && r.there)
-                r.scale[u * r.side->s_head] = finite ? __fdiv_rn(m, S::kTop) : __uint_as_float(0x7fffffffu);
-        }
-        if (!r.there) continue;
-#pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
             const int j = (i * LANES + int(lane)) * V;
-            if (j >= r.side->dim) continue;
-            if constexpr (S::kBytes == 1) {
-#pragma unroll
-                for (int k = 0; k < V; ++k) v[u][i][k] = finite ? __fmul_rn(v[u][i][k], inv) : 0.0f;
-            }
-            store_codes<STORE, V>(r.codes + u * r.side->head + int64_t(j) * S::kBytes, v[u][i]);
+            if (j < r.side->dim) turn<T, V, TURN>(a, r, j, v[i]);
         }
+    }
+    float inv = 1.0f;
+    bool finite = true;
+    if constexpr (S::kBytes == 1) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+            if ((i * LANES + int(lane)) * V < r.side->dim) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) most = max(most, __float_as_uint(v[i][k]) & 0x7fffffffu);
+            }
+        const uint32_t mask = LANES == 32 ? 0xffffffffu
+                                          : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
+#pragma unroll
+        for (int d = LANES / 2; d; d /= 2) most = max(most, __shfl_xor_sync(mask, most, d));
+        finite = most < 0x7f800000u;
+        const float m = fmaxf(__uint_as_float(most), 7.8886090522101181e-31f);  // 2^-100
+        inv = __fdiv_rn(S::kTop, m);
+        if (lane == 0 && r.there) *r.scale = finite ? __fdiv_rn(m, S::kTop) : __uint_as_float(0x7fffffffu);
+    }
+    if (!r.there) return;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+        const int j = (i * LANES + int(lane)) * V;
+        if (j >= r.side->dim) continue;
+        if constexpr (S::kBytes == 1) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[i][k] = finite ? __fmul_rn(v[i][k], inv) : 0.0f;
+        }
+        store_codes<STORE, V>(r.codes + int64_t(j) * S::kBytes, v[i]);
     }
 }
 
-template <typename T, int STORE, int V, int LANES, int CHUNKS, int U>
+template <typename T, int STORE, int V, int LANES, int CHUNKS>
 __global__ void __launch_bounds__(kCacheThreads)
 rope_cache_read_kernel(const __grid_constant__ CacheArgs a) {
     using S = Store<STORE>;
     enter_after_predecessor();
     const uint64_t t = uint64_t(blockIdx.x) * kCacheThreads + threadIdx.x;
     const uint32_t lane = threadIdx.x % LANES;
-    const uint64_t group = t / LANES;
-    if (group >= a.groups) return;
-    const RowAt r = locate<U>(a, uint32_t(group));
-    float v[U][CHUNKS][V], scale[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        scale[u] = 1.0f;
-        if constexpr (S::kBytes == 1) {
-            if (r.there) scale[u] = __ldg(r.scale + u * r.side->s_head);
-        }
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-            const int j = (i * LANES + int(lane)) * V;
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[u][i][k] = 0.0f;
-            if (r.there && j < r.side->dim)
-                load_codes<STORE, V>(r.codes + u * r.side->head + int64_t(j) * S::kBytes, v[u][i]);
-        }
+    const uint64_t row = t / LANES;
+    if (row >= a.rows) return;
+    const RowAt r = locate(a, uint32_t(row));
+    float v[CHUNKS][V], scale = 1.0f;
+    if constexpr (S::kBytes == 1) {
+        if (r.there) scale = __ldg(r.scale);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < CHUNKS; ++i) {
+        const int j = (i * LANES + int(lane)) * V;
 #pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-            const int j = (i * LANES + int(lane)) * V;
-            if (j >= r.side->dim) continue;
-            if constexpr (S::kBytes == 1) {
+        for (int k = 0; k < V; ++k) v[i][k] = 0.0f;
+        if (r.there && j < r.side->dim) load_codes<STORE, V>(r.codes + int64_t(j) * S::kBytes, v[i]);
+    }
 #pragma unroll
-                for (int k = 0; k < V; ++k) v[u][i][k] = r.there ? __fmul_rn(v[u][i][k], scale[u]) : 0.0f;
-            }
-            store_row<T, V>(r.dense + u * r.side->row_head + int64_t(j) * int(sizeof(T)), v[u][i]);
+    for (int i = 0; i < CHUNKS; ++i) {
+        const int j = (i * LANES + int(lane)) * V;
+        if (j >= r.side->dim) continue;
+        if constexpr (S::kBytes == 1) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[i][k] = r.there ? __fmul_rn(v[i][k], scale) : 0.0f;
         }
+        store_row<T, V>(r.dense + int64_t(j) * int(sizeof(T)), v[i]);
+    }
 }
 
 // ------------------------------------------------------------------------
 // kernel selection (instantiated in one .cu per dense type)
 // ------------------------------------------------------------------------
 
-template <typename T, int STORE, bool WRITE, int V, int LANES, int CHUNKS, int U>
+template <typename T, int STORE, bool WRITE, int V, int LANES, int CHUNKS>
 const void* pick_cache_turn(const CachePlan& p) {
-    if constexpr (!WRITE)
-        return reinterpret_cast<const void*>(&rope_cache_read_kernel<T, STORE, V, LANES, CHUNKS, U>);
+    if constexpr (!WRITE) return reinterpret_cast<const void*>(&rope_cache_read_kernel<T, STORE, V, LANES, CHUNKS>);
     else if constexpr (V == 1)
-        return reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, U, false>);
+        return reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, false>);
     else
-        return p.turn ? reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, U, true>)
-                      : reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, U, false>);
-}
-
-template <typename T, int STORE, bool WRITE, int CHUNKS>
-const void* pick_cache_heads(const CachePlan& p) {
-    if constexpr (sizeof(T) == 2 && Store<STORE>::kBytes == 1) {
-        if (p.heads == 2) return pick_cache_turn<T, STORE, WRITE, 8, 8, CHUNKS, 2>(p);
-    }
-    return pick_cache_turn<T, STORE, WRITE, 8, 8, CHUNKS, 1>(p);
+        return p.turn ? reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, true>)
+                      : reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, false>);
 }
 
 // Rows of up to 64 / 128 / 192 / 256 / 1024 elements in 8-element accesses, or
@@ -385,16 +360,16 @@ const void* pick_cache_heads(const CachePlan& p) {
 template <typename T, int STORE, bool WRITE>
 const void* pick_cache_row(const CachePlan& p) {
     if (p.vec == 8) {
-        if (p.lanes == 32) return pick_cache_turn<T, STORE, WRITE, 8, 32, 4, 1>(p);
+        if (p.lanes == 32) return pick_cache_turn<T, STORE, WRITE, 8, 32, 4>(p);
         switch (p.chunks) {
-            case 1: return pick_cache_heads<T, STORE, WRITE, 1>(p);
-            case 2: return pick_cache_heads<T, STORE, WRITE, 2>(p);
-            case 3: return pick_cache_heads<T, STORE, WRITE, 3>(p);
-            default: return pick_cache_heads<T, STORE, WRITE, 4>(p);
+            case 1: return pick_cache_turn<T, STORE, WRITE, 8, 8, 1>(p);
+            case 2: return pick_cache_turn<T, STORE, WRITE, 8, 8, 2>(p);
+            case 3: return pick_cache_turn<T, STORE, WRITE, 8, 8, 3>(p);
+            default: return pick_cache_turn<T, STORE, WRITE, 8, 8, 4>(p);
         }
     }
-    return p.chunks <= 4 ? pick_cache_turn<T, STORE, WRITE, 1, 32, 4, 1>(p)
-                         : pick_cache_turn<T, STORE, WRITE, 1, 32, 32, 1>(p);
+    return p.chunks <= 4 ? pick_cache_turn<T, STORE, WRITE, 1, 32, 4>(p)
+                         : pick_cache_turn<T, STORE, WRITE, 1, 32, 32>(p);
 }
 
 template <typename T, bool WRITE>

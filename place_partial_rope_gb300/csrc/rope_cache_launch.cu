@@ -13,7 +13,7 @@ rope_status_t launch(const CachePlan& plan, const CacheArgs& args, bool write, r
         *err = "internal error: no kernel instance for this plan";
         return ROPE_ERR_CUDA;
     }
-    const uint64_t threads = uint64_t(args.groups) * plan.lanes;
+    const uint64_t threads = uint64_t(args.rows) * plan.lanes;
     void* params[] = {const_cast<CacheArgs*>(&args)};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -170,22 +170,19 @@ rope_status_t run_rows(const rope_kv_cache_t* c, CachePlan plan, CacheArgs a, bo
     plan.vec = w ? 8 : 1;
     plan.lanes = w && dim <= 256 ? 8 : 32;
     plan.chunks = static_cast<int>((dim + plan.vec * plan.lanes - 1) / (plan.vec * plan.lanes));
-    // two heads a group where that is built (16-bit rows, 8-bit codes): back to
-    // back TODO
-    plan.heads = plan.lanes == 8 && c->heads % 2 == 0 && plan.dtype != ROPE_FP32 && code_size(c->dtype) == 1 ? 2 : 1;
     if (!w) plan.turn = false;
     a.total = uint64_t(c->pages) * uint64_t(c->page_size);
     a.page_size = c->page_size;
     a.div_page = FastDiv::make(static_cast<uint32_t>(c->page_size));
     a.heads = static_cast<int32_t>(c->heads);
     a.first = keys ? 0 : 1;
-    const int64_t per = c->heads * (keys && values ? 2 : 1) / plan.heads;
+    const int64_t per = c->heads * (keys && values ? 2 : 1);
     a.div_rows = FastDiv::make(static_cast<uint32_t>(per));
     const int64_t most = (int64_t(1) << 31) / per;  // tokens of one launch
     for (int64_t t = 0; t < T; t += most) {
         const int64_t n = T - t < most ? T - t : most;
         CacheArgs p = a;
-        p.groups = static_cast<uint32_t>(n * per);
+        p.rows = static_cast<uint32_t>(n * per);
         p.slots += t;
         for (CacheSide& s : p.side)
             if (s.rows) s.rows += t * s.row_tok;
