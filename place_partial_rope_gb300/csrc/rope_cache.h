@@ -42,7 +42,7 @@ struct CacheArgs {
 struct CachePlan {
     int dtype;      // rope_dtype_t of the dense rows
     int store;      // rope_cache_dtype_t
-    int vec;        // elements per access: 8 (16-byte accesses of a 16-bit row) or 1
+    int vec;        // elements per access: 16 (reading codes), 8 or 1
     int lanes;      // lanes per row, a power of two <= 32
     int chunks;     // accesses per lane
     bool turn;      // the rotation's partner and cos/sin come as whole accesses

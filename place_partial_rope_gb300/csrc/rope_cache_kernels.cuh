@@ -25,7 +25,9 @@
 // or four heads of a token, their loads issued together and one slot looked up,
 // was slower: reading 65536 rows of 8 heads of 128 fp8 codes took 97 and 148 us
 // against 77 with one.)  Rows that are not aligned for 8-element accesses go one
-// element an access (V 1).
+// element an access (V 1).  8-bit rows are read by four lanes in accesses of 16
+// codes: 69 us against 75 in the case above; writing them so took 160 us for
+// 16411 tokens (and reading back) of 16 heads of 192 + 128, against 117.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -70,8 +72,11 @@ template <>
 struct Store<ROPE_CACHE_INT8> {
     static constexpr int kBytes = 1;
     static constexpr float kTop = 127.0f;
+    // The nearest integer of |v| <= 127, ties to even, in the low byte: the sum
+    // with 1.5 * 2^23 has it in its last bits (a conversion instruction runs at
+    // a quarter of the rate of an addition).
     static __device__ __forceinline__ uint32_t put(float v) {
-        return static_cast<uint32_t>(__float2int_rn(v)) & 0xffu;
+        return __float_as_uint(__fadd_rn(v, 12582912.0f));
     }
     static __device__ __forceinline__ float get(uint32_t w) {
         return static_cast<float>(static_cast<int8_t>(w & 0xffu));
@@ -83,7 +88,7 @@ template <int STORE, int V>
 __device__ __forceinline__ void store_codes(char* p, const float* v) {
     using S = Store<STORE>;
     if constexpr (V == 1) {
-        if constexpr (S::kBytes == 1) *reinterpret_cast<uint8_t*>(p) = static_cast<uint8_t>(S::put(v[0]));
+        if constexpr (S::kBytes == 1) *reinterpret_cast<uint8_t*>(p) = static_cast<uint8_t>(S::put(v[0]) & 0xffu);
         else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(S::put(v[0]));
     } else {
         constexpr int W = V * S::kBytes / 4;
@@ -97,8 +102,8 @@ __device__ __forceinline__ void store_codes(char* p, const float* v) {
                                                              __NV_SATFINITE, __NV_E4M3);
                 w.w[i] = lo | (hi << 16);
             } else if constexpr (S::kBytes == 1) {
-                w.w[i] = S::put(v[4 * i]) | (S::put(v[4 * i + 1]) << 8) | (S::put(v[4 * i + 2]) << 16) |
-                         (S::put(v[4 * i + 3]) << 24);
+                w.w[i] = __byte_perm(__byte_perm(S::put(v[4 * i]), S::put(v[4 * i + 1]), 0x0040),
+                                     __byte_perm(S::put(v[4 * i + 2]), S::put(v[4 * i + 3]), 0x0040), 0x5410);
             } else {
                 w.w[i] = S::put(v[2 * i]) | (S::put(v[2 * i + 1]) << 16);
             }
@@ -296,13 +301,20 @@ rope_cache_write_kernel(const __grid_constant__ CacheArgs a) {
         if (lane == 0 && r.there) *r.scale = finite ? __fdiv_rn(m, S::kTop) : __uint_as_float(0x7fffffffu);
     }
     if (!r.there) return;
+    if (!finite) {  // rare
+        inv = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[i][k] = 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
         const int j = (i * LANES + int(lane)) * V;
         if (j >= r.side->dim) continue;
         if constexpr (S::kBytes == 1) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) v[i][k] = finite ? __fmul_rn(v[i][k], inv) : 0.0f;
+            for (int k = 0; k < V; ++k) v[i][k] = __fmul_rn(v[i][k], inv);
         }
         store_codes<STORE, V>(r.codes + int64_t(j) * S::kBytes, v[i]);
     }
@@ -355,10 +367,20 @@ const void* pick_cache_turn(const CachePlan& p) {
                       : reinterpret_cast<const void*>(&rope_cache_write_kernel<T, STORE, V, LANES, CHUNKS, false>);
 }
 
-// Rows of up to 64 / 128 / 192 / 256 / 1024 elements in 8-element accesses, or
-// of up to 128 / 1024 in single elements.
+// Rows of up to 64 / 128 / 192 / 256 / 1024 elements in 8-element accesses (16
+// when 8-bit rows are read), or of up to 128 / 1024 in single elements.
 template <typename T, int STORE, bool WRITE>
 const void* pick_cache_row(const CachePlan& p) {
+    if constexpr (!WRITE && Store<STORE>::kBytes == 1) {
+        if (p.vec == 16) {
+            switch (p.chunks) {
+                case 1: return pick_cache_turn<T, STORE, WRITE, 16, 4, 1>(p);
+                case 2: return pick_cache_turn<T, STORE, WRITE, 16, 4, 2>(p);
+                case 3: return pick_cache_turn<T, STORE, WRITE, 16, 4, 3>(p);
+                default: return pick_cache_turn<T, STORE, WRITE, 16, 4, 4>(p);
+            }
+        }
+    }
     if (p.vec == 8) {
         if (p.lanes == 32) return pick_cache_turn<T, STORE, WRITE, 8, 32, 4>(p);
         switch (p.chunks) {

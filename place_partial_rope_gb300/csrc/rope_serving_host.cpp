@@ -118,10 +118,10 @@ CacheSide side_of(const rope_kv_cache_t* c, bool values, void* rows, const int64
     return s;
 }
 
-// Whether a side's rows allow 8-element accesses.
-bool wide(const rope_kv_cache_t* c, const CacheSide& s) {
-    const int64_t ce = 8 * code_size(c->dtype);
-    bool ok = s.dim % 8 == 0 && aligned(s.rows, 16) && aligned(s.codes, ce);
+// Whether a side's rows allow accesses of n (8 or 16) elements.
+bool wide(const rope_kv_cache_t* c, const CacheSide& s, int n) {
+    const int64_t ce = n * code_size(c->dtype);
+    bool ok = s.dim % n == 0 && aligned(s.rows, 16) && aligned(s.codes, ce);
     const int64_t dense[2] = {s.row_tok, s.row_head}, codes[3] = {s.page, s.tok, s.head};
     for (int64_t v : dense) ok = ok && v % 16 == 0;
     for (int64_t v : codes) ok = ok && v % ce == 0;
@@ -159,16 +159,18 @@ bool rows_overlap(const Rows& a, const Rows& b) {
 // whose row index fits 32 bits.
 template <typename Launch>
 rope_status_t run_rows(const rope_kv_cache_t* c, CachePlan plan, CacheArgs a, bool keys, bool values,
-                       int64_t T, Launch&& go) {
+                       bool write, int64_t T, Launch&& go) {
     int64_t dim = 0;
-    bool w = true;
+    bool w = true, w16 = !write && code_size(c->dtype) == 1;
     for (int i = 0; i < 2; ++i) {
         if (!(i ? values : keys)) continue;
         if (a.side[i].dim > dim) dim = a.side[i].dim;
-        w = w && wide(c, a.side[i]);
+        w = w && wide(c, a.side[i], 8);
+        w16 = w16 && wide(c, a.side[i], 16);
     }
-    plan.vec = w ? 8 : 1;
-    plan.lanes = w && dim <= 256 ? 8 : 32;
+    if (w16 && dim <= 256) plan.vec = 16, plan.lanes = 4;
+    else if (w) plan.vec = 8, plan.lanes = dim <= 256 ? 8 : 32;
+    else plan.vec = 1, plan.lanes = 32;
     plan.chunks = static_cast<int>((dim + plan.vec * plan.lanes - 1) / (plan.vec * plan.lanes));
     if (!w) plan.turn = false;
     a.total = uint64_t(c->pages) * uint64_t(c->page_size);
@@ -261,7 +263,7 @@ rope_status_t cache_write(const rope_kv_cache_t* c, const void* k, const void* v
     } else {
         plan.turn = true;  // nothing turns: either instance will do
     }
-    return run_rows(c, plan, a, true, v != nullptr, T,
+    return run_rows(c, plan, a, true, v != nullptr, true, T,
                     [&](const CachePlan& p, const CacheArgs& q, const char** err) {
                         return launch_cache_write(p, q, stream, err);
                     });
@@ -303,7 +305,7 @@ rope_status_t cache_read(const rope_kv_cache_t* c, const int64_t* slots, int64_t
     CachePlan plan{};
     plan.dtype = dtype;
     plan.store = c->dtype;
-    return run_rows(c, plan, a, k != nullptr, v != nullptr, T,
+    return run_rows(c, plan, a, k != nullptr, v != nullptr, false, T,
                     [&](const CachePlan& p, const CacheArgs& q, const char** err) {
                         return launch_cache_read(p, q, stream, err);
                     });
