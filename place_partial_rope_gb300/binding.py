@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -130,14 +131,14 @@ def load_library() -> ctypes.CDLL:
     for name in ("rope_partial_inplace_fwd_axes", "rope_partial_inplace_bwd_axes"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
-        fn.argtypes = [vp, vp, ctypes.c_int, i64, i64, i64, i64, i32, vp, i64p, i64p, ctypes.c_int,
+        fn.argtypes = [vp, vp, ctypes.c_int, i64, i64, i64, i64, i32, vp, vp, vp, ctypes.c_int,
                        ctypes.c_int, d, i64, i64, ctypes.c_int, vp]
     for name, argtypes in (
-            ("rope_partial_cache_write", [vp, vp, vp, ctypes.c_int, i64, i64p, i64p, vp, vp, vp, i64, i64,
+            ("rope_partial_cache_write", [vp, vp, vp, ctypes.c_int, i64, vp, vp, vp, vp, vp, i64, i64,
                                           i64, i64, ctypes.c_int, vp]),
-            ("rope_partial_cache_read", [vp, vp, i64, vp, vp, ctypes.c_int, i64p, i64p, vp]),
-            ("rope_partial_tree_attention", [vp, vp, ctypes.c_int, i64, i64, i64p, vp, vp, i64, i64, vp,
-                                             i64, i64, vp, i64, vp, i64p, vp, d, vp, i64, vp]),
+            ("rope_partial_cache_read", [vp, vp, i64, vp, vp, ctypes.c_int, vp, vp, vp]),
+            ("rope_partial_tree_attention", [vp, vp, ctypes.c_int, i64, i64, vp, vp, vp, i64, i64, vp,
+                                             i64, i64, vp, i64, vp, vp, vp, d, vp, i64, vp]),
             ("rope_partial_tree_attention_workspace", [vp, ctypes.c_int, i64, i64, i32, i64p]),
             ("rope_partial_tree_mask", [vp, i64, i64, vp])):
         fn = getattr(lib, name)
@@ -447,20 +448,26 @@ def rope_partial_token_shard(B: int, S: int, rank: int, world: int):
 # rotary positions with several axes, the paged cache and attention over it
 # ------------------------------------------------------------------------
 
-_I64x2 = ctypes.c_int64 * 2
-_I64x3 = ctypes.c_int64 * 3
-# the handle of torch's current stream of a device, without a Stream object
-# around it (a microsecond less per call); the public way where it is missing
+# Small host arrays go to the library as packed bytes: making them is a call,
+# where a ctypes array is several (these calls are short enough for that to
+# count).  Checks raise through _refuse only where they fail, so that no message
+# is put together for a call that is right.
+_pack2, _pack3 = struct.Struct("=2q").pack, struct.Struct("=3q").pack
+# the handle of torch's current stream of a device, and the current device,
+# without a Stream object or a context around them; the public ways where these
+# are missing
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(fn, args, stream, device) -> None:
     """Call fn(*args, stream) with `device` current; raise on an error status."""
+    index = device.index
     if stream is None and _raw_stream is not None:
-        handle = _raw_stream(device.index)
+        handle = _raw_stream(index)
     else:
         handle = _stream_handle(stream, device)
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -469,28 +476,37 @@ def _launch(fn, args, stream, device) -> None:
         _raise_for(_lib, st)
 
 
-def _require(cond, message: str) -> None:
-    if not cond:
-        raise RopeError(ROPE_ERR_INVALID, message)
+def _refuse(message: str):
+    raise RopeError(ROPE_ERR_INVALID, message)
 
 
 def _axes_call(name, x, positions, sections, start, end, base, mode, order, spectrum, stream):
     lib = _lib or load_library()
-    _require(x.dim() == 4, "x must be 4-D (B, S, N, D)")
-    _require(x.dtype in DTYPE_CODE, f"unsupported dtype {x.dtype}")
-    _require(x.is_cuda and x.is_contiguous(), "x must be a contiguous CUDA tensor")
-    _require(positions.dim() == 3 and positions.dtype == torch.int32,
-             "positions must be a 3-D int32 tensor (axes, B|1, S|1)")
-    _require(positions.device == x.device, "positions must be on x's device")
-    _require(order in ORDER_CODE, f"order {order!r} is not 'blocked' or 'interleaved'")
-    _require(spectrum in SPECTRUM_CODE, f"spectrum {spectrum!r} is not 'shared' or 'own'")
-    n = len(sections)
-    _require(n == positions.shape[0], "there must be one section for each axis of the positions")
+    if x.dim() != 4:
+        _refuse("x must be 4-D (B, S, N, D)")
+    dtype = DTYPE_CODE.get(x.dtype)
+    if dtype is None:
+        _refuse(f"unsupported dtype {x.dtype}")
+    if not x.is_cuda or not x.is_contiguous():
+        _refuse("x must be a contiguous CUDA tensor")
+    if positions.dim() != 3 or positions.dtype is not torch.int32:
+        _refuse("positions must be a 3-D int32 tensor (axes, B|1, S|1)")
+    device = x.device
+    if positions.device != device:
+        _refuse("positions must be on x's device")
+    if order not in ORDER_CODE:
+        _refuse(f"order {order!r} is not 'blocked' or 'interleaved'")
+    if spectrum not in SPECTRUM_CODE:
+        _refuse(f"spectrum {spectrum!r} is not 'shared' or 'own'")
+    if mode not in MODE_CODE:
+        _mode_code(mode)
+    n, shape = len(sections), positions.shape
+    if n != shape[0]:
+        _refuse("there must be one section for each axis of the positions")
     _launch(getattr(lib, name),
-            (x.data_ptr(), positions.data_ptr(), DTYPE_CODE[x.dtype], *x.shape, n,
-             (ctypes.c_int32 * n)(*sections), _I64x3(*positions.shape), _I64x3(*positions.stride()),
-             ORDER_CODE[order], SPECTRUM_CODE[spectrum], base, start, end, _mode_code(mode)),
-            stream, x.device)
+            (x.data_ptr(), positions.data_ptr(), dtype, *x.shape, n, struct.pack(f"={n}i", *sections),
+             _pack3(*shape), _pack3(*positions.stride()), ORDER_CODE[order], SPECTRUM_CODE[spectrum], base,
+             start, end, MODE_CODE[mode]), stream, device)
 
 
 def rope_partial_inplace_fwd_axes(x, positions, sections, start: int, end: int, base: float = 10000.0,
@@ -520,47 +536,53 @@ class KVCache:
     page_size, heads).  ``v`` may be None (keys only)."""
 
     def __init__(self, k, v=None, k_scale=None, v_scale=None):
-        tensors = [t for t in (k, v, k_scale, v_scale) if t is not None]
-        _require(k.dim() == 4 and (v is None or v.dim() == 4),
-                 "k and v must be 4-D (pages, page_size, heads, dim)")
-        _require(k.dtype in CACHE_CODE and (v is None or v.dtype == k.dtype),
-                 f"unsupported cache dtype {k.dtype}, or v of another")
-        _require(v is None or v.shape[:3] == k.shape[:3], "k and v must share pages, page_size and heads")
-        _require(all(t.is_cuda and t.device == k.device for t in tensors),
-                 "the cache must be CUDA tensors on one device")
+        if k.dim() != 4 or (v is not None and v.dim() != 4):
+            _refuse("k and v must be 4-D (pages, page_size, heads, dim)")
+        if k.dtype not in CACHE_CODE or (v is not None and v.dtype != k.dtype):
+            _refuse(f"unsupported cache dtype {k.dtype}, or v of another")
+        if v is not None and v.shape[:3] != k.shape[:3]:
+            _refuse("k and v must share pages, page_size and heads")
+        for t in (k, v, k_scale, v_scale):
+            if t is not None and (not t.is_cuda or t.device != k.device):
+                _refuse("the cache must be CUDA tensors on one device")
         for t in (k, v):
-            _require(t is None or t.shape[3] <= 1 or t.stride(3) == 1,
-                     "the last dim of k and v must be contiguous")
+            if t is not None and t.shape[3] > 1 and t.stride(3) != 1:
+                _refuse("the last dim of k and v must be contiguous")
         for t in (k_scale, v_scale):
-            _require(t is None or (t.dtype == torch.float32 and t.shape == k.shape[:3]),
-                     "scales must be fp32 (pages, page_size, heads)")
+            if t is not None and (t.dtype != torch.float32 or t.shape != k.shape[:3]):
+                _refuse("scales must be fp32 (pages, page_size, heads)")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.device
+        self.heads, self.k_dim, self.v_dim = k.shape[2], k.shape[3], 0 if v is None else v.shape[3]
 
         def ptr(t):
             return None if t is None else t.data_ptr()
 
         def strides(t):
-            return _I64x3(*t.stride()[:3]) if t is not None else _I64x3()
+            return (ctypes.c_int64 * 3)(*(t.stride()[:3] if t is not None else ()))
 
-        self._c = RopeKVCache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), *k.shape,
-                              0 if v is None else v.shape[3], strides(k), strides(v),
-                              strides(k_scale), strides(v_scale), CACHE_CODE[k.dtype], 0)
+        self._c = RopeKVCache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), *k.shape, self.v_dim,
+                              strides(k), strides(v), strides(k_scale), strides(v_scale),
+                              CACHE_CODE[k.dtype], 0)
         self._ref = ctypes.addressof(self._c)
 
 
 def _rows_of(t, cache, dim, what):
-    _require(t.dim() == 3 and t.shape[1] == cache._c.heads and t.shape[2] == dim,
-             f"{what} must be (tokens, {cache._c.heads}, {dim})")
-    _require(t.device == cache.device, f"{what} must be on the cache's device")
-    _require(t.shape[2] <= 1 or t.stride(2) == 1, f"the last dim of {what} must be contiguous")
-    return t.data_ptr(), _I64x2(*t.stride()[:2])
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != cache.heads or shape[2] != dim:
+        _refuse(f"{what} must be (tokens, {cache.heads}, {dim})")
+    if t.device != cache.device:
+        _refuse(f"{what} must be on the cache's device")
+    st = t.stride()
+    if st[2] != 1 and dim > 1:
+        _refuse(f"the last dim of {what} must be contiguous")
+    return t.data_ptr(), _pack2(st[0], st[1])
 
 
 def _slots_of(slots, cache, tokens):
-    _require(slots.dtype == torch.int64 and slots.dim() == 1 and slots.is_contiguous() and
-             slots.device == cache.device and (tokens is None or slots.shape[0] == tokens),
-             "slots must be a contiguous int64 vector on the cache's device, one per token")
+    if (slots.dtype is not torch.int64 or slots.dim() != 1 or not slots.is_contiguous() or
+            slots.device != cache.device or slots.shape[0] != tokens):
+        _refuse("slots must be a contiguous int64 vector on the cache's device, one per token")
     return slots.data_ptr()
 
 
@@ -572,29 +594,31 @@ def rope_partial_cache_write(cache: KVCache, k, v, slots, cos=None, sin=None, st
     skips its token), quantised where the cache holds 8 bits.  k and v stay as
     they are."""
     lib = _lib or load_library()
-    c = cache._c
-    _require(k.dtype in DTYPE_CODE and (v is None or v.dtype == k.dtype),
-             f"unsupported dtype {k.dtype}, or v of another")
-    kp, ks = _rows_of(k, cache, c.k_dim, "k")
-    vp, vs = (None, None)
-    if v is not None:
-        vp, vs = _rows_of(v, cache, c.v_dim, "v")
-        _require(v.shape[0] == k.shape[0], "k and v must hold the same tokens")
+    dtype = DTYPE_CODE.get(k.dtype)
+    if dtype is None or (v is not None and v.dtype != k.dtype):
+        _refuse(f"unsupported dtype {k.dtype}, or v of another")
+    if mode not in MODE_CODE:
+        _mode_code(mode)
+    kp, ks = _rows_of(k, cache, cache.k_dim, "k")
     T = k.shape[0]
-    cp = sp = None
+    vp = vs = cp = sp = None
+    if v is not None:
+        vp, vs = _rows_of(v, cache, cache.v_dim, "v")
+        if v.shape[0] != T:
+            _refuse("k and v must hold the same tokens")
     cst = sst = 0
     if cos is not None or sin is not None:
         for t in (cos, sin):
-            _require(t is not None and t.dim() == 2 and t.dtype == k.dtype and t.device == cache.device and
-                     t.shape[0] in (1, T) and t.shape[1] == end - start and
-                     (t.shape[1] <= 1 or t.stride(1) == 1),
-                     "cos and sin must be (tokens or 1, end - start) of k's dtype with a contiguous last dim")
+            if (t is None or t.dim() != 2 or t.dtype != k.dtype or t.device != cache.device or
+                    t.shape[0] not in (1, T) or t.shape[1] != end - start or
+                    (t.shape[1] > 1 and t.stride(1) != 1)):
+                _refuse("cos and sin must be (tokens or 1, end - start) of k's dtype with a contiguous last dim")
         cp, sp = cos.data_ptr(), sin.data_ptr()
         cst = cos.stride(0) if cos.shape[0] > 1 else 0
         sst = sin.stride(0) if sin.shape[0] > 1 else 0
     _launch(lib.rope_partial_cache_write,
-            (cache._ref, kp, vp, DTYPE_CODE[k.dtype], T, ks, vs, _slots_of(slots, cache, T), cp, sp, cst,
-             sst, start, end, _mode_code(mode)), stream, cache.device)
+            (cache._ref, kp, vp, dtype, T, ks, vs, _slots_of(slots, cache, T), cp, sp, cst, sst, start, end,
+             MODE_CODE[mode]), stream, cache.device)
 
 
 def rope_partial_cache_read(cache: KVCache, slots, k=None, v=None, stream=None) -> None:
@@ -602,20 +626,22 @@ def rope_partial_cache_read(cache: KVCache, slots, k=None, v=None, stream=None) 
     (T, heads, v_dim), either of which may be None; a slot outside the cache
     gives zeros."""
     lib = _lib or load_library()
-    c = cache._c
     kp = ks = vp = vs = None
     T, dtype = slots.shape[0], None
-    for t in (k, v):
-        if t is not None:
-            _require(t.dtype in DTYPE_CODE and dtype in (None, t.dtype), "k and v must share a dtype")
-            _require(t.shape[0] == T, "k and v must have a row for each slot")
-            dtype = t.dtype
+    if k is not None:
+        kp, ks = _rows_of(k, cache, cache.k_dim, "k")
+        dtype = k.dtype
+    if v is not None:
+        vp, vs = _rows_of(v, cache, cache.v_dim, "v")
+        if dtype is not None and v.dtype != dtype:
+            _refuse("k and v must share a dtype")
+        dtype = v.dtype
     if dtype is None:
         return
-    if k is not None:
-        kp, ks = _rows_of(k, cache, c.k_dim, "k")
-    if v is not None:
-        vp, vs = _rows_of(v, cache, c.v_dim, "v")
+    if dtype not in DTYPE_CODE:
+        _refuse(f"unsupported dtype {dtype}")
+    if (k is not None and k.shape[0] != T) or (v is not None and v.shape[0] != T):
+        _refuse("k and v must have a row for each slot")
     _launch(lib.rope_partial_cache_read,
             (cache._ref, _slots_of(slots, cache, T), T, kp, vp, DTYPE_CODE[dtype], ks, vs), stream,
             cache.device)
@@ -639,7 +665,8 @@ def tree_attention_workspace(q, cache: KVCache, max_q: int) -> torch.Tensor:
     and ``max_q``.  A program keeps it: calls that follow each other on one
     stream can share it."""
     lib = _lib or load_library()
-    _require(q.dim() == 3 and q.dtype in DTYPE_CODE, "q must be (tokens, heads, dim) of bf16 or fp16")
+    if q.dim() != 3 or q.dtype not in DTYPE_CODE:
+        _refuse("q must be (tokens, heads, dim) of bf16 or fp16")
     need = ctypes.c_int64()
     with torch.cuda.device(cache.device):
         st = lib.rope_partial_tree_attention_workspace(cache._ref, DTYPE_CODE[q.dtype], q.shape[1],
@@ -661,28 +688,37 @@ def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, 
     tokens of a request) to Tq, and the workspace is made for the call when
     none is given."""
     lib = _lib or load_library()
-    c = cache._c
-    _require(q.dim() == 3 and q.shape[2] == c.k_dim and q.dtype in DTYPE_CODE,
-             f"q must be (tokens, heads, {c.k_dim}) of bf16 or fp16")
-    Tq, Hq = q.shape[0], q.shape[1]
-    _require(out.dtype == q.dtype and out.shape == (Tq, Hq, c.v_dim),
-             f"out must be ({Tq}, {Hq}, {c.v_dim}) of q's dtype")
-    _require((q.stride(2) == 1 or c.k_dim == 1) and (out.stride(2) == 1 or c.v_dim == 1),
-             "the last dim of q and out must be contiguous")
+    dev, kd, vd = cache.device, cache.k_dim, cache.v_dim
+    dtype = DTYPE_CODE.get(q.dtype)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != kd or dtype is None:
+        _refuse(f"q must be (tokens, heads, {kd}) of bf16 or fp16")
+    Tq, Hq = shape[0], shape[1]
+    if out.dtype != q.dtype or out.shape != (Tq, Hq, vd):
+        _refuse(f"out must be ({Tq}, {Hq}, {vd}) of q's dtype")
+    qs, os_ = q.stride(), out.stride()
+    if (qs[2] != 1 and kd > 1) or (os_[2] != 1 and vd > 1):
+        _refuse("the last dim of q and out must be contiguous")
     R = kv_len.shape[0]
-    _require(q_start.dtype == torch.int32 and kv_len.dtype == torch.int32 and
-             q_start.shape == (R + 1,) and kv_len.dim() == 1 and q_start.is_contiguous() and
-             kv_len.is_contiguous(), "q_start and kv_len must be contiguous int32 vectors of R + 1 and R")
-    _require(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == R and
-             (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
-             "page_table must be int32 (R, pages) with a contiguous last dim")
-    _require(lse is None or (lse.dtype == torch.float32 and lse.shape == (Tq, Hq) and lse.is_contiguous()),
-             "lse must be contiguous fp32 (Tq, Hq)")
-    _require(tree is None or (tree.dtype == torch.int64 and tree.dim() == 2 and tree.shape[0] == Tq and
-                              tree.is_contiguous()), "tree must be contiguous int64 (Tq, words)")
-    dev = cache.device
-    for t in (q, out, q_start, kv_len, page_table, lse, tree, workspace):
-        _require(t is None or t.device == dev, "every tensor must be on the cache's device")
+    if (q_start.dtype is not torch.int32 or kv_len.dtype is not torch.int32 or kv_len.dim() != 1 or
+            q_start.shape != (R + 1,) or not q_start.is_contiguous() or not kv_len.is_contiguous()):
+        _refuse("q_start and kv_len must be contiguous int32 vectors of R + 1 and R")
+    pt = page_table.shape
+    if page_table.dtype is not torch.int32 or len(pt) != 2 or pt[0] != R:
+        _refuse("page_table must be int32 (R, pages) with a contiguous last dim")
+    pst = page_table.stride()
+    if pt[1] > 1 and pst[1] != 1:
+        _refuse("page_table must be int32 (R, pages) with a contiguous last dim")
+    lp = tp = None
+    words = 0
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (Tq, Hq) or not lse.is_contiguous():
+            _refuse("lse must be contiguous fp32 (Tq, Hq)")
+        lp = lse.data_ptr()
+    if tree is not None:
+        if tree.dtype is not torch.int64 or tree.dim() != 2 or tree.shape[0] != Tq or not tree.is_contiguous():
+            _refuse("tree must be contiguous int64 (Tq, words)")
+        tp, words = tree.data_ptr(), tree.shape[1]
     if max_q is None:
         max_q = max(1, Tq)
     if workspace is None:
@@ -691,12 +727,13 @@ def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, 
             # made on the current stream, used on another: the allocator must know
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                     else torch.cuda.ExternalStream(int(stream), device=dev))
-    _require(workspace.is_contiguous(), "workspace must be contiguous")
+    for t in (q, out, q_start, kv_len, page_table, lse, tree, workspace):
+        if t is not None and t.device != dev:
+            _refuse("every tensor must be on the cache's device")
+    if not workspace.is_contiguous():
+        _refuse("workspace must be contiguous")
     _launch(lib.rope_partial_tree_attention,
-            (cache._ref, q.data_ptr(), DTYPE_CODE[q.dtype], Tq, Hq, _I64x2(*q.stride()[:2]),
-             q_start.data_ptr(), kv_len.data_ptr(), R, max_q, page_table.data_ptr(), page_table.shape[1],
-             page_table.stride(0) if R > 1 else page_table.shape[1],
-             None if tree is None else tree.data_ptr(), 0 if tree is None else tree.shape[1],
-             out.data_ptr(), _I64x2(*out.stride()[:2]), None if lse is None else lse.data_ptr(),
-             c.k_dim ** -0.5 if scale is None else scale, workspace.data_ptr(),
-             workspace.numel() * workspace.element_size()), stream, dev)
+            (cache._ref, q.data_ptr(), dtype, Tq, Hq, _pack2(qs[0], qs[1]), q_start.data_ptr(),
+             kv_len.data_ptr(), R, max_q, page_table.data_ptr(), pt[1], pst[0] if R > 1 else pt[1], tp, words,
+             out.data_ptr(), _pack2(os_[0], os_[1]), lp, kd ** -0.5 if scale is None else scale,
+             workspace.data_ptr(), workspace.nbytes), stream, dev)

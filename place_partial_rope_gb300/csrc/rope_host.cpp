@@ -676,6 +676,7 @@ rope_status_t run_axes(int dir, void* x, const int32_t* positions, int dtype, in
     table.pos_a = ps[0];
     table.axes = axes;
     int32_t dealt[ROPE_MAX_AXES] = {0, 0, 0, 0};
+    double power[ROPE_MAX_AXES] = {}, ratio[ROPE_MAX_AXES] = {};
     int a = 0;
     const int64_t pairs = L / 2;
     for (int64_t k = 0; k < pairs; ++k) {
@@ -684,9 +685,14 @@ rope_status_t run_axes(int dir, void* x, const int32_t* positions, int dtype, in
         while (dealt[a] == sections[a]) a = a + 1 == axes ? 0 : a + 1;
         const int32_t j = dealt[a]++;
         table.axis[k] = static_cast<uint8_t>(a);
-        const double part = spectrum == ROPE_SPECTRUM_SHARED ? double(k) / double(pairs)
-                                                             : double(j) / double(sections[a]);
-        const double w = pow(base, -part);
+        // base^(-i/of) by pow() at every 16th i, by products between (each adds
+        // half an ulp of double; two fp32 parts keep 48 bits)
+        const int64_t i = spectrum == ROPE_SPECTRUM_SHARED ? k : j;
+        const double of = spectrum == ROPE_SPECTRUM_SHARED ? double(pairs) : double(sections[a]);
+        const int c = spectrum == ROPE_SPECTRUM_SHARED ? 0 : a;
+        if (i == 0) ratio[c] = pow(base, -1.0 / of);
+        power[c] = i % 16 == 0 ? (i == 0 ? 1.0 : pow(base, -double(i) / of)) : power[c] * ratio[c];
+        const double w = power[c];
         table.hi[k] = static_cast<float>(w);
         table.lo[k] = static_cast<float>(w - static_cast<double>(table.hi[k]));
         if (order == ROPE_AXES_INTERLEAVED) a = a + 1 == axes ? 0 : a + 1;
