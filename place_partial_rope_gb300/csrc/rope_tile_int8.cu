@@ -5,11 +5,9 @@
 namespace rope {
 
 TreeKernel tile_kernel_int8(const TreePlan& p) {
-    const bool pair = p.rows == 256;
-    if (p.dk == 64) return pair ? tile_kernel<ROPE_CACHE_INT8, 64, 64, true>() : tile_kernel<ROPE_CACHE_INT8, 64, 64, false>();
-    if (p.dk == 128)
-        return pair ? tile_kernel<ROPE_CACHE_INT8, 128, 128, true>() : tile_kernel<ROPE_CACHE_INT8, 128, 128, false>();
-    return pair ? tile_kernel<ROPE_CACHE_INT8, 192, 128, true>() : tile_kernel<ROPE_CACHE_INT8, 192, 128, false>();
+    if (p.dk == 64) return pick_tile_rows<ROPE_CACHE_INT8, 64, 64>(p);
+    if (p.dk == 128) return pick_tile_rows<ROPE_CACHE_INT8, 128, 128>(p);
+    return pick_tile_rows<ROPE_CACHE_INT8, 192, 128>(p);
 }
 
 }  // namespace rope

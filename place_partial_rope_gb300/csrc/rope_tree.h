@@ -53,7 +53,7 @@ struct TreePlan {
     int dtype;    // rope_dtype_t of q
     int store;    // rope_cache_dtype_t
     int dk, dv;   // row lengths the kernel is built for (>= the call's)
-    int rows;     // query rows of a tile: 16 (narrow kernel), 128 or 256 (tile kernel)
+    int rows;     // query rows of a tile: 16 (narrow kernel), 32, 64, 128 or 256 (tile kernel)
 };
 
 // The kernel for rows of Dk and Dv, `rows` query rows a key head and pages of

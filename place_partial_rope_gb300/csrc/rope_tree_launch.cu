@@ -139,7 +139,10 @@ void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, TreePlan* p) {
     else if (Dk <= 128) p->dk = 128, p->dv = 128;
     else if (Dk <= 192 && Dv <= 128) p->dk = 192, p->dv = 128;
     else p->dk = 256, p->dv = 256;
-    p->rows = p->dk == 256 || rows <= 16 || page_size % 8 ? 16 : rows <= 128 ? 128 : 256;
+    const bool wide = p->store == ROPE_CACHE_BF16 || p->store == ROPE_CACHE_FP16;
+    if (p->dk == 256 || rows <= 16 || page_size % 8) p->rows = 16;
+    else if (rows <= 32 && (wide || p->dk < 192)) p->rows = 32;
+    else p->rows = rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
 }
 
 rope_status_t tree_blocks(const TreePlan& p, int sm_count, int* blocks, const char** err) {

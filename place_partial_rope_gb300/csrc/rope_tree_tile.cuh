@@ -47,16 +47,18 @@
 
 namespace rope {
 
-template <int STORE_, int DK_, int DV_, bool PAIR_>
+template <int STORE_, int DK_, int DV_, int ROWS_>
 struct TileCfg {
     static constexpr int STORE = STORE_, DK = DK_, DV = DV_;
-    static constexpr bool PAIR = PAIR_;
+    static constexpr int ROWS = ROWS_;  // query rows of a tile: 32, 64, 128 or 256
+    static constexpr bool PAIR = ROWS == 256;
+    static constexpr int SPLIT = PAIR ? 1 : 128 / ROWS;  // copies of the rows in tensor memory
     static constexpr bool kWide = STORE == ROPE_CACHE_BF16 || STORE == ROPE_CACHE_FP16;  // 16-bit codes
     static constexpr bool BF16 = STORE == ROPE_CACHE_BF16;
     // cache rows of a tile: 128 where shared memory holds two tiles of that
     // (a product of 64 columns takes three quarters of the time of 128)
     static constexpr int TN = DK == 64 || (!PAIR && (kWide || DK == 128)) || (kWide && DK == 128) ? 128 : 64;
-    static constexpr int ROWS = PAIR ? 256 : 128;
+    static constexpr int COLS = TN / SPLIT;  // columns of s that a thread sees to
     static constexpr int QTILE = 128 * DK * 2, Q_BYTES = QTILE * (PAIR ? 2 : 1);
     // keys and values have rings of their own: a tile's keys are done with when
     // s is there, its values only after the softmax
@@ -137,8 +139,9 @@ __device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity,
 // The 256 threads of the softmax groups.
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// The 192 threads that see to tiles between the fetch and the products.
-constexpr int kHelpers = 192;
+// The 192 threads that see to tiles between the fetch and the products; 8-bit:
+// one half of them to keys, one to values.
+constexpr int kHelpers = 192, kTeam = 96;
 __device__ __forceinline__ void helpers_sync() { asm volatile("bar.sync 2, 192;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -163,6 +166,17 @@ __device__ __forceinline__ void tmem_ld32(float* r, uint32_t at) {
         : "r"(at)
         : "memory");
 }
+
+__device__ __forceinline__ void tmem_ld16(float* r, uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : ROPE_R8(r, 0), ROPE_R8(r, 8)
+        : "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_here16(float* r) { asm volatile("" : ROPE_B8(r, 0), ROPE_B8(r, 8)); }
 
 // After tmem_wait_ld: what was loaded is not touched before this.
 __device__ __forceinline__ void tmem_here32(float* r) {
@@ -385,23 +399,26 @@ struct Tile {
     // Codes to fp16, in a tile's layout; rows from `valid` on become zeros.
     // Eight threads take 16 codes each of two successive rows: 64 of either row,
     // in an order that meets all banks both reading rows of codes and writing
-    // lines (128 lanes: the second row's other half).  The helpers' step from
-    // one such unit to the next is a multiple of eight rows, so a thread's
-    // addresses differ by constants and a unit costs a load, twelve conversion
-    // instructions and two stores: a helper is one warp in turn with few
-    // others, so that its instructions count at their latency.
+    // lines (128 lanes: the second row's other half).  A team's step from one
+    // such unit to the next is 4 or 8 rows modulo 8, so a thread's addresses
+    // differ by constants from one or two places, and a unit costs a load,
+    // twelve conversion instructions and two stores: a helper warp has few others
+    // to take turns with, so its instructions count at their latency.
     template <int D>
     static __device__ __forceinline__ void widen(uint32_t raw, uint32_t to, int id, int valid) {
-        constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kHelpers / 8, N = (UNITS + STEP - 1) / STEP;
+        constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kTeam / 8, N = (UNITS + STEP - 1) / STEP;
         constexpr int ROWS = STEP / G * 2;  // from a unit to the thread's next
-        static_assert(STEP % G == 0 && ROWS % 8 == 0, "the same place in the swizzle");
+        static_assert(STEP % G == 0 && ROWS % 4 == 0, "one of two places in the swizzle");
         const int u = id >> 3, odd = (id >> 2) & 1;
         const int row = u / G * 2 + odd, ch = ((G == 2 && odd ? u % G ^ 1 : u % G) << 2) + (id & 3);
         raw += row * D + ch * 16;
+        // four rows on, chunk c of a line lies where c ^ 4 would
         const uint32_t lo = to + line_at(row, 2 * ch), hi = to + line_at(row, 2 * ch + 1);
-        constexpr int B = (N + 1) / 2;
+        const uint32_t lo4 = to + line_at(row, (2 * ch) ^ 4), hi4 = to + line_at(row, (2 * ch + 1) ^ 4);
+        constexpr int B = 4;
 #pragma unroll
         for (int i0 = 0; i0 < N; i0 += B) {
+            // a few loads, then their conversions: the loads do not wait for each other
             uint32_t w[B][4];
 #pragma unroll
             for (int i = 0; i < B; ++i)
@@ -417,62 +434,75 @@ struct Tile {
                     h[2 * j] = codes_to_half2<C::STORE, false>(w[i][j]);
                     h[2 * j + 1] = codes_to_half2<C::STORE, true>(w[i][j]);
                 }
-                sts128(lo + (i0 + i) * (ROWS * 128), h[0], h[1], h[2], h[3]);
-                sts128(hi + (i0 + i) * (ROWS * 128), h[4], h[5], h[6], h[7]);
+                const bool four = ((i0 + i) * ROWS) % 8 != 0;
+                sts128((four ? lo4 : lo) + (i0 + i) * (ROWS * 128), h[0], h[1], h[2], h[3]);
+                sts128((four ? hi4 : hi) + (i0 + i) * (ROWS * 128), h[4], h[5], h[6], h[7]);
             }
         }
     }
 
-    // 8-bit: the helpers turn codes into fp16 tiles and bring the scales.
+    // 8-bit: the helpers turn codes into fp16 tiles and bring the scales, one
+    // team keys (VALUES false), one values.
+    template <bool VALUES>
     __device__ __forceinline__ void widen_tiles(const Place& place, int id) const {
         constexpr uint32_t SLOTS = C::SLOTS, RAWS = C::RAWS > 0 ? C::RAWS : 1;
+        const float* scales = VALUES ? a.vs : a.ks;
+        const int64_t* st = VALUES ? a.vs_st : a.ks_st;
+        unsigned long long* full = VALUES ? sync->v_full : sync->k_full;
+        unsigned long long* empty = VALUES ? sync->v_empty : sync->k_empty;
+        constexpr int MORE = C::TN > kTeam ? 2 : 1;  // rows of a thread: id, and id + 96 for some
+        const bool second = MORE == 2 && id < C::TN - kTeam;
         Walk walk(place);
         RunAt step;
         uint32_t n = 0, run = 0;
         while (next_run<C::ROWS, C::TN>(a, walk, step)) {
             const RunAt x = step;
-            Look now{-1, 0};
-            if (id < C::TN) now = look(x, x.t0 * C::TN + id);
-            for (int it = 0; it < x.count; ++it, ++n) {
-                const uint32_t slot = n % SLOTS;
-                const int j0 = (x.t0 + it) * C::TN;
-                float* sc = reinterpret_cast<float*>(smem + C::SC_AT + n % C::SCS * C::SC);
-                const bool there = now.page >= 0 && now.page < a.pages;
-                float scale[2] = {0.0f, 0.0f};
-                if (there) {
-                    scale[0] = __ldg(a.ks + now.page * a.ks_st[0] + int64_t(now.off) * a.ks_st[1] + int64_t(x.h) * a.ks_st[2]);
-                    scale[1] = __ldg(a.vs + now.page * a.vs_st[0] + int64_t(now.off) * a.vs_st[1] + int64_t(x.h) * a.vs_st[2]);
-                }
-                if (id < C::TN && it + 1 < x.count) now = look(x, j0 + C::TN + id);
-                else now.page = -1;
+            const int first = x.t0 * C::TN, prefix = x.rq.len - x.rq.n;
+            Look now[MORE];
+            now[0] = look(x, id < C::TN ? first + id : x.rq.len);
+            if (MORE == 2) now[MORE - 1] = look(x, second ? first + kTeam + id : x.rq.len);
 #pragma unroll 1
-                for (int values = 0; values < 2; ++values) {
-                    const uint32_t item = 2 * n + values, r = item % RAWS;
-                    bar_wait(&sync->raw_full[r], (item / RAWS) & 1, sync);
-                    if (n >= SLOTS)
-                        bar_wait(values ? &sync->v_empty[slot] : &sync->k_empty[slot], (n / SLOTS - 1) & 1, sync);
-                    const uint32_t raw = smem_addr(smem + C::RAW_AT) + r * C::RAW;
-                    const uint32_t to = smem_addr(smem) + (values ? C::V_AT + slot * C::V_SLOT : C::K_AT + slot * C::K_SLOT);
-                    if (C::DV == C::DK || !values) widen<C::DK>(raw, to, id, x.rq.len - j0);
-                    else widen<C::DV>(raw, to, id, x.rq.len - j0);
-                    float v = values ? scale[1] : scale[0];
-                    if (values) {
+            for (int it = 0; it < x.count; ++it, ++n) {
+                const uint32_t slot = n % SLOTS, item = 2 * n + (VALUES ? 1 : 0), r = item % RAWS;
+                const int j0 = first + it * C::TN;
+                float* sc = reinterpret_cast<float*>(smem + C::SC_AT + n % C::SCS * C::SC) + (VALUES ? C::TN : 0);
+                float scale[MORE];
+#pragma unroll
+                for (int k = 0; k < MORE; ++k) {
+                    scale[k] = 0.0f;
+                    if (now[k].page >= 0 && now[k].page < a.pages)
+                        scale[k] = __ldg(scales + now[k].page * st[0] + int64_t(now[k].off) * st[1] + int64_t(x.h) * st[2]);
+                    const int j = j0 + C::TN + id + kTeam * k;
+                    now[k] = look(x, (k ? second : id < C::TN) && it + 1 < x.count ? j : x.rq.len);
+                }
+                bar_wait(&sync->raw_full[r], (item / RAWS) & 1, sync);
+                if (n >= SLOTS) bar_wait(&empty[slot], (n / SLOTS - 1) & 1, sync);
+                widen<VALUES ? C::DV : C::DK>(smem_addr(smem + C::RAW_AT) + r * C::RAW,
+                                              smem_addr(smem) + (VALUES ? C::V_AT + slot * C::V_SLOT : C::K_AT + slot * C::K_SLOT),
+                                              id, x.rq.len - j0);
+                float most = 0.0f;
+#pragma unroll
+                for (int k = 0; k < MORE; ++k) {
+                    float v = scale[k];
+                    if (VALUES) {
                         // a drafted row's scale that is not finite is taken out (see add_not_finite)
-                        if (j0 + id >= x.rq.len - x.rq.n && !(fabsf(v) <= 3.4028234663852886e38f)) {
+                        if (j0 + id + kTeam * k >= prefix && !(fabsf(v) <= 3.4028234663852886e38f)) {
                             v = 0.0f;
                             sync->patch[run & 7] = 1;
                         }
-                        if (id < C::TN) sc[C::TN + id] = v;
-                        // (scales are not negative: their bits order like them)
-                        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.0f)));
-                        if ((id & 31) == 0 && id < 128) sc[2 * C::TN + (id >> 5)] = __uint_as_float(most);
-                    } else if (id < C::TN) {
-                        sc[id] = v;
+                        most = fmaxf(most, v);
                     }
-                    to_async_proxy();
-                    bar_arrive(&sync->raw_empty[r]);
-                    bar_arrive(values ? &sync->v_full[slot] : &sync->k_full[slot]);
+                    if (k ? second : id < C::TN) sc[id + kTeam * k] = v;
                 }
+                if (VALUES) {
+                    // (scales are not negative: their bits order like them)
+                    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+                    if ((id & 31) == 0) sc[C::TN + (id >> 5)] = __uint_as_float(bits);
+                    if (id == 0) sc[C::TN + 3] = 0.0f;
+                }
+                to_async_proxy();
+                bar_arrive(&sync->raw_empty[r]);
+                bar_arrive(&full[slot]);
             }
             ++run;
         }
@@ -610,7 +640,7 @@ struct Tile {
     // The row tile's queries: 16-bit as they are, or fp16 in [-2, 2); returns
     // what the row's s is multiplied by.
     __device__ __forceinline__ float stage_queries(const RunAt& x, int w, int row) const {
-        const int at = x.m * C::ROWS + (C::PAIR ? 128 * w : 0) + row;
+        const int at = x.m * C::ROWS + (C::PAIR ? 128 * w : 0) + row % (C::PAIR ? 128 : C::ROWS);
         const bool there = at < x.rq.n * a.G;
         uint32_t tok = 0, g = 0;
         if (there) a.div_group.divmod(uint32_t(at), tok, g);
@@ -759,7 +789,10 @@ struct Tile {
             bar_arrive(&sync->q_full);
 
             const int rows = x.rq.n * a.G;
-            const int at = x.m * C::ROWS + (C::PAIR ? 128 * w : 0) + row;
+            // the thread's query row, and the columns of s that it sees to (of 32 or
+            // 64 query rows each warp or pair of warps has a copy, and its own columns)
+            const int mine = C::PAIR ? row : row % C::ROWS, lo = row / (C::PAIR ? 128 : C::ROWS) * C::COLS;
+            const int at = x.m * C::ROWS + (C::PAIR ? 128 * w : 0) + mine;
             const bool active = at - (row & 31) < rows;  // the warp has a row
             const int tok = min(int(a.div_group.div(uint32_t(at))), x.rq.n - 1);
             const int prefix = x.rq.len - x.rq.n, nv = C::PAIR ? 2 * x.count : x.count;
@@ -789,7 +822,7 @@ struct Tile {
                     }
                     if (part) {
 #pragma unroll 1
-                        for (int c = 0; c < C::TN; c += 32)
+                        for (int c = lo; c < lo + C::COLS; c += 32)
                             mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c));
                         tmem_wait_st();
                     }
@@ -798,11 +831,11 @@ struct Tile {
                     // instruction cache beside the helpers' (with s held, the
                     // roles' code missed it and every role ran at a third of its
                     // speed); the rows are bound by HBM, so the second read hides.
-                    constexpr int HELD = C::kWide ? C::TN : 32;
+                    constexpr int HELD = C::kWide ? C::COLS : 32;
                     float s[HELD], top = -INFINITY;
                     const uint32_t from = lanes + s_col(w);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < C::TN; c0 += HELD) {
+                    for (int c0 = lo; c0 < lo + C::COLS; c0 += HELD) {
 #pragma unroll
                         for (int c = 0; c < HELD; c += 32) tmem_ld32(s + c, from + c0 + c);
                         tmem_wait_ld();
@@ -824,7 +857,7 @@ struct Tile {
                     const float base = C::kBias - (m == -INFINITY ? 0.0f : m) - (C::kWide ? 0.0f : exponent(vref));
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
-                    for (int c0 = 0; c0 < C::TN; c0 += HELD) {
+                    for (int c0 = lo; c0 < lo + C::COLS; c0 += HELD) {
                         if constexpr (!C::kWide) {
                             // (p of the columns before lies over s of columns before those)
                             tmem_ld32(s, from + c0);
@@ -837,6 +870,13 @@ struct Tile {
                             weights32(s + c, sc + C::TN + c0 + c, factor, base, sum, from + (c0 + c) / 2);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    if constexpr (C::SPLIT > 1) {
+                        // weights of 0 in the columns of the other copies
+                        const uint32_t none[16] = {};
+#pragma unroll 1
+                        for (int c = 0; c < C::TN; c += 32)
+                            if (c < lo || c >= lo + C::COLS) tmem_st16(from + c / 2, none);
+                    }
                     tmem_wait_st();
                 }
                 tmem_before();
@@ -848,7 +888,8 @@ struct Tile {
                 tmem_after();
             }
             if constexpr (!C::kWide) l *= vref;
-            finish(x, w, row, at, at < rows, active, nv, m, l, vref, sync->patch[run & 7] != 0, ml, lanes);
+            if constexpr (C::PAIR) finish(x, w, row, at, at < rows, active, m, l, vref, sync->patch[run & 7], lanes);
+            else gather(x, w, row, active, nv, m, l, vref, &sync->patch[run & 7], ml, lanes);
             tmem_before();
             groups_sync();  // queries, O and ml are done with
             if (tid == 0) sync->patch[run & 7] = 0;
@@ -858,77 +899,127 @@ struct Tile {
         if (tid == 0) a.meta[blockIdx.x] = meta;
     }
 
-    // The results of a run.  A thread holds a row, which it would write 16 bytes
-    // at a time, 32 rows an instruction; rows go through shared memory (the
-    // queries' place; 32 words of 32 rows a warp, words swizzled by the row), so
-    // that a warp writes 128 bytes of a row at once.
-    __device__ __forceinline__ void finish(const RunAt& x, int w, int row, int at, bool there, bool active, int nv,
-                                           float m, float l, float vref, bool patch, float2* ml,
-                                           uint32_t lanes) const {
-        float f = C::kWide ? 1.0f : vref;
-        const bool alone = C::PAIR || nv == 1;  // one group has the row to itself
+    // The results of a run of a pair.  A thread holds a row, which it would write
+    // 16 bytes at a time, 32 rows an instruction; rows go through shared memory
+    // (the queries' place; 32 words of 32 rows a warp, words swizzled by the
+    // row), so that a warp writes 64 bytes of a row at once.  A part is written as
+    // it is held, columns first.
+    __device__ __forceinline__ void finish(const RunAt& x, int w, int row, int at, bool there, bool active, float m,
+                                           float l, float vref, bool patch, uint32_t lanes) const {
+        if (!active) return;
         const int lane = row & 31;
-        float top = m;
-        if (!alone) {
-            // the groups took turns at the tiles
-            ml[w * 128 + row] = make_float2(m, l);
-            groups_sync();
-            const float2 other = ml[(1 - w) * 128 + row];
-            top = fmaxf(m, other.x);
-            const float base = top == -INFINITY ? 0.0f : top, own = pow2(m - base);
-            f *= own;
-            l = l * own + other.y * pow2(other.x - base);
-        }
         if (sync->dead) l = NAN;
-        const bool whole = x.slot < 0, mine = alone ? (C::PAIR || w == 0) : w == 0;
+        const bool whole = x.slot < 0;
         OutAt to{nullptr, nullptr};
-        float norm = 1.0f;
-        if (mine && there) {
+        float norm = C::kWide ? 1.0f : vref;
+        if (there) {
             if (whole) {
                 to = out_at(a, x.rq.qs, x.h, at);
-                if (to.lse) *to.lse = lse_of(top, l, C::kBias);
-                norm = l == 0.0f ? 0.0f : 1.0f / l;  // a token that has seen no row gives zeros
+                if (to.lse) *to.lse = lse_of(m, l, C::kBias);
+                norm *= l == 0.0f ? 0.0f : 1.0f / l;  // a token that has seen no row gives zeros
             } else {
-                a.part_ml[x.slot * C::ROWS + (C::PAIR ? 128 * w : 0) + row] = make_float2(top, l);
+                a.part_ml[x.slot * C::ROWS + 128 * w + row] = make_float2(m, l);
             }
         }
-        float* words = reinterpret_cast<float*>(smem + (C::PAIR ? w * C::QTILE : 0)) + (row >> 5) * 1024;
+        float* words = reinterpret_cast<float*>(smem + w * C::QTILE) + (row >> 5) * 1024;
 #pragma unroll 1
         for (int c = 0; c < C::DV; c += 32) {
             float o[32];
-            if (active && (mine || !alone)) {
-                tmem_ld32(o, lanes + o_col(w) + c);
+            tmem_ld32(o, lanes + o_col(w) + c);
+            tmem_wait_ld();
+            tmem_here32(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= norm;
+            if (patch && there) add_not_finite<C::STORE, C::TN, 32>(a, x, at, c, o);
+            if (whole) {
+                write32(words, o, to.out, c, lane);
+            } else {
+                // (rows that are not there have a place too)
+                using P = PartAt<C::ROWS, C::DV>;
+                float* part = a.part + P::block(x.slot, 4 * w + (row >> 5)) + c * 32 + lane;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) part[j * 32] = o[j];
+            }
+        }
+    }
+
+    // The results of a run whose groups, and whose copies of the rows, each saw to
+    // tiles and columns of their own: (m, l) and O of 2 SPLIT sources are joined
+    // through shared memory (O in the queries' place, 16 columns at a time,
+    // rows side by side).
+    __device__ __forceinline__ void gather(const RunAt& x, int w, int row, bool active, int nv, float m, float l,
+                                           float vref, const volatile uint32_t* patched, float2* ml,
+                                           uint32_t lanes) const {
+        constexpr int R = C::ROWS, SRC = 2 * C::SPLIT, ITEMS = R * 4;  // items: a row's four columns
+        const int tid = w * 128 + row, mine = row % R, src = w * C::SPLIT + row / R;
+        const bool none = w >= nv;  // a group without a tile
+        ml[src * R + mine] = none ? make_float2(-INFINITY, 0.0f) : make_float2(m, l);
+        groups_sync();
+        const bool patch = *patched != 0;  // (after both groups have waited for their products)
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < SRC; ++k) top = fmaxf(top, ml[k * R + mine].x);
+        const float base = top == -INFINITY ? 0.0f : top;
+        const float f = none ? 0.0f : pow2(m - base) * (C::kWide ? 1.0f : vref);
+        const uint32_t words = smem_addr(smem), own = words + (src * 16 * R + mine) * 4;
+        const bool whole = x.slot < 0;
+        const int rows = x.rq.n * a.G;
+#pragma unroll 1
+        for (int c = 0; c < C::DV; c += 16) {
+            float o[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = 0.0f;
+            if (active && !none) {
+                tmem_ld16(o, lanes + o_col(w) + c);
                 tmem_wait_ld();
-                tmem_here32(o);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] *= f;
+                tmem_here16(o);
             }
-            if (!alone) {
-                if (active && w == 1) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) words[lane * 32 + (j ^ lane)] = o[j];
-                }
-                groups_sync();
-                if (active && w == 0) {
+            for (int j = 0; j < 16; ++j)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(own + j * R * 4), "f"(o[j] * f) : "memory");
+            groups_sync();
+#pragma unroll 1
+            for (int i = tid; i < ITEMS; i += 256) {
+                const int r = i % R, q = i / R * 4, at = x.m * R + r;
+                if (at >= rows) continue;
+                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] += words[lane * 32 + (j ^ lane)];
+                for (int k = 0; k < SRC; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float z;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(words + ((k * 16 + q + j) * R + r) * 4));
+                        y[j] += z;
+                    }
+                if (patch) add_not_finite<C::STORE, C::TN, 4>(a, x, at, c + q, y);
+                float t = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < SRC; ++k) t = fmaxf(t, ml[k * R + r].x);
+                const float b = t == -INFINITY ? 0.0f : t;
+#pragma unroll
+                for (int k = 0; k < SRC; ++k) {
+                    const float2 z = ml[k * R + r];
+                    sum += z.y * pow2(z.x - b);
                 }
-            }
-            if (active && mine) {
-                if (patch && there) add_not_finite<C::STORE, C::TN, 32>(a, x, at, c, o);
+                if (sync->dead) sum = NAN;
                 if (whole) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] *= norm;
-                    write32(words, o, to.out, c, lane);
+                    const OutAt to = out_at(a, x.rq.qs, x.h, at);
+                    if (c + q == 0 && to.lse) *to.lse = lse_of(t, sum, C::kBias);
+                    if (c + q < a.Dv) {
+                        const float n = sum == 0.0f ? 0.0f : 1.0f / sum;  // a token that has seen no row gives zeros
+                        *reinterpret_cast<uint2*>(to.out + (c + q) * 2) =
+                            a.bf16 ? make_uint2(pack2<true>(y[0] * n, y[1] * n), pack2<true>(y[2] * n, y[3] * n))
+                                   : make_uint2(pack2<false>(y[0] * n, y[1] * n), pack2<false>(y[2] * n, y[3] * n));
+                    }
                 } else {
-                    // (rows that are not there have a place too)
-                    using P = PartAt<C::ROWS, C::DV>;
-                    float* part = a.part + P::block(x.slot, (C::PAIR ? 4 * w : 0) + (row >> 5)) + c * 32 + lane;
+                    using P = PartAt<R, C::DV>;
+                    float* part = a.part + P::block(x.slot, r / 32) + (c + q) * 32 + r % 32;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) part[j * 32] = o[j];
+                    for (int j = 0; j < 4; ++j) part[j * 32] = y[j];
+                    if (c + q == 0) a.part_ml[x.slot * R + r] = make_float2(t, sum);
                 }
             }
-            if (!alone) groups_sync();
+            groups_sync();
         }
     }
 
@@ -972,14 +1063,14 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     const int warp = int(threadIdx.x) >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
-            // 16-bit: the fetch itself, or one helper for all; 8-bit: every helper
-            bar_init(&sync->k_full[i], C::kWide ? 1 : kHelpers);
+            // 16-bit: the fetch itself, or one helper for all; 8-bit: a team of helpers
+            bar_init(&sync->k_full[i], C::kWide ? 1 : kTeam);
             bar_init(&sync->k_empty[i], 1);
-            bar_init(&sync->v_full[i], C::kWide ? 1 : kHelpers);
+            bar_init(&sync->v_full[i], C::kWide ? 1 : kTeam);
             bar_init(&sync->v_empty[i], 1);
             bar_init(&sync->fix_full[i], 1);
             bar_init(&sync->raw_full[i], 1);
-            bar_init(&sync->raw_empty[i], kHelpers);
+            bar_init(&sync->raw_empty[i], kTeam);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&sync->s_full[i], 1);
@@ -1018,7 +1109,8 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         } else {
             const int id = int(threadIdx.x) - (warp < 12 ? 256 : 320);
             if constexpr (C::kWide) tile.mend_tiles(place, id);
-            else tile.widen_tiles(place, id);
+            else if (id < kTeam) tile.template widen_tiles<false>(place, id);
+            else tile.template widen_tiles<true>(place, id - kTeam);
         }
     }
     tmem_before();
@@ -1029,12 +1121,22 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     }
 }
 
-template <int STORE, int DK, int DV, bool PAIR>
+template <int STORE, int DK, int DV, int ROWS>
 TreeKernel tile_kernel() {
-    using C = TileCfg<STORE, DK, DV, PAIR>;
+    using C = TileCfg<STORE, DK, DV, ROWS>;
     return TreeKernel{reinterpret_cast<const void*>(&rope_tree_tile_kernel<C>),
                       reinterpret_cast<const void*>(&rope_tree_join_kernel<C::ROWS, DV>), C::SMEM, kTileThreads,
                       C::TN, C::kBias};
+}
+
+template <int STORE, int DK, int DV>
+TreeKernel pick_tile_rows(const TreePlan& p) {
+    // a copy sees to 32 columns at least
+    if constexpr (TileCfg<STORE, DK, DV, 32>::TN == 128)
+        if (p.rows == 32) return tile_kernel<STORE, DK, DV, 32>();
+    if (p.rows <= 64) return tile_kernel<STORE, DK, DV, 64>();
+    if (p.rows == 128) return tile_kernel<STORE, DK, DV, 128>();
+    return tile_kernel<STORE, DK, DV, 256>();
 }
 
 }  // namespace rope
