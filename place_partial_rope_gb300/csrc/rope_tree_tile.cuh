@@ -66,7 +66,7 @@ struct TileCfg {
     // 8-bit: the codes of a tile's keys or values, before they become fp16
     static constexpr int RAW = kWide ? 0 : TN * DK;
     static constexpr int RAWS = kWide ? 0 : (TN == 128 && DK == 128) || (PAIR && DK == 192) ? 3 : 4;
-    static constexpr int MISC = PAIR ? 512 : 2560;
+    static constexpr int ML = PAIR ? 0 : 2048, FACTORS = kWide ? 0 : ROWS * 4, MISC = ML + FACTORS + 1024;
     static constexpr int kSmemMax = 232448;
     static constexpr int fit(int slots) {
         return Q_BYTES + slots * (K_SLOT + V_SLOT) + RAWS * RAW + (kWide ? 0 : (slots + 2) * (TN * 8 + 16)) + MISC <=
@@ -80,11 +80,12 @@ struct TileCfg {
     static constexpr int RAW_AT = V_AT + SLOTS * V_SLOT;
     static constexpr int SC_AT = RAW_AT + RAWS * RAW;
     static constexpr int MISC_AT = SC_AT + SCS * SC;
-    // in MISC: (m, l) of both groups (split rows only), then TileSync
-    static constexpr int ML_AT = MISC_AT, SYNC_AT = MISC_AT + (PAIR ? 0 : 2048);
+    // in MISC: (m, l) of a row's sources, the rows' factors, TileSync
+    static constexpr int ML_AT = MISC_AT, FACTOR_AT = ML_AT + ML, SYNC_AT = FACTOR_AT + FACTORS;
     static constexpr int SMEM = MISC_AT + MISC;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f;
     static constexpr float kLag = 8.0f;
+    static_assert(SYNC_AT + 896 <= SMEM, "TileSync");
     static_assert(fit(SLOTS), "two tiles fit");
 };
 
@@ -99,6 +100,9 @@ struct TileSync {
     uint32_t tmem;
     volatile uint32_t dead;
     volatile uint32_t patch[8];  // of run r at r % 8: values were taken out
+    volatile uint32_t runs;      // runs that are in `run`, and
+    volatile uint32_t last;      // how many there will be (~0: not known yet)
+    RunAt run[8];                // run r at r % 8: the fetching warp, which is ahead, writes them for the others
 };
 
 __device__ __forceinline__ void bar_init(unsigned long long* b, uint32_t count) {
@@ -325,6 +329,36 @@ struct Tile {
         }
     }
 
+    // The fetching warp writes run r down for the other roles.  It is at most a
+    // few tiles ahead of them (the rings' places), so eight places do.
+    __device__ __forceinline__ void publish(const RunAt& x, uint32_t r, bool there, int lane) const {
+        if (lane == 0) {
+            if (there) {
+                sync->run[r & 7] = x;
+                __threadfence_block();
+                sync->runs = r + 1;
+            } else {
+                __threadfence_block();
+                sync->last = r;
+            }
+        }
+        __syncwarp();
+    }
+
+    // Run r, when the block has one.
+    __device__ __forceinline__ bool take(uint32_t r, RunAt& x) const {
+        for (uint32_t i = 0; i < kPolls; ++i) {
+            if (sync->runs > r) {
+                __threadfence_block();
+                x = sync->run[r & 7];
+                return true;
+            }
+            if (sync->last <= r || sync->dead) return false;
+        }
+        sync->dead = 1;
+        return false;
+    }
+
     // The warp that fetches tiles, keys and values in turn, across runs, as far
     // ahead as the rings allow.  Rows of pages that are not there (no such row,
     // or a number outside the cache) are filled with zeros by the fetch.
@@ -335,6 +369,8 @@ struct Tile {
         RunAt step;
         bool more = next_run<C::ROWS, C::TN>(a, walk, step);
         RunAt x = step;
+        uint32_t runs = 0;
+        publish(x, runs++, more, lane);
         Look now{-1, 0};
         if (more) now = look(x, x.t0 * C::TN + lane * a.box);
         int it = 0;
@@ -346,6 +382,7 @@ struct Tile {
             if (it + 1 == x.count) {
                 more = next_run<C::ROWS, C::TN>(a, walk, step);
                 x = step;
+                publish(x, runs++, more, lane);
                 it = 0;
             } else {
                 ++it;
@@ -444,7 +481,7 @@ struct Tile {
     // 8-bit: the helpers turn codes into fp16 tiles and bring the scales, one
     // team keys (VALUES false), one values.
     template <bool VALUES>
-    __device__ __forceinline__ void widen_tiles(const Place& place, int id) const {
+    __device__ __forceinline__ void widen_tiles(int id) const {
         constexpr uint32_t SLOTS = C::SLOTS, RAWS = C::RAWS > 0 ? C::RAWS : 1;
         const float* scales = VALUES ? a.vs : a.ks;
         const int64_t* st = VALUES ? a.vs_st : a.ks_st;
@@ -452,11 +489,9 @@ struct Tile {
         unsigned long long* empty = VALUES ? sync->v_empty : sync->k_empty;
         constexpr int MORE = C::TN > kTeam ? 2 : 1;  // rows of a thread: id, and id + 96 for some
         const bool second = MORE == 2 && id < C::TN - kTeam;
-        Walk walk(place);
-        RunAt step;
+        RunAt x;
         uint32_t n = 0, run = 0;
-        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
-            const RunAt x = step;
+        while (take(run, x)) {
             const int first = x.t0 * C::TN, prefix = x.rq.len - x.rq.n;
             Look now[MORE];
             now[0] = look(x, id < C::TN ? first + id : x.rq.len);
@@ -511,13 +546,11 @@ struct Tile {
     // 16-bit: in tiles with more than context rows, rows past the request's
     // become zeros (what the page holds there may be anything), and so do
     // drafted rows' values that are not finite (see add_not_finite).
-    __device__ __forceinline__ void mend_tiles(const Place& place, int id) const {
+    __device__ __forceinline__ void mend_tiles(int id) const {
         constexpr uint32_t SLOTS = C::SLOTS;
-        Walk walk(place);
-        RunAt step;
+        RunAt x;
         uint32_t n = 0, run = 0, par = 0;  // a parity bit for each slot
-        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
-            const RunAt x = step;
+        while (take(run, x)) {
             const int prefix = x.rq.len - x.rq.n;
             for (int it = 0; it < x.count; ++it, ++n) {
                 const int j0 = (x.t0 + it) * C::TN;
@@ -561,16 +594,15 @@ struct Tile {
 
     // The thread that issues the products.  A group's chain is s, (its
     // softmax), O; whichever group's next step is ready goes next.
-    __device__ __forceinline__ void products(const Place& place) const {
+    __device__ __forceinline__ void products() const {
         constexpr uint32_t QK = mma_shape<C::BF16, C::TN, false>();
         constexpr uint32_t PV = mma_shape<C::BF16, C::DV, true>();
-        Walk walk(place);
-        RunAt step;
         constexpr uint32_t SLOTS = C::SLOTS;
         const uint32_t q_at = smem_addr(smem), k_at = smem_addr(smem + C::K_AT), v_at = smem_addr(smem + C::V_AT);
-        uint32_t before = 0, q_par = 0, p_par = 0;  // p_par: a bit for each group
-        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
-            const int count = step.count;
+        uint32_t before = 0, run = 0, q_par = 0, p_par = 0;  // p_par: a bit for each group
+        RunAt x;
+        while (take(run++, x)) {
+            const int count = x.count;
             bar_wait(&sync->q_full, q_par, sync);
             q_par ^= 1;
             tmem_after();
@@ -637,58 +669,70 @@ struct Tile {
 
     // ---------------------------------------------------------- softmax
 
-    // The row tile's queries: 16-bit as they are, or fp16 in [-2, 2); returns
-    // what the row's s is multiplied by.
-    __device__ __forceinline__ float stage_queries(const RunAt& x, int w, int row) const {
-        const int at = x.m * C::ROWS + (C::PAIR ? 128 * w : 0) + row % (C::PAIR ? 128 : C::ROWS);
-        const bool there = at < x.rq.n * a.G;
-        uint32_t tok = 0, g = 0;
-        if (there) a.div_group.divmod(uint32_t(at), tok, g);
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] +
-                                                          int64_t(x.h * a.G + int(g)) * a.q_st[1]);
-        constexpr int CH = C::DK / 8;
-        const int chunks = there ? a.Dk / 8 : 0;
-        float factor = a.scale_log2, down = 1.0f;
-        if constexpr (!C::kWide) {
-            uint32_t most = 0;
+    // The row tile's queries: 16-bit as they are, or fp16 in [-2, 2) with what
+    // the row's s is multiplied by in `factor` (by row).  Eight lanes a row; rows
+    // of a tile of 32 or 64 are stored once for each copy.
+    __device__ __forceinline__ void stage_queries(const RunAt& x, int tid, float* factor) const {
+        constexpr int N = C::DK / 64, EACH = 32;  // chunks of a lane; rows of the 256 threads
+        constexpr int TOGETHER = C::ROWS / EACH < 4 ? C::ROWS / EACH : 4;
+        const int sub = tid & 7;
 #pragma unroll 1
-            for (int c = 0; c < CH; c += 8) {
-                uint4 y[8];  // in flight together
+        for (int r0 = tid >> 3; r0 < C::ROWS; r0 += EACH * TOGETHER) {
+            uint4 y[TOGETHER][N];  // in flight together
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = c + i < chunks ? __ldg(src + c + i) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < TOGETHER; ++i) {
+                const int at = x.m * C::ROWS + r0 + EACH * i;
+                const bool there = at < x.rq.n * a.G;
+                uint32_t tok = 0, g = 0;
+                if (there) a.div_group.divmod(uint32_t(at), tok, g);
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] +
+                                                                  int64_t(x.h * a.G + int(g)) * a.q_st[1]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // the largest |q| of bit patterns: bf16 and fp16 order alike
-                    most = max(most, max(max(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
-                                         max(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu)) >> 16);
-                    most = max(most, max(max(y[i].x & 0x7fffu, y[i].y & 0x7fffu), max(y[i].z & 0x7fffu, y[i].w & 0x7fffu)));
+                for (int k = 0; k < N; ++k) {
+                    const int ch = 8 * k + sub;
+                    y[i][k] = there && ch * 8 < a.Dk ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
                 }
             }
-            const float big = a.bf16 ? __uint_as_float(most << 16)
-                                     : __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
-            const float p = row_power(__float_as_uint(big));
-            down = one_over_power(p);
-            factor *= p;
-        }
-        // up to 128 rows, both groups' threads of a row store a part of it each
-        const uint32_t to = smem_addr(smem) + (C::PAIR ? w * C::QTILE : 0) + row * 128;
-#pragma unroll 1
-        for (int c = C::PAIR ? 0 : 8 * w; c < CH; c += C::PAIR ? 8 : 16) {
-            uint4 y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = c + i < chunks ? __ldg(src + c + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < TOGETHER; ++i) {
+                const int row = r0 + EACH * i;
+                float down = 1.0f;
                 if constexpr (!C::kWide) {
-                    float f[8];
-                    widen8(y[i], a.bf16, f);
-                    y[i] = half8(f, down);
+                    // the largest |q| of bit patterns: bf16 and fp16 order alike
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        const uint4 z = y[i][k];
+                        most = max(most, max(max(z.x & 0x7fff0000u, z.y & 0x7fff0000u),
+                                             max(z.z & 0x7fff0000u, z.w & 0x7fff0000u)) >> 16);
+                        most = max(most, max(max(z.x & 0x7fffu, z.y & 0x7fffu), max(z.z & 0x7fffu, z.w & 0x7fffu)));
+                    }
+#pragma unroll
+                    for (int d = 4; d; d /= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+                    const float big = a.bf16 ? __uint_as_float(most << 16)
+                                             : __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+                    const float p = row_power(__float_as_uint(big));
+                    down = one_over_power(p);
+                    if (sub == 0) factor[row] = p * a.scale_log2;
                 }
-                sts128(to + (c >> 3) * 16384 + ((i ^ (row & 7)) << 4), y[i].x, y[i].y, y[i].z, y[i].w);
+                const uint32_t to = smem_addr(smem) + (C::PAIR ? row / 128 * C::QTILE : 0) + row % 128 * 128 +
+                                    ((sub ^ (row & 7)) << 4);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    uint4 z = y[i][k];
+                    if constexpr (!C::kWide) {
+                        float f[8];
+                        widen8(z, a.bf16, f);
+                        z = half8(f, down);
+                    }
+#pragma unroll
+                    for (int copy = 0; copy < C::SPLIT; ++copy)
+                        sts128(to + k * 16384 + copy * (C::ROWS * 128), z.x, z.y, z.z, z.w);
+                }
             }
         }
-        return factor;
     }
+
 
     // 32 scores of a row times the keys' scales.
     static __device__ __forceinline__ void scale32(float* s, const float* scale) {
@@ -777,14 +821,13 @@ struct Tile {
         const int tid = int(threadIdx.x), row = tid & 127;
         const uint32_t lanes = tmem + (uint32_t(row & 96) << 16);  // this warp's lanes
         float2* ml = reinterpret_cast<float2*>(smem + C::ML_AT);
-        Walk walk(place);
-        RunAt step;
+        RunAt x;
         uint32_t before = 0, run = 0, s_par = 0, o_par = 0;
         TreeMeta meta{0, place.chunk, 0, 0, 0, 0};
-        while (next_run<C::ROWS, C::TN>(a, walk, step)) {
-            const RunAt x = step;
+        while (take(run, x)) {
             if (run == 0) meta = meta_of(place, x);
-            const float factor = stage_queries(x, w, row);
+            float* factors = reinterpret_cast<float*>(smem + C::FACTOR_AT);
+            stage_queries(x, tid, factors);
             to_async_proxy();
             bar_arrive(&sync->q_full);
 
@@ -796,6 +839,11 @@ struct Tile {
             const bool active = at - (row & 31) < rows;  // the warp has a row
             const int tok = min(int(a.div_group.div(uint32_t(at))), x.rq.n - 1);
             const int prefix = x.rq.len - x.rq.n, nv = C::PAIR ? 2 * x.count : x.count;
+            float factor = a.scale_log2;
+            if constexpr (!C::kWide) {
+                groups_sync();
+                factor = factors[(C::PAIR ? 128 * w : 0) + mine];
+            }
             float m = -INFINITY, l = 0.0f, vref = 8.2718061255302767e-25f;  // 2^-80
 
 #pragma unroll 1
@@ -826,12 +874,12 @@ struct Tile {
                             mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c));
                         tmem_wait_st();
                     }
-                    // 16-bit: s is held in registers.  8-bit: it is read twice, 32
-                    // columns at a time, in loops small enough to stay in the
+                    // s is held in registers; 128 columns of 8-bit rows are read twice, 32
+                    // at a time, in loops small enough to stay in the
                     // instruction cache beside the helpers' (with s held, the
                     // roles' code missed it and every role ran at a third of its
                     // speed); the rows are bound by HBM, so the second read hides.
-                    constexpr int HELD = C::kWide ? C::COLS : 32;
+                    constexpr int HELD = C::kWide || C::COLS <= 64 ? C::COLS : 32;
                     float s[HELD], top = -INFINITY;
                     const uint32_t from = lanes + s_col(w);
 #pragma unroll 1
@@ -858,7 +906,7 @@ struct Tile {
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
                     for (int c0 = lo; c0 < lo + C::COLS; c0 += HELD) {
-                        if constexpr (!C::kWide) {
+                        if constexpr (HELD < C::COLS) {
                             // (p of the columns before lies over s of columns before those)
                             tmem_ld32(s, from + c0);
                             tmem_wait_ld();
@@ -950,7 +998,7 @@ struct Tile {
     __device__ __forceinline__ void gather(const RunAt& x, int w, int row, bool active, int nv, float m, float l,
                                            float vref, const volatile uint32_t* patched, float2* ml,
                                            uint32_t lanes) const {
-        constexpr int R = C::ROWS, SRC = 2 * C::SPLIT, ITEMS = R * 4;  // items: a row's four columns
+        constexpr int R = C::ROWS, SRC = 2 * C::SPLIT;
         const int tid = w * 128 + row, mine = row % R, src = w * C::SPLIT + row / R;
         const bool none = w >= nv;  // a group without a tile
         ml[src * R + mine] = none ? make_float2(-INFINITY, 0.0f) : make_float2(m, l);
@@ -962,8 +1010,33 @@ struct Tile {
         const float base = top == -INFINITY ? 0.0f : top;
         const float f = none ? 0.0f : pow2(m - base) * (C::kWide ? 1.0f : vref);
         const uint32_t words = smem_addr(smem), own = words + (src * 16 * R + mine) * 4;
+        // the thread also writes four columns of the 16 of row tid % R (of R = 128,
+        // eight), whose sums are the same all along
         const bool whole = x.slot < 0;
-        const int rows = x.rq.n * a.G;
+        const int r = tid % R, at = x.m * R + r, q0 = tid / R * 4;
+        const bool writes = q0 < 16 && at < x.rq.n * a.G;
+        float t = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < SRC; ++k) t = fmaxf(t, ml[k * R + r].x);
+#pragma unroll
+        for (int k = 0; k < SRC; ++k) {
+            const float2 z = ml[k * R + r];
+            sum += z.y * pow2(z.x - (t == -INFINITY ? 0.0f : t));
+        }
+        if (sync->dead) sum = NAN;
+        const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;  // a token that has seen no row gives zeros
+        char* out = nullptr;
+        float* part = nullptr;
+        if (writes) {
+            if (whole) {
+                const OutAt to = out_at(a, x.rq.qs, x.h, at);
+                if (q0 == 0 && to.lse) *to.lse = lse_of(t, sum, C::kBias);
+                out = to.out;
+            } else {
+                part = a.part + PartAt<R, C::DV>::block(x.slot, r / 32) + r % 32;
+                if (q0 == 0) a.part_ml[x.slot * R + r] = make_float2(t, sum);
+            }
+        }
 #pragma unroll 1
         for (int c = 0; c < C::DV; c += 16) {
             float o[16];
@@ -978,45 +1051,33 @@ struct Tile {
             for (int j = 0; j < 16; ++j)
                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(own + j * R * 4), "f"(o[j] * f) : "memory");
             groups_sync();
-#pragma unroll 1
-            for (int i = tid; i < ITEMS; i += 256) {
-                const int r = i % R, q = i / R * 4, at = x.m * R + r;
-                if (at >= rows) continue;
-                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (writes) {
 #pragma unroll
-                for (int k = 0; k < SRC; ++k)
+                for (int q = q0; q < 16; q += (R == 128 ? 8 : 16)) {
+                    float z[SRC][4], y[4];
+#pragma unroll
+                    for (int k = 0; k < SRC; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            asm volatile("ld.shared.f32 %0, [%1];"
+                                         : "=f"(z[k][j])
+                                         : "r"(words + ((k * 16 + q + j) * R + r) * 4));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float z;
-                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(words + ((k * 16 + q + j) * R + r) * 4));
-                        y[j] += z;
+                        y[j] = z[0][j];
+#pragma unroll
+                        for (int k = 1; k < SRC; ++k) y[j] += z[k][j];
                     }
-                if (patch) add_not_finite<C::STORE, C::TN, 4>(a, x, at, c + q, y);
-                float t = -INFINITY, sum = 0.0f;
+                    if (patch) add_not_finite<C::STORE, C::TN, 4>(a, x, at, c + q, y);
+                    if (out) {
+                        if (c + q < a.Dv)
+                            *reinterpret_cast<uint2*>(out + (c + q) * 2) =
+                                a.bf16 ? make_uint2(pack2<true>(y[0] * norm, y[1] * norm), pack2<true>(y[2] * norm, y[3] * norm))
+                                       : make_uint2(pack2<false>(y[0] * norm, y[1] * norm), pack2<false>(y[2] * norm, y[3] * norm));
+                    } else {
 #pragma unroll
-                for (int k = 0; k < SRC; ++k) t = fmaxf(t, ml[k * R + r].x);
-                const float b = t == -INFINITY ? 0.0f : t;
-#pragma unroll
-                for (int k = 0; k < SRC; ++k) {
-                    const float2 z = ml[k * R + r];
-                    sum += z.y * pow2(z.x - b);
-                }
-                if (sync->dead) sum = NAN;
-                if (whole) {
-                    const OutAt to = out_at(a, x.rq.qs, x.h, at);
-                    if (c + q == 0 && to.lse) *to.lse = lse_of(t, sum, C::kBias);
-                    if (c + q < a.Dv) {
-                        const float n = sum == 0.0f ? 0.0f : 1.0f / sum;  // a token that has seen no row gives zeros
-                        *reinterpret_cast<uint2*>(to.out + (c + q) * 2) =
-                            a.bf16 ? make_uint2(pack2<true>(y[0] * n, y[1] * n), pack2<true>(y[2] * n, y[3] * n))
-                                   : make_uint2(pack2<false>(y[0] * n, y[1] * n), pack2<false>(y[2] * n, y[3] * n));
+                        for (int j = 0; j < 4; ++j) part[(c + q + j) * 32] = y[j];
                     }
-                } else {
-                    using P = PartAt<R, C::DV>;
-                    float* part = a.part + P::block(x.slot, r / 32) + (c + q) * 32 + r % 32;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[j * 32] = y[j];
-                    if (c + q == 0) a.part_ml[x.slot * R + r] = make_float2(t, sum);
                 }
             }
             groups_sync();
@@ -1081,6 +1142,8 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         bar_init(&sync->done, 1);
         sync->dead = 0;
         for (int i = 0; i < 8; ++i) sync->patch[i] = 0;
+        sync->runs = 0;
+        sync->last = ~0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 12) {
@@ -1102,15 +1165,15 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 12) {
-            if (threadIdx.x == 12 * 32) tile.products(place);
+            if (threadIdx.x == 12 * 32) tile.products();
             __syncwarp();
         } else if (warp == 13) {
             tile.fetches(place, &km, &vm);
         } else {
             const int id = int(threadIdx.x) - (warp < 12 ? 256 : 320);
-            if constexpr (C::kWide) tile.mend_tiles(place, id);
-            else if (id < kTeam) tile.template widen_tiles<false>(place, id);
-            else tile.template widen_tiles<true>(place, id - kTeam);
+            if constexpr (C::kWide) tile.mend_tiles(id);
+            else if (id < kTeam) tile.template widen_tiles<false>(id);
+            else tile.template widen_tiles<true>(id - kTeam);
         }
     }
     tmem_before();
