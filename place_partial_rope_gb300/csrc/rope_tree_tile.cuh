@@ -438,43 +438,48 @@ struct Tile {
     // in an order that meets all banks both reading rows of codes and writing
     // lines (128 lanes: the second row's other half).  A team's step from one
     // such unit to the next is 4 or 8 rows modulo 8, so a thread's addresses
-    // differ by constants from one or two places, and a unit costs a load,
-    // twelve conversion instructions and two stores: a helper warp has few others
-    // to take turns with, so its instructions count at their latency.
+    // differ by constants from two places, and a unit costs a load, twelve
+    // conversion instructions and two stores.  Two units a turn of a short loop:
+    // unrolled (11 units) the helpers' code pushed the other roles' out of the
+    // instruction cache, and 48 requests of 12000 fp8 rows took 354 us, not 273.
     template <int D>
     static __device__ __forceinline__ void widen(uint32_t raw, uint32_t to, int id, int valid) {
-        constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kTeam / 8, N = (UNITS + STEP - 1) / STEP;
+        constexpr int G = D / 64, UNITS = C::TN / 2 * G, STEP = kTeam / 8;
         constexpr int ROWS = STEP / G * 2;  // from a unit to the thread's next
         static_assert(STEP % G == 0 && ROWS % 4 == 0, "one of two places in the swizzle");
         const int u = id >> 3, odd = (id >> 2) & 1;
         const int row = u / G * 2 + odd, ch = ((G == 2 && odd ? u % G ^ 1 : u % G) << 2) + (id & 3);
         raw += row * D + ch * 16;
         // four rows on, chunk c of a line lies where c ^ 4 would
-        const uint32_t lo = to + line_at(row, 2 * ch), hi = to + line_at(row, 2 * ch + 1);
-        const uint32_t lo4 = to + line_at(row, (2 * ch) ^ 4), hi4 = to + line_at(row, (2 * ch + 1) ^ 4);
-        constexpr int B = 4;
+        constexpr int TURN = ROWS % 8 ? 4 : 0;
+        uint32_t lo = to + line_at(row, 2 * ch), hi = to + line_at(row, 2 * ch + 1);
+        uint32_t lo1 = to + line_at(row, (2 * ch) ^ TURN) + ROWS * 128;
+        uint32_t hi1 = to + line_at(row, (2 * ch + 1) ^ TURN) + ROWS * 128;
+        int left = UNITS - u;
+        valid -= row;
+#pragma unroll 1
+        for (; left > 0; left -= 2 * STEP) {
+            uint32_t w[2][4], h[8];
+            lds128(w[0], raw);
+            if (left > STEP) lds128(w[1], raw + ROWS * D);
 #pragma unroll
-        for (int i0 = 0; i0 < N; i0 += B) {
-            // a few loads, then their conversions: the loads do not wait for each other
-            uint32_t w[B][4];
-#pragma unroll
-            for (int i = 0; i < B; ++i)
-                if (i0 + i < N && (UNITS % STEP == 0 || i0 + i < N - 1 || u + (N - 1) * STEP < UNITS))
-                    lds128(w[i], raw + (i0 + i) * (ROWS * D));
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                if (i0 + i >= N || !(UNITS % STEP == 0 || i0 + i < N - 1 || u + (N - 1) * STEP < UNITS)) continue;
-                if (row + (i0 + i) * ROWS >= valid) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // codes of 0
-                uint32_t h[8];
+            for (int i = 0; i < 2; ++i) {
+                if (i == 1 && left <= STEP) break;
+                if (i * ROWS >= valid) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;  // codes of 0
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     h[2 * j] = codes_to_half2<C::STORE, false>(w[i][j]);
                     h[2 * j + 1] = codes_to_half2<C::STORE, true>(w[i][j]);
                 }
-                const bool four = ((i0 + i) * ROWS) % 8 != 0;
-                sts128((four ? lo4 : lo) + (i0 + i) * (ROWS * 128), h[0], h[1], h[2], h[3]);
-                sts128((four ? hi4 : hi) + (i0 + i) * (ROWS * 128), h[4], h[5], h[6], h[7]);
+                sts128(i ? lo1 : lo, h[0], h[1], h[2], h[3]);
+                sts128(i ? hi1 : hi, h[4], h[5], h[6], h[7]);
             }
+            raw += 2 * ROWS * D;
+            lo += 2 * ROWS * 128;
+            hi += 2 * ROWS * 128;
+            lo1 += 2 * ROWS * 128;
+            hi1 += 2 * ROWS * 128;
+            valid -= 2 * ROWS;
         }
     }
 
@@ -510,6 +515,10 @@ struct Tile {
                     const int j = j0 + C::TN + id + kTeam * k;
                     now[k] = look(x, (k ? second : id < C::TN) && it + 1 < x.count ? j : x.rq.len);
                 }
+                // In a ring of an odd number of places the team before in this
+                // place was the other one: until it has emptied the place, the
+                // parity of raw_full may still be that of the item before that.
+                if (RAWS % 2 && item >= RAWS) bar_wait(&sync->raw_empty[r], (item / RAWS - 1) & 1, sync);
                 bar_wait(&sync->raw_full[r], (item / RAWS) & 1, sync);
                 if (n >= SLOTS) bar_wait(&empty[slot], (n / SLOTS - 1) & 1, sync);
                 widen<VALUES ? C::DV : C::DK>(smem_addr(smem + C::RAW_AT) + r * C::RAW,
@@ -610,8 +619,14 @@ struct Tile {
             // next steps of group w and of the other one
             int s_mine = 0, s_other = 1, p_mine = 0, p_other = 1, left = nv, w = 0;
             uint32_t spins = 0;
+            // With an odd number of slots the tile before in a tile's slot is the
+            // other group's: until that one's product is under way, the parity
+            // of the slot's barrier may still be that of the tile before that.
+            constexpr bool TURNS = !C::PAIR && SLOTS % 2;
+            // (8-bit: rolled, for the instruction cache's sake, see widen)
+            constexpr int ISSUE = C::kWide ? 16 : 1;
             while (left > 0) {
-                if (s_mine > p_mine) {
+                if (s_mine > p_mine && (!TURNS || p_other + 1 >= p_mine)) {
                     const int t = C::PAIR ? p_mine >> 1 : p_mine;
                     const uint32_t n = before + t, slot = n % SLOTS;
                     if (bar_poll(&sync->p_full[w], (p_par >> w) & 1) && bar_poll(&sync->v_full[slot], (n / SLOTS) & 1)) {
@@ -619,7 +634,7 @@ struct Tile {
                         const uint64_t vs = smem_matrix(v_at + slot * C::V_SLOT, C::TN * 128);
                         const uint32_t d = tmem + o_col(w), p = tmem + s_col(w);
                         const bool add = p_mine > 1;
-#pragma unroll
+#pragma unroll(ISSUE)
                         for (int k = 0; k < C::TN / 16; ++k) mma_ts(d, p + 8 * k, vs + k * (2048 >> 4), PV, add || k > 0);
                         p_par ^= 1u << w;
                         p_mine += 2;
@@ -630,7 +645,7 @@ struct Tile {
                         spins = 0;
                     }
                 }
-                if (s_mine == p_mine && s_mine < nv) {
+                if (s_mine == p_mine && s_mine < nv && (!TURNS || s_other + 1 >= s_mine)) {
                     const int t = C::PAIR ? s_mine >> 1 : s_mine;
                     const uint32_t n = before + t, slot = n % SLOTS;
                     if (bar_poll(&sync->k_full[slot], (n / SLOTS) & 1)) {
@@ -638,7 +653,7 @@ struct Tile {
                         const uint64_t ks = smem_matrix(k_at + slot * C::K_SLOT, 16);
                         const uint64_t q = smem_matrix(q_at + (C::PAIR ? w * C::QTILE : 0), 16);
                         const uint32_t d = tmem + s_col(w);
-#pragma unroll
+#pragma unroll(ISSUE)
                         for (int k = 0; k < C::DK / 16; ++k)
                             mma_ss(d, q + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
                                    ks + (((k >> 2) * (C::TN * 128) + (k & 3) * 32) >> 4), QK, k > 0);
@@ -852,6 +867,7 @@ struct Tile {
                 const uint32_t n = before + t;
                 const float* sc = reinterpret_cast<const float*>(smem + C::SC_AT + n % C::SCS * C::SC);
                 bar_wait(&sync->s_full[w], s_par, sync);
+                __syncwarp();
                 s_par ^= 1;
                 tmem_after();
                 if (active) {
@@ -859,6 +875,7 @@ struct Tile {
                     if constexpr (!C::kWide) {
                         // the scales came with the keys and the values
                         bar_wait(&sync->v_full[n % C::SLOTS], (n / C::SLOTS) & 1, sync);
+                        __syncwarp();
                         const float4 y = *reinterpret_cast<const float4*>(sc + 2 * C::TN);
                         const float u = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
                         if (u > vref) {
@@ -874,12 +891,12 @@ struct Tile {
                             mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c));
                         tmem_wait_st();
                     }
-                    // s is held in registers; 128 columns of 8-bit rows are read twice, 32
+                    // 16-bit: s is held in registers.  8-bit: it is read twice, 32
                     // at a time, in loops small enough to stay in the
                     // instruction cache beside the helpers' (with s held, the
                     // roles' code missed it and every role ran at a third of its
                     // speed); the rows are bound by HBM, so the second read hides.
-                    constexpr int HELD = C::kWide || C::COLS <= 64 ? C::COLS : 32;
+                    constexpr int HELD = C::kWide ? C::COLS : 32;
                     float s[HELD], top = -INFINITY;
                     const uint32_t from = lanes + s_col(w);
 #pragma unroll 1
@@ -932,6 +949,7 @@ struct Tile {
             }
             if (w < nv) {
                 bar_wait(&sync->o_full[w], o_par, sync);
+                __syncwarp();
                 o_par ^= 1;
                 tmem_after();
             }
