@@ -315,9 +315,10 @@ rope_status_t cache_read(const rope_kv_cache_t* c, const int64_t* slots, int64_t
 // attention
 // ------------------------------------------------------------------------
 
-// What the kernel choice depends on: types, row lengths, and the query rows
-// that share a key head.
-rope_status_t tree_plan(const rope_kv_cache_t* c, int dtype, int64_t Hq, int64_t max_q, TreePlan* p) {
+// What the kernel choice depends on: types, row lengths, the query rows that
+// share a key head, and the cache tiles (of 128 rows) that there can be.
+rope_status_t tree_plan(const rope_kv_cache_t* c, int dtype, int64_t Hq, int64_t max_q, int64_t tiles,
+                        TreePlan* p) {
     if (dtype != ROPE_BF16 && dtype != ROPE_FP16)
         return fail(ROPE_ERR_INVALID, "attention takes bf16 (0) or fp16 (1), not dtype %d", dtype);
     if (code_size(c->dtype) == 2 && c->dtype != dtype)
@@ -334,7 +335,7 @@ rope_status_t tree_plan(const rope_kv_cache_t* c, int dtype, int64_t Hq, int64_t
     p->dtype = dtype;
     p->store = c->dtype;
     choose_tree(static_cast<int>(c->k_dim), static_cast<int>(c->v_dim), max_q * (Hq / c->heads),
-                c->page_size, p);
+                c->page_size, tiles, p);
     return ROPE_OK;
 }
 
@@ -349,10 +350,12 @@ rope_status_t tree_attention(const rope_kv_cache_t* c, const void* q, int dtype,
     int64_t kb, vb;
     rope_status_t st = check_cache(c, &kb, &vb);
     if (st != ROPE_OK) return st;
-    TreePlan p{};
-    st = tree_plan(c, dtype, Hq, max_q, &p);
-    if (st != ROPE_OK) return st;
     constexpr int64_t kInt = (int64_t(1) << 31) - 1;
+    // (sizes that overflow here are refused below)
+    const double room = double(R) * double(c->heads) * (double(max_pages) * double(c->page_size) / 128.0 + 1.0);
+    TreePlan p{};
+    st = tree_plan(c, dtype, Hq, max_q, room < 1e15 ? static_cast<int64_t>(room) : kInt, &p);
+    if (st != ROPE_OK) return st;
     if (Tq < 0 || Tq > kInt / Hq || R < 0 || R > (1 << 24))
         return fail(ROPE_ERR_INVALID, "Tq=%lld query tokens, R=%lld requests", (long long)Tq,
                     (long long)R);
@@ -506,13 +509,18 @@ rope_status_t rope_partial_tree_attention_workspace(const rope_kv_cache_t* cache
     int64_t kb, vb;
     rope_status_t st = check_cache(cache, &kb, &vb);
     if (st != ROPE_OK) return st;
-    TreePlan p{};
-    st = tree_plan(cache, static_cast<int>(dtype), Hq, max_q, &p);
-    if (st != ROPE_OK) return st;
-    const char* err = nullptr;
-    int blocks = 0;
-    if (tree_blocks(p, sm_count, &blocks, &err) != ROPE_OK) return fail(ROPE_ERR_CUDA, "%s", err);
-    *bytes = tree_workspace(p, blocks);
+    int64_t most = 0;
+    for (int many = 0; many < 2; ++many) {  // a call of few cache tiles, and of many
+        TreePlan p{};
+        st = tree_plan(cache, static_cast<int>(dtype), Hq, max_q, many ? int64_t(1) << 31 : 0, &p);
+        if (st != ROPE_OK) return st;
+        const char* err = nullptr;
+        int blocks = 0;
+        if (tree_blocks(p, sm_count, &blocks, &err) != ROPE_OK) return fail(ROPE_ERR_CUDA, "%s", err);
+        const int64_t need = tree_workspace(p, blocks);
+        if (need > most) most = need;
+    }
+    *bytes = most;
     return ROPE_OK;
 }
 

@@ -58,7 +58,7 @@ struct TreePlan {
 
 // The kernel for rows of Dk and Dv, `rows` query rows a key head and pages of
 // `page_size` rows.
-void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, TreePlan* p);
+void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, int64_t tiles, TreePlan* p);
 
 // The grid of a plan: the blocks that are resident on the device (sm_count
 // 0), or an upper bound of that for a device of sm_count SMs.

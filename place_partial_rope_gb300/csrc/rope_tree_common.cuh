@@ -513,6 +513,7 @@ struct TreeKernel {
     int smem, threads;
     int tile;  // cache rows of a tile
     float bias;
+    int regs;  // registers of a block that its warps share out among them; 0: they do not
 };
 
 // defined in rope_tree_*.cu (up to 16 query rows) and rope_tile_*.cu

@@ -57,7 +57,13 @@ rope_status_t resident(const TreeKernel& k, Resident* out, const char** err) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r.per_sm, k.main, k.threads, k.smem);
+    cudaFuncAttributes at{};
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k.main);
     if (e != cudaSuccess) return cuda_fail(e, err);
+    if (at.numRegs * k.threads < k.regs) {  // a share that is not there would be waited for
+        *err = "the attention kernel was built with too few registers";
+        return ROPE_ERR_CUDA;
+    }
     if (r.per_sm < 1) {
         *err = "the attention kernel does not fit this device";
         return ROPE_ERR_CUDA;
@@ -128,21 +134,34 @@ rope_status_t launch(const void* f, dim3 grid, int threads, int smem, void** par
 
 }  // namespace
 
-// Up to 16 query rows, the narrow kernel's matrix instructions waste less than
-// 128-row ones would: TODO measured.  Beyond that the tile kernel, with both
-// row tiles of a pair from 129 rows on, so that each cache row is fetched once
-// for 256 query rows.  It fetches boxes of at least 8 rows of a page; pages
-// that those do not divide, and rows of more than 192 lanes (whose O does not
-// fit tensor memory twice), stay with the narrow kernel.
-void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, TreePlan* p) {
+// Which kernel: by types, row lengths, the query rows of a key head, and the cache
+// tiles (128 rows of one key head) that the page table has room for.  Both sides
+// of each border, in us (32 requests of 8000 rows, 8 key heads, 128 + 128 lanes
+// unless it says otherwise):
+//   16-bit, up to 16 query rows: narrow 201, 64-row tiles 179; 8 requests of 4096
+//   rows 59 and 44.  But 4 requests of 4096 rows 28 and 32, and one of 4097 rows
+//   with 2 key heads 13.3 and 13.8, the tile kernel's start being the longer one:
+//   to 8 tiles an SM, the narrow kernel.
+//   fp8, up to 16 rows: narrow 174, 64-row tiles 193 (codes become fp16 in registers
+//   there, in shared memory here).  32 rows: 323 and 189.
+//   64 rows: 64-row tiles 182 (bf16) and 197 (fp8), 128-row tiles 185 and 210.
+//   256 rows: a pair of tiles that share the cache's, 253 (bf16) and 522 (fp8);
+//   128-row tiles, the cache read twice, 351 and 430, as fp8 pairs have room for
+//   64-row cache tiles only; with 64-lane rows, which have room for more, 215
+//   and 330 against 263 and 367; fp8 rows of 192 + 128, 612 and 625.
+// Tensor copies take boxes of at least 8 rows of a page; pages that those do not
+// divide, and rows of more than 192 lanes (whose O does not fit tensor memory
+// twice), stay with the narrow kernel.
+void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, int64_t tiles, TreePlan* p) {
+    constexpr int64_t kFewTiles = 8 * 152;
     if (Dk <= 64) p->dk = 64, p->dv = 64;
     else if (Dk <= 128) p->dk = 128, p->dv = 128;
     else if (Dk <= 192 && Dv <= 128) p->dk = 192, p->dv = 128;
     else p->dk = 256, p->dv = 256;
     const bool wide = p->store == ROPE_CACHE_BF16 || p->store == ROPE_CACHE_FP16;
-    if (p->dk == 256 || rows <= 16 || page_size % 8) p->rows = 16;
-    else if (rows <= 32 && (wide || p->dk < 192)) p->rows = 32;
-    else p->rows = rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    if (p->dk == 256 || page_size % 8 || (rows <= 16 && (!wide || tiles <= kFewTiles)))
+        p->rows = 16;
+    else p->rows = rows <= 64 ? 64 : rows <= 128 || !(wide || p->dk == 64) ? 128 : 256;
 }
 
 rope_status_t tree_blocks(const TreePlan& p, int sm_count, int* blocks, const char** err) {

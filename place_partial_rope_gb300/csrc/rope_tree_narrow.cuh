@@ -617,7 +617,7 @@ TreeKernel narrow_kernel() {
     using C = NarrowCfg<STORE, DK, DV, TN, (per <= 32768 ? 3 : 2)>;
     return TreeKernel{reinterpret_cast<const void*>(&rope_tree_narrow_kernel<C>),
                       reinterpret_cast<const void*>(&rope_tree_join_kernel<C::ROWS, DV>), C::SMEM,
-                      kNarrowThreads, C::TN, C::kBias};
+                      kNarrowThreads, C::TN, C::kBias, 0};
 }
 
 }  // namespace rope

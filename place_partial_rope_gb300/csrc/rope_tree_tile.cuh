@@ -50,7 +50,7 @@ namespace rope {
 template <int STORE_, int DK_, int DV_, int ROWS_>
 struct TileCfg {
     static constexpr int STORE = STORE_, DK = DK_, DV = DV_;
-    static constexpr int ROWS = ROWS_;  // query rows of a tile: 32, 64, 128 or 256
+    static constexpr int ROWS = ROWS_;  // query rows of a tile: 64, 128 or 256
     static constexpr bool PAIR = ROWS == 256;
     static constexpr int SPLIT = PAIR ? 1 : 128 / ROWS;  // copies of the rows in tensor memory
     static constexpr bool kWide = STORE == ROPE_CACHE_BF16 || STORE == ROPE_CACHE_FP16;  // 16-bit codes
@@ -1177,6 +1177,7 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     const Tile<C> tile{a, smem, sync, sync->tmem};
 
     // registers: 128 a thread at launch; 256 x 192 + 256 x 64 of the same 65536
+    // (the host sees to it that the launch has them)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         tile.softmax(place, warp >> 2);
@@ -1207,17 +1208,15 @@ TreeKernel tile_kernel() {
     using C = TileCfg<STORE, DK, DV, ROWS>;
     return TreeKernel{reinterpret_cast<const void*>(&rope_tree_tile_kernel<C>),
                       reinterpret_cast<const void*>(&rope_tree_join_kernel<C::ROWS, DV>), C::SMEM, kTileThreads,
-                      C::TN, C::kBias};
+                      C::TN, C::kBias, 256 * 192 + 256 * 64};
 }
 
 template <int STORE, int DK, int DV>
 TreeKernel pick_tile_rows(const TreePlan& p) {
-    // a copy sees to 32 columns at least
-    if constexpr (TileCfg<STORE, DK, DV, 32>::TN == 128)
-        if (p.rows == 32) return tile_kernel<STORE, DK, DV, 32>();
     if (p.rows <= 64) return tile_kernel<STORE, DK, DV, 64>();
-    if (p.rows == 128) return tile_kernel<STORE, DK, DV, 128>();
-    return tile_kernel<STORE, DK, DV, 256>();
+    if constexpr (TileCfg<STORE, DK, DV, 128>::kWide || DK == 64)
+        if (p.rows == 256) return tile_kernel<STORE, DK, DV, 256>();
+    return tile_kernel<STORE, DK, DV, 128>();
 }
 
 }  // namespace rope

@@ -186,6 +186,22 @@ def test_long_contexts_are_split_and_joined(n, store):
     c.check(*a)
 
 
+@pytest.mark.parametrize("store", ["bf16", "fp16", "fp8"])
+def test_few_query_rows_over_many_tiles(store):
+    """One to three tokens a request at a batch whose cache is large: another
+    kernel than that of a few requests (16-bit), and the workspace serves both."""
+    rng = np.random.default_rng(11)
+    ns = rng.integers(1, 4, 56).tolist()
+    lens = (rng.integers(0, 700, 56) + ns).tolist()
+    lens[7], lens[8] = ns[7], 2048
+    dtype = "fp16" if store == "fp16" else "bf16"
+    c = Case(dtype, store, ns, lens, 2, 4, 64, 64, page=16, seed=5)
+    q = c.q.to(DEV)
+    one, few = (binding.tree_attention_workspace(q, c.cache, n) for n in (1, 3))
+    assert one.numel() == few.numel()
+    c.check(*c.run(workspace=few))
+
+
 def test_a_wrong_hint_costs_time_only():
     c = Case("bf16", "bf16", [33, 5], [200, 90], 2, 4, 128, 128, page=16, seed=3)
     for hint in (1, 8, 20, 1000):
