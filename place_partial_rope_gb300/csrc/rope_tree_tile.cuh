@@ -623,7 +623,8 @@ struct Tile {
             // other group's: until that one's product is under way, the parity
             // of the slot's barrier may still be that of the tile before that.
             constexpr bool TURNS = !C::PAIR && SLOTS % 2;
-            // (8-bit: rolled, for the instruction cache's sake, see widen)
+            // (8-bit: rolled, for the instruction cache's sake, see widen; 16-bit pairs
+            // took 118 us with this rolled and 105 without)
             constexpr int ISSUE = C::kWide ? 16 : 1;
             while (left > 0) {
                 if (s_mine > p_mine && (!TURNS || p_other + 1 >= p_mine)) {
@@ -891,12 +892,13 @@ struct Tile {
                             mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c));
                         tmem_wait_st();
                     }
-                    // 16-bit: s is held in registers.  8-bit: it is read twice, 32
-                    // at a time, in loops small enough to stay in the
-                    // instruction cache beside the helpers' (with s held, the
-                    // roles' code missed it and every role ran at a third of its
-                    // speed); the rows are bound by HBM, so the second read hides.
-                    constexpr int HELD = C::kWide ? C::COLS : 32;
+                    // s is held in registers by 16-bit rows, and by 8-bit pairs (whose rows
+                    // have 64 lanes: 57 us against 62 for 2 requests of 131072 rows and
+                    // 200 query rows).  Other 8-bit rows: it is read twice, 32 columns
+                    // at a time, in loops small enough to stay in the instruction
+                    // cache beside the helpers' (a batch of 48 requests of up to
+                    // 12000 fp8 rows: 258 us, and 270 with s held).
+                    constexpr int HELD = C::kWide || C::PAIR ? C::COLS : 32;
                     float s[HELD], top = -INFINITY;
                     const uint32_t from = lanes + s_col(w);
 #pragma unroll 1
