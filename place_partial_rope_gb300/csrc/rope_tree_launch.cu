@@ -104,11 +104,19 @@ rope_status_t map_of(CUtensorMap* map, const void* base, int dim, const TreeArgs
     const cuuint64_t sizes[4] = {cuuint64_t(dim), cuuint64_t(a.Hk), cuuint64_t(a.page_size), cuuint64_t(a.pages)};
     const cuuint64_t strides[3] = {a.Hk > 1 ? cuuint64_t(st[2]) : 16, a.page_size > 1 ? cuuint64_t(st[1]) : 16,
                                    a.pages > 1 ? cuuint64_t(st[0]) : 16};
+    // L2 fetches no more than a head's row: with 256 bytes for fp8 rows of 128 the
+    // neighbouring head's came along, and went before its turn (980 MB read for 618);
+    // bf16 rows of 192 + 128, 32 requests of 8000 rows: 240 us, and 225 so
+    const int row = dim * (wide ? 2 : 1);
+    const CUtensorMapL2promotion promotion = row % 256 == 0   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                             : row % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                             : row % 64 == 0  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                              : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     const cuuint32_t box[4] = {cuuint32_t(lanes), 1, cuuint32_t(a.box), 1}, steps[4] = {1, 1, 1, 1};
     const CUresult r = encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                               const_cast<void*>(base), sizes, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         *err = "the cache's sizes or strides do not fit a tensor map";
         return ROPE_ERR_CUDA;
