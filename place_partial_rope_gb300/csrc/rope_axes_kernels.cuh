@@ -14,6 +14,9 @@
 // for them).  A thread loads the token's positions on every axis up front
 // (at most four loads that a warp shares, in flight with those of x) and picks
 // one per pair by two selects, rather than one dependent load per pair.
+// Measured: 2 videos of 16 x 30 x 52 patches, 24 heads of 128 bf16 lanes (614 MB),
+// 93.2 us, 6.6 TB/s or 0.99 of the measured copy rate; a call on 256 patches
+// takes 8 us, the host's time.
 #pragma once
 #include "rope_axes.h"
 #include "rope_kernels.cuh"

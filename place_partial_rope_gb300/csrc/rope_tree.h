@@ -44,16 +44,16 @@ struct TreeArgs {
 // The group of row tiles that a block's first unit lies in, when it began in
 // an earlier block (nt > 0): written by the block, read by the join kernel.
 struct TreeMeta {
-    int64_t u0;     // the group's first unit
+    int64_t u0;     // the unit of the group's first tile
     int64_t chunk;  // units per block
-    int32_t r, h, m, nt;
+    int32_t r, h, m, nt, lead;
 };
 
 struct TreePlan {
     int dtype;    // rope_dtype_t of q
     int store;    // rope_cache_dtype_t
     int dk, dv;   // row lengths the kernel is built for (>= the call's)
-    int rows;     // query rows of a tile: 16 (narrow kernel), 32, 64, 128 or 256 (tile kernel)
+    int rows;     // query rows of a tile: 16 (narrow kernel), 64, 128 or 256 (tile kernel)
 };
 
 // The kernel for rows of Dk and Dv, `rows` query rows a key head and pages of

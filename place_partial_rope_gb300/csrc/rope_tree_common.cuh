@@ -1,7 +1,7 @@
 // rope_tree_common.cuh -- what the attention kernels share: the division of
 // the work, the visibility of cache rows, the joining of parts.
 //
-// Units of work are (request, key head, row tile, cache tile), in that order;
+// Units of work are (request, key head, row tile, cache tile), in that order (see kLead);
 // every block takes an equal, contiguous run of them (one block per resident
 // slot), so a long request is spread over many blocks and short ones share a
 // block.  A block that holds a whole (request, head, row tile) writes the
@@ -163,12 +163,21 @@ __device__ __forceinline__ uint4 half8(const float* f, float by) {
 // the division of the work
 // ------------------------------------------------------------------------
 
-// Units of request r: key heads x row tiles x cache tiles (a request with no
+// Request r: groups (key heads x row tiles) of nt cache tiles (a request with no
 // cache rows still has a tile, so that its results are written).
 struct Request {
     int qs, n, len, mt, nt;
-    int64_t units;
+    int64_t groups;
+
+    __device__ __forceinline__ int64_t units(int lead) const { return groups * (nt + lead); }
 };
+
+// A run of tiles costs its block its tiles and, once, what takes about as long as
+// kLead of them: queries brought, the pipeline filled and drained, results written.
+// So a group counts kLead units before those of its tiles (where a block has
+// many tiles; a few are better cut evenly).  48 requests of 90 to 12000 rows,
+// of which some blocks had four runs and some forty: @@LEAD.
+constexpr int kLead = 4;
 
 template <int ROWS, int TN>
 __device__ __forceinline__ Request request(const TreeArgs& a, int r) {
@@ -180,35 +189,52 @@ __device__ __forceinline__ Request request(const TreeArgs& a, int r) {
     q.len = min(max(__ldg(a.kv_len + r), 0), a.max_len);
     q.mt = static_cast<int>((int64_t(q.n) * a.G + ROWS - 1) / ROWS);
     q.nt = max(1, (q.len + TN - 1) / TN);
-    q.units = q.n == 0 ? 0 : int64_t(a.Hk) * q.mt * q.nt;
+    q.groups = q.n == 0 ? 0 : int64_t(a.Hk) * q.mt;
     return q;
 }
 
 // A block's units, and the request that holds the first of them.
 struct Place {
-    int r;
+    int r, lead;
     int64_t base, start, end, chunk;  // base: units before request r
 };
 
 // Sum the requests' units, cut them into equal runs, and find this block's.
-// All THREADS threads of the block take part; `scratch` holds THREADS / 32 + 2
+// All THREADS threads of the block take part; `scratch` holds THREADS / 16 + 2
 // numbers of shared memory.
 template <int ROWS, int TN, int THREADS>
 __device__ __forceinline__ Place find_place(const TreeArgs& a, int64_t* scratch) {
     constexpr int WARPS = THREADS / 32;
     int64_t* warp_sum = scratch;
-    int64_t* found = scratch + WARPS;
+    int64_t* warp_groups = scratch + WARPS;
+    int64_t* found = scratch + 2 * WARPS;
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    int64_t mine = 0;
-    for (int r = tid; r < a.R; r += THREADS) mine += request<ROWS, TN>(a, r).units;
+    int64_t mine = 0, groups = 0;
+    for (int r = tid; r < a.R; r += THREADS) {
+        const Request q = request<ROWS, TN>(a, r);
+        mine += q.units(0);
+        groups += q.groups;
+    }
 #pragma unroll
-    for (int d = 16; d; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-    if (lane == 0) warp_sum[warp] = mine;
+    for (int d = 16; d; d /= 2) {
+        mine += __shfl_xor_sync(0xffffffffu, mine, d);
+        groups += __shfl_xor_sync(0xffffffffu, groups, d);
+    }
+    if (lane == 0) {
+        warp_sum[warp] = mine;
+        warp_groups[warp] = groups;
+    }
     if (tid == 0) found[0] = a.R;
     __syncthreads();
     int64_t total = 0;
-    for (int w = 0; w < WARPS; ++w) total += warp_sum[w];
+    groups = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        total += warp_sum[w];
+        groups += warp_groups[w];
+    }
     Place p;
+    p.lead = total >= int64_t(gridDim.x) * 8 ? kLead : 0;
+    total += groups * p.lead;
     p.chunk = (total + gridDim.x - 1) / gridDim.x;
     if (p.chunk < 1) p.chunk = 1;
     p.start = int64_t(blockIdx.x) * p.chunk;
@@ -219,7 +245,7 @@ __device__ __forceinline__ Place find_place(const TreeArgs& a, int64_t* scratch)
     int64_t before = 0;
     for (int r0 = 0; r0 < a.R; r0 += THREADS) {
         const int r = r0 + tid;
-        const int64_t u = r < a.R ? request<ROWS, TN>(a, r).units : 0;
+        const int64_t u = r < a.R ? request<ROWS, TN>(a, r).units(p.lead) : 0;
         int64_t sum = u;  // inclusive over the warp
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -253,47 +279,71 @@ struct RunAt {
     int64_t slot;  // where a part goes; -1: the run is whole
 };
 
-// A block's runs, one after the other; several warps may each walk them.
+// A block's runs, one after the other; several warps may each walk them.  The
+// group of the run is looked up once, by division, and then counted on.
 struct Walk {
-    int64_t u, base, end;
-    int r;
+    Request q;
+    int64_t u, end, g0;  // g0: the group's first unit (of its lead)
+    int r, h, m, lead;
     bool first;
-
-    __device__ __forceinline__ explicit Walk(const Place& p) : u(p.start), base(p.base), end(p.end), r(p.r), first(true) {}
 };
 
 template <int ROWS, int TN>
-__device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out) {
-    while (w.u < w.end && w.r < a.R) {
-        const Request q = request<ROWS, TN>(a, w.r);
-        if (w.u >= w.base + q.units) {
-            w.base += q.units;
-            ++w.r;
-            continue;
-        }
-        const int64_t per = int64_t(q.mt) * q.nt, at = w.u - w.base;
-        RunAt x;
-        x.rq = q;
-        x.r = w.r;
-        x.h = static_cast<int>(at / per);
-        const int rest = static_cast<int>(at - x.h * per);
-        x.m = rest / q.nt;
-        x.t0 = rest - x.m * q.nt;
-        x.count = static_cast<int>(min(int64_t(q.nt - x.t0), w.end - w.u));
-        x.slot = x.count == q.nt ? int64_t(-1) : int64_t(blockIdx.x) * 2 + (w.first ? 0 : 1);
-        w.first = false;
-        w.u += x.count;
-        out = x;
-        return true;
+__device__ __forceinline__ Walk walk_from(const TreeArgs& a, const Place& p) {
+    Walk w{};
+    w.u = p.start;
+    w.end = p.end;
+    w.lead = p.lead;
+    w.first = true;
+    if (w.u < w.end) {
+        w.r = p.r;
+        w.q = request<ROWS, TN>(a, w.r);
+        const int each = w.q.nt + w.lead;
+        const int64_t group = (w.u - p.base) / each;
+        w.h = static_cast<int>(group / w.q.mt);
+        w.m = static_cast<int>(group - int64_t(w.h) * w.q.mt);
+        w.g0 = p.base + group * each;
     }
-    return false;
+    return w;
+}
+
+template <int ROWS, int TN>
+__device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out) {
+    if (w.u >= w.end) return false;
+    if (w.u >= w.g0 + w.lead + w.q.nt) {  // the next group; there is one, as units are left
+        w.g0 = w.u;
+        if (++w.m == w.q.mt) {
+            w.m = 0;
+            if (++w.h == a.Hk) {
+                w.h = 0;
+                do {
+                    if (++w.r >= a.R) return false;
+                    w.q = request<ROWS, TN>(a, w.r);
+                } while (w.q.groups == 0);
+            }
+        }
+    }
+    const int off = static_cast<int>(w.u - w.g0), before = max(w.lead - off, 0);  // units before the run's first tile
+    if (w.end - w.u <= before) return false;
+    RunAt x;
+    x.rq = w.q;
+    x.r = w.r;
+    x.h = w.h;
+    x.m = w.m;
+    x.t0 = max(off - w.lead, 0);
+    x.count = static_cast<int>(min(int64_t(w.q.nt - x.t0), w.end - w.u - before));
+    x.slot = x.count == w.q.nt ? int64_t(-1) : int64_t(blockIdx.x) * 2 + (w.first ? 0 : 1);
+    w.first = false;
+    w.u += before + x.count;
+    out = x;
+    return true;
 }
 
 // What the join kernel needs to know of a block: the group that its first run
 // belongs to, when that began in an earlier block.
 __device__ __forceinline__ TreeMeta meta_of(const Place& p, const RunAt& x) {
-    if (x.t0 == 0) return TreeMeta{0, p.chunk, 0, 0, 0, 0};
-    return TreeMeta{p.start - x.t0, p.chunk, x.r, x.h, x.m, x.rq.nt};
+    if (x.t0 == 0) return TreeMeta{0, p.chunk, 0, 0, 0, 0, p.lead};
+    return TreeMeta{p.start - x.t0, p.chunk, x.r, x.h, x.m, x.rq.nt, p.lead};
 }
 
 // Which of the 32 rows from j drafted token i of a request sees.
@@ -387,7 +437,9 @@ struct PartAt {
 // side.  Few parts: a warp takes a piece of 32 columns of a block of rows,
 // alone, its lanes being rows (of two columns, when there are 16).  Many: a
 // block takes a piece of 8 columns, its warps the parts in turn, joined
-// through shared memory in the same order every time.
+// through shared memory in the same order every time.  Measured alone, from
+// HBM: 32 MB of parts (pairs of tiles cut by 151 borders) 14 us, 1.1 MB of a
+// single token's 10 us.
 template <int ROWS, int DV>
 __global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __grid_constant__ TreeArgs a,
                                                                       float bias) {
@@ -409,8 +461,9 @@ __global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __gr
     const int rbs = (left + RB - 1) / RB;
     const int own = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y), all = (parts - 1) * int(gridDim.y);
     // part p of the group: block `from` holds it second unless the group
-    // begins with the block's run; the others hold it first
-    auto slot = [&](int p) { return (from + p) * 2 + (p == 0 && from * w.chunk != w.u0 ? 1 : 0); };
+    // begins with the block's run (or before it, with the units of its lead);
+    // the others hold it first
+    auto slot = [&](int p) { return (from + p) * 2 + (p == 0 && from * w.chunk < w.u0 - w.lead ? 1 : 0); };
 
     if (parts <= WARPS) {
         constexpr int E = RB;  // words of a lane

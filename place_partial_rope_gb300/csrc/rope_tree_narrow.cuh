@@ -38,6 +38,10 @@
 // lanes that needs no shuffle: the sum over k may run in any order as long as
 // q is permuted alike, and the columns of O may come in any order as long as
 // the end puts them back; see query_frags and value_codes.
+//   Measured (device, 8 query rows a key head, 8 key heads, 128 + 128 lanes): 32
+// requests of 8000 fp8 rows 174 us, 3.0 TB/s (0.45 of the measured copy rate),
+// what it issues bounding it; one request of 4097 bf16 rows and 2 key heads,
+// 11 us, and 10 for the join: latencies.
 #pragma once
 #include "rope_tree_common.cuh"
 
@@ -594,8 +598,8 @@ __global__ void __launch_bounds__(kNarrowThreads) rope_tree_narrow_kernel(const 
     extern __shared__ __align__(128) char smem[];
     after_predecessor();
     const Place p = find_place<C::ROWS, C::TN, kNarrowThreads>(a, reinterpret_cast<int64_t*>(smem));
-    Walk walk(p);
-    TreeMeta meta{0, p.chunk, 0, 0, 0, 0};
+    Walk walk = walk_from<C::ROWS, C::TN>(a, p);
+    TreeMeta meta{0, p.chunk, 0, 0, 0, 0, p.lead};
     RunAt step;
     bool first = true;
     __syncthreads();  // the place's scratch is done with

@@ -1,5 +1,5 @@
-// rope_tree_tile.cuh -- attention of more than 16 query rows a key head (trees
-// of drafted tokens, chunks of prompts) over a paged cache, on tcgen05.
+// rope_tree_tile.cuh -- attention of many query rows a key head (batches of tokens,
+// trees of drafted tokens, chunks of prompts) over a paged cache, on tcgen05.
 //
 // Mathematics: that of rope_tree_narrow.cuh, on tiles of 128 query rows.  Two
 // differences.  The maximum that weights refer to may lag: it moves (and O
@@ -14,8 +14,15 @@
 // What bounds it.  128 x TN x (Dk + Dv) multiply-adds a tile against TN (Dk +
 // Dv) cache elements: 128 query rows take 1024 cycles of tensor pipe a tile
 // of 128 x 128 + 128, and 16-bit rows 2800 cycles of this card's HBM share per
-// SM.  So up to 128 rows it is bound by HBM (8-bit: 1400 cycles), and beyond
-// that by the tensor pipe and the exponentials.
+// SM.  So up to 128 rows 16 bits are bound by HBM (32 requests of 8000 rows, 8
+// key heads: 182 us, 5.8 TB/s), and a pair of tiles by the chain s -> p -> O of
+// its two groups: 12 requests of 6000 to 8200 rows and 240 to 256 query rows,
+// 105 us, 0.43 of the measured matrix rate, the tensor pipe 41 % busy.  (The
+// product on the first half of a row's weights, while the thread was at the second,
+// took 121 us.)  8-bit rows would take 1400 cycles of HBM and take 3000: each
+// code passes through shared memory four times and the helpers' and groups' code
+// presses on the instruction cache (87 % of its requests hit): 48 requests of 90 to
+// 12000 rows, 260 us, 2.4 TB/s.  (24 warps, twice the helpers: 265 us.)
 //
 // How.  One block an SM, 16 warps with one role each:
 //   0-3, 4-7  two softmax groups.  A thread owns a query row (a lane of tensor
@@ -28,7 +35,7 @@
 //             for keys, whose lanes run along the sum, and values, whose lanes
 //             run along the columns), and helpers touch only the last tiles of a
 //             request.  8-bit rows land as codes, and helpers write them to
-//             such tiles as fp16.
+//             such tiles as fp16, one team of 96 threads keys and one values.
 //   12        the one thread that issues tcgen05.mma: s = q k into tensor
 //             memory, O += p v with p from tensor memory.
 // Each softmax group has its own s (128 columns) and O (128 columns), all 512
@@ -37,6 +44,12 @@
 // false) the groups take the run's tiles in turn and are joined when it ends;
 // beyond that (PAIR) they are two row tiles against the same cache tile, which
 // then is read once for 256 rows.
+//   Tiles of up to 64 query rows (ROWS 64) are in tensor memory twice, as the upper
+// and the lower 64 lanes, and each copy sees to half the columns: its weights in
+// the other half are zeros, so the two O's are parts that add up.  So all 256
+// threads of the groups have work.
+//   The fetching warp alone walks the division of the work (request, head, tiles);
+// it writes each run down in shared memory for the others.
 //   Every wait is bounded: a wait that gives up sets `dead`, later waits
 // return at once, and the run's rows come out as NaN.
 //   Page sizes that are no multiple of 8 are left to rope_tree_narrow.cuh.
@@ -365,12 +378,14 @@ struct Tile {
     __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* km, const CUtensorMap* vm) const {
         const int lane = int(threadIdx.x) & 31;
         constexpr uint32_t SLOTS = C::SLOTS, RAWS = C::RAWS > 0 ? C::RAWS : 1;
-        Walk walk(place);
+        Walk walk = walk_from<C::ROWS, C::TN>(a, place);
         RunAt step;
         bool more = next_run<C::ROWS, C::TN>(a, walk, step);
         RunAt x = step;
         uint32_t runs = 0;
         publish(x, runs++, more, lane);
+        if (lane == 0)
+            a.meta[blockIdx.x] = more ? meta_of(place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, place.lead};
         Look now{-1, 0};
         if (more) now = look(x, x.t0 * C::TN + lane * a.box);
         int it = 0;
@@ -379,16 +394,11 @@ struct Tile {
             const uint32_t slot = n % SLOTS;
             const int tile = x.t0 + it, h = x.h;
             const bool part = (tile + 1) * C::TN > x.rq.len - x.rq.n;  // more than context rows
-            if (it + 1 == x.count) {
-                more = next_run<C::ROWS, C::TN>(a, walk, step);
-                x = step;
-                publish(x, runs++, more, lane);
-                it = 0;
-            } else {
-                ++it;
-            }
+            // the next tile's pages: looked up before this one's fetch, but for a
+            // run's first, as the fetch is not to wait for the walk
+            const bool last = it + 1 == x.count;
             Look next{-1, 0};
-            if (more) next = look(x, (x.t0 + it) * C::TN + lane * a.box);
+            if (!last) next = look(x, (tile + 1) * C::TN + lane * a.box);
 #pragma unroll 1
             for (int values = 0; values < 2; ++values) {
                 const uint32_t item = 2 * n + values, r = item % RAWS;
@@ -408,6 +418,14 @@ struct Tile {
                     if (item >= RAWS) bar_wait(&sync->raw_empty[r], (item / RAWS - 1) & 1, sync);
                 }
                 fetch(values ? vm : km, values ? C::DV : C::DK, now, h, to, lane, bar);
+            }
+            ++it;
+            if (last) {
+                more = next_run<C::ROWS, C::TN>(a, walk, step);
+                x = step;
+                publish(x, runs++, more, lane);
+                it = 0;
+                if (more) next = look(x, x.t0 * C::TN + lane * a.box);
             }
             now = next;
         }
@@ -833,15 +851,13 @@ struct Tile {
         return float(int(__float_as_uint(power) >> 23) - 127);
     }
 
-    __device__ __forceinline__ void softmax(const Place& place, int w) const {
+    __device__ __forceinline__ void softmax(int w) const {
         const int tid = int(threadIdx.x), row = tid & 127;
         const uint32_t lanes = tmem + (uint32_t(row & 96) << 16);  // this warp's lanes
         float2* ml = reinterpret_cast<float2*>(smem + C::ML_AT);
         RunAt x;
         uint32_t before = 0, run = 0, s_par = 0, o_par = 0;
-        TreeMeta meta{0, place.chunk, 0, 0, 0, 0};
         while (take(run, x)) {
-            if (run == 0) meta = meta_of(place, x);
             float* factors = reinterpret_cast<float*>(smem + C::FACTOR_AT);
             stage_queries(x, tid, factors);
             to_async_proxy();
@@ -964,7 +980,6 @@ struct Tile {
             before += x.count;
             ++run;
         }
-        if (tid == 0) a.meta[blockIdx.x] = meta;
     }
 
     // The results of a run of a pair.  A thread holds a row, which it would write
@@ -1182,7 +1197,7 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     // (the host sees to it that the launch has them)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        tile.softmax(place, warp >> 2);
+        tile.softmax(warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 12) {
