@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __gr
     // part p of the group: block `from` holds it second unless the group
     // begins with the block's run (or before it, with the units of its lead);
     // the others hold it first
-    auto slot = [&](int p) { return (from + p) * 2 + (p == 0 && from * w.chunk < w.u0 - w.lead ? 1 : 0); };
+    const int64_t second = from * w.chunk < w.u0 - w.lead ? 1 : 0;
+    auto slot = [&](int p) { return (from + p) * 2 + (p == 0 ? second : 0); };
 
     if (parts <= WARPS) {
         constexpr int E = RB;  // words of a lane
