@@ -174,9 +174,10 @@ struct Request {
 
 // A run of tiles costs its block its tiles and, once, what takes about as long as
 // kLead of them: queries brought, the pipeline filled and drained, results written.
-// So a group counts kLead units before those of its tiles (where a block has
-// many tiles; a few are better cut evenly).  48 requests of 90 to 12000 rows,
-// of which some blocks had four runs and some forty: @@LEAD.
+// So a group counts kLead units before those of its tiles, where a block has
+// several tiles.  48 requests of 90 to 12000 fp8 rows, of which some blocks had
+// four runs and some forty: 0 264 us, 2 252, 3 240, 4 232, 6 233; 12 requests of
+// 6000 to 8200 bf16 rows: 112.9, 110.7, 110.6, 108.6, 112.2.
 constexpr int kLead = 4;
 
 template <int ROWS, int TN>
@@ -437,11 +438,12 @@ struct PartAt {
 // side.  Few parts: a warp takes a piece of 32 columns of a block of rows,
 // alone, its lanes being rows (of two columns, when there are 16).  Many: a
 // block takes a piece of 8 columns, its warps the parts in turn, joined
-// through shared memory in the same order every time.  Measured alone, from
-// HBM: 32 MB of parts (pairs of tiles cut by 151 borders) 14 us, 1.1 MB of a
-// single token's 10 us.
+// through shared memory in the same order every time.  80 registers (three
+// blocks an SM), so that a warp's loads of two parts are in flight together: 32 MB
+// of parts (pairs of tiles cut by 151 borders) 11 us, where 64 registers took
+// 14.6 and two blocks of 126 12.2.
 template <int ROWS, int DV>
-__global__ void __launch_bounds__(kJoinThreads) rope_tree_join_kernel(const __grid_constant__ TreeArgs a,
+__global__ void __launch_bounds__(kJoinThreads, 3) rope_tree_join_kernel(const __grid_constant__ TreeArgs a,
                                                                       float bias) {
     using P = PartAt<ROWS, DV>;
     constexpr int WARPS = kJoinThreads / 32, RB = P::RB, CW = 8, WORDS = CW * RB;

@@ -17,12 +17,12 @@
 // SM.  So up to 128 rows 16 bits are bound by HBM (32 requests of 8000 rows, 8
 // key heads: 182 us, 5.8 TB/s), and a pair of tiles by the chain s -> p -> O of
 // its two groups: 12 requests of 6000 to 8200 rows and 240 to 256 query rows,
-// 105 us, 0.43 of the measured matrix rate, the tensor pipe 41 % busy.  (The
+// 101 us, 0.44 of the measured matrix rate, the tensor pipe 43 % busy.  (The
 // product on the first half of a row's weights, while the thread was at the second,
-// took 121 us.)  8-bit rows would take 1400 cycles of HBM and take 3000: each
+// took 121 us, not 105.)  8-bit rows would take 1400 cycles of HBM and take 3000: each
 // code passes through shared memory four times and the helpers' and groups' code
 // presses on the instruction cache (87 % of its requests hit): 48 requests of 90 to
-// 12000 rows, 260 us, 2.4 TB/s.  (24 warps, twice the helpers: 265 us.)
+// 12000 rows, 229 us, 2.7 TB/s.  (24 warps, twice the helpers: no faster.)
 //
 // How.  One block an SM, 16 warps with one role each:
 //   0-3, 4-7  two softmax groups.  A thread owns a query row (a lane of tensor
@@ -913,7 +913,7 @@ struct Tile {
                     // 200 query rows).  Other 8-bit rows: it is read twice, 32 columns
                     // at a time, in loops small enough to stay in the instruction
                     // cache beside the helpers' (a batch of 48 requests of up to
-                    // 12000 fp8 rows: 258 us, and 270 with s held).
+                    // 12000 fp8 rows: 258 us, and 276 with s held).
                     constexpr int HELD = C::kWide || C::PAIR ? C::COLS : 32;
                     float s[HELD], top = -INFINITY;
                     const uint32_t from = lanes + s_col(w);
