@@ -22,7 +22,7 @@
 // took 121 us, not 105.)  8-bit rows would take 1400 cycles of HBM and take 3000: each
 // code passes through shared memory four times and the helpers' and groups' code
 // presses on the instruction cache (87 % of its requests hit): 48 requests of 90 to
-// 12000 rows, 229 us, 2.7 TB/s.  (24 warps, twice the helpers: no faster.)
+// 12000 rows, 219 us, 2.8 TB/s.  (24 warps, twice the helpers: no faster.)
 //
 // How.  One block an SM, 16 warps with one role each:
 //   0-3, 4-7  two softmax groups.  A thread owns a query row (a lane of tensor
