@@ -51,7 +51,8 @@
 //   The fetching warp alone walks the division of the work (request, head, tiles);
 // it writes each run down in shared memory for the others.
 //   Every wait is bounded: a wait that gives up sets `dead`, later waits
-// return at once, and the run's rows come out as NaN.
+// return at once, and the rows of the run at hand come out as NaN (of later
+// runs nothing is written).
 //   Page sizes that are no multiple of 8 are left to rope_tree_narrow.cuh.
 #pragma once
 #include <cuda.h>
@@ -78,7 +79,7 @@ struct TileCfg {
     static constexpr int K_SLOT = TN * DK * 2, V_SLOT = TN * DV * 2;
     // 8-bit: the codes of a tile's keys or values, before they become fp16
     static constexpr int RAW = kWide ? 0 : TN * DK;
-    static constexpr int RAWS = kWide ? 0 : (TN == 128 && DK == 128) || (PAIR && DK == 192) ? 3 : 4;
+    static constexpr int RAWS = kWide ? 0 : TN == 128 && DK == 128 ? 3 : 4;
     static constexpr int ML = PAIR ? 0 : 2048, FACTORS = kWide ? 0 : ROWS * 4, MISC = ML + FACTORS + 1024;
     static constexpr int kSmemMax = 232448;
     static constexpr int fit(int slots) {
