@@ -218,7 +218,10 @@ rope_status_t rope_partial_cache_read(const rope_kv_cache_t* cache, const int64_
  * heads divides Hq.  Rows of q, out and the cache must start on 16-byte
  * boundaries.  Sums are fp32; the products of q with k and of exp(s) with v
  * run on tensor cores in bf16 (bf16 caches) or fp16 (the others) with fp32
- * accumulation, exp(s) being rounded to that type once.
+ * accumulation, exp(s) being rounded to that type once.  Pages of a multiple
+ * of 8 rows, and up to 192 + 128 lanes, are the fast case: others read the
+ * cache once for each 16 query rows of a key head.  A call captured in a graph
+ * may be replayed with other contents of the device arrays.
  */
 rope_status_t rope_partial_tree_attention(const rope_kv_cache_t* cache, const void* q,
                                           rope_dtype_t dtype, int64_t Tq, int64_t Hq,

@@ -202,6 +202,23 @@ def test_few_query_rows_over_many_tiles(store):
     c.check(*c.run(workspace=few))
 
 
+@pytest.mark.parametrize("store,most", [("bf16", 3), ("fp8", 3), ("bf16", 20), ("int8", 20)])
+def test_short_and_long_requests_together(store, most):
+    """Many tiles a block, where a request's start counts as several of them
+    when the work is cut: short requests between long ones, and empty ones."""
+    rng = np.random.default_rng(most)
+    ns = rng.integers(1, most + 1, 64).tolist()
+    lens = [n + int(x) for n, x in zip(ns, np.exp(rng.uniform(0, 6, 64)))]
+    for r in range(3, 64, 7):
+        lens[r] = int(rng.integers(8000, 10000))
+    ns[10] = ns[11] = 0
+    lens[11] = 0
+    c = Case("bf16", store, ns, lens, 4, 2, 16, 16, page=32, seed=most)
+    a, b = c.run(), c.run()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c.check(*a)
+
+
 def test_a_wrong_hint_costs_time_only():
     c = Case("bf16", "bf16", [33, 5], [200, 90], 2, 4, 128, 128, page=16, seed=3)
     for hint in (1, 8, 20, 1000):
