@@ -890,6 +890,7 @@ struct Tile {
                 tmem_after();
                 if (active) {
                     const bool part = j0 + C::TN > prefix;  // more than context rows
+                    float shrink = 1.0f;  // what l and O are multiplied by
                     if constexpr (!C::kWide) {
                         // the scales came with the keys and the values
                         bar_wait(&sync->v_full[n % C::SLOTS], (n / C::SLOTS) & 1, sync);
@@ -897,10 +898,9 @@ struct Tile {
                         const float4 y = *reinterpret_cast<const float4*>(sc + 2 * C::TN);
                         const float u = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
                         if (u > vref) {
-                            const float p = power_above(u), f = vref / p;
+                            const float p = power_above(u);
+                            shrink = vref / p;
                             vref = p;
-                            l *= f;
-                            if (v > 1) rescale(lanes + o_col(w), f);
                         }
                     }
                     if (part) {
@@ -932,11 +932,15 @@ struct Tile {
                     }
                     top *= factor;
                     const bool up = top > m + C::kLag || (m == -INFINITY && top > m);
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float f = up ? pow2(m - top) : 1.0f;
-                        if (up) m = top;
-                        l *= f;
-                        if (v > 1) rescale(lanes + o_col(w), f);
+                    if (up) {
+                        shrink *= pow2(m - top);
+                        m = top;
+                    }
+                    // (both factors at once: a second rescale would read columns that the
+                    // first one's stores, which are asynchronous, may not have reached)
+                    if (__any_sync(0xffffffffu, shrink != 1.0f)) {
+                        l *= shrink;
+                        if (v > 1) rescale(lanes + o_col(w), shrink);
                     }
                     const float base = C::kBias - (m == -INFINITY ? 0.0f : m) - (C::kWide ? 0.0f : exponent(vref));
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
