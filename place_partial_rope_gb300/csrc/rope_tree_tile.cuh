@@ -373,6 +373,24 @@ struct Tile {
         return false;
     }
 
+    // The same for the N threads of a role that barrier ID counts, or (0) for the
+    // lanes of a warp: all of them go on or none does.  Where a wait gives up just
+    // as a run is written down, one thread may find the run and the next one
+    // `dead`; a barrier that some do not reach would be waited for without end.
+    template <int ID, int N = 32>
+    __device__ __forceinline__ bool take_all(uint32_t r, RunAt& x) const {
+        const bool mine = take(r, x);
+        if constexpr (ID == 0) return __all_sync(0xffffffffu, mine);
+        __syncwarp();
+        uint32_t all;
+        asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, %3, p;\n"
+                     "selp.u32 %0, 1, 0, q;\n}"
+                     : "=r"(all)
+                     : "r"(uint32_t(mine)), "n"(ID), "n"(N)
+                     : "memory");
+        return all != 0;
+    }
+
     // The warp that fetches tiles, keys and values in turn, across runs, as far
     // ahead as the rings allow.  Rows of pages that are not there (no such row,
     // or a number outside the cache) are filled with zeros by the fetch.
@@ -391,7 +409,7 @@ struct Tile {
         if (more) now = look(x, x.t0 * C::TN + lane * a.box);
         int it = 0;
         uint32_t n = 0, fix_par = 0, fixed = 0;  // a bit for each slot: fix_full's parity, and whether it was used last
-        for (; more && !sync->dead; ++n) {
+        for (; more && !given_up(); ++n) {
             const uint32_t slot = n % SLOTS;
             const int tile = x.t0 + it, h = x.h;
             const bool part = (tile + 1) * C::TN > x.rq.len - x.rq.n;  // more than context rows
@@ -441,6 +459,9 @@ struct Tile {
         for (uint32_t k = 2 * n > RAWS ? 2 * n - RAWS : 0; !C::kWide && k < 2 * n; ++k)
             landed(&sync->raw_full[k % RAWS], (k / RAWS) & 1);
     }
+
+    // For a whole warp, whose lanes may find `dead` at different times.
+    __device__ __forceinline__ bool given_up() const { return __any_sync(0xffffffffu, sync->dead); }
 
     static __device__ __forceinline__ void landed(unsigned long long* b, uint32_t parity) {
         for (uint32_t i = 0; i < kSpins && !bar_test(b, parity); ++i) {
@@ -515,7 +536,7 @@ struct Tile {
         const bool second = MORE == 2 && id < C::TN - kTeam;
         RunAt x;
         uint32_t n = 0, run = 0;
-        while (take(run, x)) {
+        while (take_all<0>(run, x)) {
             const int first = x.t0 * C::TN, prefix = x.rq.len - x.rq.n;
             Look now[MORE];
             now[0] = look(x, id < C::TN ? first + id : x.rq.len);
@@ -578,7 +599,7 @@ struct Tile {
         constexpr uint32_t SLOTS = C::SLOTS;
         RunAt x;
         uint32_t n = 0, run = 0, par = 0;  // a parity bit for each slot
-        while (take(run, x)) {
+        while (take_all<2, kHelpers>(run, x)) {
             const int prefix = x.rq.len - x.rq.n;
             for (int it = 0; it < x.count; ++it, ++n) {
                 const int j0 = (x.t0 + it) * C::TN;
@@ -858,7 +879,7 @@ struct Tile {
         float2* ml = reinterpret_cast<float2*>(smem + C::ML_AT);
         RunAt x;
         uint32_t before = 0, run = 0, s_par = 0, o_par = 0;
-        while (take(run, x)) {
+        while (take_all<1, 256>(run, x)) {
             float* factors = reinterpret_cast<float*>(smem + C::FACTOR_AT);
             stage_queries(x, tid, factors);
             to_async_proxy();
