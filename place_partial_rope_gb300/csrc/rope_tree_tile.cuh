@@ -298,6 +298,7 @@ __host__ __device__ constexpr uint32_t o_col(int w) { return 256 + uint32_t(w) *
 
 template <class C>
 struct Tile {
+    using Cfg = C;
     const TreeArgs& a;
     char* smem;
     TileSync* sync;
@@ -392,7 +393,8 @@ struct Tile {
     }
 
     // The warp that fetches tiles, keys and values in turn, across runs, as far
-    // ahead as the rings allow.  Rows of pages that are not there (no such row,
+    // ahead as the rings allow.  A fetch that a wait before it did not allow is
+    // not made: its barrier may still count the last one's bytes.  Rows of pages that are not there (no such row,
     // or a number outside the cache) are filled with zeros by the fetch.
     __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* km, const CUtensorMap* vm) const {
         const int lane = int(threadIdx.x) & 31;
@@ -408,8 +410,9 @@ struct Tile {
         Look now{-1, 0};
         if (more) now = look(x, x.t0 * C::TN + lane * a.box);
         int it = 0;
-        uint32_t n = 0, fix_par = 0, fixed = 0;  // a bit for each slot: fix_full's parity, and whether it was used last
-        for (; more && !given_up(); ++n) {
+        uint32_t n = 0, items = 0;  // tiles, and fetches of keys or values
+        uint32_t fix_par = 0, fixed = 0;  // a bit for each slot: fix_full's parity, and whether it was used last
+        for (bool on = true; more && on; ++n) {
             const uint32_t slot = n % SLOTS;
             const int tile = x.t0 + it, h = x.h;
             const bool part = (tile + 1) * C::TN > x.rq.len - x.rq.n;  // more than context rows
@@ -419,13 +422,20 @@ struct Tile {
             Look next{-1, 0};
             if (!last) next = look(x, (tile + 1) * C::TN + lane * a.box);
 #pragma unroll 1
-            for (int values = 0; values < 2; ++values) {
-                const uint32_t item = 2 * n + values, r = item % RAWS;
+            for (int values = 0; values < 2; ++values, ++items) {
+                const uint32_t r = items % RAWS;
                 unsigned long long* bar = &sync->raw_full[r];
                 uint32_t to = smem_addr(smem + C::RAW_AT) + r * C::RAW;
                 if constexpr (C::kWide) {
                     if (n >= SLOTS)
                         bar_wait(values ? &sync->v_empty[slot] : &sync->k_empty[slot], (n / SLOTS - 1) & 1, sync);
+                } else {
+                    if (items >= RAWS) bar_wait(&sync->raw_empty[r], (items / RAWS - 1) & 1, sync);
+                }
+                // once a wait has given up, the place may be in use, or its last fetch under way
+                on = !given_up();
+                if (!on) break;
+                if constexpr (C::kWide) {
                     to = smem_addr(smem) + (values ? C::V_AT + slot * C::V_SLOT : C::K_AT + slot * C::K_SLOT);
                     bar = values ? &sync->v_full[slot] : &sync->k_full[slot];
                     if (values) {
@@ -433,13 +443,11 @@ struct Tile {
                         fix_par ^= uint32_t(part) << slot;
                         if (part) bar = &sync->fix_full[slot];
                     }
-                } else {
-                    if (item >= RAWS) bar_wait(&sync->raw_empty[r], (item / RAWS - 1) & 1, sync);
                 }
                 fetch(values ? vm : km, values ? C::DV : C::DK, now, h, to, lane, bar);
             }
             ++it;
-            if (last) {
+            if (last && on) {
                 more = next_run<C::ROWS, C::TN>(a, walk, step);
                 x = step;
                 publish(x, runs++, more, lane);
@@ -448,15 +456,14 @@ struct Tile {
             }
             now = next;
         }
-        if (!sync->dead) return;
-        // a wait gave up: the block may not end before its copies have
-        for (uint32_t k = n > SLOTS ? n - SLOTS : 0; C::kWide && k < n; ++k) {
-            const uint32_t slot = k % SLOTS, par = (k / SLOTS) & 1;
-            const bool f = fixed >> slot & 1;
-            landed(&sync->k_full[slot], par);
-            landed(f ? &sync->fix_full[slot] : &sync->v_full[slot], f ? ~(fix_par >> slot) & 1 : par);
+        // the block may not end before its fetches have, whether or not anyone still waits for them
+        for (uint32_t k = items > 2 * SLOTS ? items - 2 * SLOTS : 0; C::kWide && k < items; ++k) {
+            const uint32_t slot = k / 2 % SLOTS, par = (k / 2 / SLOTS) & 1;
+            if (k % 2 == 0) landed(&sync->k_full[slot], par);
+            else if (fixed >> slot & 1) landed(&sync->fix_full[slot], ~(fix_par >> slot) & 1);
+            else landed(&sync->v_full[slot], par);
         }
-        for (uint32_t k = 2 * n > RAWS ? 2 * n - RAWS : 0; !C::kWide && k < 2 * n; ++k)
+        for (uint32_t k = items > RAWS ? items - RAWS : 0; !C::kWide && k < items; ++k)
             landed(&sync->raw_full[k % RAWS], (k / RAWS) & 1);
     }
 
@@ -1176,10 +1183,12 @@ struct Tile {
     }
 };
 
-template <class C>
+// T: Tile<C>, or roles derived from it.
+template <class T>
 __global__ void __launch_bounds__(kTileThreads, 1)
 rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap km,
                       const __grid_constant__ CUtensorMap vm) {
+    using C = typename T::Cfg;
     extern __shared__ __align__(1024) char smem[];
     TileSync* sync = reinterpret_cast<TileSync*>(smem + C::SYNC_AT);
     const int warp = int(threadIdx.x) >> 5;
@@ -1217,7 +1226,7 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     tmem_before();
     __syncthreads();
     tmem_after();
-    const Tile<C> tile{a, smem, sync, sync->tmem};
+    const T tile{a, smem, sync, sync->tmem};
 
     // registers: 128 a thread at launch; 256 x 192 + 256 x 64 of the same 65536
     // (the host sees to it that the launch has them)
@@ -1249,7 +1258,7 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 template <int STORE, int DK, int DV, int ROWS>
 TreeKernel tile_kernel() {
     using C = TileCfg<STORE, DK, DV, ROWS>;
-    return TreeKernel{reinterpret_cast<const void*>(&rope_tree_tile_kernel<C>),
+    return TreeKernel{reinterpret_cast<const void*>(&rope_tree_tile_kernel<Tile<C>>),
                       reinterpret_cast<const void*>(&rope_tree_join_kernel<C::ROWS, DV>), C::SMEM, kTileThreads,
                       C::TN, C::kBias, 256 * 192 + 256 * 64};
 }

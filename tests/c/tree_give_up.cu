@@ -4,13 +4,30 @@
 //   agree   threads of a role ask for the next run while `dead` is set and the
 //           run is written down at about the same time: all of them take it or
 //           none does.
+//   fetch   the fetching warp with nobody to empty the rings: it gives up after
+//           about 1.5 s, and what it has fetched by then is left as it is.
 //
 // Prints "ok ..." or what differed.
 #include <stdint.h>
 #include <stdio.h>
 #include <string.h>
 
+#include "rope_tree_launch.cu"
 #include "rope_tree_tile.cuh"
+
+// The kernel that launch_tree() and tree_blocks() get, whatever the plan.
+static rope::TreeKernel g_kernel;
+
+namespace rope {
+TreeKernel narrow_kernel_bf16(const TreePlan&) { return g_kernel; }
+TreeKernel narrow_kernel_fp16(const TreePlan&) { return g_kernel; }
+TreeKernel narrow_kernel_fp8(const TreePlan&) { return g_kernel; }
+TreeKernel narrow_kernel_int8(const TreePlan&) { return g_kernel; }
+TreeKernel tile_kernel_bf16(const TreePlan&) { return g_kernel; }
+TreeKernel tile_kernel_fp16(const TreePlan&) { return g_kernel; }
+TreeKernel tile_kernel_fp8(const TreePlan&) { return g_kernel; }
+TreeKernel tile_kernel_int8(const TreePlan&) { return g_kernel; }
+}  // namespace rope
 
 using namespace rope;
 
@@ -92,10 +109,153 @@ static int agree(const char* what) {
     return h[2] != 0 || h[0] == 0 || h[1] == 0;
 }
 
+// ---------------------------------------------------------------- a small call
+
+// R requests of one token and LEN rows each, one key head, 64 lanes, pages of 64
+// rows in order; key codes of tile t (128 rows) are 1 + t, values' 65 + t.
+template <class C, int R, int LEN>
+struct Call {
+    static constexpr int E = C::kWide ? 2 : 1, PAGES = R * LEN / 64, ELEMS = PAGES * 64 * 64;
+    static_assert(LEN % 128 == 0, "whole tiles");
+    TreePlan p{C::BF16 ? ROPE_BF16 : ROPE_FP16, C::STORE, 64, 64, C::ROWS};
+    TreeArgs a{};
+    int blocks = 0;
+    char* ws = nullptr;
+
+    template <class T>
+    int make(bool several) {
+        using K = TreeKernel;
+        g_kernel = K{reinterpret_cast<const void*>(&rope_tree_tile_kernel<T>),
+                     reinterpret_cast<const void*>(&rope_tree_join_kernel<C::ROWS, 64>), C::SMEM, kTileThreads, C::TN,
+                     C::kBias, 256 * 192 + 256 * 64};
+        const char* err = "";
+        // (also: a kernel whose launch lacks the registers that it shares out is refused here)
+        if (tree_blocks(p, 0, &blocks, &err) != ROPE_OK) {
+            printf("FAIL %s\n", err);
+            return 1;
+        }
+        if (!several) blocks = 1;
+        char* codes[2];
+        static char host[ELEMS * 2];
+        for (int v = 0; v < 2; ++v) {
+            for (int i = 0; i < ELEMS; ++i) {
+                const int code = 1 + 64 * v + i / 64 % LEN / 128;
+                if (E == 1) host[i] = char(code);
+                else host[2 * i] = char(code), host[2 * i + 1] = 0;
+            }
+            CHECK(cudaMalloc(&codes[v], ELEMS * E));
+            CHECK(cudaMemcpy(codes[v], host, ELEMS * E, cudaMemcpyHostToDevice));
+        }
+        static int32_t table[PAGES], start[R + 1], len[R];
+        static float ones[PAGES * 64];
+        for (int i = 0; i < PAGES; ++i) table[i] = i;
+        for (int r = 0; r <= R; ++r) start[r] = r;
+        for (int r = 0; r < R; ++r) len[r] = LEN;
+        for (float& x : ones) x = 1.0f;
+        void *dt, *ds, *dl, *ones_at, *q, *out, *lse;
+        CHECK(cudaMalloc(&dt, sizeof table));
+        CHECK(cudaMalloc(&ds, sizeof start));
+        CHECK(cudaMalloc(&dl, sizeof len));
+        CHECK(cudaMalloc(&ones_at, sizeof ones));
+        CHECK(cudaMalloc(&q, R * 128));
+        CHECK(cudaMalloc(&out, R * 128));
+        CHECK(cudaMalloc(&lse, R * 4));
+        CHECK(cudaMalloc(&ws, tree_workspace(p, blocks)));
+        CHECK(cudaMemcpy(dt, table, sizeof table, cudaMemcpyHostToDevice));
+        CHECK(cudaMemcpy(ds, start, sizeof start, cudaMemcpyHostToDevice));
+        CHECK(cudaMemcpy(dl, len, sizeof len, cudaMemcpyHostToDevice));
+        CHECK(cudaMemcpy(ones_at, ones, sizeof ones, cudaMemcpyHostToDevice));
+        CHECK(cudaMemset(q, 0, R * 128));
+        CHECK(cudaMemset(out, 0, R * 128));
+        CHECK(cudaMemset(lse, 0, R * 4));
+        CHECK(cudaMemset(ws, 0, tree_workspace(p, blocks)));
+        a.k = codes[0];
+        a.v = codes[1];
+        a.ks = a.vs = C::kWide ? nullptr : static_cast<float*>(ones_at);
+        for (int64_t* st : {a.k_st, a.v_st}) st[0] = 64 * 64 * E, st[1] = 64 * E, st[2] = 64 * E;
+        for (int64_t* st : {a.ks_st, a.vs_st}) st[0] = 64, st[1] = 1, st[2] = 1;
+        a.q = static_cast<char*>(q);
+        a.out = static_cast<char*>(out);
+        a.lse = static_cast<float*>(lse);
+        a.q_st[0] = a.q_st[1] = a.o_st[0] = a.o_st[1] = 128;
+        a.q_start = static_cast<int32_t*>(ds);
+        a.kv_len = static_cast<int32_t*>(dl);
+        a.table = static_cast<int32_t*>(dt);
+        a.table_stride = LEN / 64;
+        a.R = a.Tq = R;
+        a.Hk = a.G = a.Hq = 1;
+        a.Dk = a.Dv = 64;
+        a.pages = PAGES;
+        a.page_size = 64;
+        a.max_len = LEN;
+        a.div_page = FastDiv::make(64);
+        a.div_group = FastDiv::make(1);
+        a.scale_log2 = 0.125f;
+        a.bf16 = C::BF16;
+        return 0;
+    }
+
+    int launch() {
+        const char* err = "";
+        if (launch_tree(p, a, ws, blocks, nullptr, &err) != ROPE_OK) {
+            printf("FAIL %s\n", err);
+            return 1;
+        }
+        CHECK(cudaDeviceSynchronize());
+        return 0;
+    }
+};
+
+// ---------------------------------------------------------------- fetch
+
+struct Seen {
+    uint32_t dead;
+    char smem[232448];
+};
+__device__ Seen g_seen;
+
+// Nobody but the fetching warp, which shows what is in shared memory at its end.
+template <class C>
+struct FetchAlone : Tile<C> {
+    __device__ void softmax(int) const {}
+    __device__ void products() const {}
+    __device__ void mend_tiles(int) const {}
+    template <bool VALUES>
+    __device__ void widen_tiles(int) const {}
+    __device__ void fetches(const Place& place, const CUtensorMap* km, const CUtensorMap* vm) const {
+        Tile<C>::fetches(place, km, vm);
+        for (int i = int(threadIdx.x) % 32; i < C::RAW_AT + C::RAWS * C::RAW; i += 32) g_seen.smem[i] = this->smem[i];
+        g_seen.dead = this->sync->dead;
+    }
+};
+
+// The rings hold the first tiles: keys and values of as many as there are
+// places, and not a byte of the next one.
+template <class C>
+static int fetch_alone(const char* what) {
+    constexpr int TILES = 6;
+    static Call<C, 1, 128 * TILES> call;
+    static Seen seen;
+    if (call.template make<FetchAlone<C>>(false) || call.launch()) return 1;
+    CHECK(cudaMemcpyFromSymbol(&seen, g_seen, sizeof seen));
+    int wrong = 0;
+    for (int v = 0; v < 2; ++v)
+        for (int s = 0; s < (C::kWide ? C::SLOTS : C::RAWS / 2); ++s) {
+            const int at = C::kWide ? (v ? C::V_AT : C::K_AT) + s * C::K_SLOT : C::RAW_AT + (2 * s + v) * C::RAW;
+            const int code = 1 + 64 * v + s;
+            for (int i = 0; i < 128 * 64 * call.E; ++i) wrong += seen.smem[at + i] != (call.E == 2 && i % 2 ? 0 : code);
+        }
+    printf("%s: gave up %u, bytes of another tile %d\n", what, seen.dead, wrong);
+    return seen.dead != 1 || wrong != 0;
+}
+
 int main(int argc, char** argv) {
     const char* mode = argc > 1 ? argv[1] : "";
     int bad = 1;
     if (!strcmp(mode, "agree")) bad = agree<1, 256>("groups") | agree<2, 192>("helpers") | agree<0, 32>("a warp");
+    if (!strcmp(mode, "fetch"))
+        bad = fetch_alone<TileCfg<ROPE_CACHE_BF16, 64, 64, 64>>("bf16") |
+              fetch_alone<TileCfg<ROPE_CACHE_FP8, 64, 64, 64>>("fp8");
     printf(bad ? "FAIL\n" : "ok\n");
     return bad;
 }
