@@ -50,9 +50,9 @@
 // threads of the groups have work.
 //   The fetching warp alone walks the division of the work (request, head, tiles);
 // it writes each run down in shared memory for the others.
-//   Every wait is bounded: a wait that gives up sets `dead`, later waits
-// return at once, and the rows of the run at hand come out as NaN (of later
-// runs nothing is written).
+//   Every wait is bounded, to about 1.5 s: a wait that gives up sets `dead`, later
+// waits return at once, the threads of a role leave together, fetches under way
+// are waited for, and every result that the block has a share in becomes NaN.
 //   Page sizes that are no multiple of 8 are left to rope_tree_narrow.cuh.
 #pragma once
 #include <cuda.h>
@@ -1024,7 +1024,6 @@ struct Tile {
                                            float l, float vref, bool patch, uint32_t lanes) const {
         if (!active) return;
         const int lane = row & 31;
-        if (sync->dead) l = NAN;
         const bool whole = x.slot < 0;
         OutAt to{nullptr, nullptr};
         float norm = C::kWide ? 1.0f : vref;
@@ -1091,7 +1090,6 @@ struct Tile {
             const float2 z = ml[k * R + r];
             sum += z.y * pow2(z.x - (t == -INFINITY ? 0.0f : t));
         }
-        if (sync->dead) sum = NAN;
         const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;  // a token that has seen no row gives zeros
         char* out = nullptr;
         float* part = nullptr;
@@ -1149,6 +1147,28 @@ struct Tile {
                 }
             }
             groups_sync();
+        }
+    }
+
+    // The block's results, when one of its waits has given up: NaN in all of them,
+    // those of the block's other runs too, and in its parts, whose joined results
+    // then are NaN.  By the 256 threads of the softmax groups, after all roles.
+    __device__ __noinline__ void give_up(const Place& place) const {
+        const int tid = int(threadIdx.x);
+        Walk walk = walk_from<C::ROWS, C::TN>(a, place);
+        RunAt x;
+        while (next_run<C::ROWS, C::TN>(a, walk, x)) {
+            const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
+            if (x.slot >= 0) {
+                for (int r = tid; r < C::ROWS; r += 256) a.part_ml[x.slot * C::ROWS + r] = make_float2(-INFINITY, NAN);
+                continue;
+            }
+            for (int i = tid; i < left * (C::DV / 2); i += 256) {
+                const int c = i % (C::DV / 2) * 2;
+                const OutAt to = out_at(a, x.rq.qs, x.h, first + i / (C::DV / 2));
+                if (c < a.Dv) *reinterpret_cast<uint32_t*>(to.out + c * 2) = 0x7fff7fffu;  // NaN of either type
+                if (c == 0 && to.lse) *to.lse = NAN;
+            }
         }
     }
 
@@ -1249,6 +1269,7 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     }
     tmem_before();
     __syncthreads();
+    if (warp < 8 && sync->dead) tile.give_up(place);
     if (warp == 12) {
         tmem_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sync->tmem));

@@ -6,6 +6,10 @@
 //           none does.
 //   fetch   the fetching warp with nobody to empty the rings: it gives up after
 //           about 1.5 s, and what it has fetched by then is left as it is.
+//   call    whole calls without the thread that issues the products, or without
+//           the softmax, in every second block: they end, and the results that
+//           those blocks had a share in are NaN, joined ones too; the others
+//           are right.
 //
 // Prints "ok ..." or what differed.
 #include <stdint.h>
@@ -249,6 +253,60 @@ static int fetch_alone(const char* what) {
     return seen.dead != 1 || wrong != 0;
 }
 
+// ---------------------------------------------------------------- call
+
+template <class C>
+struct NoProducts : Tile<C> {
+    __device__ void products() const {
+        if (blockIdx.x % 2 == 0) Tile<C>::products();
+    }
+};
+
+template <class C>
+struct NoSoftmax : Tile<C> {
+    __device__ void softmax(int w) const {
+        if (blockIdx.x % 2 == 0) Tile<C>::softmax(w);
+    }
+};
+
+// Queries are zeros, so a result is the mean of the values: whole where the
+// request's tiles are all in even blocks, and NaN where one is in an odd block.
+template <class T, class C>
+static int whole_calls(const char* what, bool fails) {
+    constexpr int R = 40, TILES = 7;
+    static Call<C, R, 128 * TILES> call;
+    if (call.template make<T>(true)) return 1;
+    // 8 units a block and 7 a request: some requests lie in one block, some in two
+    call.blocks = 36;
+    if (call.launch()) return 1;
+    static uint16_t out[R][64];
+    static float lse[R];
+    CHECK(cudaMemcpy(out, call.a.out, sizeof out, cudaMemcpyDeviceToHost));
+    CHECK(cudaMemcpy(lse, call.a.lse, sizeof lse, cudaMemcpyDeviceToHost));
+    const int chunk = (R * TILES + call.blocks - 1) / call.blocks;  // (so few units a block count no leads)
+    int wrong = 0, given_up = 0;
+    for (int r = 0; r < R; ++r) {
+        bool odd = false;
+        for (int u = r * TILES; u < (r + 1) * TILES; ++u) odd = odd || u / chunk % 2 == 1;
+        const bool none = odd && fails;
+        given_up += none;
+        wrong += none ? !(lse[r] != lse[r]) : !(lse[r] > 6.7 && lse[r] < 6.9);  // log 896
+        for (int c = 0; c < 64; ++c) {
+            const bool nan = C::BF16 ? (out[r][c] & 0x7fff) > 0x7f80 : (out[r][c] & 0x7fff) > 0x7c00;
+            wrong += nan != none;
+        }
+    }
+    printf("%s: %d of %d requests given up, %d numbers wrong\n", what, given_up, R, wrong);
+    return wrong != 0 || (fails && (given_up == 0 || given_up == R));
+}
+
+template <class C>
+static int whole_calls_of(const char* what) {
+    printf("%s\n", what);
+    return whole_calls<Tile<C>, C>("all roles", false) | whole_calls<NoProducts<C>, C>("without products", true) |
+           whole_calls<NoSoftmax<C>, C>("without softmax", true);
+}
+
 int main(int argc, char** argv) {
     const char* mode = argc > 1 ? argv[1] : "";
     int bad = 1;
@@ -256,6 +314,11 @@ int main(int argc, char** argv) {
     if (!strcmp(mode, "fetch"))
         bad = fetch_alone<TileCfg<ROPE_CACHE_BF16, 64, 64, 64>>("bf16") |
               fetch_alone<TileCfg<ROPE_CACHE_FP8, 64, 64, 64>>("fp8");
+    if (!strcmp(mode, "call"))
+        bad = whole_calls_of<TileCfg<ROPE_CACHE_BF16, 64, 64, 64>>("bf16") |
+              whole_calls_of<TileCfg<ROPE_CACHE_FP8, 64, 64, 64>>("fp8") |
+              whole_calls_of<TileCfg<ROPE_CACHE_BF16, 64, 64, 256>>("bf16, pairs") |
+              whole_calls_of<TileCfg<ROPE_CACHE_FP8, 64, 64, 256>>("fp8, pairs");
     printf(bad ? "FAIL\n" : "ok\n");
     return bad;
 }

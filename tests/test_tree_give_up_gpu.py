@@ -23,7 +23,7 @@ def program(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("mode", ["agree", "fetch"])
+@pytest.mark.parametrize("mode", ["agree", "fetch", "call"])
 def test_give_up(program, mode):
     r = subprocess.run([program, mode], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.endswith("ok\n"), r.stdout + r.stderr
