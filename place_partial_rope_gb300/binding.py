@@ -171,6 +171,14 @@ def _stream_handle(stream, device) -> int:
     return int(stream)
 
 
+def _stream_of(stream, device):
+    """The stream object of what a call takes as ``stream`` (not None)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 def _marshal(x: torch.Tensor, r1: torch.Tensor, r2: torch.Tensor, host: bool = False):
     if x.dim() != 4:
         raise RopeError(ROPE_ERR_INVALID, f"x must be 4-D (B, S, N, D), got {x.dim()}-D")
@@ -721,12 +729,13 @@ def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, 
         tp, words = tree.data_ptr(), tree.shape[1]
     if max_q is None:
         max_q = max(1, Tq)
-    if workspace is None:
+    if workspace is None and stream is None:
         workspace = tree_attention_workspace(q, cache, max_q)
-        if stream is not None:
-            # made on the current stream, used on another: the allocator must know
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream), device=dev))
+    elif workspace is None:
+        # made on the stream that uses it: memory that another stream's work frees
+        # is handed out again before that work has run
+        with torch.cuda.stream(_stream_of(stream, dev)):
+            workspace = tree_attention_workspace(q, cache, max_q)
     for t in (q, out, q_start, kv_len, page_table, lse, tree, workspace):
         if t is not None and t.device != dev:
             _refuse("every tensor must be on the cache's device")
