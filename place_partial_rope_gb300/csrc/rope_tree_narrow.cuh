@@ -13,7 +13,8 @@
 //   8-bit caches: s_j gets the key's scale after the product, and p_j the
 // value's before the rounding: p_j u_j / w with u_j the value's scale and w a
 // power of two that is at least the largest u so far (O is multiplied by
-// w_old / w_new, exactly, when it grows).  Codes become fp16 exactly, so the
+// w_old / w_new, exactly, when it grows), over the rows that the query row sees:
+// what the others hold has no effect on it.  Codes become fp16 exactly, so the
 // products are in fp16; q is brought to [-2, 2) by a power of two per row,
 // which fp16 holds at bf16's precision whatever q's range, and which goes
 // back into s.
@@ -284,7 +285,7 @@ struct Narrow {
 
         float mrow[2], lrow[2], qf[2], O[C::ND][4];
         int tok[2];
-        float vref = kLeastPower;
+        float vref[2] = {kLeastPower, kLeastPower};
         bool patch = false;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -400,32 +401,45 @@ struct Narrow {
                 lrow[b] = lrow[b] * shrink[b] + sum;
             }
 
-            // ---- 8-bit: weights times the values' scales over their power of two
+            // ---- 8-bit: weights times the values' scales over their power of two, which
+            // is the query row's own: of the rows that it sees
             if constexpr (!C::kWide) {
                 float2 u[C::NT];
-                float top = 0.0f;
+                float top[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int n = 0; n < C::NT; ++n) {
-                    u[n] = *reinterpret_cast<const float2*>(sv + jw + 8 * n + 2 * t);
-                    top = fmaxf(top, fmaxf(u[n].x, u[n].y));
+                for (int n = 0; n < C::NT; ++n) u[n] = *reinterpret_cast<const float2*>(sv + jw + 8 * n + 2 * t);
+                if (whole) {
+#pragma unroll
+                    for (int n = 0; n < C::NT; ++n) top[0] = fmaxf(top[0], fmaxf(u[n].x, u[n].y));
+                    top[1] = top[0];
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int n = 0; n < C::NT; ++n) {
+                            const uint32_t two = sees[b] >> (8 * n + 2 * t);
+                            top[b] = fmaxf(top[b], fmaxf(two & 1u ? u[n].x : 0.0f, two & 2u ? u[n].y : 0.0f));
+                        }
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if (top > vref) {
-                    const float w = power_above(top), f = vref / w;
-                    vref = w;
-                    moved = true;
-                    shrink[0] *= f;
-                    shrink[1] *= f;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], 1));
+                    top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], 2));
+                    if (top[b] > vref[b]) {
+                        const float w = power_above(top[b]), f = vref[b] / w;
+                        vref[b] = w;
+                        moved = true;
+                        shrink[b] *= f;
+                    }
                 }
-                const float back = one_over_power(vref);
+                const float back[2] = {one_over_power(vref[0]), one_over_power(vref[1])};
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float p = S[n][e];
                         // a row that is not seen adds nothing, whatever its scale
-                        S[n][e] = p == 0.0f ? 0.0f : p * (((e & 1) ? u[n].y : u[n].x) * back);
+                        S[n][e] = p == 0.0f ? 0.0f : p * (((e & 1) ? u[n].y : u[n].x) * back[e >> 1]);
                     }
             }
 
@@ -522,7 +536,7 @@ struct Narrow {
     }
 
     // Join the warps' m, l, O of each row and write the result or the part.
-    __device__ __forceinline__ void finish(int warp, float vref, const float* mrow, const float* lrow,
+    __device__ __forceinline__ void finish(int warp, const float* vref, const float* mrow, const float* lrow,
                                            float (*O)[4], bool patch) const {
         const int tid = int(threadIdx.x), lane = tid & 31, g = lane >> 2, t = lane & 3;
         float2* ml = reinterpret_cast<float2*>(smem + C::ML_AT);
@@ -542,7 +556,7 @@ struct Narrow {
 #pragma unroll
             for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, ml[w * C::ROWS + row].x);
             float f = pow2(mrow[b] - (top == -INFINITY ? 0.0f : top));
-            if constexpr (!C::kWide) f *= vref;
+            if constexpr (!C::kWide) f *= vref[b];
             float* to = part + warp * (C::ROWS * C::DV) + row;
 #pragma unroll
             for (int d = 0; d < C::ND; ++d)

@@ -5,6 +5,7 @@ import torch
 
 import serving_ref as ref
 from gpu_util import DEV
+from place_partial_rope_gb300 import binding
 from test_tree_gpu import Case
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +43,53 @@ def test_a_value_scale_and_a_score_that_grow_in_one_tile(G, d, store):
     c.rows = {"k": numbers(c.k, c.ks, store), "v": numbers(c.v, c.vs, store)}
     out, lse = c.run(scale=1.0)
     c.check(out, lse, scale=1.0)
+
+
+# tokens, query heads, lanes: the narrow kernel
+ROWS = [(6, 2, 128), (6, 1, 256), (15, 1, 64)]
+
+
+def one_row_apart(store, n, G, d, spoil):
+    """A call in which only token 3 sees row prefix + 3, whose bytes `spoil`
+    changes (page and place given); its results and those without the change."""
+    got = []
+    for spoilt in (True, False):
+        c = Case("bf16", store, [n], [n + 270], 1, G, d, d, page=16, seed=n + G)
+        # token i hangs on i - 1, but for token 3, which hangs on the context and has no children
+        c.words = binding.rope_partial_tree_mask([-1, 0, 1, -1] + [2 if i == 4 else i - 1 for i in range(4, n)]).numpy()
+        if spoilt:
+            spoil(c, *divmod(int(c.slots[0][270 + 3]), c.page))
+        got.append((c, *c.run()))
+    keep = [i for i in range(n) if i != 3]
+    (c, out, lse), (_, want, want_lse) = got
+    assert torch.isfinite(want).all() and torch.isfinite(want_lse).all()
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+    assert (lse[3] - want_lse[3]).abs().max() <= 1e-5  # the keys are as they were
+    return c, out
+
+
+@pytest.mark.parametrize("store", ["fp8", "int8"])
+@pytest.mark.parametrize("n,G,d", ROWS)
+@pytest.mark.parametrize("scale", [float("inf"), 1e30, 2.0 ** 60, 3e38])
+def test_a_value_scale_that_others_do_not_see(n, G, d, scale, store):
+    """An infinite or huge scale of a drafted row changes no token that does not
+    see the row; the one that does gets what the row says.  Its bound: a weight
+    is off by u of the largest product of weight and scale, so a result by u of
+    the largest sum over columns."""
+    def spoil(c, page, off):
+        c.vs[page, off] = scale
+        c.rows["v"] = numbers(c.v, c.vs, store)
+
+    c, out = one_row_apart(store, n, G, d, spoil)
+    if scale > 1e38:  # infinity, or numbers past bf16's range
+        assert not torch.isfinite(out[3]).all()
+        return
+    sees = ref.tree_sees(n, c.lens[0], 270, c.words)[3:4]
+    for h in range(G):
+        q = c.q[3:4, h].double().numpy()
+        k, v = (c.rows[x][c.slots[0], 0] for x in ("k", "v"))
+        o, _, mag = ref.tree_attention(q, k, v, sees, d ** -0.5)
+        big = d ** -0.5 * (abs(q) @ abs(k).T).max()
+        e = (d + 8) * 2.0 ** -24 * big + 2.0 ** -21
+        err = abs(out[3, h].double().cpu().numpy() - o[0])
+        assert (err <= (2.0 ** -11 + 4 * e) * mag.max() + 2.0 ** -8 * abs(o[0])).all()
