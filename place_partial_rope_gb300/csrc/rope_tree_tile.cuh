@@ -7,8 +7,8 @@
 // so p reaches 2^8 at most and the sums stay exact in fp32; O lives in tensor
 // memory, where rescaling it costs a read and a write of the whole
 // accumulator.  And the fp16 bias is 2^7, which leaves p below 2^15.  8-bit: O
-// and l are both kept in units of 1 / w (w the power of two above the values'
-// scales), so that a weight is 2^(s - m - log2 w) u, one product; w starts at
+// and l are both kept in units of 1 / w (w the power of two above the scales of the
+// values that the query row sees), so that a weight is 2^(s - m - log2 w) u, one product; w starts at
 // 2^-80.
 //
 // What bounds it.  128 x TN x (Dk + Dv) multiply-adds a tile against TN (Dk +
@@ -811,17 +811,22 @@ struct Tile {
         }
     }
 
-    // 32 scores in tensor memory: scaled (8-bit), and -inf where the bit is not set.
-    static __device__ __forceinline__ void mask32(uint32_t at, const float* scale, uint32_t bits) {
+    // 32 scores in tensor memory: scaled (8-bit), and -inf where the bit is not
+    // set.  Returns the largest of u and the values' scales (8-bit) whose bit is.
+    static __device__ __forceinline__ float mask32(uint32_t at, const float* scale, uint32_t bits, float u) {
         float s[32];
         tmem_ld32(s, at);
         tmem_wait_ld();
         tmem_here32(s);
         if constexpr (!C::kWide) scale32(s, scale);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (!(bits >> j & 1u)) s[j] = -INFINITY;
+        for (int j = 0; j < 32; ++j) {
+            const bool in = bits >> j & 1u;
+            if (!in) s[j] = -INFINITY;
+            if constexpr (!C::kWide) u = fmaxf(u, in ? scale[C::TN + j] : 0.0f);
+        }
         tmem_st32(at, reinterpret_cast<const uint32_t*>(s));
+        return u;
     }
 
     static __device__ __forceinline__ float max_of32(const float* s) {
@@ -919,23 +924,28 @@ struct Tile {
                 if (active) {
                     const bool part = j0 + C::TN > prefix;  // more than context rows
                     float shrink = 1.0f;  // what l and O are multiplied by
+                    float u = 0.0f;       // 8-bit: the largest scale of the values that the row sees
                     if constexpr (!C::kWide) {
                         // the scales came with the keys and the values
                         bar_wait(&sync->v_full[n % C::SLOTS], (n / C::SLOTS) & 1, sync);
                         __syncwarp();
-                        const float4 y = *reinterpret_cast<const float4*>(sc + 2 * C::TN);
-                        const float u = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-                        if (u > vref) {
-                            const float p = power_above(u);
-                            shrink = vref / p;
-                            vref = p;
+                        if (!part) {
+                            const float4 y = *reinterpret_cast<const float4*>(sc + 2 * C::TN);
+                            u = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
                         }
                     }
                     if (part) {
 #pragma unroll 1
                         for (int c = lo; c < lo + C::COLS; c += 32)
-                            mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c));
+                            u = mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c), u);
                         tmem_wait_st();
+                    }
+                    if constexpr (!C::kWide) {
+                        if (u > vref) {
+                            const float p = power_above(u);
+                            shrink = vref / p;
+                            vref = p;
+                        }
                     }
                     // s is held in registers by 16-bit rows, and by 8-bit pairs (whose rows
                     // have 64 lanes: 57 us against 62 for 2 requests of 131072 rows and
