@@ -108,6 +108,19 @@ __device__ __forceinline__ float value16(uint32_t x) {
     else return __half2float(__ushort_as_half(static_cast<unsigned short>(x)));
 }
 
+// Puts 0 in the place of e4m3 codes of NaN (0x7f and 0xff) in four words; not
+// zero when there were any.
+__device__ __forceinline__ uint32_t take_out_nan4(uint32_t* w) {
+    uint32_t found = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t m = ((w[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // the top bit of such bytes
+        w[j] &= ~((m >> 7) * 0xffu);
+        found |= m;
+    }
+    return found;
+}
+
 // The power of two of a query row's largest |q| (its bit pattern `most`),
 // kept within [2^-100, 2^100]; a row that is not finite needs none.
 __device__ __forceinline__ float row_power(uint32_t most) {
@@ -367,7 +380,8 @@ __device__ __forceinline__ uint32_t sees32(const TreeArgs& a, int qs, int i, int
     return in & (jj < 0 ? (bits << -jj) | ((1u << -jj) - 1u) : bits);
 }
 
-// A drafted row's values that are not finite (8-bit: whose scale is not) are
+// A drafted row's values that are not finite (8-bit: whose scale is not, or e4m3
+// codes of NaN) are
 // taken out of the product (a weight of 0 times infinity would reach the tokens that do not
 // see the row) and added here to the tokens that do see it, which end up not
 // finite in those columns whatever the weight: N columns from c of query row
@@ -393,8 +407,11 @@ __device__ __noinline__ void add_not_finite(const TreeArgs& a, const RunAt x, in
         } else {
             // a scale that is not finite makes the whole row so
             const float y = __ldg(a.vs + page * a.vs_st[0] + int64_t(off) * a.vs_st[1] + int64_t(x.h) * a.vs_st[2]);
-            if (!(fabsf(y) <= 3.4028234663852886e38f))
-                for (int k = 0; k < N; ++k) o[k] = NAN;
+            const bool whole = !(fabsf(y) <= 3.4028234663852886e38f);
+            const uint8_t* v = reinterpret_cast<const uint8_t*>(a.v + page * a.v_st[0] + int64_t(off) * a.v_st[1] +
+                                                                int64_t(x.h) * a.v_st[2]);
+            for (int k = 0; k < N && c + k < a.Dv; ++k)
+                if (whole || (STORE == ROPE_CACHE_FP8 && (__ldg(v + c + k) & 0x7f) == 0x7f)) o[k] = NAN;
         }
     }
 }

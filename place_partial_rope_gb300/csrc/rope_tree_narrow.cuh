@@ -131,6 +131,7 @@ struct Narrow {
     RunAt x;
 
     static constexpr bool BF16 = C::STORE == ROPE_CACHE_BF16;
+    static constexpr bool kMend = C::STORE != ROPE_CACHE_INT8;  // a value itself may be not finite
 
     // the page and offset of the tile's row `tid` (page -1: no such row)
     __device__ __forceinline__ int2 lookup(int tile) const {
@@ -450,7 +451,7 @@ struct Narrow {
                     for (int e = 0; e < 4; ++e) O[d][e] *= shrink[e >> 1];
             }
 
-            if constexpr (C::kWide) {
+            if constexpr (kMend) {
                 if (!whole && take_out_not_finite(ring + C::K_BYTES, prefix - tile * C::TN)) patch = true;
             }
 
@@ -511,17 +512,30 @@ struct Narrow {
         }
     }
 
-    // Puts zeros in the place of values that are not finite in the tile's rows
-    // from `from` on; whether there were any (see add_not_finite).
+    // Puts zeros in the place of values that are not finite (e4m3: of codes of NaN)
+    // in the tile's rows from `from` on; whether there were any (see add_not_finite).
     static __device__ __noinline__ bool take_out_not_finite(char* v, int from) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(v);
         bool found = false;
-        for (int i = max(from, 0) * (C::DV / 2) + int(threadIdx.x); i < C::TN * C::DV / 2; i += kNarrowThreads) {
-            const uint32_t y = w[i];
-            const bool lo = not_finite<C::STORE>(y & 0xffffu), hi = not_finite<C::STORE>(y >> 16);
-            if (lo || hi) {
-                found = true;
-                w[i] = (lo ? 0u : y & 0xffffu) | (hi ? 0u : y & 0xffff0000u);
+        if constexpr (C::kWide) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(v);
+            for (int i = max(from, 0) * (C::DV / 2) + int(threadIdx.x); i < C::TN * C::DV / 2; i += kNarrowThreads) {
+                const uint32_t y = w[i];
+                const bool lo = not_finite<C::STORE>(y & 0xffffu), hi = not_finite<C::STORE>(y >> 16);
+                if (lo || hi) {
+                    found = true;
+                    w[i] = (lo ? 0u : y & 0xffffu) | (hi ? 0u : y & 0xffff0000u);
+                }
+            }
+        } else {
+            constexpr int CH = C::DV / 16;
+            for (int i = max(from, 0) * CH + int(threadIdx.x); i < C::TN * CH; i += kNarrowThreads) {
+                const uint32_t at = smem_addr(v) + value_at<C>(i / CH, i % CH);
+                uint32_t w[4];
+                lds128(w, at);
+                if (take_out_nan4(w)) {
+                    found = true;
+                    sts128(at, w[0], w[1], w[2], w[3]);
+                }
             }
         }
         return __syncthreads_or(found);
@@ -582,7 +596,7 @@ struct Narrow {
             for (int w = 0; w < C::WARPS; ++w)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[k] += part[w * (C::ROWS * C::DV) + (c + k) * C::ROWS + row];
-            if constexpr (C::kWide) {
+            if constexpr (kMend) {
                 if (patch) add_not_finite<C::STORE, C::TN, 4>(a, x, at, c, o);
             }
             if (x.slot >= 0) {

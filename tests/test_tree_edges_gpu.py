@@ -95,3 +95,15 @@ def test_a_value_scale_that_others_do_not_see(n, G, d, scale, store):
         e = (d + 8) * 2.0 ** -24 * big + 2.0 ** -21
         err = abs(out[3, h].double().cpu().numpy() - o[0])
         assert (err <= (2.0 ** -11 + 4 * e) * mag.max() + 2.0 ** -8 * abs(o[0])).all()
+
+
+@pytest.mark.parametrize("n,G,d", ROWS)
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+def test_a_code_of_nan_that_others_do_not_see(n, G, d, code):
+    """e4m3 codes of NaN in a drafted row's values: the token that sees them gets
+    NaN in their columns, and nobody else does."""
+    def spoil_values(c, page, off):
+        c.v.view(torch.uint8)[page, off, :, 1::2] = code
+
+    _, out = one_row_apart("fp8", n, G, d, spoil_values)
+    assert torch.isnan(out[3, :, 1::2]).all() and torch.isfinite(out[3, :, 0::2]).all()
