@@ -335,7 +335,7 @@ rope_status_t tree_plan(const rope_kv_cache_t* c, int dtype, int64_t Hq, int64_t
     p->dtype = dtype;
     p->store = c->dtype;
     choose_tree(static_cast<int>(c->k_dim), static_cast<int>(c->v_dim), max_q * (Hq / c->heads),
-                c->page_size, tiles, p);
+                c->pages, c->page_size, tiles, p);
     return ROPE_OK;
 }
 
@@ -420,10 +420,11 @@ rope_status_t tree_attention(const rope_kv_cache_t* c, const void* q, int dtype,
                     (long long)workspace_bytes, (long long)need);
 
     TreeArgs a{};
-    a.k = static_cast<const char*>(c->k);
-    a.v = static_cast<const char*>(c->v);
-    a.ks = c->k_scale;
-    a.vs = c->v_scale;
+    // (no pages: no row is read, but the kernel forms an address all the same)
+    a.k = static_cast<const char*>(c->pages ? c->k : q);
+    a.v = static_cast<const char*>(c->pages ? c->v : q);
+    a.ks = c->pages ? c->k_scale : static_cast<const float*>(q);
+    a.vs = c->pages ? c->v_scale : static_cast<const float*>(q);
     for (int i = 0; i < 3; ++i) {
         a.k_st[i] = c->k_stride[i] * ce;
         a.v_st[i] = c->v_stride[i] * ce;

@@ -56,9 +56,9 @@ struct TreePlan {
     int rows;     // query rows of a tile: 16 (narrow kernel), 64, 128 or 256 (tile kernel)
 };
 
-// The kernel for rows of Dk and Dv, `rows` query rows a key head and pages of
-// `page_size` rows.
-void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, int64_t tiles, TreePlan* p);
+// The kernel for rows of Dk and Dv, `rows` query rows a key head and `pages` pages
+// of `page_size` rows, `tiles` cache tiles of which the page table has room for.
+void choose_tree(int Dk, int Dv, int64_t rows, int64_t pages, int64_t page_size, int64_t tiles, TreePlan* p);
 
 // The grid of a plan: the blocks that are resident on the device (sm_count
 // 0), or an upper bound of that for a device of sm_count SMs.

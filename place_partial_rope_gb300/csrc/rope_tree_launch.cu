@@ -159,15 +159,16 @@ rope_status_t launch(const void* f, dim3 grid, int threads, int smem, void** par
 //   and 330 against 263 and 367; fp8 rows of 192 + 128, 612 and 625.
 // Tensor copies take boxes of at least 8 rows of a page; pages that those do not
 // divide, and rows of more than 192 lanes (whose O does not fit tensor memory
-// twice), stay with the narrow kernel.
-void choose_tree(int Dk, int Dv, int64_t rows, int64_t page_size, int64_t tiles, TreePlan* p) {
+// twice), stay with the narrow kernel.  So does a cache without pages: a tensor
+// map has no dim of 0.
+void choose_tree(int Dk, int Dv, int64_t rows, int64_t pages, int64_t page_size, int64_t tiles, TreePlan* p) {
     constexpr int64_t kFewTiles = 8 * 152;
     if (Dk <= 64) p->dk = 64, p->dv = 64;
     else if (Dk <= 128) p->dk = 128, p->dv = 128;
     else if (Dk <= 192 && Dv <= 128) p->dk = 192, p->dv = 128;
     else p->dk = 256, p->dv = 256;
     const bool wide = p->store == ROPE_CACHE_BF16 || p->store == ROPE_CACHE_FP16;
-    if (p->dk == 256 || page_size % 8 || (rows <= 16 && (!wide || tiles <= kFewTiles)))
+    if (p->dk == 256 || pages == 0 || page_size % 8 || (rows <= 16 && (!wide || tiles <= kFewTiles)))
         p->rows = 16;
     else p->rows = rows <= 64 ? 64 : rows <= 128 || !(wide || p->dk == 64) ? 128 : 256;
 }

@@ -1,0 +1,31 @@
+"""The C ABI of include/rope_serving.h at the edges of what it takes, without a
+GPU (see test_serving_boundary.py)."""
+import ctypes
+
+import pytest
+
+from place_partial_rope_gb300 import binding
+from test_serving_boundary import OK, cache
+
+I64 = ctypes.c_int64
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load_library()
+
+
+def workspace(lib, c, dtype, Hq, max_q):
+    n = I64()
+    assert lib.rope_partial_tree_attention_workspace(ctypes.byref(c), dtype, Hq, max_q, 152, ctypes.byref(n)) == OK
+    return n.value
+
+
+@pytest.mark.parametrize("store", [0, 3, 4])
+def test_a_cache_without_pages_has_one_kernel(lib, store):
+    """The one for few query rows, whatever the hint: a tensor map, which the
+    others fetch through, cannot be empty."""
+    few = workspace(lib, cache(store=3), 0, 2, 1)  # 8-bit, up to 16 query rows a key head: that kernel
+    empty = cache(store=store, pages=0, k=None, v=None, k_scale=None, v_scale=None)
+    for max_q in (1, 60, 200):
+        assert workspace(lib, empty, 0, 2, max_q) == few

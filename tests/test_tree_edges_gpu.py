@@ -107,3 +107,26 @@ def test_a_code_of_nan_that_others_do_not_see(n, G, d, code):
 
     _, out = one_row_apart("fp8", n, G, d, spoil_values)
     assert torch.isnan(out[3, :, 1::2]).all() and torch.isfinite(out[3, :, 0::2]).all()
+
+
+@pytest.mark.parametrize("store", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,G", [(2, 2), (30, 1), (40, 4)])
+def test_a_cache_without_pages(n, G, store):
+    """No rows at all, and (every page number lying outside) rows of zeros."""
+    dtype = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn}[store]
+    k, v = (torch.empty((0, 16, 1, 64), dtype=dtype, device=DEV) for _ in range(2))
+    s = [torch.empty((0, 16, 1), device=DEV) if store == "fp8" else None for _ in range(2)]
+    cache = binding.KVCache(k, v, *s)
+    q = torch.randn((n, G, 64), device=DEV).to(torch.bfloat16)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    for length, width in ((0, 0), (0, 4), (n, 4)):
+        out, lse = torch.full_like(q, 7.0), torch.full((n, G), 7.0, device=DEV)
+        binding.rope_partial_tree_attention(q, cache, i32(0, n), i32(length),
+                                            torch.zeros((1, width), dtype=torch.int32, device=DEV), out, lse=lse)
+        torch.cuda.synchronize()
+        assert not out.any()
+        if length == 0:
+            assert torch.isneginf(lse).all()
+        else:  # a chain: token i sees i + 1 rows with a score of 0
+            want = torch.log(torch.arange(1, n + 1, device=DEV).double())[:, None].expand(n, G)
+            assert (lse.double() - want).abs().max() <= 2.0 ** -20
