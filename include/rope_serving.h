@@ -208,7 +208,7 @@ rope_status_t rope_partial_cache_read(const rope_kv_cache_t* cache, const int64_
  *   out          (Tq, Hq, v_dim) of `dtype`, strides out_stride; tokens
  *                outside every request are left as they are
  *   lse          (Tq, Hq) fp32, contiguous, or null
- *   scale        > 0 and finite
+ *   scale        > 0; times log2(e) a normal fp32 number
  *   workspace    at least rope_partial_tree_attention_workspace() bytes,
  *                16-byte aligned, for this call alone until it has run; its
  *                contents do not matter

@@ -2,6 +2,7 @@
 // for the paged cache and the attention over it: argument checks, the choice
 // of kernel and the launches.  No CUDA call is made for a rejected or empty
 // call.
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -368,8 +369,9 @@ rope_status_t tree_attention(const rope_kv_cache_t* c, const void* q, int dtype,
                     (long long)table_stride, (long long)max_pages);
     if (tree && (words < 1 || words > kInt / 64))
         return fail(ROPE_ERR_INVALID, "tree_words=%lld must be positive", (long long)words);
-    if (!(scale > 0.0) || !isfinite(scale))
-        return fail(ROPE_ERR_INVALID, "scale %g must be a finite number > 0", scale);
+    const float scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    if (!(scale > 0.0) || !isfinite(scale_log2) || scale_log2 < FLT_MIN)
+        return fail(ROPE_ERR_INVALID, "scale %g must be a number > 0 that fp32 holds (times log2(e))", scale);
     if (Tq == 0 || R == 0) return ROPE_OK;
     if (!q || !out || !q_stride || !out_stride || !q_start || !kv_len)
         return fail(ROPE_ERR_NULLPTR, "q, out, their strides, q_start or kv_len is null");
@@ -456,7 +458,7 @@ rope_status_t tree_attention(const rope_kv_cache_t* c, const void* q, int dtype,
     a.max_len = static_cast<int32_t>(max_pages * c->page_size);
     a.div_page = FastDiv::make(static_cast<uint32_t>(c->page_size));
     a.div_group = FastDiv::make(static_cast<uint32_t>(Hq / c->heads));
-    a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.bf16 = dtype == ROPE_BF16;
     if (launch_tree(p, a, workspace, blocks, stream, &err) != ROPE_OK)
         return fail(ROPE_ERR_CUDA, "%s", err);

@@ -130,6 +130,12 @@ __device__ __forceinline__ float row_power(uint32_t most) {
                                : min(max(e, uint32_t(27) << 23), uint32_t(227) << 23));
 }
 
+// What a score is multiplied by in base 2, kept a normal number: 0 times the -inf
+// of a row that is not seen, or infinity times a score of 0, would be NaN.
+__device__ __forceinline__ float row_factor(float p, float scale_log2) {
+    return fminf(fmaxf(p * scale_log2, 1.17549435e-38f), 3.40282347e+38f);
+}
+
 __device__ __forceinline__ float one_over_power(float p) {  // of a power of two
     return __uint_as_float(0x7f000000u - __float_as_uint(p));
 }

@@ -220,7 +220,7 @@ struct Narrow {
 #pragma unroll
             for (int d = PER / 2; d; d /= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
             const float p = row_power(most), down = one_over_power(p);
-            if (sub == 0) reinterpret_cast<float*>(smem + C::QF_AT)[row] = p * a.scale_log2;
+            if (sub == 0) reinterpret_cast<float*>(smem + C::QF_AT)[row] = row_factor(p, a.scale_log2);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int ch = sub + i * PER;

@@ -798,7 +798,7 @@ struct Tile {
                                              : __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
                     const float p = row_power(__float_as_uint(big));
                     down = one_over_power(p);
-                    if (sub == 0) factor[row] = p * a.scale_log2;
+                    if (sub == 0) factor[row] = row_factor(p, a.scale_log2);
                 }
                 const uint32_t to = smem_addr(smem) + (C::PAIR ? row / 128 * C::QTILE : 0) + row % 128 * 128 +
                                     ((sub ^ (row & 7)) << 4);

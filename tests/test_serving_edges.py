@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from place_partial_rope_gb300 import binding
-from test_serving_boundary import OK, cache
+from test_serving_boundary import INVALID, OK, attend, cache, message
 
 I64 = ctypes.c_int64
 
@@ -29,3 +29,12 @@ def test_a_cache_without_pages_has_one_kernel(lib, store):
     empty = cache(store=store, pages=0, k=None, v=None, k_scale=None, v_scale=None)
     for max_q in (1, 60, 200):
         assert workspace(lib, empty, 0, 2, max_q) == few
+
+
+@pytest.mark.parametrize("scale", [1e300, 1e39, 3.0e38, 1e-39, 1e-300])
+def test_a_scale_that_fp32_does_not_hold_is_refused(lib, scale):
+    """The kernels multiply by scale * log2(e) in fp32: infinity times a score of
+    0, or 0 times the -inf of a row that is not seen, would be NaN."""
+    assert attend(lib, cache(), scale=scale) == INVALID
+    assert "scale" in message(lib)
+    assert attend(lib, cache(), scale=scale, Tq=0) == INVALID

@@ -130,3 +130,27 @@ def test_a_cache_without_pages(n, G, store):
         else:  # a chain: token i sees i + 1 rows with a score of 0
             want = torch.log(torch.arange(1, n + 1, device=DEV).double())[:, None].expand(n, G)
             assert (lse.double() - want).abs().max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("store", ["bf16", "fp16", "fp8", "int8"])
+@pytest.mark.parametrize("n,G", [(2, 2), (30, 1), (40, 4)])
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -120])
+def test_scores_of_nearly_zero(n, G, scale, store):
+    """A scale so small that every score is 0 to fp32, with queries of zeros among
+    the others: the mean of the rows that a token sees."""
+    dtype = "fp16" if store == "fp16" else "bf16"
+    c = Case(dtype, store, [n], [n + 90], 1, G, 64, 64, page=16, seed=n)
+    c.q[0] = 0
+    c.check(*c.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("n,G", [(2, 2), (30, 1), (40, 4)])
+def test_large_scales_and_queries_of_zeros(n, G):
+    """8-bit: a query row's power of two times the scale stays a number."""
+    c = Case("bf16", "fp8", [n], [n + 90], 1, G, 64, 64, page=16, seed=n)
+    c.q[:] = 0
+    c.check(*c.run(scale=2.0 ** 100), scale=2.0 ** 100)
+    c.q[:, :, 0] = 2.0 ** 100  # scores past fp32, but the keys' lane is 0
+    c.k.view(torch.uint8)[..., 0] = 0
+    c.rows["k"][..., 0] = 0
+    c.check(*c.run(scale=2.0 ** 100), scale=2.0 ** 100)
