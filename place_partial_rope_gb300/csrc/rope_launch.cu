@@ -114,24 +114,29 @@ rope_status_t kernel_blocks_per_sm(const Plan& plan, int* blocks, const char** e
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, err);
     const int slot = (dev >= 0 && dev < kMaxDevices) ? dev : 0;
-    {
-        std::lock_guard<std::mutex> lk(g_occ_mu);
-        auto it = g_occ[slot].find(f);
-        if (it != g_occ[slot].end()) {
-            *blocks = it->second;
-            return ROPE_OK;
+    try {
+        {
+            std::lock_guard<std::mutex> lk(g_occ_mu);
+            auto it = g_occ[slot].find(f);
+            if (it != g_occ[slot].end()) {
+                *blocks = it->second;
+                return ROPE_OK;
+            }
         }
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, 0);
+        if (e != cudaSuccess) return cuda_fail(e, err);
+        if (n > kBlocksPerSmCap) n = kBlocksPerSmCap;
+        {
+            std::lock_guard<std::mutex> lk(g_occ_mu);
+            g_occ[slot][f] = n;
+        }
+        *blocks = n;
+        return ROPE_OK;
+    } catch (...) {  // the callers are C
+        *err = "out of host memory";
+        return ROPE_ERR_CUDA;
     }
-    int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, 0);
-    if (e != cudaSuccess) return cuda_fail(e, err);
-    if (n > kBlocksPerSmCap) n = kBlocksPerSmCap;
-    {
-        std::lock_guard<std::mutex> lk(g_occ_mu);
-        g_occ[slot][f] = n;
-    }
-    *blocks = n;
-    return ROPE_OK;
 }
 
 rope_status_t launch_piece(const Plan& plan, const KernelArgs& args, const FreqTable* freq,

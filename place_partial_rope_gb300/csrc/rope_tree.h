@@ -69,4 +69,24 @@ int64_t tree_workspace(const TreePlan& p, int blocks);
 rope_status_t launch_tree(const TreePlan& p, const TreeArgs& args, void* workspace, int blocks,
                           rope_stream_t stream, const char** err);
 
+// A plan's kernels, and what their launch needs.
+struct TreeKernel {
+    const void* main;
+    const void* join;
+    int smem, threads;
+    int tile;  // cache rows of a tile
+    float bias;
+    int regs;  // registers of a block that its warps share out among them; 0: they do not
+};
+
+// defined in rope_tree_*.cu (up to 16 query rows) and rope_tile_*.cu
+TreeKernel narrow_kernel_bf16(const TreePlan& p);
+TreeKernel narrow_kernel_fp16(const TreePlan& p);
+TreeKernel narrow_kernel_fp8(const TreePlan& p);
+TreeKernel narrow_kernel_int8(const TreePlan& p);
+TreeKernel tile_kernel_bf16(const TreePlan& p);
+TreeKernel tile_kernel_fp16(const TreePlan& p);
+TreeKernel tile_kernel_fp8(const TreePlan& p);
+TreeKernel tile_kernel_int8(const TreePlan& p);
+
 }  // namespace rope

@@ -586,23 +586,4 @@ __global__ void __launch_bounds__(kJoinThreads, 3) rope_tree_join_kernel(const _
     }
 }
 
-struct TreeKernel {
-    const void* main;
-    const void* join;
-    int smem, threads;
-    int tile;  // cache rows of a tile
-    float bias;
-    int regs;  // registers of a block that its warps share out among them; 0: they do not
-};
-
-// defined in rope_tree_*.cu (up to 16 query rows) and rope_tile_*.cu
-TreeKernel narrow_kernel_bf16(const TreePlan& p);
-TreeKernel narrow_kernel_fp16(const TreePlan& p);
-TreeKernel narrow_kernel_fp8(const TreePlan& p);
-TreeKernel narrow_kernel_int8(const TreePlan& p);
-TreeKernel tile_kernel_bf16(const TreePlan& p);
-TreeKernel tile_kernel_fp16(const TreePlan& p);
-TreeKernel tile_kernel_fp8(const TreePlan& p);
-TreeKernel tile_kernel_int8(const TreePlan& p);
-
 }  // namespace rope

@@ -36,24 +36,15 @@ rope_status_t cuda_fail(cudaError_t e, const char** err) {
     return ROPE_ERR_CUDA;
 }
 
-// The kernel's resident blocks on the current device; the first call for a
-// device and kernel also allows its shared memory.
-rope_status_t resident(const TreeKernel& k, Resident* out, const char** err) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, err);
-    if (dev < 0 || dev >= kMaxDevices) {
-        *err = "device number out of range";
-        return ROPE_ERR_CUDA;
-    }
-    std::lock_guard<std::mutex> lk(g_mu);
+// The kernel's resident blocks on device `dev`, under the lock.
+rope_status_t resident_on(int dev, const TreeKernel& k, Resident* out, const char** err) {
     auto it = g_resident[dev].find(k.main);
     if (it != g_resident[dev].end()) {
         *out = it->second;
         return ROPE_OK;
     }
     Resident r{};
-    e = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    cudaError_t e = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r.per_sm, k.main, k.threads, k.smem);
@@ -72,6 +63,25 @@ rope_status_t resident(const TreeKernel& k, Resident* out, const char** err) {
     g_resident[dev][k.main] = r;
     *out = r;
     return ROPE_OK;
+}
+
+// The kernel's resident blocks on the current device; the first call for a
+// device and kernel also allows its shared memory.
+rope_status_t resident(const TreeKernel& k, Resident* out, const char** err) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, err);
+    if (dev < 0 || dev >= kMaxDevices) {
+        *err = "device number out of range";
+        return ROPE_ERR_CUDA;
+    }
+    try {
+        std::lock_guard<std::mutex> lk(g_mu);
+        return resident_on(dev, k, out, err);
+    } catch (...) {  // the callers are C
+        *err = "out of host memory";
+        return ROPE_ERR_CUDA;
+    }
 }
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
