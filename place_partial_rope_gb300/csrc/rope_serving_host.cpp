@@ -99,18 +99,21 @@ bool in_cache(const rope_kv_cache_t* c, int64_t kb, int64_t vb, const void* p, i
            (c->v_scale && overlaps(p, n, c->v_scale, 4 * span(shape, c->v_scale_stride, 3, 1, 1)));
 }
 
-CacheSide side_of(const rope_kv_cache_t* c, bool values, void* rows, const int64_t* stride, int e) {
+// (The stride of a dim of one is not looked at by any call: 0 does for the kernels.)
+int64_t step(int64_t size, int64_t stride) { return size > 1 ? stride : 0; }
+
+CacheSide side_of(const rope_kv_cache_t* c, bool values, void* rows, int64_t T, const int64_t* stride, int e) {
     const int ce = code_size(c->dtype);
     const int64_t* st = values ? c->v_stride : c->k_stride;
     const int64_t* ss = values ? c->v_scale_stride : c->k_scale_stride;
     CacheSide s{};
     s.rows = static_cast<char*>(rows);
-    s.row_tok = stride[0] * e;
-    s.row_head = stride[1] * e;
+    s.row_tok = step(T, stride[0]) * e;
+    s.row_head = step(c->heads, stride[1]) * e;
     s.codes = static_cast<char*>(values ? c->v : c->k);
-    s.page = st[0] * ce;
-    s.tok = st[1] * ce;
-    s.head = st[2] * ce;
+    s.page = step(c->pages, st[0]) * ce;
+    s.tok = step(c->page_size, st[1]) * ce;
+    s.head = step(c->heads, st[2]) * ce;
     s.scale = values ? c->v_scale : c->k_scale;
     s.s_page = ss[0];
     s.s_tok = ss[1];
@@ -242,8 +245,8 @@ rope_status_t cache_write(const rope_kv_cache_t* c, const void* k, const void* v
     if (c->pages == 0) return ROPE_OK;  // every slot lies outside
 
     CacheArgs a{};
-    a.side[0] = side_of(c, false, const_cast<void*>(k), k_stride, e);
-    if (v) a.side[1] = side_of(c, true, const_cast<void*>(v), v_stride, e);
+    a.side[0] = side_of(c, false, const_cast<void*>(k), T, k_stride, e);
+    if (v) a.side[1] = side_of(c, true, const_cast<void*>(v), T, v_stride, e);
     a.slots = slots;
     a.start = static_cast<int32_t>(start);
     a.half = static_cast<int32_t>(L / 2);
@@ -254,8 +257,8 @@ rope_status_t cache_write(const rope_kv_cache_t* c, const void* k, const void* v
     if (L) {
         a.cos = static_cast<const char*>(cos);
         a.sin = static_cast<const char*>(sin);
-        a.cos_tok = cos_stride * e;
-        a.sin_tok = sin_stride * e;
+        a.cos_tok = step(T, cos_stride) * e;
+        a.sin_tok = step(T, sin_stride) * e;
         // 8-element accesses that lie wholly inside or outside the slice,
         // and whose half-split partners are whole accesses too
         plan.turn = start % 8 == 0 && (a.half_mode ? (L / 2) % 8 == 0 : L % 8 == 0) &&
@@ -300,8 +303,8 @@ rope_status_t cache_read(const rope_kv_cache_t* c, const int64_t* slots, int64_t
         return fail(ROPE_ERR_INVALID, "the outputs overlap each other, the slots or the cache");
 
     CacheArgs a{};
-    if (k) a.side[0] = side_of(c, false, k, k_stride, e);
-    if (v) a.side[1] = side_of(c, true, v, v_stride, e);
+    if (k) a.side[0] = side_of(c, false, k, T, k_stride, e);
+    if (v) a.side[1] = side_of(c, true, v, T, v_stride, e);
     a.slots = slots;
     CachePlan plan{};
     plan.dtype = dtype;
@@ -385,8 +388,11 @@ rope_status_t tree_attention(const rope_kv_cache_t* c, const void* q, int dtype,
         return fail(ROPE_ERR_INVALID, "strides of q and out must be >= 0, and keep the rows of out apart");
     bool ok = aligned(q, 16) && aligned(out, 16) && aligned(c->k, 16) && aligned(c->v, 16) &&
               aligned(workspace, 16);
-    for (int i = 0; i < 2; ++i) ok = ok && q_stride[i] * 2 % 16 == 0 && out_stride[i] * 2 % 16 == 0;
-    for (int i = 0; i < 3; ++i) ok = ok && c->k_stride[i] * ce % 16 == 0 && c->v_stride[i] * ce % 16 == 0;
+    const int64_t slots[3] = {c->pages, c->page_size, c->heads};
+    for (int i = 0; i < 2; ++i)
+        ok = ok && step(shape[i], q_stride[i]) * 2 % 16 == 0 && step(shape[i], out_stride[i]) * 2 % 16 == 0;
+    for (int i = 0; i < 3; ++i)
+        ok = ok && step(slots[i], c->k_stride[i]) * ce % 16 == 0 && step(slots[i], c->v_stride[i]) * ce % 16 == 0;
     if (!ok)
         return fail(ROPE_ERR_INVALID, "the rows of q, out and the cache and the workspace must start "
                     "on 16-byte boundaries");
@@ -428,8 +434,8 @@ rope_status_t tree_attention(const rope_kv_cache_t* c, const void* q, int dtype,
     a.ks = c->pages ? c->k_scale : static_cast<const float*>(q);
     a.vs = c->pages ? c->v_scale : static_cast<const float*>(q);
     for (int i = 0; i < 3; ++i) {
-        a.k_st[i] = c->k_stride[i] * ce;
-        a.v_st[i] = c->v_stride[i] * ce;
+        a.k_st[i] = step(slots[i], c->k_stride[i]) * ce;
+        a.v_st[i] = step(slots[i], c->v_stride[i]) * ce;
         a.ks_st[i] = c->k_scale_stride[i];
         a.vs_st[i] = c->v_scale_stride[i];
     }
@@ -437,8 +443,8 @@ rope_status_t tree_attention(const rope_kv_cache_t* c, const void* q, int dtype,
     a.out = static_cast<char*>(out);
     a.lse = lse;
     for (int i = 0; i < 2; ++i) {
-        a.q_st[i] = q_stride[i] * 2;
-        a.o_st[i] = out_stride[i] * 2;
+        a.q_st[i] = step(shape[i], q_stride[i]) * 2;
+        a.o_st[i] = step(shape[i], out_stride[i]) * 2;
     }
     a.q_start = q_start;
     a.kv_len = kv_len;

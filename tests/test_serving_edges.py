@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from place_partial_rope_gb300 import binding
-from test_serving_boundary import INVALID, OK, attend, cache, message
+from test_serving_boundary import INVALID, OK, attend, cache, i64, message
 
 I64 = ctypes.c_int64
 
@@ -38,3 +38,26 @@ def test_a_scale_that_fp32_does_not_hold_is_refused(lib, scale):
     assert attend(lib, cache(), scale=scale) == INVALID
     assert "scale" in message(lib)
     assert attend(lib, cache(), scale=scale, Tq=0) == INVALID
+
+
+ONE = [  # a dim of one, with a stride that would break the 16-byte rule
+    (dict(), dict(Tq=1, qst=(257, 64))),
+    (dict(), dict(Tq=1, ost=(257, 64))),
+    (dict(heads=1), dict(Hq=1, Tq=4, qst=(64, 3), ost=(64, 3))),
+    (dict(heads=1, k_stride=i64(1024, 64, 1)), dict()),
+    (dict(pages=1, v_stride=i64(7, 128, 64)), dict()),
+    (dict(page=1, k_stride=i64(128, 9, 64)), dict()),
+]
+
+
+@pytest.mark.parametrize("c,kw", ONE)
+def test_the_stride_of_a_dim_of_one_does_not_count(lib, c, kw):
+    """(With a workspace of no bytes, so that nothing is launched anywhere.)"""
+    assert attend(lib, cache(**c), nbytes=0, **kw) != OK
+    assert "16-byte" not in message(lib)
+
+
+@pytest.mark.parametrize("c,kw", [(dict(), dict(qst=(257, 64))), (dict(k_stride=i64(1031, 64, 64)), dict())])
+def test_the_stride_of_other_dims_does(lib, c, kw):
+    assert attend(lib, cache(heads=1, **c), nbytes=0, Hq=1, **kw) == INVALID
+    assert "16-byte" in message(lib)

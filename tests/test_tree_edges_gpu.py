@@ -154,3 +154,35 @@ def test_large_scales_and_queries_of_zeros(n, G):
     c.k.view(torch.uint8)[..., 0] = 0
     c.rows["k"][..., 0] = 0
     c.check(*c.run(scale=2.0 ** 100), scale=2.0 ** 100)
+
+
+@pytest.mark.parametrize("store", ["bf16", "fp8"])
+@pytest.mark.parametrize("G", [2, 40])
+def test_strides_of_dims_of_one(G, store):
+    """One token, one key head and one page, whose strides are no multiples of
+    anything: results, and rows written and read, as with the usual ones."""
+    c = Case("bf16", store, [1], [60], 1, G, 64, 64, page=64, tree=None, seed=G, spare=0)
+    want, _ = c.run()
+
+    def odd(t, dims):
+        st = [101 + 2 * i if i in dims else s for i, s in enumerate(t.stride())]
+        return t.as_strided(t.shape, st)
+
+    q, qs, ln, table, _ = c.device()
+    k, v = odd(c.k, (0, 2)), odd(c.v, (0, 2))
+    ks, vs = (None, None) if c.ks is None else (odd(c.ks, (0, 2)), odd(c.vs, (0, 2)))
+    cache = binding.KVCache(k, v, ks, vs)
+    out = torch.empty((1, G, 64), dtype=torch.bfloat16, device=DEV)
+    binding.rope_partial_tree_attention(odd(q, (0,)), cache, qs, ln, table, odd(out, (0,)), max_q=1)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    slot = torch.tensor([61], device=DEV)
+    rows = [torch.randn((1, 1, 64), device=DEV).to(torch.bfloat16) for _ in range(2)]
+    binding.rope_partial_cache_write(cache, odd(rows[0], (0, 1)), odd(rows[1], (0, 1)), slot)
+    a, b = ([torch.empty_like(r) for r in rows] for _ in range(2))
+    binding.rope_partial_cache_read(cache, slot, odd(a[0], (0, 1)), odd(a[1], (0, 1)))
+    binding.rope_partial_cache_read(c.cache, slot, *b)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for x, y in zip(a, rows):
+        assert (x.double() - y.double()).abs().max() <= 2.0 ** -4 * y.abs().max()
