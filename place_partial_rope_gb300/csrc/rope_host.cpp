@@ -562,6 +562,15 @@ rope_status_t run_qk(int dir, void* q, void* k, const void* r1, const void* r2, 
     return launch_all(dir, kInterleave, dtype, seg, nseg, r1, r2, Rq.empty ? Rk : Rq, B, S, stream);
 }
 
+// base^(-i/of) as two fp32 parts.  By pow() for every pair: products of a power and
+// a ratio, which are cheaper, differ from it in the last bit of `lo` for a quarter of
+// the pairs, and far positions show it.
+void frequency(double base, int64_t i, int64_t of, float* hi, float* lo) {
+    const double w = pow(base, -double(i) / double(of));
+    *hi = static_cast<float>(w);
+    *lo = static_cast<float>(w - static_cast<double>(*hi));
+}
+
 // The positions call: cos/sin of theta_k = p * base^(-2k/L) computed in
 // the kernel from one int32 position per (b, s).
 rope_status_t run_pos(int dir, void* x, const int32_t* positions, int dtype, int64_t B, int64_t S,
@@ -601,11 +610,7 @@ rope_status_t run_pos(int dir, void* x, const int32_t* positions, int dtype, int
     pc.pos = positions;
     pc.pos_b = ps[0];
     pc.pos_s = ps[1];
-    for (int64_t k = 0; k < L / 2; ++k) {
-        const double w = pow(base, -2.0 * double(k) / double(L));
-        pc.freq.hi[k] = static_cast<float>(w);
-        pc.freq.lo[k] = static_cast<float>(w - static_cast<double>(pc.freq.hi[k]));
-    }
+    for (int64_t k = 0; k < L / 2; ++k) frequency(base, k, L / 2, &pc.freq.hi[k], &pc.freq.lo[k]);
     const Seg seg{x, N, D, start};
     return launch_all(dir, mode, dtype, &seg, 1, nullptr, nullptr, R, B, S, stream, &pc);
 }
@@ -676,7 +681,6 @@ rope_status_t run_axes(int dir, void* x, const int32_t* positions, int dtype, in
     table.pos_a = ps[0];
     table.axes = axes;
     int32_t dealt[ROPE_MAX_AXES] = {0, 0, 0, 0};
-    double power[ROPE_MAX_AXES] = {}, ratio[ROPE_MAX_AXES] = {};
     int a = 0;
     const int64_t pairs = L / 2;
     for (int64_t k = 0; k < pairs; ++k) {
@@ -685,16 +689,8 @@ rope_status_t run_axes(int dir, void* x, const int32_t* positions, int dtype, in
         while (dealt[a] == sections[a]) a = a + 1 == axes ? 0 : a + 1;
         const int32_t j = dealt[a]++;
         table.axis[k] = static_cast<uint8_t>(a);
-        // base^(-i/of) by pow() at every 16th i, by products between (each adds
-        // half an ulp of double; two fp32 parts keep 48 bits)
-        const int64_t i = spectrum == ROPE_SPECTRUM_SHARED ? k : j;
-        const double of = spectrum == ROPE_SPECTRUM_SHARED ? double(pairs) : double(sections[a]);
-        const int c = spectrum == ROPE_SPECTRUM_SHARED ? 0 : a;
-        if (i == 0) ratio[c] = pow(base, -1.0 / of);
-        power[c] = i % 16 == 0 ? (i == 0 ? 1.0 : pow(base, -double(i) / of)) : power[c] * ratio[c];
-        const double w = power[c];
-        table.hi[k] = static_cast<float>(w);
-        table.lo[k] = static_cast<float>(w - static_cast<double>(table.hi[k]));
+        if (spectrum == ROPE_SPECTRUM_SHARED) frequency(base, k, pairs, &table.hi[k], &table.lo[k]);
+        else frequency(base, j, sections[a], &table.hi[k], &table.lo[k]);
         if (order == ROPE_AXES_INTERLEAVED) a = a + 1 == axes ? 0 : a + 1;
     }
 
