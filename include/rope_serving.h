@@ -222,7 +222,7 @@ rope_status_t rope_partial_cache_read(const rope_kv_cache_t* cache, const int64_
  * of 8 rows, and up to 192 + 128 lanes, are the fast case: others read the
  * cache once for each 16 query rows of a key head.  A call captured in a graph
  * may be replayed with other contents of the device arrays.  Waits inside the
- * kernels are bounded: should one run out (1.5 s; the device is at fault), the
+ * kernels are bounded: should nothing move for seconds (the device is at fault), the
  * results that depend on it are NaN, and the call ends.
  */
 rope_status_t rope_partial_tree_attention(const rope_kv_cache_t* cache, const void* q,

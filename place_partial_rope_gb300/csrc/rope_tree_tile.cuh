@@ -50,7 +50,7 @@
 // threads of the groups have work.
 //   The fetching warp alone walks the division of the work (request, head, tiles);
 // it writes each run down in shared memory for the others.
-//   Every wait is bounded, to about 1.5 s: a wait that gives up sets `dead`, later
+//   Every wait is bounded, to some seconds: one that gives up sets `dead`, later
 // waits return at once, the threads of a role leave together, fetches under way
 // are waited for, and every result that the block has a share in becomes NaN.
 //   Page sizes that are no multiple of 8 are left to rope_tree_narrow.cuh.
@@ -99,12 +99,13 @@ struct TileCfg {
     static constexpr int SMEM = MISC_AT + MISC;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f;
     static constexpr float kLag = 8.0f;
-    static_assert(SYNC_AT + 896 <= SMEM, "TileSync");
+    static constexpr int kSyncMax = 896;
+    static_assert(SYNC_AT + kSyncMax <= SMEM, "TileSync");
     static_assert(fit(SLOTS), "two tiles fit");
 };
 
-constexpr uint32_t kSpins = 1u << 20;  // tries of one wait before it gives up
-constexpr uint32_t kPolls = 1u << 26;  // looks of the issuing thread, which does not pause
+constexpr uint32_t kSpins = 1u << 20;  // tries of one wait before it gives up: 1.5 s and more
+constexpr uint32_t kPolls = 1u << 26;  // looks of a thread that does not pause
 
 struct TileSync {
     unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
@@ -116,8 +117,10 @@ struct TileSync {
     volatile uint32_t patch[8];  // of run r at r % 8: values were taken out
     volatile uint32_t runs;      // runs that are in `run`, and
     volatile uint32_t last;      // how many there will be (~0: not known yet)
+    volatile uint32_t beat;      // 16-bit: tiles fetched
     RunAt run[8];                // run r at r % 8: the fetching warp, which is ahead, writes them for the others
 };
+static_assert(sizeof(TileSync) <= TileCfg<ROPE_CACHE_FP8, 64, 64, 64>::kSyncMax, "its place in shared memory");
 
 __device__ __forceinline__ void bar_init(unsigned long long* b, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
@@ -150,6 +153,22 @@ __device__ __forceinline__ void bar_wait(unsigned long long* b, uint32_t parity,
     for (uint32_t i = 0; i < kSpins; ++i) {
         if (bar_test(b, parity)) return;
         if (s->dead) return;
+    }
+    s->dead = 1;
+}
+
+// For those that may rightly wait for the whole of a run (16-bit helpers, whose
+// tiles are its last; 7 s for 2^29 rows and 256 query rows): gives up when no
+// tile has been fetched between two such stretches.
+__device__ __forceinline__ void bar_wait_run(unsigned long long* b, uint32_t parity, TileSync* s) {
+    for (uint32_t seen = ~0u;;) {
+        for (uint32_t i = 0; i < kSpins; ++i) {
+            if (bar_test(b, parity)) return;
+            if (s->dead) return;
+        }
+        const uint32_t now = s->beat;
+        if (now == seen) break;
+        seen = now;
     }
     s->dead = 1;
 }
@@ -360,15 +379,22 @@ struct Tile {
         __syncwarp();
     }
 
-    // Run r, when the block has one.
+    // Run r, when the block has one.  IDLE: of a role that may wait for a whole run
+    // (see bar_wait_run).
+    template <bool IDLE = false>
     __device__ __forceinline__ bool take(uint32_t r, RunAt& x) const {
-        for (uint32_t i = 0; i < kPolls; ++i) {
-            if (sync->runs > r) {
-                __threadfence_block();
-                x = sync->run[r & 7];
-                return true;
+        for (uint32_t seen = ~0u;;) {
+            for (uint32_t i = 0; i < kPolls; ++i) {
+                if (sync->runs > r) {
+                    __threadfence_block();
+                    x = sync->run[r & 7];
+                    return true;
+                }
+                if (sync->last <= r || sync->dead) return false;
             }
-            if (sync->last <= r || sync->dead) return false;
+            const uint32_t now = sync->beat;
+            if (!IDLE || now == seen) break;
+            seen = now;
         }
         sync->dead = 1;
         return false;
@@ -378,9 +404,9 @@ struct Tile {
     // lanes of a warp: all of them go on or none does.  Where a wait gives up just
     // as a run is written down, one thread may find the run and the next one
     // `dead`; a barrier that some do not reach would be waited for without end.
-    template <int ID, int N = 32>
+    template <int ID, int N = 32, bool IDLE = false>
     __device__ __forceinline__ bool take_all(uint32_t r, RunAt& x) const {
-        const bool mine = take(r, x);
+        const bool mine = take<IDLE>(r, x);
         if constexpr (ID == 0) return __all_sync(0xffffffffu, mine);
         __syncwarp();
         uint32_t all;
@@ -446,6 +472,7 @@ struct Tile {
                 }
                 fetch(values ? vm : km, values ? C::DV : C::DK, now, h, to, lane, bar);
             }
+            if (C::kWide && lane == 0) sync->beat = n;
             ++it;
             if (last && on) {
                 more = next_run<C::ROWS, C::TN>(a, walk, step);
@@ -628,13 +655,13 @@ struct Tile {
         constexpr uint32_t SLOTS = C::SLOTS;
         RunAt x;
         uint32_t n = 0, run = 0, par = 0;  // a parity bit for each slot
-        while (take_all<2, kHelpers>(run, x)) {
+        while (take_all<2, kHelpers, true>(run, x)) {
             const int prefix = x.rq.len - x.rq.n;
             for (int it = 0; it < x.count; ++it, ++n) {
                 const int j0 = (x.t0 + it) * C::TN;
                 if (j0 + C::TN <= prefix) continue;
                 const uint32_t slot = n % SLOTS;
-                bar_wait(&sync->fix_full[slot], (par >> slot) & 1, sync);
+                bar_wait_run(&sync->fix_full[slot], (par >> slot) & 1, sync);
                 par ^= 1u << slot;
                 const uint32_t to = smem_addr(smem + C::V_AT) + slot * C::V_SLOT;
                 const int from = max(prefix - j0, 0), valid = x.rq.len - j0;
@@ -1266,6 +1293,7 @@ rope_tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         for (int i = 0; i < 8; ++i) sync->patch[i] = 0;
         sync->runs = 0;
         sync->last = ~0u;
+        sync->beat = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 12) {

@@ -5,7 +5,7 @@
 //           run is written down at about the same time: all of them take it or
 //           none does.
 //   fetch   the fetching warp with nobody to empty the rings: it gives up after
-//           about 1.5 s, and what it has fetched by then is left as it is.
+//           some seconds, and what it has fetched by then is left as it is.
 //   call    whole calls without the thread that issues the products, or without
 //           the softmax, in every second block: they end, and the results that
 //           those blocks had a share in are NaN, joined ones too; the others
@@ -75,6 +75,7 @@ __global__ void agree_kernel(const TreeArgs a, int rounds, unsigned* took, unsig
             sync.dead = 0;
             sync.runs = 0;
             sync.last = ~0u;
+            sync.beat = 0;
         }
         __syncthreads();
         if (tid < 256) {

@@ -186,3 +186,26 @@ def test_strides_of_dims_of_one(G, store):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     for x, y in zip(a, rows):
         assert (x.double() - y.double()).abs().max() <= 2.0 ** -4 * y.abs().max()
+
+
+def test_a_call_of_seconds():
+    """A run of a block that takes longer than any wait inside the kernel may
+    stand still: 152 tokens of 256 heads over 2^29 rows (one page, over and over).
+    The bound is loose: 2^22 fp32 sums of one thread follow each other, each rounded
+    by up to 2^-24 of the sum, so l and O are within a quarter."""
+    n, G, page = 152, 256, 4096
+    length = 2 ** 29
+    dtype = torch.bfloat16
+    g = torch.Generator().manual_seed(0)
+    k, v = (torch.randn((1, page, 1, 64), generator=g).to(torch.float16).to(DEV) for _ in range(2))
+    cache = binding.KVCache(k.to(dtype), v.to(dtype))
+    q = (torch.randn((n, G, 64), generator=g) / 8).to(DEV, torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty((n, G), device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    table = torch.zeros((1, length // page), dtype=torch.int32, device=DEV)
+    binding.rope_partial_tree_attention(q, cache, i32(0, n), i32(length), table, out, lse=lse, scale=1.0)
+    torch.cuda.synchronize()
+    kk, vv = (t.to(dtype).to(torch.float16).double()[0, :, 0] for t in (k, v))
+    s = q.double() @ kk.T
+    assert (lse.double() - torch.logsumexp(s, -1) - np.log(length / page)).abs().max() <= -np.log(0.75)
+    assert (out.double() - s.softmax(-1) @ vv).abs().max() <= 0.5 / 0.75 * vv.abs().max()
