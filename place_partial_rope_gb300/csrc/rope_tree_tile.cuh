@@ -860,21 +860,27 @@ struct Tile {
         }
     }
 
-    // 32 scores in tensor memory: scaled (8-bit), and -inf where the bit is not
-    // set.  Returns the largest of u and the values' scales (8-bit) whose bit is.
-    static __device__ __forceinline__ float mask32(uint32_t at, const float* scale, uint32_t bits, float u) {
+    // 32 scores in tensor memory: scaled (8-bit), and -inf where the bit is not set.
+    static __device__ __forceinline__ void mask32(uint32_t at, const float* scale, uint32_t bits) {
         float s[32];
         tmem_ld32(s, at);
         tmem_wait_ld();
         tmem_here32(s);
         if constexpr (!C::kWide) scale32(s, scale);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const bool in = bits >> j & 1u;
-            if (!in) s[j] = -INFINITY;
-            if constexpr (!C::kWide) u = fmaxf(u, in ? scale[C::TN + j] : 0.0f);
-        }
+        for (int j = 0; j < 32; ++j)
+            if (!(bits >> j & 1u)) s[j] = -INFINITY;
         tmem_st32(at, reinterpret_cast<const uint32_t*>(s));
+    }
+
+    // The largest of 32 scales whose bit is set, and of u.
+    static __device__ __noinline__ float largest_seen(const float* scale, uint32_t bits, float u) {
+#pragma unroll 1
+        for (int j = 0; j < 32; j += 4, bits >>= 4) {
+            const float4 y = *reinterpret_cast<const float4*>(scale + j);
+            u = fmaxf(fmaxf(fmaxf(u, bits & 1u ? y.x : 0.0f), bits & 2u ? y.y : 0.0f),
+                      fmaxf(bits & 4u ? y.z : 0.0f, bits & 8u ? y.w : 0.0f));
+        }
         return u;
     }
 
@@ -985,8 +991,11 @@ struct Tile {
                     }
                     if (part) {
 #pragma unroll 1
-                        for (int c = lo; c < lo + C::COLS; c += 32)
-                            u = mask32(lanes + s_col(w) + c, sc + c, sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c), u);
+                        for (int c = lo; c < lo + C::COLS; c += 32) {
+                            const uint32_t bits = sees32(a, x.rq.qs, tok, prefix, x.rq.len, j0 + c);
+                            mask32(lanes + s_col(w) + c, sc + c, bits);
+                            if constexpr (!C::kWide) u = largest_seen(sc + C::TN + c, bits, u);
+                        }
                         tmem_wait_st();
                     }
                     if constexpr (!C::kWide) {
