@@ -132,31 +132,49 @@ bool wide(const rope_kv_cache_t* c, const CacheSide& s, int n) {
     return ok;
 }
 
-// A tensor of (tokens, heads) rows: the bytes of one token, the bytes between
-// tokens and the bytes spanned in all.
+// A tensor of (tokens, heads) rows: the bytes of a row, of a token's rows and of
+// all, and the bytes between heads and between tokens (0: there is one).
 struct Rows {
     const void* p;
-    int64_t one, step, all;
+    int64_t row, one, all, head, step;
 };
 
 Rows rows_of(const void* p, int64_t tokens, int64_t heads, const int64_t* stride, int64_t row, int e) {
-    if (!p) return Rows{nullptr, 0, 0, 0};
-    const int64_t one = (row + (heads > 1 ? (heads - 1) * stride[1] : 0)) * e;
-    return Rows{p, one, tokens > 1 ? stride[0] * e : 0,
-                one + (tokens > 1 ? (tokens - 1) * stride[0] * e : 0)};
+    if (!p) return Rows{};
+    const int64_t h = step(heads, stride[1]) * e, t = step(tokens, stride[0]) * e;
+    const int64_t one = row * e + (heads - 1) * h;
+    return Rows{p, row * e, one, one + (tokens - 1) * t, h, t};
+}
+
+// The bytes from a to the first of the places b + k * step that is not before it.
+int64_t behind(const void* a, const void* b, int64_t step) {
+    const uint64_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return pb >= pa ? int64_t((pb - pa) % uint64_t(step)) : int64_t((step - int64_t((pa - pb) % uint64_t(step))) % step);
+}
+
+// Whether na bytes from 0 and nb bytes from `gap`, each repeated every `step`
+// bytes, never meet.
+bool apart(int64_t na, int64_t gap, int64_t nb, int64_t step) {
+    return na <= step && nb <= step && gap % step >= na && gap % step + nb <= step;
 }
 
 // Whether two such tensors may share a byte.  Slices of one packed tensor
-// (queries beside results, keys beside values) lie between each other: with
-// one token step, they are apart when their bytes within a step are.
+// (queries beside results, keys beside values) lie between each other.  With one
+// step between tokens, they are apart when their bytes within it are.  With one
+// step between heads also when their rows within that are, if a head of one token
+// cannot meet a head of another: there is one token, the tokens' step is a multiple
+// of the heads', or both tensors' tokens lie in the same steps.
 bool rows_overlap(const Rows& a, const Rows& b) {
     if (!a.p || !b.p || !overlaps(a.p, a.all, b.p, b.all)) return false;
-    const int64_t step = a.step ? a.step : b.step;
-    if (step <= 0 || (a.step && b.step && a.step != b.step) || a.one > step || b.one > step) return true;
-    const uint64_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
-    const int64_t gap = pb >= pa ? int64_t((pb - pa) % uint64_t(step))
-                                 : int64_t((step - int64_t((pa - pb) % uint64_t(step))) % step);
-    return gap < a.one || gap + b.one > step;
+    if ((a.step && b.step && a.step != b.step) || (a.head && b.head && a.head != b.head)) return true;
+    const int64_t step = a.step ? a.step : b.step, head = a.head ? a.head : b.head;
+    const int64_t ab = step ? behind(a.p, b.p, step) : 0, ba = step ? behind(b.p, a.p, step) : 0;
+    if (step && apart(a.one, ab, b.one, step)) return false;
+    if (!head) return true;
+    if (step == 0 || step % head == 0) return !apart(a.row, behind(a.p, b.p, head), b.row, head);
+    if (a.one > step || b.one > step) return true;
+    if (ab + b.one <= step) return !apart(a.row, ab, b.row, head);
+    return ba + a.one > step || !apart(b.row, ba, a.row, head);
 }
 
 // What write and read have in common: T rows a token, split into launches
