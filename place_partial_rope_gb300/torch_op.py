@@ -136,26 +136,34 @@ def register() -> None:
     _lib = lib
 
 
+def _op(name: str, back: bool):
+    """The operator of that name, or the one of its backward."""
+    return getattr(getattr(torch.ops, NAMESPACE), name + "_backward" if back else name)
+
+
 class InplacePartialRotaryMulFn(torch.autograd.Function):
-    """Autograd for the in-place rotation: r1 and r2 get no gradient."""
+    """Autograd for the in-place rotation, or (``back``) its transpose, which is
+    its gradient as it is the transpose's: r1 and r2 get no gradient."""
 
     @staticmethod
-    def forward(ctx, x, r1, r2, rotary_mode, partial_slice):
-        getattr(torch.ops, NAMESPACE).inplace_partial_rotary_mul(
-            x, r1, r2, rotary_mode=rotary_mode, partial_slice=list(partial_slice))
+    def forward(ctx, x, r1, r2, rotary_mode, partial_slice, back=False):
+        _op(_FWD, back)(x, r1, r2, rotary_mode=rotary_mode, partial_slice=list(partial_slice))
         ctx.mark_dirty(x)
         ctx.save_for_backward(r1, r2)
         ctx.rotary_mode = rotary_mode
         ctx.partial_slice = list(partial_slice)
+        ctx.back = back
         return x
 
     @staticmethod
     def backward(ctx, grad):
         r1, r2 = ctx.saved_tensors
         g = grad.clone(memory_format=torch.contiguous_format)
-        getattr(torch.ops, NAMESPACE).inplace_partial_rotary_mul_backward(
-            g, r1, r2, rotary_mode=ctx.rotary_mode, partial_slice=ctx.partial_slice)
-        return g, None, None, None, None
+        if torch.is_grad_enabled():  # a graph of the gradient is wanted
+            g = InplacePartialRotaryMulFn.apply(g, r1, r2, ctx.rotary_mode, ctx.partial_slice, not ctx.back)
+        else:
+            _op(_FWD, not ctx.back)(g, r1, r2, rotary_mode=ctx.rotary_mode, partial_slice=ctx.partial_slice)
+        return g, None, None, None, None, None
 
 
 def inplace_partial_rotary_mul(x: torch.Tensor, r1: torch.Tensor, r2: torch.Tensor, *,
@@ -175,22 +183,26 @@ def inplace_partial_rotary_mul(x: torch.Tensor, r1: torch.Tensor, r2: torch.Tens
 
 
 class InplaceAxesRotaryMulFn(torch.autograd.Function):
-    """Autograd for the rotation with several axes: the positions get no gradient."""
+    """Autograd for the rotation with several axes, or (``back``) its transpose:
+    the positions get no gradient."""
 
     @staticmethod
-    def forward(ctx, x, positions, sections, kwargs):
-        getattr(torch.ops, NAMESPACE).inplace_axes_rotary_mul(x, positions, sections, **kwargs)
+    def forward(ctx, x, positions, sections, kwargs, back=False):
+        _op(_AXES_FWD, back)(x, positions, sections, **kwargs)
         ctx.mark_dirty(x)
         ctx.save_for_backward(positions)
-        ctx.sections, ctx.kwargs = sections, kwargs
+        ctx.sections, ctx.kwargs, ctx.back = sections, kwargs, back
         return x
 
     @staticmethod
     def backward(ctx, grad):
         (positions,) = ctx.saved_tensors
         g = grad.clone(memory_format=torch.contiguous_format)
-        getattr(torch.ops, NAMESPACE).inplace_axes_rotary_mul_backward(g, positions, ctx.sections, **ctx.kwargs)
-        return g, None, None, None
+        if torch.is_grad_enabled():
+            g = InplaceAxesRotaryMulFn.apply(g, positions, ctx.sections, ctx.kwargs, not ctx.back)
+        else:
+            _op(_AXES_FWD, not ctx.back)(g, positions, ctx.sections, **ctx.kwargs)
+        return g, None, None, None, None
 
 
 def inplace_axes_rotary_mul(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int], *,
