@@ -110,7 +110,7 @@ typedef enum {
    page_size, heads, v_dim), in ELEMENT strides for the first three dims and
    a contiguous last dim, so that a head-major page is a matter of strides.
    k_scale and v_scale, (pages, page_size, heads), are needed for the 8-bit
-   types and null for the others.  A cache without values has v == null and
+   types (values' scales are not negative) and null for the others.  A cache without values has v == null and
    v_dim == 0.  Slot s is token s % page_size of page s / page_size. */
 typedef struct {
     void* k;
@@ -218,7 +218,12 @@ rope_status_t rope_partial_cache_read(const rope_kv_cache_t* cache, const int64_
  * heads divides Hq.  Rows of q, out and the cache must start on 16-byte
  * boundaries.  Sums are fp32; the products of q with k and of exp(s) with v
  * run on tensor cores in bf16 (bf16 caches) or fp16 (the others) with fp32
- * accumulation, exp(s) being rounded to that type once.  Pages of a multiple
+ * accumulation, exp(s) being rounded to that type once.  In fp16, what is
+ * rounded (for 8-bit caches exp(s) times the value's scale) is counted from the
+ * token's largest: below 2^-29 (2^-21 for more than 16 query rows a key head) of it
+ * the rounding grows, below 2^-39 (2^-31) the row vanishes.  For 8-bit
+ * caches q is rounded to fp16 after a power of two that brings the row's
+ * largest lane to [1, 2).  Pages of a multiple
  * of 8 rows, and up to 192 + 128 lanes, are the fast case: others read the
  * cache once for each 16 query rows of a key head.  A call captured in a graph
  * may be replayed with other contents of the device arrays.  Waits inside the

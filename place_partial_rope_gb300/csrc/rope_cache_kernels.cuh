@@ -29,8 +29,9 @@
 // codes: 69 us against 75 in the case above; writing them so took 160 us for
 // 16411 tokens (and reading back) of 16 heads of 192 + 128, against 117.
 // Measured: those 16411 bf16 tokens into int8, 70 us for 254 MB, 0.54 of the
-// measured copy rate: the rotation, maximum and rounding of a row issue 2.4
-// instructions a cycle on each SM, and the loads wait behind them.  Back,
+// measured copy rate: a row is a chain of loads, rotation, maximum and rounding, of
+// which 64 registers a thread let half the warps be in flight (2.4 of 4 instructions a
+// cycle, 5.4 long-scoreboard stalls an issue).  Back,
 // 46 us, 0.84; the 65536 rows above 69 us (407 MB), 0.89.
 #pragma once
 #include <cuda_fp8.h>

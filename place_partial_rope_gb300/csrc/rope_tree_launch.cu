@@ -156,14 +156,14 @@ rope_status_t launch(const void* f, dim3 grid, int threads, int smem, void** par
 // tiles (128 rows of one key head) that the page table has room for.  Both sides
 // of each border, in us (32 requests of 8000 rows, 8 key heads, 128 + 128 lanes
 // unless it says otherwise):
-//   16-bit, up to 16 query rows: narrow 201, 64-row tiles 179; 8 requests of 4096
+//   16-bit, up to 16 query rows: narrow 201, 64-row tiles 175; 8 requests of 4096
 //   rows 59 and 44.  But 4 requests of 4096 rows 28 and 32, and one of 4097 rows
 //   with 2 key heads 13.3 and 13.8, the tile kernel's start being the longer one:
-//   to 8 tiles an SM, the narrow kernel.
-//   fp8, up to 16 rows: narrow 174, 64-row tiles 193 (codes become fp16 in registers
+//   to 8 tiles an SM (of this card's 152), the narrow kernel.
+//   fp8, up to 16 rows: narrow 176, 64-row tiles 193 (codes become fp16 in registers
 //   there, in shared memory here).  32 rows: 323 and 189.
-//   64 rows: 64-row tiles 182 (bf16) and 197 (fp8), 128-row tiles 185 and 210.
-//   256 rows: a pair of tiles that share the cache's, 253 (bf16) and 522 (fp8);
+//   64 rows: 64-row tiles 182 (bf16) and 190 (fp8), 128-row tiles 185 and 210.
+//   256 rows: a pair of tiles that share the cache's, 249 (bf16) and 522 (fp8);
 //   128-row tiles, the cache read twice, 351 and 430, as fp8 pairs have room for
 //   64-row cache tiles only; with 64-lane rows, which have room for more, 215
 //   and 330 against 263 and 367; fp8 rows of 192 + 128, 612 and 625.
@@ -172,7 +172,7 @@ rope_status_t launch(const void* f, dim3 grid, int threads, int smem, void** par
 // twice), stay with the narrow kernel.  So does a cache without pages: a tensor
 // map has no dim of 0.
 void choose_tree(int Dk, int Dv, int64_t rows, int64_t pages, int64_t page_size, int64_t tiles, TreePlan* p) {
-    constexpr int64_t kFewTiles = 8 * 152;
+    constexpr int64_t kFewTiles = 8 * 152;  // (the plan is made without a device, too)
     if (Dk <= 64) p->dk = 64, p->dv = 64;
     else if (Dk <= 128) p->dk = 128, p->dv = 128;
     else if (Dk <= 192 && Dv <= 128) p->dk = 192, p->dv = 128;

@@ -40,9 +40,9 @@
 // q is permuted alike, and the columns of O may come in any order as long as
 // the end puts them back; see query_frags and value_codes.
 //   Measured (device, 8 query rows a key head, 8 key heads, 128 + 128 lanes): 32
-// requests of 8000 fp8 rows 174 us, 3.0 TB/s (0.45 of the measured copy rate),
+// requests of 8000 fp8 rows 176 us, 3.0 TB/s (0.45 of the measured copy rate),
 // what it issues bounding it; one request of 4097 bf16 rows and 2 key heads,
-// 11 us, and 10 for the join: latencies.
+// 11 us, and 9 for the join (cold caches): latencies.
 #pragma once
 #include "rope_tree_common.cuh"
 

@@ -8,8 +8,8 @@
 // memory, where rescaling it costs a read and a write of the whole
 // accumulator.  And the fp16 bias is 2^7, which leaves p below 2^15.  8-bit: O
 // and l are both kept in units of 1 / w (w the power of two above the scales of the
-// values that the query row sees), so that a weight is 2^(s - m - log2 w) u, one product; w starts at
-// 2^-80.
+// values that the query row sees), so that a weight is 2^(s - m - log2 w) u, one
+// product; w starts at 2^-80.
 //
 // What bounds it.  128 x TN x (Dk + Dv) multiply-adds a tile against TN (Dk +
 // Dv) cache elements: 128 query rows take 1024 cycles of tensor pipe a tile
@@ -17,12 +17,12 @@
 // SM.  So up to 128 rows 16 bits are bound by HBM (32 requests of 8000 rows, 8
 // key heads: 182 us, 5.8 TB/s), and a pair of tiles by the chain s -> p -> O of
 // its two groups: 12 requests of 6000 to 8200 rows and 240 to 256 query rows,
-// 101 us, 0.44 of the measured matrix rate, the tensor pipe 43 % busy.  (The
+// 103 us, 0.43 of the measured matrix rate, the tensor pipe 40 % busy.  (The
 // product on the first half of a row's weights, while the thread was at the second,
 // took 121 us, not 105.)  8-bit rows would take 1400 cycles of HBM and take 3000: each
 // code passes through shared memory four times and the helpers' and groups' code
-// presses on the instruction cache (87 % of its requests hit): 48 requests of 90 to
-// 12000 rows, 219 us, 2.8 TB/s.  (24 warps, twice the helpers: no faster.)
+// presses on the instruction cache (86 % of its requests hit): 48 requests of 90 to
+// 12000 rows, 223 us, 2.8 TB/s.  (24 warps, twice the helpers: no faster.)
 //
 // How.  One block an SM, 16 warps with one role each:
 //   0-3, 4-7  two softmax groups.  A thread owns a query row (a lane of tensor
@@ -783,7 +783,7 @@ struct Tile {
 
     // The row tile's queries: 16-bit as they are, or fp16 in [-2, 2) with what
     // the row's s is multiplied by in `factor` (by row).  Eight lanes a row; rows
-    // of a tile of 32 or 64 are stored once for each copy.
+    // of a tile of 64 are stored once for each copy.
     __device__ __forceinline__ void stage_queries(const RunAt& x, int tid, float* factor) const {
         constexpr int N = C::DK / 64, EACH = 32;  // chunks of a lane; rows of the 256 threads
         constexpr int TOGETHER = C::ROWS / EACH < 4 ? C::ROWS / EACH : 4;
@@ -953,8 +953,8 @@ struct Tile {
             bar_arrive(&sync->q_full);
 
             const int rows = x.rq.n * a.G;
-            // the thread's query row, and the columns of s that it sees to (of 32 or
-            // 64 query rows each warp or pair of warps has a copy, and its own columns)
+            // the thread's query row, and the columns of s that it sees to (of
+            // 64 query rows each pair of warps has a copy, and its own columns)
             const int mine = C::PAIR ? row : row % C::ROWS, lo = row / (C::PAIR ? 128 : C::ROWS) * C::COLS;
             const int at = x.m * C::ROWS + (C::PAIR ? 128 * w : 0) + mine;
             const bool active = at - (row & 31) < rows;  // the warp has a row
@@ -1006,8 +1006,8 @@ struct Tile {
                         }
                     }
                     // s is held in registers by 16-bit rows, and by 8-bit pairs (whose rows
-                    // have 64 lanes: 57 us against 62 for 2 requests of 131072 rows and
-                    // 200 query rows).  Other 8-bit rows: it is read twice, 32 columns
+                    // have 64 lanes: 57 us against 62 when measured, for 2 requests of 131072 rows
+                    // and 200 query rows).  Other 8-bit rows: it is read twice, 32 columns
                     // at a time, in loops small enough to stay in the instruction
                     // cache beside the helpers' (a batch of 48 requests of up to
                     // 12000 fp8 rows: 258 us, and 276 with s held).
