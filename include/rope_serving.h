@@ -149,7 +149,7 @@ typedef struct {
  * infinity or a NaN stores a NaN scale and codes of 0, so that it reads back
  * as NaN.
  *
- * Sizes: k_dim even when there is a rotation, k_dim and v_dim <= 1024.
+ * Sizes: k_dim and v_dim <= 1024, odd ones too.
  * The inputs must not overlap the cache.  T == 0 is a no-op.
  */
 rope_status_t rope_partial_cache_write(const rope_kv_cache_t* cache, const void* k, const void* v,

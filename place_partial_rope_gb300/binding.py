@@ -693,8 +693,8 @@ def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, 
     pages page_table[r] (int32).  ``tree`` (Tq, words) int64 holds the bits of
     the drafted tokens that each token sees (``rope_partial_tree_mask``); None
     is a chain.  ``scale`` defaults to 1 / sqrt(k_dim), ``max_q`` (the most
-    tokens of a request) to Tq, and the workspace is made for the call when
-    none is given."""
+    tokens of a request) to Tq, and the workspace is made for the call, on its
+    stream, when none is given."""
     lib = _lib or load_library()
     dev, kd, vd = cache.device, cache.k_dim, cache.v_dim
     dtype = DTYPE_CODE.get(q.dtype)

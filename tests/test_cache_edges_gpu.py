@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import serving_ref as ref
 from gpu_util import DEV
 from place_partial_rope_gb300 import binding
 
@@ -25,3 +26,19 @@ def test_keys_and_values_read_into_one_tensor(dk, dv, store):
     binding.rope_partial_cache_read(cache, slots, packed[..., :dk], packed[..., dk:])
     torch.cuda.synchronize()
     assert torch.equal(packed, torch.cat(want, -1))
+
+
+@pytest.mark.parametrize("mode", ["interleave", "half"])
+@pytest.mark.parametrize("dk,start,end", [(65, 0, 64), (65, 1, 65), (127, 30, 100), (3, 1, 3)])
+def test_a_rotation_in_rows_of_an_odd_length(dk, start, end, mode):
+    T, heads, L = 19, 2, end - start
+    k = torch.zeros((2, 16, heads, dk), dtype=torch.float16, device=DEV)
+    new = torch.randn((T, heads, dk), device=DEV)
+    cos, sin = torch.rand((T, L), device=DEV), torch.rand((T, L), device=DEV)
+    slots = torch.randperm(32, device=DEV)[:T]
+    binding.rope_partial_cache_write(binding.KVCache(k), new, None, slots, cos, sin, start, end, mode)
+    torch.cuda.synchronize()
+    x, c, s = new[..., start:end].cpu().numpy(), cos.cpu().numpy(), sin.cpu().numpy()
+    want = new.cpu().numpy().copy()
+    want[..., start:end] = ref.rotate_rows_fp32(x, c, s, 0, L, mode)
+    assert torch.equal(k.flatten(0, 1)[slots].cpu(), torch.from_numpy(want).half())
