@@ -79,7 +79,7 @@ __global__ void agree_kernel(const TreeArgs a, int rounds, unsigned* took, unsig
         }
         __syncthreads();
         if (tid < 256) {
-            pause(hash(seed + uint32_t(tid) / 32) & 255u);
+            pause((hash(seed ^ 55u) & 511u) + (hash(seed + uint32_t(tid) / 32) & 127u));
             RunAt x;
             if (tid < N || ID == 0) answer[tid] = tile.template take_all<ID, N>(0, x);
         } else if (tid == 256) {
