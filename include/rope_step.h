@@ -1,0 +1,114 @@
+/*
+ * rope_step.h -- C ABI of the operators on either side of the paged cache of
+ * rope_serving.h in a model's step:
+ *
+ *   rope_partial_norm_fwd / _bwd      root-mean-square norm of query and key rows and
+ *                                     the rotation of a slice of them, in one pass
+ *
+ * Conventions are those of rope_partial.h and rope_serving.h: plain C, device
+ * pointers on the current CUDA device, int64 sizes, ELEMENT strides, the
+ * caller's stream, nothing allocated, nothing synchronised; arguments are
+ * checked on the host before anything is launched, an invalid call changes
+ * nothing and returns an error status, and rope_last_error_message()
+ * describes it.
+ */
+#ifndef ROPE_STEP_H
+#define ROPE_STEP_H
+
+#include "rope_serving.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------------------
+ * Norm and rotation of rows in one pass
+ * ------------------------------------------------------------------------ */
+
+/* The rows of the queries or of the keys: (B, S, heads, D) with ELEMENT strides
+   of the first three dims (>= 0; that of a dim of one is not looked at) and a
+   contiguous last dim. */
+typedef struct {
+    const void* x;          /* the rows before the norm */
+    void* out;              /* forward: the result; backward: the gradient of x */
+    const void* grad;       /* backward: the gradient of the result; else not used */
+    const void* weight;     /* one factor for each normed lane, or null (all 1) */
+    float* rstd;            /* (B, S, heads) contiguous, 1 / root mean square of each row:
+                               forward: written, unless null; backward: read */
+    float* weight_grad;     /* backward: the gradient of the weight (one fp32 for each
+                               normed lane), overwritten; null: not wanted */
+    int64_t heads;
+    int64_t x_stride[3], out_stride[3], grad_stride[3];
+} rope_norm_rows_t;
+
+/*
+ * rope_partial_norm_fwd -- for each row x of the queries and, where k is not
+ * null, of the keys:
+ *
+ *     r   = 1 / sqrt(eps + sum of x_j^2 over the normed lanes / their number)
+ *     y_j = x_j r weight_j on the lanes [norm_start, norm_end), x_j elsewhere
+ *     out = y with the lanes [start, end) rotated as in rope_partial_inplace_fwd_mode
+ *
+ * Everything is computed in fp32 and rounded once when it is stored (rows whose
+ * squares fp32 does not hold are not normed rightly).
+ *
+ *   q, k           k may be null.  Both have D lanes, and the same norm and slice.
+ *   dtype          of x, out, grad, cos and sin: bf16, fp16 or fp32
+ *   weight_dtype   of the weights: dtype, or fp32
+ *   D              1 .. 1024, odd ones too
+ *   norm_start, norm_end   0 <= norm_start < norm_end <= D
+ *   eps            >= 0 and finite
+ *   cos, sin       rows of end - start elements of `dtype` at ELEMENT strides
+ *                  {batch, token} (>= 0; 0: one row for all); null when start == end
+ *   start, end, mode   as for rope_partial_inplace_fwd_mode; any start
+ *
+ * out may be x itself (the same address and strides: in place); otherwise no
+ * output may share a byte with another output or with anything that is read.
+ * Rows of 16-byte aligned addresses, strides and lengths are the fast case.  A
+ * batch without rows is a no-op.
+ */
+rope_status_t rope_partial_norm_fwd(const rope_norm_rows_t* q, const rope_norm_rows_t* k,
+                                    rope_dtype_t dtype, rope_dtype_t weight_dtype, int64_t B,
+                                    int64_t S, int64_t D, int64_t norm_start, int64_t norm_end,
+                                    double eps, const void* cos, const void* sin,
+                                    const int64_t cos_stride[2], const int64_t sin_stride[2],
+                                    int64_t start, int64_t end, rope_mode_t mode,
+                                    rope_stream_t stream);
+
+/*
+ * rope_partial_norm_bwd -- the gradients of the forward.  With g the transposed
+ * rotation of grad (the forward's cos and sin), u_j = x_j rstd and n normed
+ * lanes:
+ *
+ *     weight_grad_j = sum over all rows of g_j u_j
+ *     out_j = rstd (weight_j g_j - u_j sum_i(weight_i g_i u_i) / n) on the normed
+ *     lanes, g_j elsewhere
+ *
+ * x, rstd and grad are read, out is written; out may be grad itself (the same
+ * address and strides).  cos and sin get no gradient.  Sums are fp32, in an
+ * order that depends on sizes and the device alone, so a call repeated gives
+ * the same bits.
+ *
+ *   workspace   rope_partial_norm_workspace() bytes, 16-byte aligned, for this
+ *               call alone until it has run; its contents do not matter.  Null
+ *               when no weight_grad is wanted.
+ * A batch without rows gives weight gradients of zero.
+ */
+rope_status_t rope_partial_norm_bwd(const rope_norm_rows_t* q, const rope_norm_rows_t* k,
+                                    rope_dtype_t dtype, rope_dtype_t weight_dtype, int64_t B,
+                                    int64_t S, int64_t D, int64_t norm_start, int64_t norm_end,
+                                    const void* cos, const void* sin, const int64_t cos_stride[2],
+                                    const int64_t sin_stride[2], int64_t start, int64_t end,
+                                    rope_mode_t mode, void* workspace, int64_t workspace_bytes,
+                                    rope_stream_t stream);
+
+/* The bytes of workspace that a backward with `normed` = norm_end - norm_start lanes
+   needs on the current device (sm_count > 0: on a device with that many SMs, without
+   touching the GPU). */
+rope_status_t rope_partial_norm_workspace(int64_t normed, int32_t sm_count, int64_t* bytes);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ROPE_STEP_H */

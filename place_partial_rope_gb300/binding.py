@@ -1,5 +1,5 @@
-"""ctypes binding of ``librope_partial.so`` (C ABI: ``include/rope_partial.h``
-and ``include/rope_serving.h``).
+"""ctypes binding of ``librope_partial.so`` (C ABI: ``include/rope_partial.h``,
+``include/rope_serving.h`` and ``include/rope_step.h``).
 
 Argument marshalling only: every step of the operation runs in the library's
 CUDA kernels.  PyTorch supplies device memory and the current stream.  If the
@@ -24,6 +24,11 @@ paged cache:
     rope_partial_cache_read(cache, slots, k, v)
     rope_partial_tree_attention(q, cache, q_start, kv_len, page_table, out, ...)
     rope_partial_tree_mask(parents), tree_attention_workspace(q, cache, max_q)
+
+And on either side of that cache in a model's step:
+
+    rope_partial_norm_fwd(q, k, q_weight, k_weight, cos, sin, start, end, ...)
+    rope_partial_norm_bwd(dq, dk, q, k, ...), norm_workspace(q, k)
 """
 from __future__ import annotations
 
@@ -141,6 +146,14 @@ def load_library() -> ctypes.CDLL:
                                              i64, i64, vp, i64, vp, vp, vp, d, vp, i64, vp]),
             ("rope_partial_tree_attention_workspace", [vp, ctypes.c_int, i64, i64, i32, i64p]),
             ("rope_partial_tree_mask", [vp, i64, i64, vp])):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = argtypes
+    norm = [vp, vp, ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, i64]
+    for name, argtypes in (
+            ("rope_partial_norm_fwd", norm + [d, vp, vp, vp, vp, i64, i64, ctypes.c_int, vp]),
+            ("rope_partial_norm_bwd", norm + [vp, vp, vp, vp, i64, i64, ctypes.c_int, vp, i64, vp]),
+            ("rope_partial_norm_workspace", [i64, i32, i64p])):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = argtypes
@@ -746,3 +759,142 @@ def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, 
              kv_len.data_ptr(), R, max_q, page_table.data_ptr(), pt[1], pst[0] if R > 1 else pt[1], tp, words,
              out.data_ptr(), _pack2(os_[0], os_[1]), lp, kd ** -0.5 if scale is None else scale,
              workspace.data_ptr(), workspace.nbytes), stream, dev)
+
+
+# ------------------------------------------------------------------------
+# norm and rotation of rows in one pass
+# ------------------------------------------------------------------------
+
+_pack_rows = struct.Struct("=6Q10q").pack  # rope_norm_rows_t
+
+
+def _norm_side(what, x, out, grad, weight, rstd, weight_grad, shape, dtype, device, normed):
+    """One tensor's rope_norm_rows_t; ``shape`` is (B, S, D) of the queries."""
+    B, S, D = shape
+    for t, name in ((x, "" if grad is None else " (x)"), (out, " out"), (grad, " gradient")):
+        if t is None:
+            continue
+        if t.dim() != 4 or t.shape[0] != B or t.shape[1] != S or t.shape[3] != D or t.shape[2] != x.shape[2]:
+            _refuse(f"{what}{name} must be ({B}, {S}, heads, {D})")
+        if t.dtype is not dtype or t.device != device:
+            _refuse(f"{what}{name} must be {dtype} on {device}")
+        if D > 1 and t.stride(3) != 1:
+            _refuse(f"the last dim of {what}{name} must be contiguous")
+    N = x.shape[2]
+    for t, name in ((weight, "weight"), (weight_grad, "weight gradient")):
+        if t is not None and (t.dim() != 1 or t.shape[0] != normed or not t.is_contiguous() or t.device != device):
+            _refuse(f"{what}'s {name} must be a contiguous vector of {normed} on {device}")
+    if weight_grad is not None and weight_grad.dtype is not torch.float32:
+        _refuse(f"{what}'s weight gradient must be fp32")
+    if rstd is not None and (rstd.dtype is not torch.float32 or rstd.shape != (B, S, N) or
+                             not rstd.is_contiguous() or rstd.device != device):
+        _refuse(f"{what}'s rstd must be contiguous fp32 ({B}, {S}, {N}) on {device}")
+
+    def ptr(t):
+        return 0 if t is None else t.data_ptr()
+
+    return _pack_rows(x.data_ptr(), out.data_ptr(), ptr(grad), ptr(weight), ptr(rstd), ptr(weight_grad), N,
+                      *x.stride()[:3], *out.stride()[:3], *((0, 0, 0) if grad is None else grad.stride()[:3]))
+
+
+def _norm_call(name, q, k, grads, outs, weights, rstds, weight_grads, cos, sin, start, end, norm, mode, back, extra,
+               stream):
+    lib = _lib or load_library()
+    if q.dim() != 4:
+        _refuse("q must be 4-D (B, S, heads, D)")
+    dtype, device, shape = q.dtype, q.device, q.shape
+    code = DTYPE_CODE.get(dtype)
+    if code is None:
+        _refuse(f"unsupported dtype {dtype}")
+    if not q.is_cuda:
+        _refuse("q must be a CUDA tensor")
+    B, S, D = shape[0], shape[1], shape[3]
+    n0, n1 = (0, D) if norm is None else norm
+    if mode not in MODE_CODE:
+        _mode_code(mode)
+    wtype = None
+    for w, x in zip(weights, (q, k)):
+        if w is None:
+            continue
+        if x is None or (wtype is not None and w.dtype is not wtype) or w.dtype not in DTYPE_CODE:
+            _refuse("a weight needs its rows, and both weights one dtype")
+        wtype = w.dtype
+    rows = [None, None]
+    for i, x in enumerate((q, k)):
+        if x is None:
+            if any(t is not None for t in (grads[i], outs[i], rstds[i], weight_grads[i])):
+                _refuse("without k there is nothing else of k's")
+            continue
+        what = "k" if i else "q"
+        if back and (grads[i] is None or rstds[i] is None):
+            _refuse(f"{what}'s gradient and rstd are needed")
+        out = outs[i] if outs[i] is not None else (grads[i] if back else x)
+        rows[i] = _norm_side(what, x, out, grads[i], weights[i], rstds[i], weight_grads[i], (B, S, D), dtype, device,
+                             n1 - n0)
+    cp = sp = cst = sst = None
+    if start != end:
+        for t in (cos, sin):
+            if (t is None or t.dim() != 4 or t.dtype is not dtype or t.device != device or
+                    t.shape[0] not in (1, B) or t.shape[1] not in (1, S) or t.shape[2] != 1 or
+                    t.shape[3] != end - start or (t.shape[3] > 1 and t.stride(3) != 1)):
+                _refuse("cos and sin must be (B|1, S|1, 1, end - start) of q's dtype with a contiguous last dim")
+
+        def steps(t):
+            return _pack2(t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+        cp, sp, cst, sst = cos.data_ptr(), sin.data_ptr(), steps(cos), steps(sin)
+    _launch(getattr(lib, name),
+            (rows[0], rows[1], code, code if wtype is None else DTYPE_CODE[wtype], B, S, D, n0, n1, *extra[0], cp, sp,
+             cst, sst, start, end, MODE_CODE[mode], *extra[1]), stream, device)
+
+
+def rope_partial_norm_fwd(q, k, q_weight, k_weight, cos, sin, start: int, end: int, eps: float = 1e-6, norm=None,
+                          mode: str = "interleave", q_out=None, k_out=None, q_rstd=None, k_rstd=None,
+                          stream=None) -> None:
+    """Root-mean-square norm of the rows of ``q`` (B, S, heads, D) and, where
+    given, ``k``, then the rotation of their lanes [start, end) by ``cos`` and
+    ``sin`` (B|1, S|1, 1, end - start), in one pass.
+
+    ``norm`` = (first, last + 1) of the normed lanes (default: all).  Weights
+    (one for each normed lane, of q's dtype or fp32) may be None.  Results go
+    to ``q_out`` and ``k_out``, or where those are None in place.  ``q_rstd``
+    and ``k_rstd`` (B, S, heads) fp32, where given, keep 1 / root mean square
+    for the backward."""
+    _norm_call("rope_partial_norm_fwd", q, k, (None, None), (q_out, k_out), (q_weight, k_weight), (q_rstd, k_rstd),
+               (None, None), cos, sin, start, end, norm, mode, False, ((eps,), ()), stream)
+
+
+def norm_workspace(q, k=None, norm=None) -> torch.Tensor:
+    """A workspace for rope_partial_norm_bwd on such rows (their number does not
+    matter).  A program keeps it: calls that follow each other on one stream
+    can share it."""
+    lib = _lib or load_library()
+    n0, n1 = (0, q.shape[-1]) if norm is None else norm
+    need = ctypes.c_int64()
+    with torch.cuda.device(q.device):
+        st = lib.rope_partial_norm_workspace(n1 - n0, 0, ctypes.byref(need))
+    _raise_for(lib, st)
+    return torch.empty(need.value, dtype=torch.uint8, device=q.device)
+
+
+def rope_partial_norm_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, start: int, end: int,
+                          norm=None, mode: str = "interleave", dq_out=None, dk_out=None, dq_weight=None,
+                          dk_weight=None, workspace=None, stream=None) -> None:
+    """The gradients of rope_partial_norm_fwd: from ``dq`` and ``dk``, those of
+    ``q`` and ``k`` (the forward's inputs) into ``dq_out`` and ``dk_out``, or
+    where those are None in place, and of the weights into ``dq_weight`` and
+    ``dk_weight`` (fp32, overwritten) where given.  The workspace is made for
+    the call, on its stream, when none is given and one is needed."""
+    if workspace is None and (dq_weight is not None or dk_weight is not None):
+        if stream is None:
+            workspace = norm_workspace(q, k, norm)
+        else:  # (see rope_partial_tree_attention)
+            with torch.cuda.stream(_stream_of(stream, q.device)):
+                workspace = norm_workspace(q, k, norm)
+    wp, wn = None, 0
+    if workspace is not None:
+        if workspace.device != q.device or not workspace.is_contiguous():
+            _refuse("workspace must be contiguous on q's device")
+        wp, wn = workspace.data_ptr(), workspace.nbytes
+    _norm_call("rope_partial_norm_bwd", q, k, (dq, dk), (dq_out, dk_out), (q_weight, k_weight), (q_rstd, k_rstd),
+               (dq_weight, dk_weight), cos, sin, start, end, norm, mode, True, ((), (wp, wn)), stream)

@@ -41,6 +41,7 @@ inline int64_t span(const int64_t* shape, const int64_t* stride, int n, int64_t 
 
 // The cache descriptor; fills the bytes that k and v span.
 inline rope_status_t check_cache(const rope_kv_cache_t* c, int64_t* k_bytes, int64_t* v_bytes) {
+    *k_bytes = *v_bytes = 0;
     if (!c) return fail(ROPE_ERR_NULLPTR, "cache is null");
     if (!valid_store(c->dtype))
         return fail(ROPE_ERR_INVALID, "cache dtype %d is not bf16 (0), fp16 (1), fp8 (3) or int8 (4)",

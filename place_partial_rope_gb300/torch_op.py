@@ -33,6 +33,12 @@ autograd; the positions get no gradient):
     inplace_axes_rotary_mul(x, positions, sections, *, rotary_mode="interleave",
                             partial_slice=None, base=10000.0, order="blocked",
                             spectrum="shared") -> None
+
+Norm and rotation of query and key rows in one pass, out of place, with gradients of
+the rows and of the weights (cos and sin get none; no second gradients):
+
+    norm_rotary(q, k, q_weight, k_weight, cos, sin, *, rotary_mode="interleave",
+                partial_slice=None, norm_slice=None, eps=1e-6) -> (q_out, k_out)
 """
 from __future__ import annotations
 
@@ -47,6 +53,8 @@ _FWD = "inplace_partial_rotary_mul"
 _BWD = "inplace_partial_rotary_mul_backward"
 _AXES_FWD = "inplace_axes_rotary_mul"
 _AXES_BWD = "inplace_axes_rotary_mul_backward"
+_NORM_FWD = "norm_rotary"
+_NORM_BWD = "norm_rotary_backward"
 _MODES = ("interleave", "half")
 
 _lib = None
@@ -112,6 +120,74 @@ def _axes_meta(x, positions, sections, rotary_mode="interleave", partial_slice=(
     return None
 
 
+def _check_norm(q, k, rotary_mode, partial_slice, norm_slice) -> None:
+    for x, what in ((q, "q"), (k, "k")):
+        if x is not None and x.dim() != 4:
+            raise ValueError(f"norm_rotary: {what} must be 4-D (B, S, N, D), got {x.dim()}-D")
+    if k is not None and (k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]):
+        raise ValueError("norm_rotary: q and k must share B, S and D")
+    if rotary_mode not in _MODES:
+        raise ValueError(f"norm_rotary: rotary_mode must be 'interleave' or 'half', got {rotary_mode!r}")
+    if len(partial_slice) != 2 or len(norm_slice) != 2:
+        raise ValueError("norm_rotary: partial_slice and norm_slice must hold 2 integers each")
+
+
+def _rows(x):
+    """x, or a copy whose last dim is contiguous."""
+    return x if x is None or x.stride(-1) == 1 or x.shape[-1] <= 1 else x.contiguous()
+
+
+def _like(x, shape=None, dtype=None):
+    """An uninitialised contiguous tensor of x's shape (or another); of nothing for None."""
+    if x is None:
+        return torch.empty(0)
+    return torch.empty(x.shape if shape is None else shape, dtype=dtype or x.dtype, device=x.device)
+
+
+def _norm_outputs(q, k):
+    return (_like(q), _like(k), _like(q, q.shape[:3], torch.float32),
+            _like(k, None if k is None else k.shape[:3], torch.float32))
+
+
+def _norm_grads(q, k, q_weight, k_weight):
+    return (_like(q), _like(k), _like(q_weight, None, torch.float32), _like(k_weight, None, torch.float32))
+
+
+def _norm_cuda(q, k, q_weight, k_weight, cos, sin, rotary_mode="interleave", partial_slice=(0, 0),
+               norm_slice=(0, 0), eps=1e-6):
+    _check_norm(q, k, rotary_mode, partial_slice, norm_slice)
+    q, k = _rows(q), _rows(k)
+    got = _norm_outputs(q, k)
+    binding.rope_partial_norm_fwd(q, k, q_weight, k_weight, cos, sin, *partial_slice, eps=eps, norm=tuple(norm_slice),
+                                  mode=rotary_mode, q_out=got[0], k_out=None if k is None else got[1], q_rstd=got[2],
+                                  k_rstd=None if k is None else got[3])
+    return got
+
+
+def _norm_cuda_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, rotary_mode="interleave",
+                   partial_slice=(0, 0), norm_slice=(0, 0)):
+    _check_norm(q, k, rotary_mode, partial_slice, norm_slice)
+    q, k = _rows(q), _rows(k)
+    got = _norm_grads(q, k, q_weight, k_weight)
+    binding.rope_partial_norm_bwd(_rows(dq), _rows(dk), q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin,
+                                  *partial_slice, norm=tuple(norm_slice), mode=rotary_mode, dq_out=got[0],
+                                  dk_out=None if k is None else got[1],
+                                  dq_weight=None if q_weight is None else got[2],
+                                  dk_weight=None if k_weight is None else got[3])
+    return got
+
+
+def _norm_meta(q, k, q_weight, k_weight, cos, sin, rotary_mode="interleave", partial_slice=(0, 0),
+               norm_slice=(0, 0), eps=1e-6):
+    _check_norm(q, k, rotary_mode, partial_slice, norm_slice)
+    return _norm_outputs(q, k)
+
+
+def _norm_meta_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, rotary_mode="interleave",
+                   partial_slice=(0, 0), norm_slice=(0, 0)):
+    return _norm_grads(q, k, q_weight, k_weight)
+
+
 def register() -> None:
     """Define the operators once per process (idempotent)."""
     global _lib
@@ -133,6 +209,15 @@ def register() -> None:
                    "str order='blocked', str spectrum='shared') -> ()")
         lib.impl(name, _axes_impl(fn), "CUDA")
         lib.impl(name, _axes_meta, "Meta")
+    rest = "*, str rotary_mode='interleave', int[2] partial_slice=[0, 0], int[2] norm_slice=[0, 0]"
+    lib.define(f"{_NORM_FWD}(Tensor q, Tensor? k, Tensor? q_weight, Tensor? k_weight, Tensor? cos, Tensor? sin, "
+               f"{rest}, float eps=1e-06) -> (Tensor, Tensor, Tensor, Tensor)")
+    lib.define(f"{_NORM_BWD}(Tensor dq, Tensor? dk, Tensor q, Tensor? k, Tensor? q_weight, Tensor? k_weight, "
+               f"Tensor q_rstd, Tensor? k_rstd, Tensor? cos, Tensor? sin, {rest}) -> (Tensor, Tensor, Tensor, Tensor)")
+    lib.impl(_NORM_FWD, _norm_cuda, "CUDA")
+    lib.impl(_NORM_FWD, _norm_meta, "Meta")
+    lib.impl(_NORM_BWD, _norm_cuda_bwd, "CUDA")
+    lib.impl(_NORM_BWD, _norm_meta_bwd, "Meta")
     _lib = lib
 
 
@@ -222,3 +307,45 @@ def inplace_axes_rotary_mul(x: torch.Tensor, positions: torch.Tensor, sections: 
     else:
         getattr(torch.ops, NAMESPACE).inplace_axes_rotary_mul(x, positions, sections, **kwargs)
     return None
+
+
+class NormRotaryFn(torch.autograd.Function):
+    """Autograd for the norm and rotation; cos and sin get no gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, kwargs, eps):
+        q_out, k_out, q_rstd, k_rstd = _op(_NORM_FWD, False)(q, k, q_weight, k_weight, cos, sin, **kwargs, eps=eps)
+        ctx.save_for_backward(q, k, q_weight, k_weight, q_rstd, k_rstd if k is not None else None, cos, sin)
+        ctx.kwargs = kwargs
+        return (q_out, k_out) if k is not None else q_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk=None):
+        q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin = ctx.saved_tensors
+        # (a weight whose gradient nobody wants takes part all the same)
+        got = _op(_NORM_FWD, True)(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, **ctx.kwargs)
+        need = ctx.needs_input_grad
+        return (got[0] if need[0] else None, got[1] if need[1] else None,
+                got[2].to(q_weight.dtype) if need[2] else None, got[3].to(k_weight.dtype) if need[3] else None,
+                None, None, None, None)
+
+
+def norm_rotary(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                k_weight: Optional[torch.Tensor], cos: Optional[torch.Tensor], sin: Optional[torch.Tensor], *,
+                rotary_mode: str = "interleave", partial_slice: Optional[Sequence[int]] = None,
+                norm_slice: Optional[Sequence[int]] = None, eps: float = 1e-6):
+    """Root-mean-square norm of the rows of ``q`` and ``k`` (which may be None) over
+    the lanes ``norm_slice`` (default: all), times the weights, then the rotation
+    of the lanes ``partial_slice`` (default: none); see
+    ``binding.rope_partial_norm_fwd``.  Returns new tensors (q_out, k_out)."""
+    register()
+    ps = [0, 0] if partial_slice is None else [int(v) for v in partial_slice]
+    ns = [0, q.shape[-1]] if norm_slice is None else [int(v) for v in norm_slice]
+    _check_norm(q, k, rotary_mode, ps, ns)
+    kwargs = dict(rotary_mode=rotary_mode, partial_slice=ps, norm_slice=ns)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight)):
+        got = NormRotaryFn.apply(q, k, q_weight, k_weight, cos, sin, kwargs, float(eps))
+        return got if k is not None else (got, None)
+    got = _op(_NORM_FWD, False)(q, k, q_weight, k_weight, cos, sin, **kwargs, eps=float(eps))
+    return got[0], got[1] if k is not None else None
