@@ -4,6 +4,8 @@
  *
  *   rope_partial_norm_fwd / _bwd      root-mean-square norm of query and key rows and
  *                                     the rotation of a slice of them, in one pass
+ *   rope_partial_cache_grow / _trim   pages, slots and positions for a batch's new
+ *                                     tokens, made on the device, and pages given back
  *
  * Conventions are those of rope_partial.h and rope_serving.h: plain C, device
  * pointers on the current CUDA device, int64 sizes, ELEMENT strides, the
@@ -106,6 +108,80 @@ rope_status_t rope_partial_norm_bwd(const rope_norm_rows_t* q, const rope_norm_r
    needs on the current device (sm_count > 0: on a device with that many SMs, without
    touching the GPU). */
 rope_status_t rope_partial_norm_workspace(int64_t normed, int32_t sm_count, int64_t* bytes);
+
+/* ------------------------------------------------------------------------
+ * Pages of the cache, slots and positions for a batch of requests
+ * ------------------------------------------------------------------------ */
+
+/*
+ * rope_partial_cache_grow -- for R requests that hold kv_len[r] cached rows and get
+ * n[r] new tokens each: pages for them, and what the calls of rope_serving.h want to
+ * know of the batch.  A request of `len` rows holds ceil(len / page_size) pages,
+ * the first entries of its row of the page table.  It needs
+ *
+ *     need[r] = ceil((kv_len[r] + n[r]) / page_size) - ceil(kv_len[r] / page_size)
+ *
+ * more.  Pages come from the top of the stack free_pages[0 .. *free_count), in the
+ * order of the requests: need[r] of them are granted when need[r] is 0, or when
+ * they and those that all earlier requests need (granted or not) are there.  A request
+ * whose pages would pass max_pages is not granted and takes part in nothing.  So a
+ * batch that asks for too much serves a front part of its requests, and those that need
+ * no page.
+ *
+ *   kv_len      device pointer to R int32, in place: granted requests grow by n[r].
+ *               Lengths are taken as within [0, max_pages * page_size].
+ *   n           device pointer to R int32; a negative number counts as 0
+ *   page_table  (R, max_pages) int32, rows page_table_stride apart, in place: the new
+ *               pages of granted requests are written behind their old ones
+ *   free_pages  device pointer to free_capacity int32 page numbers; free_count to
+ *               one int32, in place, which is taken as within [0, free_capacity]
+ *   q_start     R + 1 int32, written: offsets of the requests' tokens, those of
+ *               requests that are not granted included (q_start[R]: how many there are;
+ *               sums that pass 2^31 - 1 stay there)
+ *   slots       T int64, written: the slot (page * page_size + place) of every token of
+ *               a granted request; -1, which the cache calls skip, for the
+ *               tokens of others and for places from q_start[R] on.  Tokens from T on
+ *               are left out.
+ *   positions   T int32, or null, written: kv_len[r] (before) + i for token i of
+ *               request r, granted or not; 0 from q_start[R] on
+ *   granted     R int32, or null, written: 1 or 0
+ *
+ * Everything is read and written on the device, nothing on the host: a call captured in
+ * a graph may be replayed for other batches of R requests.  Sizes: page_size >= 1,
+ * max_pages * page_size < 2^31, R < 2^24, T < 2^31.  Nothing of what is written may
+ * share a byte with anything else.  R == 0 writes q_start[0] = 0 and the places of slots
+ * and positions.
+ */
+rope_status_t rope_partial_cache_grow(int32_t* kv_len, const int32_t* n, int64_t R,
+                                      int32_t* page_table, int64_t max_pages,
+                                      int64_t page_table_stride, const int32_t* free_pages,
+                                      int64_t free_capacity, int32_t* free_count, int64_t page_size,
+                                      int32_t* q_start, int64_t* slots, int32_t* positions,
+                                      int64_t T, int32_t* granted, rope_stream_t stream);
+
+/*
+ * rope_partial_cache_trim -- requests that keep new_len[r] of their rows (drafted
+ * tokens that were not accepted; 0: a request that has ended) give back the pages
+ * behind them:
+ *
+ *     keep[r] = min(max(new_len[r], 0), kv_len[r])
+ *
+ * The entries [ceil(keep / page_size), ceil(kv_len / page_size)) of a request's row go
+ * onto the stack and become -1 in the table, and kv_len[r] becomes keep[r].  The pages
+ * lie on the stack so that a call of rope_partial_cache_grow that is taken back
+ * leaves the stack as it was: those of the first request uppermost, and of a
+ * request's the earliest.  Pages that would pass free_capacity, which no page that came
+ * from the stack does, are dropped.
+ *
+ * Arguments as above; new_len is a device pointer to R int32 (not kv_len itself, which
+ * is written).  Entries are not looked into: what the table holds goes onto the stack.
+ * R == 0 is a no-op.
+ */
+rope_status_t rope_partial_cache_trim(int32_t* kv_len, const int32_t* new_len, int64_t R,
+                                      int32_t* page_table, int64_t max_pages,
+                                      int64_t page_table_stride, int32_t* free_pages,
+                                      int64_t free_capacity, int32_t* free_count, int64_t page_size,
+                                      rope_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -29,6 +29,9 @@ And on either side of that cache in a model's step:
 
     rope_partial_norm_fwd(q, k, q_weight, k_weight, cos, sin, start, end, ...)
     rope_partial_norm_bwd(dq, dk, q, k, ...), norm_workspace(q, k)
+    rope_partial_cache_grow(kv_len, new_tokens, page_table, free_pages, free_count, page_size,
+                            q_start, slots, ...)
+    rope_partial_cache_trim(kv_len, new_len, page_table, free_pages, free_count, page_size)
 """
 from __future__ import annotations
 
@@ -153,7 +156,9 @@ def load_library() -> ctypes.CDLL:
     for name, argtypes in (
             ("rope_partial_norm_fwd", norm + [d, vp, vp, vp, vp, i64, i64, ctypes.c_int, vp]),
             ("rope_partial_norm_bwd", norm + [vp, vp, vp, vp, i64, i64, ctypes.c_int, vp, i64, vp]),
-            ("rope_partial_norm_workspace", [i64, i32, i64p])):
+            ("rope_partial_norm_workspace", [i64, i32, i64p]),
+            ("rope_partial_cache_grow", [vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]),
+            ("rope_partial_cache_trim", [vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp])):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = argtypes
@@ -898,3 +903,63 @@ def rope_partial_norm_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos,
         wp, wn = workspace.data_ptr(), workspace.nbytes
     _norm_call("rope_partial_norm_bwd", q, k, (dq, dk), (dq_out, dk_out), (q_weight, k_weight), (q_rstd, k_rstd),
                (dq_weight, dk_weight), cos, sin, start, end, norm, mode, True, ((), (wp, wn)), stream)
+
+
+# ------------------------------------------------------------------------
+# pages of the cache, slots and positions for a batch of requests
+# ------------------------------------------------------------------------
+
+
+def _pages_args(kv_len, n, what, page_table, free_pages, free_count):
+    device = kv_len.device
+    for t, name in ((kv_len, "kv_len"), (n, what), (free_pages, "free_pages"), (free_count, "free_count")):
+        if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
+            _refuse(f"{name} must be a contiguous int32 vector")
+        if not t.is_cuda or t.device != device:
+            _refuse(f"{name} must be a CUDA tensor on kv_len's device")
+    R, pt = kv_len.shape[0], page_table.shape
+    if n.shape[0] != R:
+        _refuse(f"{what} must have a number for each request of kv_len")
+    if free_count.shape[0] != 1:
+        _refuse("free_count must be one int32")
+    if page_table.dtype is not torch.int32 or len(pt) != 2 or pt[0] != R or page_table.device != device:
+        _refuse("page_table must be int32 (R, pages) on kv_len's device, with a contiguous last dim")
+    pst = page_table.stride()
+    if pt[1] > 1 and pst[1] != 1:
+        _refuse("page_table must be int32 (R, pages) on kv_len's device, with a contiguous last dim")
+    return (kv_len.data_ptr(), n.data_ptr(), R, page_table.data_ptr(), pt[1], pst[0] if R > 1 else pt[1],
+            free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr())
+
+
+def rope_partial_cache_grow(kv_len, new_tokens, page_table, free_pages, free_count, page_size: int, q_start, slots,
+                            positions=None, granted=None, stream=None) -> None:
+    """Pages, slots and positions for ``new_tokens[r]`` tokens of each request r that
+    holds ``kv_len[r]`` cached rows, all on the device.
+
+    In place: ``kv_len`` (int32, R), ``page_table`` (int32, (R, pages)) and
+    ``free_count`` (int32, one): pages come from the top of the stack
+    ``free_pages[:free_count]`` (int32), in the order of the requests.  Written:
+    ``q_start`` (int32, R + 1) and ``slots`` (int64, T; -1 for tokens without a
+    page and for the places behind the last token), and where given ``positions``
+    (int32, T) and ``granted`` (int32, R: 0 for a request that there are no
+    pages for, which stays as it is)."""
+    lib = _lib or load_library()
+    args = _pages_args(kv_len, new_tokens, "new_tokens", page_table, free_pages, free_count)
+    R, T = args[2], slots.shape[0]
+    for t, size, name, kind in ((q_start, R + 1, "q_start", torch.int32), (slots, T, "slots", torch.int64),
+                                (positions, T, "positions", torch.int32), (granted, R, "granted", torch.int32)):
+        if t is not None and (t.dtype is not kind or t.dim() != 1 or t.shape[0] != size or not t.is_contiguous() or
+                              t.device != kv_len.device):
+            _refuse(f"{name} must be a contiguous {kind} vector of {size} on kv_len's device")
+    _launch(lib.rope_partial_cache_grow,
+            (*args, page_size, q_start.data_ptr(), slots.data_ptr(), None if positions is None else positions.data_ptr(),
+             T, None if granted is None else granted.data_ptr()), stream, kv_len.device)
+
+
+def rope_partial_cache_trim(kv_len, new_len, page_table, free_pages, free_count, page_size: int, stream=None) -> None:
+    """Requests keep ``new_len[r]`` (int32, R) of their ``kv_len[r]`` rows: the pages
+    behind them go back onto the stack, their entries in the table become -1, and
+    ``kv_len`` and ``free_count`` change in place."""
+    lib = _lib or load_library()
+    args = _pages_args(kv_len, new_len, "new_len", page_table, free_pages, free_count)
+    _launch(lib.rope_partial_cache_trim, (*args, page_size), stream, kv_len.device)

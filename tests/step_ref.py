@@ -44,3 +44,50 @@ def norm_bwd(g, x, w, r, cos, sin, start, end, n0, n1, mode):
     dmag[..., n0:n1] = r[..., None] * (abs(w) * mn + abs(u) * most)
     axes = tuple(range(g.ndim - 1))
     return dx, dmag, (gn * u).sum(axes), (mn * abs(u)).sum(axes)
+
+
+def grow(kv_len, n, table, free, count, page, T):
+    """One request after the other, as the header says; changes copies, returns them."""
+    kv_len, table = kv_len.copy(), table.copy()
+    have = top = max(0, min(int(count), len(free)))
+    slots, positions = np.full(T, -1, np.int64), np.zeros(T, np.int64)
+    start, granted, asked = [0], [], 0
+    room = table.shape[1] * page
+    for r in range(len(kv_len)):
+        old, new = min(max(int(kv_len[r]), 0), room), max(int(n[r]), 0)
+        ok = old + new <= room
+        if ok:
+            need = -(-(old + new) // page) - -(-old // page)
+            asked += need
+            ok = need == 0 or asked <= have
+        if ok:
+            for k in range(need):
+                table[r, -(-old // page) + k] = free[have - 1 - (asked - need + k)]
+            top -= need
+        for i in range(new):
+            t = start[-1] + i
+            if t < T:
+                positions[t] = old + i
+                if ok:
+                    slots[t] = int(table[r, (old + i) // page]) * page + (old + i) % page
+        kv_len[r] = old + new if ok else old
+        granted.append(int(ok))
+        start.append(start[-1] + new)
+    return kv_len, table, top, np.array(start), slots, positions, np.array(granted)
+
+
+def trim(kv_len, keep, table, free, count, page):
+    kv_len, table, free = kv_len.copy(), table.copy(), free.copy()
+    count = max(0, min(int(count), len(free)))
+    gone = []
+    for r in range(len(kv_len)):
+        old = min(max(int(kv_len[r]), 0), table.shape[1] * page)
+        new = min(max(int(keep[r]), 0), old)
+        for p in range(-(-new // page), -(-old // page)):
+            gone.append(table[r, p])
+            table[r, p] = -1
+        kv_len[r] = new
+    for k, page_number in enumerate(reversed(gone)):
+        if count + k < len(free):
+            free[count + k] = page_number
+    return kv_len, table, free, min(count + len(gone), len(free))
