@@ -6,6 +6,8 @@
  *                                     the rotation of a slice of them, in one pass
  *   rope_partial_cache_grow / _trim   pages, slots and positions for a batch's new
  *                                     tokens, made on the device, and pages given back
+ *   rope_partial_latent_attention     attention over a cache of latent rows, one for
+ *                                     all heads, whose first lanes are the values
  *
  * Conventions are those of rope_partial.h and rope_serving.h: plain C, device
  * pointers on the current CUDA device, int64 sizes, ELEMENT strides, the
@@ -182,6 +184,59 @@ rope_status_t rope_partial_cache_trim(int32_t* kv_len, const int32_t* new_len, i
                                       int64_t page_table_stride, int32_t* free_pages,
                                       int64_t free_capacity, int32_t* free_count, int64_t page_size,
                                       rope_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over latent rows
+ * ------------------------------------------------------------------------ */
+
+/*
+ * rope_partial_latent_attention -- rope_partial_tree_attention over a cache that has one
+ * row a token for all query heads, of which the first v_dim lanes are the value:
+ *
+ *     s_j = scale * q . k_j        out = sum_j exp(s_j) k_j[0 .. v_dim) / sum_j exp(s_j)
+ *
+ * (keys and values of all heads made from one latent vector, with the heads' own
+ * matrices multiplied into q and out; the row's other lanes, a rotated part that
+ * all heads share, say, count for the score alone).
+ *
+ *   cache        one head, no values (v null, v_dim 0); any of its types.  Such rows
+ *                are written by rope_partial_cache_write and read by
+ *                rope_partial_cache_read as any keys are.
+ *   v_dim        the lanes of the value, and of a row of out
+ *   other arguments, requests, trees, lengths, masks and the workspace
+ *                as for rope_partial_tree_attention: chains without a tree, tokens that
+ *                see no row (0 and -inf), tokens outside every request (left as
+ *                they are), captured calls, and that a row has no effect on a token that
+ *                does not see it.  max_q is a hint; sums are fp32; waits are
+ *                bounded.
+ *
+ * Types: a 16-bit cache must have the type of q; an 8-bit cache (whose scales may have any
+ * sign) goes with either.  Sizes: k_dim and v_dim multiples of 16, 16 <= v_dim <= k_dim <=
+ * 576, v_dim <= 512.  Rows of q, out and the cache must start on 16-byte boundaries.
+ * Products run on tensor cores in bf16 (bf16 caches) or fp16 (the others) with fp32
+ * accumulation.  exp(s), for 8-bit caches times the row's scale, is rounded to that type
+ * once; in fp16 what is below 2^-21 of the token's largest loses bits and below 2^-31
+ * vanishes (scales below 2^-80 are as small there as they are).  For 8-bit caches q is
+ * rounded to fp16 after a power of two that brings the row's largest lane to [1, 2).
+ * 16-bit rows in pages of a multiple of 8 rows are the fast case.
+ */
+rope_status_t rope_partial_latent_attention(const rope_kv_cache_t* cache, const void* q,
+                                            rope_dtype_t dtype, int64_t Tq, int64_t Hq, int64_t v_dim,
+                                            const int64_t q_stride[2], const int32_t* q_start,
+                                            const int32_t* kv_len, int64_t R, int64_t max_q,
+                                            const int32_t* page_table, int64_t max_pages,
+                                            int64_t page_table_stride, const int64_t* tree,
+                                            int64_t tree_words, void* out,
+                                            const int64_t out_stride[2], float* lse, double scale,
+                                            void* workspace, int64_t workspace_bytes,
+                                            rope_stream_t stream);
+
+/* The bytes of workspace that such a call needs on the current device (sm_count > 0: on a
+   device with that many SMs, without touching the GPU). */
+rope_status_t rope_partial_latent_attention_workspace(const rope_kv_cache_t* cache,
+                                                      rope_dtype_t dtype, int64_t Hq, int64_t v_dim,
+                                                      int64_t max_q, int32_t sm_count,
+                                                      int64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,7 @@ _BINDING_NAMES = (
     "rope_partial_inplace_bwd_axes", "KVCache", "rope_partial_cache_write",
     "rope_partial_cache_read", "rope_partial_tree_attention", "rope_partial_tree_mask",
     "tree_attention_workspace", "rope_partial_norm_fwd", "rope_partial_norm_bwd", "norm_workspace", "rope_partial_cache_grow",
-    "rope_partial_cache_trim", "prepare_fwd", "prepare_bwd", "RopeError", "load_library",
+    "rope_partial_cache_trim", "rope_partial_latent_attention", "latent_attention_workspace", "prepare_fwd", "prepare_bwd", "RopeError", "load_library",
     "library_path",
 )
 

@@ -32,6 +32,8 @@ And on either side of that cache in a model's step:
     rope_partial_cache_grow(kv_len, new_tokens, page_table, free_pages, free_count, page_size,
                             q_start, slots, ...)
     rope_partial_cache_trim(kv_len, new_len, page_table, free_pages, free_count, page_size)
+    rope_partial_latent_attention(q, cache, q_start, kv_len, page_table, out, ...)
+    latent_attention_workspace(q, cache, v_dim, max_q)
 """
 from __future__ import annotations
 
@@ -158,6 +160,9 @@ def load_library() -> ctypes.CDLL:
             ("rope_partial_norm_bwd", norm + [vp, vp, vp, vp, i64, i64, ctypes.c_int, vp, i64, vp]),
             ("rope_partial_norm_workspace", [i64, i32, i64p]),
             ("rope_partial_cache_grow", [vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]),
+            ("rope_partial_latent_attention", [vp, vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, i64, i64, vp, i64,
+                                               i64, vp, i64, vp, vp, vp, d, vp, i64, vp]),
+            ("rope_partial_latent_attention_workspace", [vp, ctypes.c_int, i64, i64, i64, i32, i64p]),
             ("rope_partial_cache_trim", [vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp])):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
@@ -701,20 +706,10 @@ def tree_attention_workspace(q, cache: KVCache, max_q: int) -> torch.Tensor:
     return torch.empty(need.value, dtype=torch.uint8, device=cache.device)
 
 
-def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, out, lse=None, tree=None,
-                                scale=None, max_q=None, workspace=None, stream=None) -> None:
-    """Attention of drafted tokens over the cache, into ``out`` (Tq, Hq, v_dim)
-    and, where given, ``lse`` (Tq, Hq) fp32.
-
-    ``q`` (Tq, Hq, k_dim); request r has the tokens [q_start[r], q_start[r+1])
-    and kv_len[r] cached rows, the last of which are those tokens' own, in the
-    pages page_table[r] (int32).  ``tree`` (Tq, words) int64 holds the bits of
-    the drafted tokens that each token sees (``rope_partial_tree_mask``); None
-    is a chain.  ``scale`` defaults to 1 / sqrt(k_dim), ``max_q`` (the most
-    tokens of a request) to Tq, and the workspace is made for the call, on its
-    stream, when none is given."""
-    lib = _lib or load_library()
-    dev, kd, vd = cache.device, cache.k_dim, cache.v_dim
+def _attention(fn, q, cache, vd, sizes, make_workspace, q_start, kv_len, page_table, out, lse, tree, scale, max_q,
+               workspace, stream):
+    """The checks and the launch of the attention calls; ``sizes`` go behind Hq."""
+    dev, kd = cache.device, cache.k_dim
     dtype = DTYPE_CODE.get(q.dtype)
     shape = q.shape
     if len(shape) != 3 or shape[2] != kd or dtype is None:
@@ -748,22 +743,40 @@ def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, 
     if max_q is None:
         max_q = max(1, Tq)
     if workspace is None and stream is None:
-        workspace = tree_attention_workspace(q, cache, max_q)
+        workspace = make_workspace(max_q)
     elif workspace is None:
         # made on the stream that uses it: memory that another stream's work frees
         # is handed out again before that work has run
         with torch.cuda.stream(_stream_of(stream, dev)):
-            workspace = tree_attention_workspace(q, cache, max_q)
+            workspace = make_workspace(max_q)
     for t in (q, out, q_start, kv_len, page_table, lse, tree, workspace):
         if t is not None and t.device != dev:
             _refuse("every tensor must be on the cache's device")
     if not workspace.is_contiguous():
         _refuse("workspace must be contiguous")
-    _launch(lib.rope_partial_tree_attention,
-            (cache._ref, q.data_ptr(), dtype, Tq, Hq, _pack2(qs[0], qs[1]), q_start.data_ptr(),
+    _launch(fn,
+            (cache._ref, q.data_ptr(), dtype, Tq, Hq, *sizes, _pack2(qs[0], qs[1]), q_start.data_ptr(),
              kv_len.data_ptr(), R, max_q, page_table.data_ptr(), pt[1], pst[0] if R > 1 else pt[1], tp, words,
              out.data_ptr(), _pack2(os_[0], os_[1]), lp, kd ** -0.5 if scale is None else scale,
              workspace.data_ptr(), workspace.nbytes), stream, dev)
+
+
+def rope_partial_tree_attention(q, cache: KVCache, q_start, kv_len, page_table, out, lse=None, tree=None,
+                                scale=None, max_q=None, workspace=None, stream=None) -> None:
+    """Attention of drafted tokens over the cache, into ``out`` (Tq, Hq, v_dim)
+    and, where given, ``lse`` (Tq, Hq) fp32.
+
+    ``q`` (Tq, Hq, k_dim); request r has the tokens [q_start[r], q_start[r+1])
+    and kv_len[r] cached rows, the last of which are those tokens' own, in the
+    pages page_table[r] (int32).  ``tree`` (Tq, words) int64 holds the bits of
+    the drafted tokens that each token sees (``rope_partial_tree_mask``); None
+    is a chain.  ``scale`` defaults to 1 / sqrt(k_dim), ``max_q`` (the most
+    tokens of a request) to Tq, and the workspace is made for the call, on its
+    stream, when none is given."""
+    lib = _lib or load_library()
+    _attention(lib.rope_partial_tree_attention, q, cache, cache.v_dim, (),
+               lambda most: tree_attention_workspace(q, cache, most), q_start, kv_len, page_table, out, lse, tree,
+               scale, max_q, workspace, stream)
 
 
 # ------------------------------------------------------------------------
@@ -963,3 +976,37 @@ def rope_partial_cache_trim(kv_len, new_len, page_table, free_pages, free_count,
     lib = _lib or load_library()
     args = _pages_args(kv_len, new_len, "new_len", page_table, free_pages, free_count)
     _launch(lib.rope_partial_cache_trim, (*args, page_size), stream, kv_len.device)
+
+
+# ------------------------------------------------------------------------
+# attention over latent rows
+# ------------------------------------------------------------------------
+
+
+def latent_attention_workspace(q, cache: KVCache, v_dim: int, max_q: int) -> torch.Tensor:
+    """A workspace for rope_partial_latent_attention with such a ``q``, ``cache``,
+    ``v_dim`` and ``max_q``.  A program keeps it: calls that follow each other on
+    one stream can share it."""
+    lib = _lib or load_library()
+    if q.dim() != 3 or q.dtype not in DTYPE_CODE:
+        _refuse("q must be (tokens, heads, dim) of bf16 or fp16")
+    need = ctypes.c_int64()
+    with torch.cuda.device(cache.device):
+        st = lib.rope_partial_latent_attention_workspace(cache._ref, DTYPE_CODE[q.dtype], q.shape[1], int(v_dim),
+                                                         int(max_q), 0, ctypes.byref(need))
+    _raise_for(lib, st)
+    return torch.empty(need.value, dtype=torch.uint8, device=cache.device)
+
+
+def rope_partial_latent_attention(q, cache: KVCache, q_start, kv_len, page_table, out, lse=None, tree=None,
+                                  scale=None, max_q=None, workspace=None, stream=None) -> None:
+    """rope_partial_tree_attention over a cache of latent rows (one head, keys only):
+    one row a token for all heads of ``q`` (Tq, Hq, k_dim), whose first v_dim lanes
+    are its value, v_dim being the last size of ``out`` (Tq, Hq, v_dim)."""
+    lib = _lib or load_library()
+    if out.dim() != 3:
+        _refuse("out must be (tokens, heads, v_dim)")
+    vd = out.shape[2]
+    _attention(lib.rope_partial_latent_attention, q, cache, vd, (vd,),
+               lambda most: latent_attention_workspace(q, cache, vd, most), q_start, kv_len, page_table, out, lse,
+               tree, scale, max_q, workspace, stream)

@@ -31,8 +31,10 @@ CU_SOURCES = ["rope_kernels_bf16.cu", "rope_kernels_fp16.cu", "rope_kernels_fp32
               "rope_tile_fp16.cu", "rope_tile_fp8.cu", "rope_tile_int8.cu", "rope_tree_launch.cu",
               "rope_norm_fwd_bf16.cu", "rope_norm_fwd_fp16.cu", "rope_norm_fwd_fp32.cu",
               "rope_norm_bwd_bf16.cu", "rope_norm_bwd_fp16.cu", "rope_norm_bwd_fp32.cu",
-              "rope_norm_launch.cu", "rope_pages.cu"]
-CPP_SOURCES = ["rope_host.cpp", "rope_serving_host.cpp", "rope_norm_host.cpp", "rope_pages_host.cpp"]
+              "rope_norm_launch.cu", "rope_pages.cu", "rope_latent_bf16.cu", "rope_latent_fp16.cu",
+              "rope_latent_fp8.cu", "rope_latent_int8.cu", "rope_latent_launch.cu"]
+CPP_SOURCES = ["rope_host.cpp", "rope_serving_host.cpp", "rope_norm_host.cpp", "rope_pages_host.cpp",
+               "rope_latent_host.cpp"]
 
 
 def _nvcc() -> str:

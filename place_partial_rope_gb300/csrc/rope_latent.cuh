@@ -1,0 +1,880 @@
+// rope_latent.cuh -- attention of many query heads over a paged cache of latent rows (one
+// row a token for all heads, whose first lanes are the value too), on tcgen05.
+//
+// Mathematics, with Q the query rows (tokens x heads) of a request and C its cache rows:
+//     S^T = C Q^T    P^T = 2^(S^T scale - m)    O^T = V^T P^T,  V = C's first lanes
+// in that transposed form: cache rows (and value lanes) are the 128 or 64 lanes of tensor
+// memory, query rows its columns.  A row's 512 sums of O in fp32 fill a quarter of a
+// lane's 512 columns so for 64 query rows (the other way round, 64 rows would use half of
+// the lanes and all columns), few query rows (16 or 32 heads) make narrow, cheap
+// products, and the two products take the same tile of C from shared memory: the first
+// with the sum along its lines, the second with it across them.
+//   The maximum that weights refer to may lag: it moves (and O and l shrink) when a score
+// has passed it by more than 2^8, so that a tile costs one vote instead of a maximum over
+// lanes.  `ref` is that maximum less a bias (7 for fp16 weights, which then stay between
+// 2^-24 and 2^15), rounded to a whole number; everything is counted from it.  8-bit rows: the score has the row's
+// scale u, the weight is 2^(s - ref) u and refers to the largest s + log2 u that the query
+// row sees (u counted as 2^-80 at least there), so weights keep that range; l is
+// the sum of 2^(s - ref).
+//
+// How.  One block an SM, 14 warps with a role each:
+//   0-3   softmax.  A thread has 2 of a tile's 64 rows and every fourth pair of columns;
+//         sums l stay in its registers for the whole run.  P^T goes to shared memory by
+//         transposing stores.  O is read and written out when a run ends.
+//   4     the one thread that issues tcgen05.mma.
+//   5     fetches tiles by tensor copies (16-bit rows, pages of a multiple of 8 rows), and
+//         walks the division of the work for all.
+//   6-13  helpers: bring the queries of a run, and other tiles: 16-bit rows by
+//         asynchronous copies, 8-bit rows as codes that become fp16 on the way.
+// Two tiles of 64 rows x 576 lanes beside 64 query rows fill shared memory.
+//   Every wait is bounded; one that gives up sets `dead`, the threads of a role leave
+// together, and every result that the block has a share in becomes NaN.
+#pragma once
+#include <cuda.h>
+
+#include "rope_latent.h"
+#include "rope_tc.cuh"
+
+namespace rope {
+
+template <int STORE_, int ROWS_, bool BOXES_>
+struct LatentCfg {
+    static constexpr int STORE = STORE_, ROWS = ROWS_, TN = kLatentKeys;
+    static constexpr bool BOXES = BOXES_;
+    static constexpr bool kWide = STORE == ROPE_CACHE_BF16 || STORE == ROPE_CACHE_FP16;
+    static constexpr bool BF16 = STORE == ROPE_CACHE_BF16;
+    static constexpr int CHUNK = TN * 128;  // 64 lanes of a tile, in bytes
+    static constexpr int CHUNKS = kLatentLanes / 64;
+    static constexpr int Q_CHUNK = ROWS * 128, Q_BYTES = CHUNKS * Q_CHUNK;
+    static constexpr int STAGE = CHUNKS * CHUNK, STAGES = 2;
+    static constexpr int K_AT = Q_BYTES, P_AT = K_AT + STAGES * STAGE, SYNC_AT = P_AT + ROWS * 128;
+    static constexpr int kSmemMax = 232448;
+    static constexpr float kBias = BF16 ? 0.0f : 7.0f, kLag = 8.0f;
+    // tensor memory: O^T in tiles of 128 value lanes, then two S^T
+    static constexpr uint32_t S_COL = 4 * ROWS;
+};
+
+struct LatentSync {
+    unsigned long long full[2], empty[2], s_full[2], p_full, q_full, q_empty, done;
+    uint32_t tmem;
+    volatile uint32_t dead;
+    volatile uint32_t patch[4];  // of run r at r % 4: values were taken out
+    volatile uint32_t runs;      // runs that are in `run`, and
+    volatile uint32_t last;      // how many there will be (~0: not known yet)
+    volatile uint32_t taken;     // runs that the softmax has begun
+    volatile uint32_t beat;      // tiles done
+    RunAt run[4];                // run r at r % 4
+    float red[4][64], fac[64], ref[64];
+};
+
+template <int ROWS>
+__device__ __forceinline__ void latent_ld(float* r, uint32_t at) {
+    if constexpr (ROWS == 64)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+            "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+            : ROPE_R8(r, 0), ROPE_R8(r, 8), ROPE_R8(r, 16), ROPE_R8(r, 24)
+            : "r"(at)
+            : "memory");
+    else if constexpr (ROWS == 32)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+            "%14, %15}, [%16];"
+            : ROPE_R8(r, 0), ROPE_R8(r, 8)
+            : "r"(at)
+            : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : ROPE_R8(r, 0)
+                     : "r"(at)
+                     : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void latent_here(float* r) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) asm volatile("" : ROPE_B8(r, i));
+}
+
+// M x N, fp32 sums; A_MN: the first factor's lines run along its rows (values).
+template <bool BF16, int M, int N, bool A_MN>
+__host__ __device__ constexpr uint32_t latent_shape() {
+    return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((A_MN ? 1u : 0u) << 15) |
+           (uint32_t(N / 8) << 17) | (uint32_t(M / 16) << 24);
+}
+
+// The logarithm of the sum l 2^ref, ref a whole number: its whole part is added apart
+// from l's own powers of two, so that a far reference costs no bits.
+__device__ __forceinline__ float latent_lse(float ref, float l) {
+    if (l == 0.0f) return -INFINITY;
+    if (!(l >= 1.17549435e-38f && l <= 3.40282347e+38f)) return (ref + log2f(l)) * 0.69314718055994531f;
+    const uint32_t bits = __float_as_uint(l);
+    const float whole = ref + static_cast<float>(int(bits >> 23) - 127);
+    return (whole + log2f(__uint_as_float((bits & 0x007fffffu) | 0x3f800000u))) * 0.69314718055994531f;
+}
+
+// Whether any of the softmax's 128 threads says so.
+__device__ __forceinline__ bool softmax_any(bool mine) {
+    uint32_t any;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, 128, p;\n"
+                 "selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(any)
+                 : "r"(uint32_t(mine))
+                 : "memory");
+    return any != 0;
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <class C>
+struct Latent {
+    using Cfg = C;
+    const TreeArgs& a;
+    char* smem;
+    LatentSync* sync;
+    uint32_t tmem;
+
+    __device__ __forceinline__ int chunks() const { return (a.Dk + 63) / 64; }
+    __device__ __forceinline__ int value_tiles() const { return (a.Dv + 127) / 128; }
+    __device__ __forceinline__ uint32_t stage(uint32_t n) const { return smem_addr(smem + C::K_AT) + (n & 1) * C::STAGE; }
+
+    // ---------------------------------------------------------- waits
+
+    __device__ __forceinline__ void wait(unsigned long long* b, uint32_t parity) const {
+        for (uint32_t i = 0; i < kSpins; ++i) {
+            if (bar_test(b, parity)) return;
+            if (sync->dead) return;
+        }
+        sync->dead = 1;
+    }
+
+    // For those that may rightly wait for a whole run: gives up when no tile has been
+    // done between two such stretches.
+    __device__ __forceinline__ void wait_run(unsigned long long* b, uint32_t parity) const {
+        for (uint32_t seen = ~0u;;) {
+            for (uint32_t i = 0; i < kSpins; ++i) {
+                if (bar_test(b, parity)) return;
+                if (sync->dead) return;
+            }
+            const uint32_t now = sync->beat;
+            if (now == seen) break;
+            seen = now;
+        }
+        sync->dead = 1;
+    }
+
+    __device__ __forceinline__ bool given_up() const { return __any_sync(0xffffffffu, sync->dead); }
+
+    // Run r, when the block has one.
+    __device__ __forceinline__ bool take(uint32_t r, RunAt& x) const {
+        for (uint32_t seen = ~0u;;) {
+            for (uint32_t i = 0; i < kPolls; ++i) {
+                if (sync->runs > r) {
+                    __threadfence_block();
+                    x = sync->run[r & 3];
+                    return true;
+                }
+                if (sync->last <= r || sync->dead) return false;
+            }
+            const uint32_t now = sync->beat;
+            if (now == seen) break;
+            seen = now;
+        }
+        sync->dead = 1;
+        return false;
+    }
+
+    // ---------------------------------------------------------- the walk, and tensor copies
+
+    // Run r for the other roles, whose place the softmax has left: with tensor copies the
+    // tiles' places see to that (a copy is at most two tiles ahead), else it is waited for.
+    __device__ __forceinline__ void publish(const RunAt& x, uint32_t r, bool there, int lane) const {
+        if (lane == 0) {
+            if (there) {
+                if constexpr (!C::BOXES) {
+                    uint32_t seen = ~0u, i = 0;
+                    while (r >= sync->taken + 4 && !sync->dead)
+                        if (++i == kPolls) {
+                            i = 0;
+                            if (sync->beat == seen) sync->dead = 1;
+                            seen = sync->beat;
+                        }
+                }
+                sync->run[r & 3] = x;
+                __threadfence_block();
+                sync->runs = r + 1;
+            } else {
+                __threadfence_block();
+                sync->last = r;
+            }
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* map) const {
+        const int lane = int(threadIdx.x) & 31;
+        Walk walk = walk_from<C::ROWS, C::TN>(a, place);
+        RunAt x;
+        uint32_t run = 0, n = 0;
+        bool first = true;
+        for (;; ++run) {
+            const bool there = next_run<C::ROWS, C::TN>(a, walk, x);
+            if (first && lane == 0)
+                a.meta[blockIdx.x] = there ? meta_of(place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, place.lead};
+            first = false;
+            publish(x, run, there, lane);
+            if (!there || given_up()) break;
+            if constexpr (C::BOXES)
+                for (int it = 0; it < x.count; ++it, ++n) {
+                    // a lane's box of rows of one page; rows that are not there are filled with zeros
+                    const int j = (x.t0 + it) * C::TN + lane * a.box;
+                    int page = -1;
+                    uint32_t p, off = 0;
+                    if (lane < C::TN / a.box && j < x.rq.len) {
+                        a.div_page.divmod(uint32_t(j), p, off);
+                        page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
+                    }
+                    if (n >= 2) wait(&sync->empty[n & 1], (n / 2 - 1) & 1);
+                    // once a wait has given up, the place may be in use, or its last copy under way
+                    if (given_up()) break;
+                    unsigned long long* bar = &sync->full[n & 1];
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+                                     "r"(chunks() * C::CHUNK)
+                                     : "memory");
+                    __syncwarp();
+                    if (lane < C::TN / a.box)
+#pragma unroll 1
+                        for (int c = 0; c < chunks(); ++c)
+                            asm volatile(
+                                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(stage(n) + c * C::CHUNK +
+                                                                            lane * a.box * 128),
+                                "l"(map), "r"(c * 64), "r"(0), "r"(int(off)), "r"(page), "r"(smem_addr(bar))
+                                : "memory");
+                }
+        }
+        // the block may not end before its copies have, whether or not anyone still waits for them
+        if constexpr (C::BOXES)
+            for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k)
+                for (uint32_t i = 0; i < kSpins && !bar_test(&sync->full[k & 1], (k / 2) & 1); ++i) {
+                }
+    }
+
+    // ---------------------------------------------------------- helpers
+
+    // Where 16 bytes (8 lanes from 8 piece) of line `row` lie.
+    template <int BYTES>
+    static __device__ __forceinline__ uint32_t line_at(int row, int piece) {
+        return uint32_t(piece >> 3) * BYTES + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+    }
+
+    // The queries of a run: eight threads a row, 32 rows a pass.
+    __device__ __forceinline__ void queries(const RunAt& x, uint32_t run, int id) const {
+        const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
+        const uint32_t to = smem_addr(smem);
+        const int pieces = a.Dk / 8;
+#pragma unroll 1
+        for (int row = id >> 3; row < C::ROWS; row += 32) {
+            const char* src = nullptr;
+            if (row < left) {
+                uint32_t tok, g;
+                a.div_group.divmod(uint32_t(first + row), tok, g);
+                src = a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] + int64_t(g) * a.q_st[1];
+            }
+            uint4 w[C::CHUNKS];
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c) {
+                const int piece = c * 8 + (id & 7);
+                w[c] = src && piece < pieces ? __ldg(reinterpret_cast<const uint4*>(src) + piece)
+                                             : make_uint4(0, 0, 0, 0);
+            }
+            if constexpr (!C::kWide) {
+                uint32_t most = 0;
+                float f[8];
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    widen8(w[c], a.bf16, f);
+                    most = max(most, most_of(f));
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+                const float p = row_power(most), by = one_over_power(p);
+                if ((id & 7) == 0) factors(run)[row] = row_factor(p, a.scale_log2);
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    widen8(w[c], a.bf16, f);
+                    w[c] = half8(f, by);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c)
+                sts128(to + line_at<C::Q_CHUNK>(row, c * 8 + (id & 7)), w[c].x, w[c].y, w[c].z, w[c].w);
+        }
+    }
+
+    __device__ __forceinline__ float* factors(uint32_t run) const {
+        return reinterpret_cast<float*>(smem + C::SYNC_AT + sizeof(LatentSync)) + (run & 1) * 64;
+    }
+    __device__ __forceinline__ float* scales(uint32_t n) const {
+        return reinterpret_cast<float*>(smem + C::SYNC_AT + sizeof(LatentSync)) + 128 + (n & 1) * 64;
+    }
+
+    // A cache row: its bytes, and its scale.
+    struct Row {
+        const char* p;  // null: there is none
+        float scale;
+    };
+
+    __device__ __forceinline__ Row row_of(const RunAt& x, int j) const {
+        Row r{nullptr, 0.0f};
+        if (j < x.rq.len) {
+            uint32_t p, off;
+            a.div_page.divmod(uint32_t(j), p, off);
+            const int page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
+            if (page >= 0 && page < a.pages) {
+                r.p = a.k + page * a.k_st[0] + int64_t(off) * a.k_st[1];
+                if constexpr (!C::kWide) r.scale = __ldg(a.ks + page * a.ks_st[0] + int64_t(off) * a.ks_st[1]);
+            }
+        }
+        return r;
+    }
+
+    // Queries of all runs and, without tensor copies, their tiles.
+    __device__ __forceinline__ void help(int id) const {
+        RunAt x;
+        uint32_t n = 0;
+        for (uint32_t run = 0;; ++run) {
+            if (!__all_sync(0xffffffffu, take(run, x))) return;
+            if (run > 0) wait_run(&sync->q_empty, (run - 1) & 1);
+            if (given_up()) return;
+            queries(x, run, id);
+            to_async_proxy();
+            bar_arrive(&sync->q_full);
+            if constexpr (!C::BOXES)
+                for (int it = 0; it < x.count; ++it, ++n) {
+                    const int row = id >> 3, sub = id & 7, pieces = a.Dk / 8;
+                    const uint32_t to = stage(n);
+                    const Row r[2] = {row_of(x, (x.t0 + it) * C::TN + row), row_of(x, (x.t0 + it) * C::TN + row + 32)};
+                    if constexpr (C::kWide) {
+                        if (n >= 2) wait(&sync->empty[n & 1], (n / 2 - 1) & 1);
+                        if (given_up()) return;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            for (int c = 0; c < chunks(); ++c) {
+                                const int piece = c * 8 + sub;
+                                const bool ok = r[i].p && piece < pieces;
+                                copy16(to + line_at<C::CHUNK>(row + 32 * i, piece), ok ? r[i].p + piece * 16 : a.k, ok);
+                            }
+                        copies_commit();
+                        copies_wait<0>();
+                    } else {
+                        // codes are asked for before the place is free
+                        uint2 w[2][C::CHUNKS];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int c = 0; c < C::CHUNKS; ++c) {
+                                const int piece = c * 8 + sub;
+                                w[i][c] = r[i].p && piece < pieces
+                                              ? __ldg(reinterpret_cast<const uint2*>(r[i].p) + piece)
+                                              : make_uint2(0, 0);
+                            }
+                        if (n >= 2) wait(&sync->empty[n & 1], (n / 2 - 1) & 1);
+                        if (given_up()) return;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                            for (int c = 0; c < C::CHUNKS; ++c)
+                                if (c < chunks())
+                                    sts128(to + line_at<C::CHUNK>(row + 32 * i, c * 8 + sub),
+                                           codes_to_half2<C::STORE, false>(w[i][c].x),
+                                           codes_to_half2<C::STORE, true>(w[i][c].x),
+                                           codes_to_half2<C::STORE, false>(w[i][c].y),
+                                           codes_to_half2<C::STORE, true>(w[i][c].y));
+                            if (sub == 0) scales(n)[row + 32 * i] = r[i].scale;
+                        }
+                    }
+                    to_async_proxy();
+                    bar_arrive(&sync->full[n & 1]);
+                }
+        }
+    }
+
+    // ---------------------------------------------------------- products
+
+    __device__ __forceinline__ void scores(uint32_t n) const {
+        constexpr uint32_t shape = latent_shape<C::BF16, C::TN, C::ROWS, false>();
+        const uint32_t q = smem_addr(smem), k = stage(n), to = tmem + C::S_COL + (n & 1) * C::ROWS;
+        wait(&sync->full[n & 1], (n / 2) & 1);
+        if (sync->dead) return;
+        tmem_after();
+        const int all = chunks();
+        for (int c = 0; c < all; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma_ss(to, smem_matrix(k + c * C::CHUNK + i * 32, 0), smem_matrix(q + c * C::Q_CHUNK + i * 32, 0), shape,
+                       c + i > 0);
+        mma_commit(&sync->s_full[n & 1]);
+    }
+
+    __device__ __forceinline__ void products() const {
+        constexpr uint32_t shape = latent_shape<C::BF16, 128, C::ROWS, true>();
+        const uint32_t p = smem_addr(smem + C::P_AT);
+        RunAt x;
+        uint32_t n = 0;
+        for (uint32_t run = 0; take(run, x); ++run) {
+            wait(&sync->q_full, run & 1);
+            scores(n);
+            if (x.count == 1) mma_commit(&sync->q_empty);
+            for (int it = 0; it < x.count; ++it, ++n) {
+                if (it + 1 < x.count) {
+                    scores(n + 1);
+                    if (it + 2 == x.count) mma_commit(&sync->q_empty);
+                }
+                wait(&sync->p_full, n & 1);
+                if (sync->dead) break;
+                tmem_after();
+                const int tiles = value_tiles();
+                for (int v = 0; v < tiles; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_ss(tmem + v * C::ROWS, smem_matrix(stage(n) + v * 2 * C::CHUNK + i * 2048, C::CHUNK),
+                               smem_matrix(p + i * 32, 0), shape, it > 0 || i > 0);
+                mma_commit(&sync->empty[n & 1]);
+                sync->beat = n + 1;
+            }
+            if (sync->dead) break;
+        }
+        // tensor memory may not go before the last product has
+        mma_commit(&sync->done);
+        for (uint32_t i = 0; i < kSpins && !bar_test(&sync->done, 0); ++i) {
+        }
+    }
+
+    // ---------------------------------------------------------- softmax
+
+    // The last tiles of a request: values of rows that are not there become zeros, and
+    // those of drafted rows that are not finite are taken out (see add_not_finite): a
+    // weight of 0 times them would reach the tokens that do not see the row.
+    __device__ __noinline__ void mend(uint32_t n, int from, int valid, uint32_t run) const {
+        const int pieces = value_tiles() * 16;
+        bool found = false;
+        for (int i = from * pieces + int(threadIdx.x); i < C::TN * pieces; i += 128) {
+            const int row = i / pieces;
+            const uint32_t at = stage(n) + line_at<C::CHUNK>(row, i - row * pieces);
+            if (row >= valid) {
+                sts128(at, 0, 0, 0, 0);
+                continue;
+            }
+            uint32_t w[4], bad = 0;
+            lds128(w, at);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                constexpr int KIND = C::BF16 ? ROPE_CACHE_BF16 : ROPE_CACHE_FP16;
+                if (not_finite<KIND>(w[j])) w[j] &= 0xffff0000u, bad = 1;
+                if (not_finite<KIND>(w[j] >> 16)) w[j] &= 0xffffu, bad = 1;
+            }
+            if (bad) {
+                found = true;
+                sts128(at, w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (found) sync->patch[run & 3] = 1;
+        __syncwarp();
+    }
+
+    // Columns of O times the factors of their rows.
+    __device__ __forceinline__ void shrink(uint32_t lanes) const {
+        const int tiles = value_tiles();
+#pragma unroll 1
+        for (int c = 0; c < tiles * C::ROWS; c += 16) {
+            float o[16];
+            tmem_ld16(o, lanes + c);
+            tmem_wait_ld();
+            tmem_here16(o);
+            const float* f = sync->fac + c % C::ROWS;
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f[i]);
+            tmem_st16(lanes + c, w);
+        }
+        tmem_wait_st();
+    }
+
+    __device__ __forceinline__ void softmax() const {
+        constexpr int NC = C::ROWS / 4, J = C::ROWS / 8;  // columns of a thread, blocks of eight
+        const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, k0 = warp * 16 + (lane >> 2),
+                  c0 = (lane & 3) * 2;
+        const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
+        // of the four 8 x 8 matrices of a transposing store, this thread names a line
+        const int mat = lane >> 3, qrow = (mat >> 1) * 8 + (lane & 7), chunk = warp * 2 + (mat & 1);
+        const uint32_t p_at = smem_addr(smem + C::P_AT) + qrow * 128 + ((chunk ^ (qrow & 7)) << 4);
+        RunAt x;
+        uint32_t n = 0;
+        for (uint32_t run = 0;; ++run) {
+            if (softmax_any(!take(run, x))) return;
+            if (tid == 0) sync->taken = run + 1;
+            const int prefix = x.rq.len - x.rq.n, first = x.m * C::ROWS;
+            float ref[NC], l[NC], qf[C::kWide ? 1 : NC];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) ref[i] = -3.40282347e+38f, l[i] = 0.0f;
+            for (int it = 0; it < x.count; ++it, ++n) {
+                const int tile = x.t0 + it;
+                const bool part = (tile + 1) * C::TN > prefix;  // more than context rows
+                float s[C::ROWS / 2], u[2] = {1.0f, 1.0f}, lu[2] = {0.0f, 0.0f};
+                wait(&sync->s_full[n & 1], (n / 2) & 1);
+                if (part || !C::kWide) wait(&sync->full[n & 1], (n / 2) & 1);  // what copies or helpers wrote is seen
+                __syncwarp();
+                tmem_after();
+                latent_ld<C::ROWS>(s, lanes + C::S_COL + (n & 1) * C::ROWS);
+                if constexpr (!C::kWide) {
+                    if (it == 0)  // written by the helpers before the tile
+#pragma unroll
+                        for (int i = 0; i < NC; ++i) qf[i] = factors(run)[(i >> 1) * 8 + c0 + (i & 1)];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        u[i] = scales(n)[k0 + 8 * i];
+                        lu[i] = log2f(fmaxf(fabsf(u[i]), 8.2718061255302767e-25f));  // 2^-80
+                    }
+                }
+                tmem_wait_ld();
+                latent_here<C::ROWS / 2>(s);
+                // scores in base 2: s becomes s scale (times the row's factors)
+                uint32_t seen = 0xffffffffu;
+#pragma unroll
+                for (int i = 0; i < C::ROWS / 2; ++i) {
+                    const int h = (i >> 1) & 1;
+                    if constexpr (C::kWide) s[i] *= a.scale_log2;
+                    else s[i] = s[i] * u[h] * qf[(i >> 2) * 2 + (i & 1)];
+                }
+                if (part) {
+                    seen = 0;
+#pragma unroll 1
+                    for (int i = 0; i < NC; ++i) {
+                        const int at = first + (i >> 1) * 8 + c0 + (i & 1);
+                        if (at >= x.rq.n * a.G) continue;
+                        const int tok = static_cast<int>(a.div_group.div(uint32_t(at)));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            seen |= (sees32(a, x.rq.qs, tok, prefix, x.rq.len, tile * C::TN + k0 + 8 * h) & 1u)
+                                    << ((i >> 1) * 4 + h * 2 + (i & 1));
+                    }
+#pragma unroll
+                    for (int i = 0; i < C::ROWS / 2; ++i)
+                        if (!(seen >> i & 1u)) s[i] = -INFINITY;
+                }
+                bool past = it == 0 || sync->dead;
+#pragma unroll
+                for (int i = 0; i < C::ROWS / 2; ++i)
+                    past = past || s[i] + lu[(i >> 1) & 1] - ref[(i >> 2) * 2 + (i & 1)] > C::kLag + C::kBias;
+                bool moved = false;
+                if (softmax_any(past)) {
+                    if (softmax_any(sync->dead)) return;
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        float top = fmaxf(s[(i >> 1) * 4 + (i & 1)] + lu[0], s[(i >> 1) * 4 + 2 + (i & 1)] + lu[1]);
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        if (lane < 4) sync->red[warp][(i >> 1) * 8 + c0 + (i & 1)] = top;
+                    }
+                    softmax_sync();
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        const int c = (i >> 1) * 8 + c0 + (i & 1);
+                        const float top = fmaxf(fmaxf(sync->red[0][c], sync->red[1][c]),
+                                                fmaxf(sync->red[2][c], sync->red[3][c]));
+                        float f = 1.0f;
+                        if (top - ref[i] > C::kLag + C::kBias || (it == 0 && top > -3.40282347e+38f)) {
+                            const float to = rintf(top - C::kBias);
+                            f = pow2(ref[i] - to);
+                            ref[i] = to;
+                            l[i] *= f;
+                        }
+                        if (tid < 4) sync->fac[c] = f;
+                    }
+                    softmax_sync();
+                    moved = it > 0;
+                }
+                // the weights' place is free, and O still, when the tile before is done
+                if (n > 0) wait(&sync->empty[(n - 1) & 1], ((n - 1) / 2) & 1);
+                __syncwarp();
+                if (moved) {
+                    tmem_after();
+                    shrink(lanes);
+                }
+#pragma unroll
+                for (int j = 0; j < J; j += 2) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // block j + k / 2, rows k % 2
+                        const int i = (j + (k >> 1)) * 4 + (k & 1) * 2, c = (j + (k >> 1)) * 2;
+                        float e[2];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            e[b] = pow2(s[i + b] - ref[c + b]);
+                            l[c + b] += e[b];
+                            if constexpr (!C::kWide) {
+                                e[b] *= u[k & 1];
+                                if (part && !(seen >> (i + b) & 1u)) e[b] = 0.0f;  // the scale need not be finite
+                            }
+                        }
+                        w[k] = pack2<C::BF16>(e[0], e[1]);
+                    }
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     p_at + j * 1024),
+                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+                if (part && C::STORE != ROPE_CACHE_INT8)
+                    mend(n, max(prefix - tile * C::TN, 0), x.rq.len - tile * C::TN, run);
+                to_async_proxy();
+                tmem_before();
+                bar_arrive(&sync->p_full);
+            }
+            // the run's results, when its last product is done
+            wait(&sync->empty[(n - 1) & 1], ((n - 1) / 2) & 1);
+            if (softmax_any(sync->dead)) return;
+            tmem_after();
+            finish(x, run, ref, l, lanes);
+            tmem_before();
+        }
+    }
+
+    __device__ __forceinline__ void finish(const RunAt& x, uint32_t run, const float* ref, float* l,
+                                           uint32_t lanes) const {
+        constexpr int NC = C::ROWS / 4;
+        const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, c0 = (lane & 3) * 2;
+        const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
+        const bool patch = sync->patch[run & 3] != 0;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = (i >> 1) * 8 + c0 + (i & 1);
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+            if (lane < 4) sync->red[warp][c] = l[i];
+            if (tid < 4) sync->ref[c] = ref[i];
+        }
+        softmax_sync();
+        if (tid == 0) sync->patch[run & 3] = 0;
+        if (tid < C::ROWS) {
+            const float all = sync->red[0][tid] + sync->red[1][tid] + sync->red[2][tid] + sync->red[3][tid];
+            const float m = all == 0.0f ? -INFINITY : sync->ref[tid];
+            sync->fac[tid] = x.slot >= 0 ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
+            if (x.slot >= 0) a.part_ml[x.slot * C::ROWS + tid] = make_float2(m, all);
+            else if (tid < left) {
+                const OutAt y = out_at(a, x.rq.qs, 0, first + tid);
+                if (y.lse) *y.lse = latent_lse(m, all);
+            }
+        }
+        softmax_sync();
+        const int tiles = value_tiles(), wide = tiles * 128;
+#pragma unroll 1
+        for (int b = 0; b < tiles * (C::ROWS / 16); ++b) {
+            const int r0 = b % (C::ROWS / 16) * 16, c = b / (C::ROWS / 16) * 128 + tid;  // its rows, the thread's lane
+            if (r0 >= left) continue;
+            float o[16];
+            tmem_ld16(o, lanes + (b / (C::ROWS / 16)) * C::ROWS + r0);
+            tmem_wait_ld();
+            tmem_here16(o);
+            if (patch)
+                for (int r = 0; r < 16; ++r)
+                    if (r0 + r < left) add_not_finite<C::STORE, C::TN, 1>(a, x, first + r0 + r, c, &o[r]);
+            if (x.slot >= 0) {
+                float* to = a.part + (x.slot * C::ROWS + r0) * wide + c;
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (r0 + r < left) to[r * wide] = o[r];
+                continue;
+            }
+            // two lanes side by side of every other row a thread
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                const float y = o[r] * sync->fac[r0 + r], z = o[r + 1] * sync->fac[r0 + r + 1];
+                const bool odd = lane & 1;
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? y : z, 1);
+                const int row = r0 + r + (odd ? 1 : 0), at = c & ~1;
+                if (row < left && at < a.Dv)
+                    *reinterpret_cast<uint32_t*>(out_at(a, x.rq.qs, 0, first + row).out + at * 2) =
+                        a.bf16 ? pack2<true>(odd ? other : y, odd ? z : other)
+                               : pack2<false>(odd ? other : y, odd ? z : other);
+            }
+        }
+        softmax_sync();  // fac, red and ref have been read
+    }
+
+    // The block's results, when one of its waits has given up: NaN in all of them, those
+    // of the block's other runs too, and in its parts, whose joined results then are NaN.
+    __device__ __noinline__ void give_up(const Place& place) const {
+        const int tid = int(threadIdx.x);
+        Walk walk = walk_from<C::ROWS, C::TN>(a, place);
+        RunAt x;
+        while (next_run<C::ROWS, C::TN>(a, walk, x)) {
+            const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
+            if (x.slot >= 0) {
+                for (int r = tid; r < C::ROWS; r += kLatentThreads)
+                    a.part_ml[x.slot * C::ROWS + r] = make_float2(-INFINITY, NAN);
+                continue;
+            }
+            for (int i = tid; i < left * (a.Dv / 2); i += kLatentThreads) {
+                const int row = i / (a.Dv / 2), c = i % (a.Dv / 2) * 2;
+                const OutAt to = out_at(a, x.rq.qs, 0, first + row);
+                *reinterpret_cast<uint32_t*>(to.out + c * 2) = 0x7fff7fffu;  // NaN of either type
+                if (c == 0 && to.lse) *to.lse = NAN;
+            }
+        }
+    }
+};
+
+template <class C>
+__global__ void __launch_bounds__(kLatentThreads, 1)
+    rope_latent_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map) {
+    extern __shared__ __align__(1024) char smem[];
+    static_assert(C::SYNC_AT + int(sizeof(LatentSync)) + (C::kWide ? 0 : 1024) <= C::kSmemMax, "shared memory");
+    LatentSync* sync = reinterpret_cast<LatentSync*>(smem + C::SYNC_AT);
+    const int warp = int(threadIdx.x) >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sync->full[i], C::BOXES ? 1 : 256);
+            bar_init(&sync->empty[i], 1);
+            bar_init(&sync->s_full[i], 1);
+        }
+        bar_init(&sync->p_full, 128);
+        bar_init(&sync->q_full, 256);
+        bar_init(&sync->q_empty, 1);
+        bar_init(&sync->done, 1);
+        sync->dead = 0;
+        for (int i = 0; i < 4; ++i) sync->patch[i] = 0;
+        sync->runs = 0;
+        sync->last = ~0u;
+        sync->taken = 0;
+        sync->beat = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sync->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    after_predecessor();
+    const Place place = find_place<C::ROWS, C::TN, kLatentThreads>(a, reinterpret_cast<int64_t*>(smem));
+    tmem_before();
+    __syncthreads();
+    tmem_after();
+    const Latent<C> it{a, smem, sync, sync->tmem};
+    if (warp < 4) {
+        it.softmax();
+    } else if (warp == 4) {
+        if ((threadIdx.x & 31) == 0) it.products();
+        __syncwarp();
+    } else if (warp == 5) {
+        it.fetches(place, &map);
+    } else {
+        it.help(int(threadIdx.x) - 192);
+    }
+    tmem_before();
+    __syncthreads();
+    if (sync->dead) it.give_up(place);
+    if (warp == 4) {
+        tmem_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sync->tmem));
+    }
+}
+
+// Puts the parts of each split (request, row tile) together: out = sum_p O_p 2^(m_p - m) /
+// sum_p l_p 2^(m_p - m).  A group cut by s block borders has s blocks here (times
+// gridDim.y), which share out its rows; a block's four teams take the parts of a row in
+// turn, four lanes a thread, and are added up in one order.
+template <int ROWS>
+__global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(const __grid_constant__ TreeArgs a) {
+    constexpr int TEAMS = 4;
+    __shared__ float4 sums[TEAMS][128];
+    __shared__ float2 team_ml[TEAMS];
+    after_predecessor();
+    const int64_t b = int64_t(blockIdx.x) + 1;
+    const TreeMeta w = a.meta[b];
+    if (w.nt == 0) return;
+    const int64_t from = w.u0 / w.chunk, to = (w.u0 + w.nt - 1) / w.chunk;
+    const int parts = static_cast<int>(to - from + 1);
+    const int qs = min(max(__ldg(a.q_start + w.r), 0), a.Tq);
+    const int n = min(max(__ldg(a.q_start + w.r + 1), qs), a.Tq) - qs;
+    const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(w.m) * ROWS));
+    const int tid = int(threadIdx.x), lane = tid & 127, team = tid >> 7, wide = (a.Dv + 127) / 128 * 128;
+    const int own = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y);
+    const int all = (parts - 1) * int(gridDim.y);
+    // part p: block `from` holds it second unless the group begins with the block's run
+    const int64_t second = from * w.chunk < w.u0 - w.lead ? 1 : 0;
+    auto slot = [&](int p) { return (from + p) * 2 + (p == 0 ? second : 0); };
+    for (int row = own; row < left; row += all) {
+        float top = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int p = team; p < parts; p += TEAMS) top = fmaxf(top, a.part_ml[slot(p) * ROWS + row].x);
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+        for (int p = team; p < parts; p += TEAMS) {
+            const float2 x = a.part_ml[slot(p) * ROWS + row];
+            const float f = pow2(x.x - base);
+            l += x.y * f;
+            if (lane * 4 < wide) {
+                const float4 y = *reinterpret_cast<const float4*>(a.part + (slot(p) * ROWS + row) * wide + lane * 4);
+                o.x += y.x * f;
+                o.y += y.y * f;
+                o.z += y.z * f;
+                o.w += y.w * f;
+            }
+        }
+        sums[team][lane] = o;
+        if (lane == 0) team_ml[team] = make_float2(top, l);
+        __syncthreads();
+        if (team == 0) {
+            top = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < TEAMS; ++t) top = fmaxf(top, team_ml[t].x);
+            const float m = top == -INFINITY ? 0.0f : top;
+            l = 0.0f;
+            o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int t = 0; t < TEAMS; ++t) {
+                const float f = pow2(team_ml[t].x - m);
+                const float4 y = sums[t][lane];
+                l += team_ml[t].y * f;
+                o.x += y.x * f;
+                o.y += y.y * f;
+                o.z += y.z * f;
+                o.w += y.w * f;
+            }
+            const float norm = l == 0.0f ? 0.0f : 1.0f / l;
+            const OutAt z = out_at(a, qs, 0, w.m * ROWS + row);
+            if (lane * 4 < a.Dv)
+                *reinterpret_cast<uint2*>(z.out + lane * 8) =
+                    a.bf16 ? make_uint2(pack2<true>(o.x * norm, o.y * norm), pack2<true>(o.z * norm, o.w * norm))
+                           : make_uint2(pack2<false>(o.x * norm, o.y * norm), pack2<false>(o.z * norm, o.w * norm));
+            if (lane == 0 && z.lse) *z.lse = latent_lse(top, l);
+        }
+        __syncthreads();
+    }
+}
+
+template <int STORE, int ROWS, bool BOXES>
+TreeKernel latent_instance() {
+    using C = LatentCfg<STORE, ROWS, BOXES>;
+    return TreeKernel{reinterpret_cast<const void*>(&rope_latent_kernel<C>),
+                      reinterpret_cast<const void*>(&rope_latent_join_kernel<ROWS>),
+                      C::SYNC_AT + int(sizeof(LatentSync)) + (C::kWide ? 0 : 1024), kLatentThreads, C::TN, 0.0f, 0};
+}
+
+template <int STORE>
+TreeKernel latent_pick(const LatentPlan& p) {
+    constexpr bool WIDE = STORE == ROPE_CACHE_BF16 || STORE == ROPE_CACHE_FP16;
+    if constexpr (WIDE)
+        if (p.boxes)
+            return p.rows == 16   ? latent_instance<STORE, 16, true>()
+                   : p.rows == 32 ? latent_instance<STORE, 32, true>()
+                                  : latent_instance<STORE, 64, true>();
+    return p.rows == 16   ? latent_instance<STORE, 16, false>()
+           : p.rows == 32 ? latent_instance<STORE, 32, false>()
+                          : latent_instance<STORE, 64, false>();
+}
+
+}  // namespace rope

@@ -1,0 +1,68 @@
+// rope_latent_launch.cu -- kernel choice, grid, workspace and launches of the attention
+// over latent rows.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "rope_latent.h"
+
+namespace rope {
+namespace {
+
+TreeKernel kernel_of(const LatentPlan& p) {
+    switch (p.store) {
+        case ROPE_CACHE_BF16: return latent_kernel_bf16(p);
+        case ROPE_CACHE_FP16: return latent_kernel_fp16(p);
+        case ROPE_CACHE_FP8: return latent_kernel_fp8(p);
+        default: return latent_kernel_int8(p);
+    }
+}
+
+}  // namespace
+
+// Tiles as narrow as the query rows allow.  Tensor copies take boxes of at least 8 rows of
+// a page, and a map has no dim of 0; 8-bit rows pass through registers anyway.
+LatentPlan choose_latent(int store, int64_t rows, int64_t pages, int64_t page_size) {
+    LatentPlan p{};
+    p.store = store;
+    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.boxes = (store == ROPE_CACHE_BF16 || store == ROPE_CACHE_FP16) && pages > 0 && page_size % 8 == 0;
+    return p;
+}
+
+rope_status_t latent_blocks(const LatentPlan& p, int sm_count, int* blocks, const char** err) {
+    if (sm_count > 0) {
+        *blocks = sm_count;
+        return ROPE_OK;
+    }
+    return tree_resident(kernel_of(p), blocks, err);
+}
+
+int64_t latent_workspace(const LatentPlan& p, int v_dim, int blocks) {
+    const int64_t rows = int64_t(2) * blocks * p.rows, wide = (v_dim + 127) / 128 * 128;
+    return rows * wide * int64_t(sizeof(float)) + rows * int64_t(sizeof(float2)) +
+           int64_t(blocks) * int64_t(sizeof(TreeMeta));
+}
+
+rope_status_t launch_latent(const LatentPlan& p, const TreeArgs& args, void* workspace, int blocks,
+                            rope_stream_t stream, const char** err) {
+    const TreeKernel k = kernel_of(p);
+    TreeArgs a = args;
+    const int64_t rows = int64_t(2) * blocks * p.rows, wide = (a.Dv + 127) / 128 * 128;
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part + rows * wide);
+    a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
+    CUtensorMap map{};
+    if (p.boxes) {
+        a.box = 8;
+        while (a.page_size % (2 * a.box) == 0 && 2 * a.box <= kLatentKeys) a.box *= 2;
+        const rope_status_t st = tree_map(&map, a.k, a.Dk, a, a.k_st, true, 64, err);
+        if (st != ROPE_OK) return st;
+    }
+    void* params[] = {&a, &map};
+    const rope_status_t st = tree_launch(k.main, blocks, 1, k.threads, k.smem, params, stream, err);
+    if (st != ROPE_OK || blocks < 2) return st;
+    void* join[] = {&a};
+    return tree_launch(k.join, blocks - 1, p.rows / 16 * 2, kLatentJoinThreads, 0, join, stream, err);
+}
+
+}  // namespace rope

@@ -79,6 +79,14 @@ struct TreeKernel {
     int regs;  // registers of a block that its warps share out among them; 0: they do not
 };
 
+// For the kernels of rope_latent.h, too: a kernel's blocks on the current device (allowing
+// its shared memory), the map of a cache tensor, and a launch.
+rope_status_t tree_resident(const TreeKernel& k, int* blocks, const char** err);
+rope_status_t tree_map(struct CUtensorMap_st* map, const void* base, int dim, const TreeArgs& a, const int64_t* st,
+                       bool wide, int lanes, const char** err);
+rope_status_t tree_launch(const void* f, int blocks, int per, int threads, int smem, void** params,
+                          rope_stream_t stream, const char** err);
+
 // defined in rope_tree_*.cu (up to 16 query rows) and rope_tile_*.cu
 TreeKernel narrow_kernel_bf16(const TreePlan& p);
 TreeKernel narrow_kernel_fp16(const TreePlan& p);

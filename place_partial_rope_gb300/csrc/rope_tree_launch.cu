@@ -194,6 +194,23 @@ rope_status_t tree_blocks(const TreePlan& p, int sm_count, int* blocks, const ch
     return st;
 }
 
+rope_status_t tree_resident(const TreeKernel& k, int* blocks, const char** err) {
+    Resident r;
+    const rope_status_t st = resident(k, &r, err);
+    if (st == ROPE_OK) *blocks = r.sms * r.per_sm;
+    return st;
+}
+
+rope_status_t tree_map(CUtensorMap* map, const void* base, int dim, const TreeArgs& a, const int64_t* st, bool wide,
+                       int lanes, const char** err) {
+    return map_of(map, base, dim, a, st, wide, lanes, err);
+}
+
+rope_status_t tree_launch(const void* f, int blocks, int per, int threads, int smem, void** params,
+                          rope_stream_t stream, const char** err) {
+    return launch(f, dim3(blocks, per), threads, smem, params, stream, err);
+}
+
 int64_t tree_workspace(const TreePlan& p, int blocks) {
     const int64_t rows = int64_t(2) * blocks * p.rows;
     return rows * p.dv * int64_t(sizeof(float)) + rows * int64_t(sizeof(float2)) +
