@@ -17,11 +17,11 @@
 // row sees (u counted as 2^-80 at least there), so weights keep that range; l is
 // the sum of 2^(s - ref).
 //
-// How.  One block an SM, 14 warps with a role each:
+// How.  One block an SM, 15 warps with a role each:
 //   0-3   softmax.  A thread has 2 of a tile's 64 rows and every fourth pair of columns;
 //         sums l stay in its registers for the whole run.  P^T goes to shared memory by
 //         transposing stores.  O is read and written out when a run ends.
-//   4     the one thread that issues tcgen05.mma.
+//   4, 14 issue tcgen05.mma: the scores', the values'.
 //   5     fetches tiles by tensor copies (16-bit rows, pages of a multiple of 8 rows), and
 //         walks the division of the work for all.
 //   6-13  helpers: bring the queries of a run, and other tiles: 16-bit rows by
@@ -50,21 +50,21 @@ struct LatentCfg {
     static constexpr int K_AT = Q_BYTES, P_AT = K_AT + STAGES * STAGE, SYNC_AT = P_AT + ROWS * 128;
     static constexpr int kSmemMax = 232448;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f, kLag = 8.0f;
+    static constexpr int MORE = kWide ? 0 : (3 * ROWS + 2 * TN) * 4;  // factors and scales
     // tensor memory: O^T in tiles of 128 value lanes, then two S^T
     static constexpr uint32_t S_COL = 4 * ROWS;
 };
 
 struct LatentSync {
-    unsigned long long full[2], empty[2], s_full[2], p_full, q_full, q_empty, done;
+    // a tile's groups of 128 lanes, and the lanes that are no value's: brought, and done with
+    unsigned long long full[2][5], empty[2][4], s_full[2], s_free[2], p_full, q_full, q_empty, run_full[3], done;
     uint32_t tmem;
     volatile uint32_t dead;
-    volatile uint32_t patch[4];  // of run r at r % 4: values were taken out
-    volatile uint32_t runs;      // runs that are in `run`, and
-    volatile uint32_t last;      // how many there will be (~0: not known yet)
+    volatile uint32_t patch[3];  // of run r at r % 3: values were taken out
     volatile uint32_t taken;     // runs that the softmax has begun
     volatile uint32_t beat;      // tiles done
-    RunAt run[4];                // run r at r % 4
-    float red[4][64], fac[64], ref[64];
+    RunAt run[3];                // run r at r % 3, when its barrier says so; of no tiles: there is none
+    float red[4][64], fac[64];  // of the softmax
 };
 
 template <int ROWS>
@@ -113,6 +113,30 @@ __device__ __forceinline__ float latent_lse(float ref, float l) {
     return (whole + log2f(__uint_as_float((bits & 0x007fffffu) | 0x3f800000u))) * 0.69314718055994531f;
 }
 
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t me;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(me));
+    return me;
+}
+
+// A product, and a commit, by the lane of the warp that has `me`.  a and b: the low words of
+// the descriptors (see smem_matrix), whose high words are one constant.
+template <bool ADD>
+__device__ __forceinline__ void mma_one(uint32_t me, uint32_t d, uint32_t a, uint32_t b, uint32_t shape) {
+    constexpr uint64_t HIGH = (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %4, 0;\n"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, %5;\n}" ::"r"(d),
+                 "l"(HIGH | a), "l"(HIGH | b), "r"(shape), "r"(me), "n"(ADD ? 1 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void commit_one(uint32_t me, unsigned long long* b) {
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_addr(b)),
+                 "r"(me)
+                 : "memory");
+}
+
 // Whether any of the softmax's 128 threads says so.
 __device__ __forceinline__ bool softmax_any(bool mine) {
     uint32_t any;
@@ -136,6 +160,10 @@ struct Latent {
 
     __device__ __forceinline__ int chunks() const { return (a.Dk + 63) / 64; }
     __device__ __forceinline__ int value_tiles() const { return (a.Dv + 127) / 128; }
+    // Groups of a tile's chunks that come and go together: the 128 lanes of each value
+    // tile, then the lanes that are no value's.
+    __device__ __forceinline__ int groups() const { return value_tiles() + (chunks() > 2 * value_tiles() ? 1 : 0); }
+    __device__ __forceinline__ int group_end(int g) const { return g < value_tiles() ? min(2 * g + 2, chunks()) : chunks(); }
     __device__ __forceinline__ uint32_t stage(uint32_t n) const { return smem_addr(smem + C::K_AT) + (n & 1) * C::STAGE; }
 
     // ---------------------------------------------------------- waits
@@ -167,55 +195,68 @@ struct Latent {
 
     // Run r, when the block has one.
     __device__ __forceinline__ bool take(uint32_t r, RunAt& x) const {
-        for (uint32_t seen = ~0u;;) {
-            for (uint32_t i = 0; i < kPolls; ++i) {
-                if (sync->runs > r) {
-                    __threadfence_block();
-                    x = sync->run[r & 3];
-                    return true;
-                }
-                if (sync->last <= r || sync->dead) return false;
-            }
-            const uint32_t now = sync->beat;
-            if (now == seen) break;
-            seen = now;
-        }
-        sync->dead = 1;
-        return false;
+        wait_run(&sync->run_full[r % 3], (r / 3) & 1);
+        if (sync->dead) return false;
+        x = sync->run[r % 3];
+        return x.count > 0;
+    }
+
+    // For group g's place of tile n: values are free when the product with them is done,
+    // the other lanes when the scores are.
+    __device__ __forceinline__ void wait_free(uint32_t n, int g) const {
+        if (n >= 2) wait(g < value_tiles() ? &sync->empty[n & 1][g] : &sync->s_full[n & 1], (n / 2 - 1) & 1);
+    }
+
+    // Until the last product of tile n is done.
+    __device__ __forceinline__ void wait_product(uint32_t n) const {
+        wait(&sync->empty[n & 1][value_tiles() - 1], (n / 2) & 1);
     }
 
     // ---------------------------------------------------------- the walk, and tensor copies
 
     // Run r for the other roles, whose place the softmax has left: with tensor copies the
     // tiles' places see to that (a copy is at most two tiles ahead), else it is waited for.
-    __device__ __forceinline__ void publish(const RunAt& x, uint32_t r, bool there, int lane) const {
+    __device__ __forceinline__ void publish(RunAt& x, uint32_t r, bool there, int lane) const {
         if (lane == 0) {
-            if (there) {
-                if constexpr (!C::BOXES) {
-                    uint32_t seen = ~0u, i = 0;
-                    while (r >= sync->taken + 4 && !sync->dead)
-                        if (++i == kPolls) {
-                            i = 0;
-                            if (sync->beat == seen) sync->dead = 1;
-                            seen = sync->beat;
-                        }
+            if constexpr (!C::BOXES) {
+                uint32_t seen = ~0u, i = 0;
+                while (r >= sync->taken + 3 && !sync->dead) {
+                    __nanosleep(200);
+                    if (++i == kSpins) {
+                        i = 0;
+                        if (sync->beat == seen) sync->dead = 1;
+                        seen = sync->beat;
+                    }
                 }
-                sync->run[r & 3] = x;
-                __threadfence_block();
-                sync->runs = r + 1;
-            } else {
-                __threadfence_block();
-                sync->last = r;
             }
+            if (!there) x.count = 0;
+            sync->run[r % 3] = x;
+            bar_arrive(&sync->run_full[r % 3]);
         }
         __syncwarp();
     }
 
+    struct Box {
+        int page, off;  // page -1: no such rows
+    };
+
+    __device__ __forceinline__ Box box_of(const RunAt& x, int tile, int lane, int boxes) const {
+        Box r{-1, 0};
+        const int j = tile * C::TN + lane * a.box;
+        if (lane < boxes && j < x.rq.len) {
+            uint32_t p, off;
+            a.div_page.divmod(uint32_t(j), p, off);
+            r.off = int(off);
+            r.page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
+        }
+        return r;
+    }
+
     __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* map) const {
-        const int lane = int(threadIdx.x) & 31;
+        const int lane = int(threadIdx.x) & 31, all = groups(), boxes = C::BOXES ? C::TN / a.box : 0;
         Walk walk = walk_from<C::ROWS, C::TN>(a, place);
         RunAt x;
-        uint32_t run = 0, n = 0;
+        uint32_t run = 0, n = 0, copies = 0;  // runs, tiles, groups of them asked for
         bool first = true;
         for (;; ++run) {
             const bool there = next_run<C::ROWS, C::TN>(a, walk, x);
@@ -224,40 +265,44 @@ struct Latent {
             first = false;
             publish(x, run, there, lane);
             if (!there || given_up()) break;
-            if constexpr (C::BOXES)
-                for (int it = 0; it < x.count; ++it, ++n) {
-                    // a lane's box of rows of one page; rows that are not there are filled with zeros
-                    const int j = (x.t0 + it) * C::TN + lane * a.box;
-                    int page = -1;
-                    uint32_t p, off = 0;
-                    if (lane < C::TN / a.box && j < x.rq.len) {
-                        a.div_page.divmod(uint32_t(j), p, off);
-                        page = __ldg(a.table + int64_t(x.r) * a.table_stride + p);
+            if constexpr (C::BOXES) {
+                // a lane's box of rows of one page, looked up a tile ahead; rows that are not there
+                // are filled with zeros
+                Box now = box_of(x, x.t0, lane, boxes);
+                bool on = true;
+                for (int it = 0; on && it < x.count; ++it, ++n) {
+                    const Box next = it + 1 < x.count ? box_of(x, x.t0 + it + 1, lane, boxes) : Box{-1, 0};
+                    const uint32_t to = stage(n) + lane * a.box * 128;
+                    for (int g = 0, c = 0; g < all; ++g) {
+                        wait_free(n, g);
+                        // once a wait has given up, the place may be in use, or its last copy under way
+                        on = !given_up();
+                        if (!on) break;
+                        const uint32_t bar = smem_addr(&sync->full[n & 1][g]);
+                        const int end = group_end(g);
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                                         "r"((end - c) * C::CHUNK)
+                                         : "memory");
+                        __syncwarp();
+                        ++copies;
+                        if (lane < boxes)
+                            for (int i = c; i < end; ++i)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                    "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + i * C::CHUNK),
+                                    "l"(map), "r"(i * 64), "r"(0), "r"(now.off), "r"(now.page), "r"(bar)
+                                    : "memory");
+                        c = end;
                     }
-                    if (n >= 2) wait(&sync->empty[n & 1], (n / 2 - 1) & 1);
-                    // once a wait has given up, the place may be in use, or its last copy under way
-                    if (given_up()) break;
-                    unsigned long long* bar = &sync->full[n & 1];
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
-                                     "r"(chunks() * C::CHUNK)
-                                     : "memory");
-                    __syncwarp();
-                    if (lane < C::TN / a.box)
-#pragma unroll 1
-                        for (int c = 0; c < chunks(); ++c)
-                            asm volatile(
-                                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                                "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(stage(n) + c * C::CHUNK +
-                                                                            lane * a.box * 128),
-                                "l"(map), "r"(c * 64), "r"(0), "r"(int(off)), "r"(page), "r"(smem_addr(bar))
-                                : "memory");
+                    now = next;
                 }
+            }
         }
         // the block may not end before its copies have, whether or not anyone still waits for them
         if constexpr (C::BOXES)
-            for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k)
-                for (uint32_t i = 0; i < kSpins && !bar_test(&sync->full[k & 1], (k / 2) & 1); ++i) {
+            for (uint32_t k = copies > 2u * all ? copies - 2 * all : 0; k < copies; ++k)
+                for (uint32_t i = 0; i < kSpins && !bar_test(&sync->full[k / all & 1][k % all], (k / all / 2) & 1); ++i) {
                 }
     }
 
@@ -274,6 +319,24 @@ struct Latent {
         const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
         const uint32_t to = smem_addr(smem);
         const int pieces = a.Dk / 8;
+        if constexpr (C::kWide) {
+            for (int row = id >> 3; row < C::ROWS; row += 32) {
+                const char* src = nullptr;
+                if (row < left) {
+                    uint32_t tok, g;
+                    a.div_group.divmod(uint32_t(first + row), tok, g);
+                    src = a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] + int64_t(g) * a.q_st[1];
+                }
+                for (int c = 0; c < chunks(); ++c) {
+                    const int piece = c * 8 + (id & 7);
+                    const bool ok = src && piece < pieces;
+                    copy16(to + line_at<C::Q_CHUNK>(row, piece), ok ? src + piece * 16 : a.q, ok);
+                }
+            }
+            copies_commit();
+            copies_wait<0>();
+            return;
+        }
 #pragma unroll 1
         for (int row = id >> 3; row < C::ROWS; row += 32) {
             const char* src = nullptr;
@@ -289,23 +352,21 @@ struct Latent {
                 w[c] = src && piece < pieces ? __ldg(reinterpret_cast<const uint4*>(src) + piece)
                                              : make_uint4(0, 0, 0, 0);
             }
-            if constexpr (!C::kWide) {
-                uint32_t most = 0;
-                float f[8];
+            uint32_t most = 0;
+            float f[8];
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    widen8(w[c], a.bf16, f);
-                    most = max(most, most_of(f));
-                }
+            for (int c = 0; c < C::CHUNKS; ++c) {
+                widen8(w[c], a.bf16, f);
+                most = max(most, most_of(f));
+            }
 #pragma unroll
-                for (int d = 1; d < 8; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-                const float p = row_power(most), by = one_over_power(p);
-                if ((id & 7) == 0) factors(run)[row] = row_factor(p, a.scale_log2);
+            for (int d = 1; d < 8; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+            const float p = row_power(most), by = one_over_power(p);
+            if ((id & 7) == 0) factors(run)[row] = row_factor(p, a.scale_log2);
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    widen8(w[c], a.bf16, f);
-                    w[c] = half8(f, by);
-                }
+            for (int c = 0; c < C::CHUNKS; ++c) {
+                widen8(w[c], a.bf16, f);
+                w[c] = half8(f, by);
             }
 #pragma unroll
             for (int c = 0; c < C::CHUNKS; ++c)
@@ -313,11 +374,14 @@ struct Latent {
         }
     }
 
+    // 8-bit: the factors of a run's query rows, and the scales of a tile's rows.  Those of run r
+    // are written when the scores of run r - 1 are done, which may be two tiles (and runs)
+    // ahead of what the softmax has read: three places.
     __device__ __forceinline__ float* factors(uint32_t run) const {
-        return reinterpret_cast<float*>(smem + C::SYNC_AT + sizeof(LatentSync)) + (run & 1) * 64;
+        return reinterpret_cast<float*>(smem + C::SYNC_AT + sizeof(LatentSync)) + run % 3 * C::ROWS;
     }
     __device__ __forceinline__ float* scales(uint32_t n) const {
-        return reinterpret_cast<float*>(smem + C::SYNC_AT + sizeof(LatentSync)) + 128 + (n & 1) * 64;
+        return reinterpret_cast<float*>(smem + C::SYNC_AT + sizeof(LatentSync)) + 3 * C::ROWS + (n & 1) * C::TN;
     }
 
     // A cache row: its bytes, and its scale.
@@ -357,7 +421,7 @@ struct Latent {
                     const uint32_t to = stage(n);
                     const Row r[2] = {row_of(x, (x.t0 + it) * C::TN + row), row_of(x, (x.t0 + it) * C::TN + row + 32)};
                     if constexpr (C::kWide) {
-                        if (n >= 2) wait(&sync->empty[n & 1], (n / 2 - 1) & 1);
+                        for (int g = 0; g < groups(); ++g) wait_free(n, g);
                         if (given_up()) return;
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -368,6 +432,8 @@ struct Latent {
                             }
                         copies_commit();
                         copies_wait<0>();
+                        to_async_proxy();
+                        for (int g = 0; g < groups(); ++g) bar_arrive(&sync->full[n & 1][g]);
                     } else {
                         // codes are asked for before the place is free
                         uint2 w[2][C::CHUNKS];
@@ -380,76 +446,111 @@ struct Latent {
                                               ? __ldg(reinterpret_cast<const uint2*>(r[i].p) + piece)
                                               : make_uint2(0, 0);
                             }
-                        if (n >= 2) wait(&sync->empty[n & 1], (n / 2 - 1) & 1);
-                        if (given_up()) return;
+                        int g = 0;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int c = 0; c < C::CHUNKS; ++c) {
+                            if (c >= chunks()) break;
+                            if (c == 0 || c == group_end(g - 1)) {
+                                wait_free(n, g++);
+                                if (given_up()) return;
+                                // (the scales of tile n - 2 have been read when its first product is done)
+                                if (c == 0 && sub == 0) scales(n)[row] = r[0].scale, scales(n)[row + 32] = r[1].scale;
+                            }
 #pragma unroll
-                            for (int c = 0; c < C::CHUNKS; ++c)
-                                if (c < chunks())
-                                    sts128(to + line_at<C::CHUNK>(row + 32 * i, c * 8 + sub),
-                                           codes_to_half2<C::STORE, false>(w[i][c].x),
-                                           codes_to_half2<C::STORE, true>(w[i][c].x),
-                                           codes_to_half2<C::STORE, false>(w[i][c].y),
-                                           codes_to_half2<C::STORE, true>(w[i][c].y));
-                            if (sub == 0) scales(n)[row + 32 * i] = r[i].scale;
+                            for (int i = 0; i < 2; ++i)
+                                sts128(to + line_at<C::CHUNK>(row + 32 * i, c * 8 + sub),
+                                       codes_to_half2<C::STORE, false>(w[i][c].x), codes_to_half2<C::STORE, true>(w[i][c].x),
+                                       codes_to_half2<C::STORE, false>(w[i][c].y), codes_to_half2<C::STORE, true>(w[i][c].y));
+                            if (c + 1 == group_end(g - 1)) {
+                                to_async_proxy();
+                                bar_arrive(&sync->full[n & 1][g - 1]);
+                            }
                         }
                     }
-                    to_async_proxy();
-                    bar_arrive(&sync->full[n & 1]);
                 }
         }
     }
 
     // ---------------------------------------------------------- products
 
-    __device__ __forceinline__ void scores(uint32_t n) const {
+    // Two warps issue products, one the scores', one the values': neither waits for what
+    // the other needs.  A whole warp goes through the loops, so that descriptors stay in
+    // uniform registers, and one lane issues: 30 to 38 cycles a product, where a lane alone
+    // took 43 and more (67, forming each descriptor anew), and the tensor pipe takes 23 to 32
+    // for the scores' and 39 to 48 for the values'.
+
+    __device__ __forceinline__ void scores() const {
         constexpr uint32_t shape = latent_shape<C::BF16, C::TN, C::ROWS, false>();
-        const uint32_t q = smem_addr(smem), k = stage(n), to = tmem + C::S_COL + (n & 1) * C::ROWS;
-        wait(&sync->full[n & 1], (n / 2) & 1);
-        if (sync->dead) return;
-        tmem_after();
-        const int all = chunks();
-        for (int c = 0; c < all; ++c)
+        const uint32_t me = elected(), q = smem_addr(smem) >> 4;
+        const int all = groups();
+        uint32_t n = 0;
+        for (uint32_t run = 0;; ++run) {
+            RunAt x;
+            if (!__all_sync(0xffffffffu, take(run, x))) break;
+            const int count = __shfl_sync(0xffffffffu, x.count, 0);
+            wait(&sync->q_full, run & 1);
+            for (int it = 0; it < count; ++it, ++n) {
+                // the softmax has read the scores before the last
+                if (n >= 2) wait(&sync->s_free[n & 1], (n / 2 - 1) & 1);
+                const uint32_t to = __shfl_sync(0xffffffffu, tmem + C::S_COL + (n & 1) * C::ROWS, 0);
+                for (int g = 0, c = 0; g < all; ++g) {
+                    wait(&sync->full[n & 1][g], (n / 2) & 1);
+                    if (given_up()) break;
+                    tmem_after();
+                    for (const int end = group_end(g); c < end; ++c) {
+                        const uint32_t k = __shfl_sync(0xffffffffu, (stage(n) + c * C::CHUNK) >> 4, 0);
+                        const uint32_t b = __shfl_sync(0xffffffffu, q + ((c * C::Q_CHUNK) >> 4), 0);
+                        if (c == 0) mma_one<false>(me, to, k, b, shape);
+                        else mma_one<true>(me, to, k, b, shape);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mma_ss(to, smem_matrix(k + c * C::CHUNK + i * 32, 0), smem_matrix(q + c * C::Q_CHUNK + i * 32, 0), shape,
-                       c + i > 0);
-        mma_commit(&sync->s_full[n & 1]);
+                        for (int i = 1; i < 4; ++i) mma_one<true>(me, to, k + i * 2, b + i * 2, shape);
+                    }
+                }
+                if (given_up()) break;
+                commit_one(me, &sync->s_full[n & 1]);
+                if (it + 1 == count) commit_one(me, &sync->q_empty);
+            }
+            if (given_up()) break;
+        }
+        commit_one(me, &sync->done);
     }
 
     __device__ __forceinline__ void products() const {
         constexpr uint32_t shape = latent_shape<C::BF16, 128, C::ROWS, true>();
-        const uint32_t p = smem_addr(smem + C::P_AT);
-        RunAt x;
+        constexpr uint32_t lead = uint32_t(C::CHUNK >> 4) << 16;
+        const uint32_t me = elected(), p = smem_addr(smem + C::P_AT) >> 4;
+        const int tiles = value_tiles();
         uint32_t n = 0;
-        for (uint32_t run = 0; take(run, x); ++run) {
-            wait(&sync->q_full, run & 1);
-            scores(n);
-            if (x.count == 1) mma_commit(&sync->q_empty);
-            for (int it = 0; it < x.count; ++it, ++n) {
-                if (it + 1 < x.count) {
-                    scores(n + 1);
-                    if (it + 2 == x.count) mma_commit(&sync->q_empty);
-                }
+        for (uint32_t run = 0;; ++run) {
+            RunAt x;
+            if (!__all_sync(0xffffffffu, take(run, x))) break;
+            const int count = __shfl_sync(0xffffffffu, x.count, 0);
+            for (int it = 0; it < count; ++it, ++n) {
                 wait(&sync->p_full, n & 1);
-                if (sync->dead) break;
+                if (given_up()) break;
                 tmem_after();
-                const int tiles = value_tiles();
-                for (int v = 0; v < tiles; ++v)
+                const uint32_t b = __shfl_sync(0xffffffffu, p, 0);
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t v = __shfl_sync(0xffffffffu, ((stage(n) + t * 2 * C::CHUNK) >> 4) | lead, 0);
+                    const uint32_t to = __shfl_sync(0xffffffffu, tmem + t * C::ROWS, 0);
+                    if (it == 0) mma_one<false>(me, to, v, b, shape);
+                    else mma_one<true>(me, to, v, b, shape);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_ss(tmem + v * C::ROWS, smem_matrix(stage(n) + v * 2 * C::CHUNK + i * 2048, C::CHUNK),
-                               smem_matrix(p + i * 32, 0), shape, it > 0 || i > 0);
-                mma_commit(&sync->empty[n & 1]);
-                sync->beat = n + 1;
+                    for (int i = 1; i < 4; ++i) mma_one<true>(me, to, v + i * 128, b + i * 2, shape);
+                    commit_one(me, &sync->empty[n & 1][t]);
+                }
+                if (me) sync->beat = n + 1;
             }
-            if (sync->dead) break;
+            if (given_up()) break;
         }
-        // tensor memory may not go before the last product has
-        mma_commit(&sync->done);
+        commit_one(me, &sync->done);
+    }
+
+    // Tensor memory may not go before the last product has.
+    __device__ __forceinline__ void all_done() const {
         for (uint32_t i = 0; i < kSpins && !bar_test(&sync->done, 0); ++i) {
         }
+        __syncwarp();
     }
 
     // ---------------------------------------------------------- softmax
@@ -480,7 +581,7 @@ struct Latent {
                 sts128(at, w[0], w[1], w[2], w[3]);
             }
         }
-        if (found) sync->patch[run & 3] = 1;
+        if (found) sync->patch[run % 3] = 1;
         __syncwarp();
     }
 
@@ -500,6 +601,21 @@ struct Latent {
             tmem_st16(lanes + c, w);
         }
         tmem_wait_st();
+    }
+
+    // Two columns (i even) of s scale - ref (8-bit: s u times the row's factor, less ref).
+    // 16-bit: what is not seen is -inf in s already; 8-bit: it becomes so here, as the scale
+    // may have any sign.
+    __device__ __forceinline__ float2 from_reference(const float* s, const float* ref, const float* qf, const float* u,
+                                                     uint32_t seen, int i) const {
+        const int c = (i >> 2) * 2, h = (i >> 1) & 1;
+        const float2 r = make_float2(-ref[c], -ref[c + 1]);
+        float2 y = make_float2(s[i], s[i + 1]);
+        if constexpr (C::kWide) return fma2(y, make_float2(a.scale_log2, a.scale_log2), r);
+        y = fma2(mul2(y, make_float2(u[h], u[h])), make_float2(qf[c], qf[c + 1]), r);
+        if (!(seen >> i & 1u)) y.x = -INFINITY;
+        if (!(seen >> i & 2u)) y.y = -INFINITY;
+        return y;
     }
 
     __device__ __forceinline__ void softmax() const {
@@ -524,7 +640,8 @@ struct Latent {
                 const bool part = (tile + 1) * C::TN > prefix;  // more than context rows
                 float s[C::ROWS / 2], u[2] = {1.0f, 1.0f}, lu[2] = {0.0f, 0.0f};
                 wait(&sync->s_full[n & 1], (n / 2) & 1);
-                if (part || !C::kWide) wait(&sync->full[n & 1], (n / 2) & 1);  // what copies or helpers wrote is seen
+                if (part || !C::kWide)  // what copies or helpers wrote is seen
+                    for (int g = 0; g < value_tiles(); ++g) wait(&sync->full[n & 1][g], (n / 2) & 1);
                 __syncwarp();
                 tmem_after();
                 latent_ld<C::ROWS>(s, lanes + C::S_COL + (n & 1) * C::ROWS);
@@ -540,14 +657,9 @@ struct Latent {
                 }
                 tmem_wait_ld();
                 latent_here<C::ROWS / 2>(s);
-                // scores in base 2: s becomes s scale (times the row's factors)
+                tmem_before();
+                bar_arrive(&sync->s_free[n & 1]);
                 uint32_t seen = 0xffffffffu;
-#pragma unroll
-                for (int i = 0; i < C::ROWS / 2; ++i) {
-                    const int h = (i >> 1) & 1;
-                    if constexpr (C::kWide) s[i] *= a.scale_log2;
-                    else s[i] = s[i] * u[h] * qf[(i >> 2) * 2 + (i & 1)];
-                }
                 if (part) {
                     seen = 0;
 #pragma unroll 1
@@ -560,20 +672,31 @@ struct Latent {
                             seen |= (sees32(a, x.rq.qs, tok, prefix, x.rq.len, tile * C::TN + k0 + 8 * h) & 1u)
                                     << ((i >> 1) * 4 + h * 2 + (i & 1));
                     }
+                    if constexpr (C::kWide)
 #pragma unroll
-                    for (int i = 0; i < C::ROWS / 2; ++i)
-                        if (!(seen >> i & 1u)) s[i] = -INFINITY;
+                        for (int i = 0; i < C::ROWS / 2; ++i)
+                            if (!(seen >> i & 1u)) s[i] = -INFINITY;
                 }
-                bool past = it == 0 || sync->dead;
+                float most[2] = {-INFINITY, -INFINITY};  // of the thread's two rows, from the reference
 #pragma unroll
-                for (int i = 0; i < C::ROWS / 2; ++i)
-                    past = past || s[i] + lu[(i >> 1) & 1] - ref[(i >> 2) * 2 + (i & 1)] > C::kLag + C::kBias;
+                for (int i = 0; i < C::ROWS / 2; i += 2) {
+                    const float2 y = from_reference(s, ref, qf, u, seen, i);
+                    most[(i >> 1) & 1] = max3(most[(i >> 1) & 1], y.x, y.y);
+                }
                 bool moved = false;
-                if (softmax_any(past)) {
+                if (softmax_any(it == 0 || sync->dead ||
+                                fmaxf(most[0] + lu[0], most[1] + lu[1]) > C::kLag + C::kBias)) {
                     if (softmax_any(sync->dead)) return;
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
-                        float top = fmaxf(s[(i >> 1) * 4 + (i & 1)] + lu[0], s[(i >> 1) * 4 + 2 + (i & 1)] + lu[1]);
+                        const int j = (i >> 1) * 4 + (i & 1);
+                        const float f = C::kWide ? a.scale_log2 : qf[C::kWide ? 0 : i];
+                        float top = C::kWide          ? s[j] * f
+                                    : seen >> j & 1u ? s[j] * u[0] * f + lu[0]
+                                                      : -INFINITY;
+                        top = fmaxf(top, C::kWide              ? s[j + 2] * f
+                                         : seen >> (j + 2) & 1u ? s[j + 2] * u[1] * f + lu[1]
+                                                                : -INFINITY);
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         if (lane < 4) sync->red[warp][(i >> 1) * 8 + c0 + (i & 1)] = top;
@@ -597,7 +720,7 @@ struct Latent {
                     moved = it > 0;
                 }
                 // the weights' place is free, and O still, when the tile before is done
-                if (n > 0) wait(&sync->empty[(n - 1) & 1], ((n - 1) / 2) & 1);
+                if (n > 0) wait_product(n - 1);
                 __syncwarp();
                 if (moved) {
                     tmem_after();
@@ -609,17 +732,18 @@ struct Latent {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {  // block j + k / 2, rows k % 2
                         const int i = (j + (k >> 1)) * 4 + (k & 1) * 2, c = (j + (k >> 1)) * 2;
-                        float e[2];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            e[b] = pow2(s[i + b] - ref[c + b]);
-                            l[c + b] += e[b];
-                            if constexpr (!C::kWide) {
-                                e[b] *= u[k & 1];
-                                if (part && !(seen >> (i + b) & 1u)) e[b] = 0.0f;  // the scale need not be finite
-                            }
+                        float2 e = from_reference(s, ref, qf, u, seen, i);
+                        e = make_float2(pow2(e.x), pow2(e.y));
+                        const float2 sum = add2(make_float2(l[c], l[c + 1]), e);
+                        l[c] = sum.x;
+                        l[c + 1] = sum.y;
+                        if constexpr (!C::kWide) {
+                            e = mul2(e, make_float2(u[k & 1], u[k & 1]));
+                            // (the scale need not be finite)
+                            if (part && !(seen >> i & 1u)) e.x = 0.0f;
+                            if (part && !(seen >> i & 2u)) e.y = 0.0f;
                         }
-                        w[k] = pack2<C::BF16>(e[0], e[1]);
+                        w[k] = pack2<C::BF16>(e.x, e.y);
                     }
                     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                                      p_at + j * 1024),
@@ -633,7 +757,7 @@ struct Latent {
                 bar_arrive(&sync->p_full);
             }
             // the run's results, when its last product is done
-            wait(&sync->empty[(n - 1) & 1], ((n - 1) / 2) & 1);
+            wait_product(n - 1);
             if (softmax_any(sync->dead)) return;
             tmem_after();
             finish(x, run, ref, l, lanes);
@@ -646,20 +770,20 @@ struct Latent {
         constexpr int NC = C::ROWS / 4;
         const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, c0 = (lane & 3) * 2;
         const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
-        const bool patch = sync->patch[run & 3] != 0;
+        const bool patch = sync->patch[run % 3] != 0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i >> 1) * 8 + c0 + (i & 1);
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
             if (lane < 4) sync->red[warp][c] = l[i];
-            if (tid < 4) sync->ref[c] = ref[i];
+            if (tid < 4) sync->fac[c] = ref[i];
         }
         softmax_sync();
-        if (tid == 0) sync->patch[run & 3] = 0;
+        if (tid == 0) sync->patch[run % 3] = 0;
         if (tid < C::ROWS) {
             const float all = sync->red[0][tid] + sync->red[1][tid] + sync->red[2][tid] + sync->red[3][tid];
-            const float m = all == 0.0f ? -INFINITY : sync->ref[tid];
+            const float m = all == 0.0f ? -INFINITY : sync->fac[tid];
             sync->fac[tid] = x.slot >= 0 ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
             if (x.slot >= 0) a.part_ml[x.slot * C::ROWS + tid] = make_float2(m, all);
             else if (tid < left) {
@@ -700,7 +824,7 @@ struct Latent {
                                : pack2<false>(odd ? other : y, odd ? z : other);
             }
         }
-        softmax_sync();  // fac, red and ref have been read
+        softmax_sync();  // fac and red have been read
     }
 
     // The block's results, when one of its waits has given up: NaN in all of them, those
@@ -730,23 +854,25 @@ template <class C>
 __global__ void __launch_bounds__(kLatentThreads, 1)
     rope_latent_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map) {
     extern __shared__ __align__(1024) char smem[];
-    static_assert(C::SYNC_AT + int(sizeof(LatentSync)) + (C::kWide ? 0 : 1024) <= C::kSmemMax, "shared memory");
+    static_assert(C::SYNC_AT + int(sizeof(LatentSync)) + C::MORE <= C::kSmemMax, "shared memory");
     LatentSync* sync = reinterpret_cast<LatentSync*>(smem + C::SYNC_AT);
     const int warp = int(threadIdx.x) >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            bar_init(&sync->full[i], C::BOXES ? 1 : 256);
-            bar_init(&sync->empty[i], 1);
+            for (int g = 0; g < 5; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : 256);
+            for (int g = 0; g < 4; ++g) bar_init(&sync->empty[i][g], 1);
             bar_init(&sync->s_full[i], 1);
+            bar_init(&sync->s_free[i], 128);
         }
         bar_init(&sync->p_full, 128);
         bar_init(&sync->q_full, 256);
         bar_init(&sync->q_empty, 1);
-        bar_init(&sync->done, 1);
+        bar_init(&sync->done, 2);
         sync->dead = 0;
-        for (int i = 0; i < 4; ++i) sync->patch[i] = 0;
-        sync->runs = 0;
-        sync->last = ~0u;
+        for (int i = 0; i < 3; ++i) {
+            sync->patch[i] = 0;
+            bar_init(&sync->run_full[i], 1);
+        }
         sync->taken = 0;
         sync->beat = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -765,13 +891,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     if (warp < 4) {
         it.softmax();
     } else if (warp == 4) {
-        if ((threadIdx.x & 31) == 0) it.products();
-        __syncwarp();
+        it.scores();
     } else if (warp == 5) {
         it.fetches(place, &map);
-    } else {
+    } else if (warp < 14) {
         it.help(int(threadIdx.x) - 192);
+    } else {
+        it.products();
     }
+    if (warp == 4) it.all_done();
     tmem_before();
     __syncthreads();
     if (sync->dead) it.give_up(place);
@@ -861,7 +989,7 @@ TreeKernel latent_instance() {
     using C = LatentCfg<STORE, ROWS, BOXES>;
     return TreeKernel{reinterpret_cast<const void*>(&rope_latent_kernel<C>),
                       reinterpret_cast<const void*>(&rope_latent_join_kernel<ROWS>),
-                      C::SYNC_AT + int(sizeof(LatentSync)) + (C::kWide ? 0 : 1024), kLatentThreads, C::TN, 0.0f, 0};
+                      C::SYNC_AT + int(sizeof(LatentSync)) + C::MORE, kLatentThreads, C::TN, 0.0f, 0};
 }
 
 template <int STORE>

@@ -9,7 +9,7 @@ namespace rope {
 constexpr int kLatentKeys = 64;      // cache rows of a tile
 constexpr int kLatentLanes = 576;    // of a row, at most
 constexpr int kLatentValues = 512;   // of those that are the value, at most
-constexpr int kLatentThreads = 448;
+constexpr int kLatentThreads = 480;
 constexpr int kLatentJoinThreads = 512;
 
 struct LatentPlan {
