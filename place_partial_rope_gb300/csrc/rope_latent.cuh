@@ -55,9 +55,22 @@ struct LatentCfg {
     static constexpr uint32_t S_COL = 4 * ROWS;
 };
 
+// A try of a wait sleeps up to 20 us: fourteen warps that looked again and again would keep
+// the two that issue products from their slots.
+constexpr uint32_t kNaps = 1u << 17;  // tries of one wait before it gives up: 2.6 s
+
+__device__ __forceinline__ bool bar_nap(unsigned long long* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(smem_addr(b)), "r"(parity), "r"(20000u)
+                 : "memory");
+    return ok != 0;
+}
+
 struct LatentSync {
-    // a tile's groups of 128 lanes, and the lanes that are no value's: brought, and done with
-    unsigned long long full[2][5], empty[2][4], s_full[2], s_free[2], p_full, q_full, q_empty, run_full[3], done;
+    // a tile's groups of lanes: brought, and done with
+    unsigned long long full[2][3], empty[2][2], s_full[2], s_free[2], p_full, q_full, q_empty, run_full[3], done;
     uint32_t tmem;
     volatile uint32_t dead;
     volatile uint32_t patch[3];  // of run r at r % 3: values were taken out
@@ -121,12 +134,11 @@ __device__ __forceinline__ uint32_t elected() {
 
 // A product, and a commit, by the lane of the warp that has `me`.  a and b: the low words of
 // the descriptors (see smem_matrix), whose high words are one constant.
-template <bool ADD>
-__device__ __forceinline__ void mma_one(uint32_t me, uint32_t d, uint32_t a, uint32_t b, uint32_t shape) {
+__device__ __forceinline__ void mma_one(uint32_t me, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
     constexpr uint64_t HIGH = (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
-    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %4, 0;\n"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, %5;\n}" ::"r"(d),
-                 "l"(HIGH | a), "l"(HIGH | b), "r"(shape), "r"(me), "n"(ADD ? 1 : 0)
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %5, 0;\nsetp.ne.b32 q, %4, 0;\n"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(HIGH | a), "l"(HIGH | b), "r"(shape), "r"(me), "r"(uint32_t(add))
                  : "memory");
 }
 
@@ -160,28 +172,39 @@ struct Latent {
 
     __device__ __forceinline__ int chunks() const { return (a.Dk + 63) / 64; }
     __device__ __forceinline__ int value_tiles() const { return (a.Dv + 127) / 128; }
-    // Groups of a tile's chunks that come and go together: the 128 lanes of each value
-    // tile, then the lanes that are no value's.
-    __device__ __forceinline__ int groups() const { return value_tiles() + (chunks() > 2 * value_tiles() ? 1 : 0); }
-    __device__ __forceinline__ int group_end(int g) const { return g < value_tiles() ? min(2 * g + 2, chunks()) : chunks(); }
+    // Groups of a tile's chunks that come and go together: the 256 lanes of two value tiles,
+    // then the lanes that are no value's.  (Groups of 128 lanes: a wait more for each, of some
+    // 100 cycles, for products that take 256.)
+    __device__ __forceinline__ int value_groups() const { return (a.Dv + 255) / 256; }
+    __device__ __forceinline__ int groups() const { return value_groups() + (chunks() > 2 * value_tiles() ? 1 : 0); }
+    __device__ __forceinline__ int group_end(int g) const {
+        return g < value_groups() ? min(min(4 * g + 4, 2 * value_tiles()), chunks()) : chunks();
+    }
     __device__ __forceinline__ uint32_t stage(uint32_t n) const { return smem_addr(smem + C::K_AT) + (n & 1) * C::STAGE; }
 
     // ---------------------------------------------------------- waits
 
-    __device__ __forceinline__ void wait(unsigned long long* b, uint32_t parity) const {
-        for (uint32_t i = 0; i < kSpins; ++i) {
-            if (bar_test(b, parity)) return;
-            if (sync->dead) return;
+    // False: it gave up, or another has.
+    __device__ __forceinline__ bool wait(unsigned long long* b, uint32_t parity) const {
+        if (bar_nap(b, parity)) return true;
+        return wait_on(b, parity);
+    }
+
+    __device__ __noinline__ bool wait_on(unsigned long long* b, uint32_t parity) const {
+        for (uint32_t i = 0; i < kNaps; ++i) {
+            if (bar_nap(b, parity)) return true;
+            if (sync->dead) return false;
         }
         sync->dead = 1;
+        return false;
     }
 
     // For those that may rightly wait for a whole run: gives up when no tile has been
     // done between two such stretches.
     __device__ __forceinline__ void wait_run(unsigned long long* b, uint32_t parity) const {
         for (uint32_t seen = ~0u;;) {
-            for (uint32_t i = 0; i < kSpins; ++i) {
-                if (bar_test(b, parity)) return;
+            for (uint32_t i = 0; i < kNaps; ++i) {
+                if (bar_nap(b, parity)) return;
                 if (sync->dead) return;
             }
             const uint32_t now = sync->beat;
@@ -203,13 +226,13 @@ struct Latent {
 
     // For group g's place of tile n: values are free when the product with them is done,
     // the other lanes when the scores are.
-    __device__ __forceinline__ void wait_free(uint32_t n, int g) const {
-        if (n >= 2) wait(g < value_tiles() ? &sync->empty[n & 1][g] : &sync->s_full[n & 1], (n / 2 - 1) & 1);
+    __device__ __forceinline__ bool wait_free(uint32_t n, int g) const {
+        return n < 2 || wait(g < value_groups() ? &sync->empty[n & 1][g] : &sync->s_full[n & 1], (n / 2 - 1) & 1);
     }
 
     // Until the last product of tile n is done.
     __device__ __forceinline__ void wait_product(uint32_t n) const {
-        wait(&sync->empty[n & 1][value_tiles() - 1], (n / 2) & 1);
+        wait(&sync->empty[n & 1][value_groups() - 1], (n / 2) & 1);
     }
 
     // ---------------------------------------------------------- the walk, and tensor copies
@@ -252,7 +275,7 @@ struct Latent {
         return r;
     }
 
-    __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* map) const {
+    __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* map, const CUtensorMap* quads) const {
         const int lane = int(threadIdx.x) & 31, all = groups(), boxes = C::BOXES ? C::TN / a.box : 0;
         Walk walk = walk_from<C::ROWS, C::TN>(a, place);
         RunAt x;
@@ -274,9 +297,8 @@ struct Latent {
                     const Box next = it + 1 < x.count ? box_of(x, x.t0 + it + 1, lane, boxes) : Box{-1, 0};
                     const uint32_t to = stage(n) + lane * a.box * 128;
                     for (int g = 0, c = 0; g < all; ++g) {
-                        wait_free(n, g);
-                        // once a wait has given up, the place may be in use, or its last copy under way
-                        on = !given_up();
+                        // where a wait has given up, the place may be in use, or its last copy under way
+                        on = __all_sync(0xffffffffu, wait_free(n, g));
                         if (!on) break;
                         const uint32_t bar = smem_addr(&sync->full[n & 1][g]);
                         const int end = group_end(g);
@@ -286,13 +308,22 @@ struct Latent {
                                          : "memory");
                         __syncwarp();
                         ++copies;
-                        if (lane < boxes)
+                        if (a.quads && end - c == 4) {
+                            // a page's 64 rows of 256 lanes in one copy
+                            if (lane == 0)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                    "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + c * C::CHUNK),
+                                    "l"(quads), "r"(0), "r"(now.off), "r"(c), "r"(now.page), "r"(bar)
+                                    : "memory");
+                        } else if (lane < boxes) {
                             for (int i = c; i < end; ++i)
                                 asm volatile(
                                     "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                                     "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + i * C::CHUNK),
                                     "l"(map), "r"(i * 64), "r"(0), "r"(now.off), "r"(now.page), "r"(bar)
                                     : "memory");
+                        }
                         c = end;
                     }
                     now = next;
@@ -421,8 +452,9 @@ struct Latent {
                     const uint32_t to = stage(n);
                     const Row r[2] = {row_of(x, (x.t0 + it) * C::TN + row), row_of(x, (x.t0 + it) * C::TN + row + 32)};
                     if constexpr (C::kWide) {
-                        for (int g = 0; g < groups(); ++g) wait_free(n, g);
-                        if (given_up()) return;
+                        bool on = true;
+                        for (int g = 0; g < groups(); ++g) on = wait_free(n, g) && on;
+                        if (!__all_sync(0xffffffffu, on)) return;
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             for (int c = 0; c < chunks(); ++c) {
@@ -451,8 +483,7 @@ struct Latent {
                         for (int c = 0; c < C::CHUNKS; ++c) {
                             if (c >= chunks()) break;
                             if (c == 0 || c == group_end(g - 1)) {
-                                wait_free(n, g++);
-                                if (given_up()) return;
+                                if (!__all_sync(0xffffffffu, wait_free(n, g++))) return;
                                 // (the scales of tile n - 2 have been read when its first product is done)
                                 if (c == 0 && sub == 0) scales(n)[row] = r[0].scale, scales(n)[row + 32] = r[1].scale;
                             }
@@ -481,32 +512,35 @@ struct Latent {
 
     __device__ __forceinline__ void scores() const {
         constexpr uint32_t shape = latent_shape<C::BF16, C::TN, C::ROWS, false>();
-        const uint32_t me = elected(), q = smem_addr(smem) >> 4;
-        const int all = groups();
+        const uint32_t me = elected(), q = __shfl_sync(0xffffffffu, smem_addr(smem) >> 4, 0);
+        const int all = chunks(), rest = 2 * value_tiles(), groups_of_values = value_groups();
         uint32_t n = 0;
         for (uint32_t run = 0;; ++run) {
             RunAt x;
             if (!__all_sync(0xffffffffu, take(run, x))) break;
             const int count = __shfl_sync(0xffffffffu, x.count, 0);
             wait(&sync->q_full, run & 1);
-            for (int it = 0; it < count; ++it, ++n) {
+            bool on = true;
+            for (int it = 0; on && it < count; ++it, ++n) {
                 // the softmax has read the scores before the last
                 if (n >= 2) wait(&sync->s_free[n & 1], (n / 2 - 1) & 1);
+                tmem_after();
                 const uint32_t to = __shfl_sync(0xffffffffu, tmem + C::S_COL + (n & 1) * C::ROWS, 0);
-                for (int g = 0, c = 0; g < all; ++g) {
-                    wait(&sync->full[n & 1][g], (n / 2) & 1);
-                    if (given_up()) break;
-                    tmem_after();
-                    for (const int end = group_end(g); c < end; ++c) {
-                        const uint32_t k = __shfl_sync(0xffffffffu, (stage(n) + c * C::CHUNK) >> 4, 0);
-                        const uint32_t b = __shfl_sync(0xffffffffu, q + ((c * C::Q_CHUNK) >> 4), 0);
-                        if (c == 0) mma_one<false>(me, to, k, b, shape);
-                        else mma_one<true>(me, to, k, b, shape);
+                const uint32_t k = __shfl_sync(0xffffffffu, stage(n) >> 4, 0), par = (n / 2) & 1;
+                unsigned long long* full = sync->full[n & 1];
 #pragma unroll
-                        for (int i = 1; i < 4; ++i) mma_one<true>(me, to, k + i * 2, b + i * 2, shape);
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    if (c >= all) break;
+                    if (c % 2 == 0) {
+                        if (c == rest) on = wait(full + groups_of_values, par);
+                        else if (c % 4 == 0 && c < rest) on = wait(full + c / 4, par);
                     }
+                    mma_one(me, to, k + c * (C::CHUNK >> 4), q + c * (C::Q_CHUNK >> 4), shape, c > 0);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i)
+                        mma_one(me, to, k + c * (C::CHUNK >> 4) + i * 2, q + c * (C::Q_CHUNK >> 4) + i * 2, shape, true);
                 }
-                if (given_up()) break;
+                on = __all_sync(0xffffffffu, on);  // (given up: the scores are whatever they are)
                 commit_one(me, &sync->s_full[n & 1]);
                 if (it + 1 == count) commit_one(me, &sync->q_empty);
             }
@@ -518,26 +552,27 @@ struct Latent {
     __device__ __forceinline__ void products() const {
         constexpr uint32_t shape = latent_shape<C::BF16, 128, C::ROWS, true>();
         constexpr uint32_t lead = uint32_t(C::CHUNK >> 4) << 16;
-        const uint32_t me = elected(), p = smem_addr(smem + C::P_AT) >> 4;
+        const uint32_t me = elected(), p = __shfl_sync(0xffffffffu, smem_addr(smem + C::P_AT) >> 4, 0);
         const int tiles = value_tiles();
         uint32_t n = 0;
         for (uint32_t run = 0;; ++run) {
             RunAt x;
             if (!__all_sync(0xffffffffu, take(run, x))) break;
             const int count = __shfl_sync(0xffffffffu, x.count, 0);
-            for (int it = 0; it < count; ++it, ++n) {
-                wait(&sync->p_full, n & 1);
-                if (given_up()) break;
+            bool on = true;
+            for (int it = 0; on && it < count; ++it, ++n) {
+                on = __all_sync(0xffffffffu, wait(&sync->p_full, n & 1));
                 tmem_after();
-                const uint32_t b = __shfl_sync(0xffffffffu, p, 0);
-                for (int t = 0; t < tiles; ++t) {
-                    const uint32_t v = __shfl_sync(0xffffffffu, ((stage(n) + t * 2 * C::CHUNK) >> 4) | lead, 0);
-                    const uint32_t to = __shfl_sync(0xffffffffu, tmem + t * C::ROWS, 0);
-                    if (it == 0) mma_one<false>(me, to, v, b, shape);
-                    else mma_one<true>(me, to, v, b, shape);
+                const uint32_t v = __shfl_sync(0xffffffffu, (stage(n) >> 4) | lead, 0);
+                const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll
-                    for (int i = 1; i < 4; ++i) mma_one<true>(me, to, v + i * 128, b + i * 2, shape);
-                    commit_one(me, &sync->empty[n & 1][t]);
+                for (int t = 0; t < 4; ++t) {
+                    if (t >= tiles) break;
+                    mma_one(me, to + t * C::ROWS, v + t * (C::CHUNK >> 3), p, shape, it > 0);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i)
+                        mma_one(me, to + t * C::ROWS, v + t * (C::CHUNK >> 3) + i * 128, p + i * 2, shape, true);
+                    if (t % 2 == 1 || t + 1 == tiles) commit_one(me, &sync->empty[n & 1][t / 2]);
                 }
                 if (me) sync->beat = n + 1;
             }
@@ -641,7 +676,7 @@ struct Latent {
                 float s[C::ROWS / 2], u[2] = {1.0f, 1.0f}, lu[2] = {0.0f, 0.0f};
                 wait(&sync->s_full[n & 1], (n / 2) & 1);
                 if (part || !C::kWide)  // what copies or helpers wrote is seen
-                    for (int g = 0; g < value_tiles(); ++g) wait(&sync->full[n & 1][g], (n / 2) & 1);
+                    for (int g = 0; g < value_groups(); ++g) wait(&sync->full[n & 1][g], (n / 2) & 1);
                 __syncwarp();
                 tmem_after();
                 latent_ld<C::ROWS>(s, lanes + C::S_COL + (n & 1) * C::ROWS);
@@ -852,15 +887,16 @@ struct Latent {
 
 template <class C>
 __global__ void __launch_bounds__(kLatentThreads, 1)
-    rope_latent_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map) {
+    rope_latent_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map,
+                       const __grid_constant__ CUtensorMap quads) {
     extern __shared__ __align__(1024) char smem[];
     static_assert(C::SYNC_AT + int(sizeof(LatentSync)) + C::MORE <= C::kSmemMax, "shared memory");
     LatentSync* sync = reinterpret_cast<LatentSync*>(smem + C::SYNC_AT);
     const int warp = int(threadIdx.x) >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            for (int g = 0; g < 5; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : 256);
-            for (int g = 0; g < 4; ++g) bar_init(&sync->empty[i][g], 1);
+            for (int g = 0; g < 3; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : 256);
+            for (int g = 0; g < 2; ++g) bar_init(&sync->empty[i][g], 1);
             bar_init(&sync->s_full[i], 1);
             bar_init(&sync->s_free[i], 128);
         }
@@ -893,7 +929,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     } else if (warp == 4) {
         it.scores();
     } else if (warp == 5) {
-        it.fetches(place, &map);
+        it.fetches(place, &map, &quads);
     } else if (warp < 14) {
         it.help(int(threadIdx.x) - 192);
     } else {

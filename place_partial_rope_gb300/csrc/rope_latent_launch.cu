@@ -51,14 +51,19 @@ rope_status_t launch_latent(const LatentPlan& p, const TreeArgs& args, void* wor
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * wide);
     a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
-    CUtensorMap map{};
+    CUtensorMap map{}, quads{};
     if (p.boxes) {
         a.box = 8;
         while (a.page_size % (2 * a.box) == 0 && 2 * a.box <= kLatentKeys) a.box *= 2;
         const rope_status_t st = tree_map(&map, a.k, a.Dk, a, a.k_st, true, 64, err);
         if (st != ROPE_OK) return st;
+        a.quads = a.box == kLatentKeys && a.Dk % 64 == 0 && a.Dk >= 256;
+        if (a.quads) {
+            const rope_status_t sq = tree_map_quads(&quads, a.k, a.Dk / 64, a, a.k_st, err);
+            if (sq != ROPE_OK) return sq;
+        }
     }
-    void* params[] = {&a, &map};
+    void* params[] = {&a, &map, &quads};
     const rope_status_t st = tree_launch(k.main, blocks, 1, k.threads, k.smem, params, stream, err);
     if (st != ROPE_OK || blocks < 2) return st;
     void* join[] = {&a};

@@ -206,6 +206,26 @@ rope_status_t tree_map(CUtensorMap* map, const void* base, int dim, const TreeAr
     return map_of(map, base, dim, a, st, wide, lanes, err);
 }
 
+rope_status_t tree_map_quads(CUtensorMap* map, const void* base, int pieces, const TreeArgs& a, const int64_t* st,
+                             const char** err) {
+    const Encode encode = encoder();
+    if (!encode) {
+        *err = "the driver has no cuTensorMapEncodeTiled";
+        return ROPE_ERR_CUDA;
+    }
+    const cuuint64_t sizes[4] = {64, cuuint64_t(a.page_size), cuuint64_t(pieces), cuuint64_t(a.pages)};
+    const cuuint64_t strides[3] = {a.page_size > 1 ? cuuint64_t(st[1]) : 16, 128, a.pages > 1 ? cuuint64_t(st[0]) : 16};
+    const cuuint32_t box[4] = {64, cuuint32_t(a.box), 4, 1}, steps[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), sizes, strides, box,
+                              steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        *err = "the cache's sizes or strides do not fit a tensor map";
+        return ROPE_ERR_CUDA;
+    }
+    return ROPE_OK;
+}
+
 rope_status_t tree_launch(const void* f, int blocks, int per, int threads, int smem, void** params,
                           rope_stream_t stream, const char** err) {
     return launch(f, dim3(blocks, per), threads, smem, params, stream, err);
