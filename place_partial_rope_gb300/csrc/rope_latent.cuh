@@ -47,10 +47,11 @@ struct LatentCfg {
     static constexpr int CHUNKS = kLatentLanes / 64;
     static constexpr int Q_CHUNK = ROWS * 128, Q_BYTES = CHUNKS * Q_CHUNK;
     static constexpr int STAGE = CHUNKS * CHUNK, STAGES = 2;
-    static constexpr int K_AT = Q_BYTES, P_AT = K_AT + STAGES * STAGE, SYNC_AT = P_AT + ROWS * 128;
+    static constexpr int K_AT = Q_BYTES, P_AT = K_AT + STAGES * STAGE, SYNC_AT = P_AT + (ROWS < 64 ? ROWS * 256 : ROWS * 128);  // (P, and results turned over)
     static constexpr int kSmemMax = 232448;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f, kLag = 8.0f;
     static constexpr int MORE = kWide ? 0 : (3 * ROWS + 2 * TN) * 4;  // factors and scales
+    static constexpr int kAhead = 3;  // tiles from one that is brought to one that is asked into L2
     // tensor memory: O^T in tiles of 128 value lanes, then two S^T
     static constexpr uint32_t S_COL = 4 * ROWS;
 };
@@ -326,6 +327,15 @@ struct Latent {
                         }
                         c = end;
                     }
+                    // a later tile is on its way from memory to L2 meanwhile
+                    if (a.quads && lane == 0 && it + C::kAhead < x.count) {
+                        const Box far = box_of(x, x.t0 + it + C::kAhead, 0, 1);
+                        if (far.page >= 0)
+                            for (int c = 0; c < chunks(); c += 4)
+                                asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                                                 quads), "r"(0), "r"(far.off), "r"(c), "r"(far.page)
+                                             : "memory");
+                    }
                     now = next;
                 }
             }
@@ -594,28 +604,28 @@ struct Latent {
     // those of drafted rows that are not finite are taken out (see add_not_finite): a
     // weight of 0 times them would reach the tokens that do not see the row.
     __device__ __noinline__ void mend(uint32_t n, int from, int valid, uint32_t run) const {
-        const int pieces = value_tiles() * 16;
+        const int pieces = value_tiles() * 16, lane = int(threadIdx.x) & 31;
         bool found = false;
-        for (int i = from * pieces + int(threadIdx.x); i < C::TN * pieces; i += 128) {
-            const int row = i / pieces;
-            const uint32_t at = stage(n) + line_at<C::CHUNK>(row, i - row * pieces);
-            if (row >= valid) {
-                sts128(at, 0, 0, 0, 0);
-                continue;
-            }
-            uint32_t w[4], bad = 0;
-            lds128(w, at);
+        for (int row = from + (int(threadIdx.x) >> 5); row < C::TN; row += 4)
+            for (int piece = lane; piece < pieces; piece += 32) {
+                const uint32_t at = stage(n) + line_at<C::CHUNK>(row, piece);
+                if (row >= valid) {
+                    sts128(at, 0, 0, 0, 0);
+                    continue;
+                }
+                uint32_t w[4], bad = 0;
+                lds128(w, at);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                constexpr int KIND = C::BF16 ? ROPE_CACHE_BF16 : ROPE_CACHE_FP16;
-                if (not_finite<KIND>(w[j])) w[j] &= 0xffff0000u, bad = 1;
-                if (not_finite<KIND>(w[j] >> 16)) w[j] &= 0xffffu, bad = 1;
+                for (int j = 0; j < 4; ++j) {
+                    constexpr int KIND = C::BF16 ? ROPE_CACHE_BF16 : ROPE_CACHE_FP16;
+                    if (not_finite<KIND>(w[j])) w[j] &= 0xffff0000u, bad = 1;
+                    if (not_finite<KIND>(w[j] >> 16)) w[j] &= 0xffffu, bad = 1;
+                }
+                if (bad) {
+                    found = true;
+                    sts128(at, w[0], w[1], w[2], w[3]);
+                }
             }
-            if (bad) {
-                found = true;
-                sts128(at, w[0], w[1], w[2], w[3]);
-            }
-        }
         if (found) sync->patch[run % 3] = 1;
         __syncwarp();
     }
@@ -702,10 +712,8 @@ struct Latent {
                         const int at = first + (i >> 1) * 8 + c0 + (i & 1);
                         if (at >= x.rq.n * a.G) continue;
                         const int tok = static_cast<int>(a.div_group.div(uint32_t(at)));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            seen |= (sees32(a, x.rq.qs, tok, prefix, x.rq.len, tile * C::TN + k0 + 8 * h) & 1u)
-                                    << ((i >> 1) * 4 + h * 2 + (i & 1));
+                        const uint32_t bits = sees32(a, x.rq.qs, tok, prefix, x.rq.len, tile * C::TN + k0);
+                        seen |= ((bits & 1u) | (bits >> 6 & 4u)) << ((i >> 1) * 4 + (i & 1));
                     }
                     if constexpr (C::kWide)
 #pragma unroll
@@ -800,6 +808,10 @@ struct Latent {
         }
     }
 
+    __device__ __forceinline__ uint32_t pack_one(float y) const {
+        return a.bf16 ? pack2<true>(y, 0.0f) : pack2<false>(y, 0.0f);
+    }
+
     __device__ __forceinline__ void finish(const RunAt& x, uint32_t run, const float* ref, float* l,
                                            uint32_t lanes) const {
         constexpr int NC = C::ROWS / 4;
@@ -827,36 +839,67 @@ struct Latent {
             }
         }
         softmax_sync();
-        const int tiles = value_tiles(), wide = tiles * 128;
+        // where the rows of results lie: in the place of the sums, which have been read
+        int64_t* rows = reinterpret_cast<int64_t*>(sync->red);
+        if (x.slot < 0) {
+            if (tid < left) rows[tid] = out_at(a, x.rq.qs, 0, first + tid).out - a.out;
+            softmax_sync();
+        }
+        // Columns (query rows) of a lane by 16 or 32.
+        constexpr int W = C::ROWS < 32 ? C::ROWS : 32;
+        const int tiles = value_tiles();
 #pragma unroll 1
-        for (int b = 0; b < tiles * (C::ROWS / 16); ++b) {
-            const int r0 = b % (C::ROWS / 16) * 16, c = b / (C::ROWS / 16) * 128 + tid;  // its rows, the thread's lane
-            if (r0 >= left) continue;
-            float o[16];
-            tmem_ld16(o, lanes + (b / (C::ROWS / 16)) * C::ROWS + r0);
-            tmem_wait_ld();
-            tmem_here16(o);
-            if (patch)
-                for (int r = 0; r < 16; ++r)
-                    if (r0 + r < left) add_not_finite<C::STORE, C::TN, 1>(a, x, first + r0 + r, c, &o[r]);
-            if (x.slot >= 0) {
-                float* to = a.part + (x.slot * C::ROWS + r0) * wide + c;
+        for (int t = 0; t < tiles; ++t) {
+            const int c = t * 128 + tid;
+#pragma unroll 1
+            for (int r0 = 0; r0 < C::ROWS; r0 += W) {
+                if (r0 >= left) break;
+                float o[W];
+                if constexpr (W == 32) tmem_ld32(o, lanes + t * C::ROWS + r0);
+                else tmem_ld16(o, lanes + t * C::ROWS + r0);
+                tmem_wait_ld();
+                latent_here<W>(o);
+                if (patch)
+#pragma unroll 1
+                    for (int r = 0; r < W && r0 + r < left; ++r) {
+                        float add = 0.0f;
+                        add_not_finite<C::STORE, C::TN, 1>(a, x, first + r0 + r, c, &add);
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (r0 + r < left) to[r * wide] = o[r];
-                continue;
-            }
-            // two lanes side by side of every other row a thread
+                        for (int k = 0; k < W; ++k) o[k] += k == r ? add : 0.0f;
+                    }
+                if (x.slot >= 0) {
+                    float* to = a.part + (x.slot * C::ROWS + r0) * kLatentValues + c;
+                    if (r0 + W <= left) {
 #pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-                const float y = o[r] * sync->fac[r0 + r], z = o[r + 1] * sync->fac[r0 + r + 1];
-                const bool odd = lane & 1;
-                const float other = __shfl_xor_sync(0xffffffffu, odd ? y : z, 1);
-                const int row = r0 + r + (odd ? 1 : 0), at = c & ~1;
-                if (row < left && at < a.Dv)
-                    *reinterpret_cast<uint32_t*>(out_at(a, x.rq.qs, 0, first + row).out + at * 2) =
-                        a.bf16 ? pack2<true>(odd ? other : y, odd ? z : other)
-                               : pack2<false>(odd ? other : y, odd ? z : other);
+                        for (int r = 0; r < W; ++r) to[r * kLatentValues] = o[r];
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < W; ++r)
+                            if (r0 + r < left) to[r * kLatentValues] = o[r];
+                    }
+                    continue;
+                }
+                // turned over in the weights' place, rows of 128 lanes: 16 bytes a thread and store
+                const uint32_t words = smem_addr(smem + C::P_AT);
+#pragma unroll
+                for (int r = 0; r < W; ++r) {
+                    const uint32_t y = pack_one(o[r] * sync->fac[r0 + r]);
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(words + r * 256 + (((tid >> 3) ^ (r & 7)) << 4) +
+                                                                 (tid & 7) * 2),
+                                 "h"(static_cast<uint16_t>(y))
+                                 : "memory");
+                }
+                softmax_sync();
+#pragma unroll
+                for (int i = 0; i < W / 8; ++i) {
+                    const int r = i * 8 + (tid >> 4), piece = tid & 15, at = t * 128 + piece * 8;
+                    if (r0 + r < left && at < a.Dv) {
+                        uint32_t w[4];
+                        lds128(w, words + r * 256 + ((piece ^ (r & 7)) << 4));
+                        *reinterpret_cast<uint4*>(a.out + rows[r0 + r] + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                softmax_sync();
             }
         }
         softmax_sync();  // fac and red have been read
@@ -963,7 +1006,7 @@ __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(co
     const int qs = min(max(__ldg(a.q_start + w.r), 0), a.Tq);
     const int n = min(max(__ldg(a.q_start + w.r + 1), qs), a.Tq) - qs;
     const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(w.m) * ROWS));
-    const int tid = int(threadIdx.x), lane = tid & 127, team = tid >> 7, wide = (a.Dv + 127) / 128 * 128;
+    const int tid = int(threadIdx.x), lane = tid & 127, team = tid >> 7;
     const int own = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y);
     const int all = (parts - 1) * int(gridDim.y);
     // part p: block `from` holds it second unless the group begins with the block's run
@@ -980,8 +1023,9 @@ __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(co
             const float2 x = a.part_ml[slot(p) * ROWS + row];
             const float f = pow2(x.x - base);
             l += x.y * f;
-            if (lane * 4 < wide) {
-                const float4 y = *reinterpret_cast<const float4*>(a.part + (slot(p) * ROWS + row) * wide + lane * 4);
+            if (lane * 4 < a.Dv) {
+                const float4 y =
+                    *reinterpret_cast<const float4*>(a.part + (slot(p) * ROWS + row) * kLatentValues + lane * 4);
                 o.x += y.x * f;
                 o.y += y.y * f;
                 o.z += y.z * f;

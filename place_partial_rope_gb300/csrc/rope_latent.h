@@ -29,7 +29,7 @@ LatentPlan choose_latent(int store, int64_t rows, int64_t pages, int64_t page_si
 // The grid: one block an SM of the device (sm_count 0: the current one's).
 rope_status_t latent_blocks(const LatentPlan& p, int sm_count, int* blocks, const char** err);
 
-int64_t latent_workspace(const LatentPlan& p, int v_dim, int blocks);
+int64_t latent_workspace(const LatentPlan& p, int blocks);
 
 rope_status_t launch_latent(const LatentPlan& p, const TreeArgs& args, void* workspace, int blocks,
                             rope_stream_t stream, const char** err);

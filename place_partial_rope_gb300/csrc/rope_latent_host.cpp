@@ -99,7 +99,7 @@ rope_status_t latent_attention(const rope_kv_cache_t* c, const void* q, int dtyp
     const char* err = nullptr;
     int blocks = 0;
     if (latent_blocks(p, 0, &blocks, &err) != ROPE_OK) return fail(ROPE_ERR_CUDA, "%s", err);
-    const int64_t need = latent_workspace(p, static_cast<int>(v_dim), blocks);
+    const int64_t need = latent_workspace(p, blocks);
     if (workspace_bytes < need)
         return fail(ROPE_ERR_INVALID, "workspace of %lld bytes; the call needs %lld", (long long)workspace_bytes,
                     (long long)need);
@@ -179,7 +179,7 @@ rope_status_t rope_partial_latent_attention_workspace(const rope_kv_cache_t* cac
     const char* err = nullptr;
     int blocks = 0;
     if (latent_blocks(p, sm_count, &blocks, &err) != ROPE_OK) return fail(ROPE_ERR_CUDA, "%s", err);
-    *bytes = latent_workspace(p, static_cast<int>(v_dim), blocks);
+    *bytes = latent_workspace(p, blocks);
     return ROPE_OK;
 }
 

@@ -37,9 +37,9 @@ rope_status_t latent_blocks(const LatentPlan& p, int sm_count, int* blocks, cons
     return tree_resident(kernel_of(p), blocks, err);
 }
 
-int64_t latent_workspace(const LatentPlan& p, int v_dim, int blocks) {
-    const int64_t rows = int64_t(2) * blocks * p.rows, wide = (v_dim + 127) / 128 * 128;
-    return rows * wide * int64_t(sizeof(float)) + rows * int64_t(sizeof(float2)) +
+int64_t latent_workspace(const LatentPlan& p, int blocks) {
+    const int64_t rows = int64_t(2) * blocks * p.rows;
+    return rows * kLatentValues * int64_t(sizeof(float)) + rows * int64_t(sizeof(float2)) +
            int64_t(blocks) * int64_t(sizeof(TreeMeta));
 }
 
@@ -47,9 +47,9 @@ rope_status_t launch_latent(const LatentPlan& p, const TreeArgs& args, void* wor
                             rope_stream_t stream, const char** err) {
     const TreeKernel k = kernel_of(p);
     TreeArgs a = args;
-    const int64_t rows = int64_t(2) * blocks * p.rows, wide = (a.Dv + 127) / 128 * 128;
+    const int64_t rows = int64_t(2) * blocks * p.rows;
     a.part = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(a.part + rows * wide);
+    a.part_ml = reinterpret_cast<float2*>(a.part + rows * kLatentValues);
     a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
     CUtensorMap map{}, quads{};
     if (p.boxes) {
