@@ -71,7 +71,7 @@ __device__ __forceinline__ bool bar_nap(unsigned long long* b, uint32_t parity) 
 
 struct LatentSync {
     // a tile's groups of lanes: brought, and done with
-    unsigned long long full[2][3], empty[2][2], s_full[2], s_free[2], p_full, q_full, q_empty, run_full[3], done;
+    unsigned long long full[2][3], empty[2][2], s_full[2], s_free[2], p_full, q_full[3], q_empty, run_full[3], done;
     uint32_t tmem;
     volatile uint32_t dead;
     volatile uint32_t patch[3];  // of run r at r % 3: values were taken out
@@ -445,70 +445,100 @@ struct Latent {
         return r;
     }
 
-    // Queries of all runs and, without tensor copies, their tiles.
+    // A tile without tensor copies, by the 128 threads of a team: eight threads a row, 16 rows
+    // a pass.
+    __device__ __forceinline__ bool load(const RunAt& x, int it, uint32_t n, int tid) const {
+        const int row = tid >> 3, sub = tid & 7, pieces = a.Dk / 8, all = groups();
+        const uint32_t to = stage(n);
+        Row r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = row_of(x, (x.t0 + it) * C::TN + row + 16 * i);
+        if constexpr (C::kWide) {
+            for (int g = 0, c = 0; g < all; ++g) {
+                if (!__all_sync(0xffffffffu, wait_free(n, g))) {
+                    copies_wait<0>();
+                    return false;
+                }
+                for (const int end = group_end(g); c < end; ++c) {
+                    const int piece = c * 8 + sub;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool ok = r[i].p && piece < pieces;
+                        copy16(to + line_at<C::CHUNK>(row + 16 * i, piece), ok ? r[i].p + piece * 16 : a.k, ok);
+                    }
+                }
+                copies_commit();
+            }
+            // groups as they come
+            for (int g = 0; g < all; ++g) {
+                if (all - g == 3) copies_wait<2>();
+                else if (all - g == 2) copies_wait<1>();
+                else copies_wait<0>();
+                to_async_proxy();
+                bar_arrive(&sync->full[n & 1][g]);
+            }
+        } else {
+            // codes are asked for before the place is free, and become fp16 on their way
+            uint2 w[4][C::CHUNKS];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    const int piece = c * 8 + sub;
+                    // (volatile: as a plain load it would be moved down to where it is used, and waited for
+                    // there, chunk after chunk)
+                    w[i][c] = make_uint2(0, 0);
+                    if (r[i].p && piece < pieces)
+                        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];"
+                                     : "=r"(w[i][c].x), "=r"(w[i][c].y)
+                                     : "l"(r[i].p + piece * 8));
+                }
+            int g = 0;
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c) {
+                if (c >= chunks()) break;
+                if (c == 0 || c == group_end(g - 1)) {
+                    if (!__all_sync(0xffffffffu, wait_free(n, g++))) return false;
+                    // (the scales of tile n - 2 have been read when its first product is done)
+                    if (c == 0 && sub == 0)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) scales(n)[row + 16 * i] = r[i].scale;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sts128(to + line_at<C::CHUNK>(row + 16 * i, c * 8 + sub), codes_to_half2<C::STORE, false>(w[i][c].x),
+                           codes_to_half2<C::STORE, true>(w[i][c].x), codes_to_half2<C::STORE, false>(w[i][c].y),
+                           codes_to_half2<C::STORE, true>(w[i][c].y));
+                if (c + 1 == group_end(g - 1)) {
+                    to_async_proxy();
+                    bar_arrive(&sync->full[n & 1][g - 1]);
+                }
+            }
+        }
+        return true;
+    }
+
+    // Queries of all runs and, without tensor copies, their tiles: two teams, one for
+    // either of the tiles' places, so that both are on their way at a time.  A team's first tile
+    // of a run comes before the queries, which have to wait for the scores of the run before.
     __device__ __forceinline__ void help(int id) const {
-        RunAt x;
-        uint32_t n = 0;
+        const uint32_t team = uint32_t(id) >> 7;
+        uint32_t n0 = 0;  // tiles of the runs before
         for (uint32_t run = 0;; ++run) {
+            RunAt x;
             if (!__all_sync(0xffffffffu, take(run, x))) return;
+            const int first = int((n0 ^ team) & 1);
+            if constexpr (!C::BOXES)
+                if (first < x.count && !load(x, first, n0 + first, id & 127)) return;
             if (run > 0) wait_run(&sync->q_empty, (run - 1) & 1);
             if (given_up()) return;
             queries(x, run, id);
             to_async_proxy();
-            bar_arrive(&sync->q_full);
+            bar_arrive(&sync->q_full[run % 3]);
             if constexpr (!C::BOXES)
-                for (int it = 0; it < x.count; ++it, ++n) {
-                    const int row = id >> 3, sub = id & 7, pieces = a.Dk / 8;
-                    const uint32_t to = stage(n);
-                    const Row r[2] = {row_of(x, (x.t0 + it) * C::TN + row), row_of(x, (x.t0 + it) * C::TN + row + 32)};
-                    if constexpr (C::kWide) {
-                        bool on = true;
-                        for (int g = 0; g < groups(); ++g) on = wait_free(n, g) && on;
-                        if (!__all_sync(0xffffffffu, on)) return;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            for (int c = 0; c < chunks(); ++c) {
-                                const int piece = c * 8 + sub;
-                                const bool ok = r[i].p && piece < pieces;
-                                copy16(to + line_at<C::CHUNK>(row + 32 * i, piece), ok ? r[i].p + piece * 16 : a.k, ok);
-                            }
-                        copies_commit();
-                        copies_wait<0>();
-                        to_async_proxy();
-                        for (int g = 0; g < groups(); ++g) bar_arrive(&sync->full[n & 1][g]);
-                    } else {
-                        // codes are asked for before the place is free
-                        uint2 w[2][C::CHUNKS];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int c = 0; c < C::CHUNKS; ++c) {
-                                const int piece = c * 8 + sub;
-                                w[i][c] = r[i].p && piece < pieces
-                                              ? __ldg(reinterpret_cast<const uint2*>(r[i].p) + piece)
-                                              : make_uint2(0, 0);
-                            }
-                        int g = 0;
-#pragma unroll
-                        for (int c = 0; c < C::CHUNKS; ++c) {
-                            if (c >= chunks()) break;
-                            if (c == 0 || c == group_end(g - 1)) {
-                                if (!__all_sync(0xffffffffu, wait_free(n, g++))) return;
-                                // (the scales of tile n - 2 have been read when its first product is done)
-                                if (c == 0 && sub == 0) scales(n)[row] = r[0].scale, scales(n)[row + 32] = r[1].scale;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                sts128(to + line_at<C::CHUNK>(row + 32 * i, c * 8 + sub),
-                                       codes_to_half2<C::STORE, false>(w[i][c].x), codes_to_half2<C::STORE, true>(w[i][c].x),
-                                       codes_to_half2<C::STORE, false>(w[i][c].y), codes_to_half2<C::STORE, true>(w[i][c].y));
-                            if (c + 1 == group_end(g - 1)) {
-                                to_async_proxy();
-                                bar_arrive(&sync->full[n & 1][g - 1]);
-                            }
-                        }
-                    }
-                }
+                for (int it = first + 2; it < x.count; it += 2)
+                    if (!load(x, it, n0 + it, id & 127)) return;
+            n0 += x.count;
         }
     }
 
@@ -529,7 +559,7 @@ struct Latent {
             RunAt x;
             if (!__all_sync(0xffffffffu, take(run, x))) break;
             const int count = __shfl_sync(0xffffffffu, x.count, 0);
-            wait(&sync->q_full, run & 1);
+            wait(&sync->q_full[run % 3], (run / 3) & 1);
             bool on = true;
             for (int it = 0; on && it < count; ++it, ++n) {
                 // the softmax has read the scores before the last
@@ -691,7 +721,8 @@ struct Latent {
                 tmem_after();
                 latent_ld<C::ROWS>(s, lanes + C::S_COL + (n & 1) * C::ROWS);
                 if constexpr (!C::kWide) {
-                    if (it == 0)  // written by the helpers before the tile
+                    if (it == 0) wait(&sync->q_full[run % 3], (run / 3) & 1);  // the helpers' factors are seen
+                    if (it == 0)
 #pragma unroll
                         for (int i = 0; i < NC; ++i) qf[i] = factors(run)[(i >> 1) * 8 + c0 + (i & 1)];
 #pragma unroll
@@ -938,19 +969,19 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const int warp = int(threadIdx.x) >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            for (int g = 0; g < 3; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : 256);
+            for (int g = 0; g < 3; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : 128);
             for (int g = 0; g < 2; ++g) bar_init(&sync->empty[i][g], 1);
             bar_init(&sync->s_full[i], 1);
             bar_init(&sync->s_free[i], 128);
         }
         bar_init(&sync->p_full, 128);
-        bar_init(&sync->q_full, 256);
         bar_init(&sync->q_empty, 1);
         bar_init(&sync->done, 2);
         sync->dead = 0;
         for (int i = 0; i < 3; ++i) {
             sync->patch[i] = 0;
             bar_init(&sync->run_full[i], 1);
+            bar_init(&sync->q_full[i], 256);
         }
         sync->taken = 0;
         sync->beat = 0;
@@ -990,13 +1021,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 
 // Puts the parts of each split (request, row tile) together: out = sum_p O_p 2^(m_p - m) /
 // sum_p l_p 2^(m_p - m).  A group cut by s block borders has s blocks here (times
-// gridDim.y), which share out its rows; a block's four teams take the parts of a row in
-// turn, four lanes a thread, and are added up in one order.
+// gridDim.y), which share out its pieces of 128 lanes of a row.  Up to 8 parts: a warp takes
+// a piece, four lanes a thread, with its parts' loads in flight together; more: a block
+// does, whose warps take the parts in turn and are added up in one order.
 template <int ROWS>
 __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(const __grid_constant__ TreeArgs a) {
-    constexpr int TEAMS = 4;
-    __shared__ float4 sums[TEAMS][128];
-    __shared__ float2 team_ml[TEAMS];
+    constexpr int WARPS = kLatentJoinThreads / 32;
+    __shared__ float4 sums[WARPS][32];
+    __shared__ float2 warp_ml[WARPS];
     after_predecessor();
     const int64_t b = int64_t(blockIdx.x) + 1;
     const TreeMeta w = a.meta[b];
@@ -1006,59 +1038,75 @@ __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(co
     const int qs = min(max(__ldg(a.q_start + w.r), 0), a.Tq);
     const int n = min(max(__ldg(a.q_start + w.r + 1), qs), a.Tq) - qs;
     const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(w.m) * ROWS));
-    const int tid = int(threadIdx.x), lane = tid & 127, team = tid >> 7;
+    const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5, quarters = (a.Dv + 127) / 128;
     const int own = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y);
     const int all = (parts - 1) * int(gridDim.y);
     // part p: block `from` holds it second unless the group begins with the block's run
     const int64_t second = from * w.chunk < w.u0 - w.lead ? 1 : 0;
-    auto slot = [&](int p) { return (from + p) * 2 + (p == 0 ? second : 0); };
-    for (int row = own; row < left; row += all) {
-        float top = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int p = team; p < parts; p += TEAMS) top = fmaxf(top, a.part_ml[slot(p) * ROWS + row].x);
+    auto slot = [&](int p) { return ((from + p) * 2 + (p == 0 ? second : 0)) * ROWS; };
+    auto write = [&](int row, int c, float4 o, float top, float l) {
+        const float norm = l == 0.0f ? 0.0f : 1.0f / l;
+        const OutAt z = out_at(a, qs, 0, w.m * ROWS + row);
+        if (c < a.Dv)
+            *reinterpret_cast<uint2*>(z.out + c * 2) =
+                a.bf16 ? make_uint2(pack2<true>(o.x * norm, o.y * norm), pack2<true>(o.z * norm, o.w * norm))
+                       : make_uint2(pack2<false>(o.x * norm, o.y * norm), pack2<false>(o.z * norm, o.w * norm));
+        if (c == 0 && z.lse) *z.lse = latent_lse(top, l);
+    };
+    // parts from p0 on, `step` apart
+    auto gather = [&](int row, int c, int p0, int step, float4& o, float& top, float& l) {
+        top = -INFINITY;
+#pragma unroll 8
+        for (int p = p0; p < parts; p += step) top = fmaxf(top, a.part_ml[slot(p) + row].x);
         const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-        for (int p = team; p < parts; p += TEAMS) {
-            const float2 x = a.part_ml[slot(p) * ROWS + row];
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        l = 0.0f;
+#pragma unroll 8
+        for (int p = p0; p < parts; p += step) {
+            const float2 x = a.part_ml[slot(p) + row];
+            const float4 y = *reinterpret_cast<const float4*>(a.part + (slot(p) + row) * kLatentValues + c);
             const float f = pow2(x.x - base);
             l += x.y * f;
-            if (lane * 4 < a.Dv) {
-                const float4 y =
-                    *reinterpret_cast<const float4*>(a.part + (slot(p) * ROWS + row) * kLatentValues + lane * 4);
-                o.x += y.x * f;
-                o.y += y.y * f;
-                o.z += y.z * f;
-                o.w += y.w * f;
-            }
+            o.x += y.x * f;
+            o.y += y.y * f;
+            o.z += y.z * f;
+            o.w += y.w * f;
         }
-        sums[team][lane] = o;
-        if (lane == 0) team_ml[team] = make_float2(top, l);
+    };
+    float4 o;
+    float top, l;
+    if (parts <= 8) {
+        for (int i = own * WARPS + warp; i < left * quarters; i += all * WARPS) {
+            const int row = i / quarters, c = (i - row * quarters) * 128 + lane * 4;
+            gather(row, c, 0, 1, o, top, l);
+            write(row, c, o, top, l);
+        }
+        return;
+    }
+    for (int i = own; i < left * quarters; i += all) {
+        const int row = i / quarters, c = (i - row * quarters) * 128 + lane * 4;
+        gather(row, c, warp, WARPS, o, top, l);
+        sums[warp][lane] = o;
+        if (lane == 0) warp_ml[warp] = make_float2(top, l);
         __syncthreads();
-        if (team == 0) {
+        if (warp == 0) {
             top = -INFINITY;
 #pragma unroll
-            for (int t = 0; t < TEAMS; ++t) top = fmaxf(top, team_ml[t].x);
-            const float m = top == -INFINITY ? 0.0f : top;
+            for (int t = 0; t < WARPS; ++t) top = fmaxf(top, warp_ml[t].x);
+            const float base = top == -INFINITY ? 0.0f : top;
             l = 0.0f;
             o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int t = 0; t < TEAMS; ++t) {
-                const float f = pow2(team_ml[t].x - m);
+            for (int t = 0; t < WARPS; ++t) {
+                const float f = pow2(warp_ml[t].x - base);
                 const float4 y = sums[t][lane];
-                l += team_ml[t].y * f;
+                l += warp_ml[t].y * f;
                 o.x += y.x * f;
                 o.y += y.y * f;
                 o.z += y.z * f;
                 o.w += y.w * f;
             }
-            const float norm = l == 0.0f ? 0.0f : 1.0f / l;
-            const OutAt z = out_at(a, qs, 0, w.m * ROWS + row);
-            if (lane * 4 < a.Dv)
-                *reinterpret_cast<uint2*>(z.out + lane * 8) =
-                    a.bf16 ? make_uint2(pack2<true>(o.x * norm, o.y * norm), pack2<true>(o.z * norm, o.w * norm))
-                           : make_uint2(pack2<false>(o.x * norm, o.y * norm), pack2<false>(o.z * norm, o.w * norm));
-            if (lane == 0 && z.lse) *z.lse = latent_lse(top, l);
+            write(row, c, o, top, l);
         }
         __syncthreads();
     }

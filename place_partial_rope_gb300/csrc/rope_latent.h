@@ -10,7 +10,7 @@ constexpr int kLatentKeys = 64;      // cache rows of a tile
 constexpr int kLatentLanes = 576;    // of a row, at most
 constexpr int kLatentValues = 512;   // of those that are the value, at most
 constexpr int kLatentThreads = 480;
-constexpr int kLatentJoinThreads = 512;
+constexpr int kLatentJoinThreads = 256;
 
 struct LatentPlan {
     int store;  // rope_cache_dtype_t

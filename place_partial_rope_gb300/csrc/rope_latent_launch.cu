@@ -25,7 +25,7 @@ LatentPlan choose_latent(int store, int64_t rows, int64_t pages, int64_t page_si
     LatentPlan p{};
     p.store = store;
     p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.boxes = (store == ROPE_CACHE_BF16 || store == ROPE_CACHE_FP16) && pages > 0 && page_size % 8 == 0;
+    p.boxes = (store == ROPE_CACHE_BF16 || store == ROPE_CACHE_FP16) && pages > 0 && page_size % 64 == 0;
     return p;
 }
 
