@@ -479,40 +479,38 @@ struct Latent {
             }
         } else {
             // codes are asked for before the place is free, and become fp16 on their way
-            uint2 w[4][C::CHUNKS];
+#pragma unroll 1
+            for (int g = 0, c0 = 0; g < all; ++g) {
+                const int end = group_end(g);
+#pragma unroll 1
+                for (int c = c0; c < end; c += 4) {
+                    uint2 w[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    const int piece = c * 8 + sub;
-                    // (volatile: as a plain load it would be moved down to where it is used, and waited for
-                    // there, chunk after chunk)
-                    w[i][c] = make_uint2(0, 0);
-                    if (r[i].p && piece < pieces)
-                        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];"
-                                     : "=r"(w[i][c].x), "=r"(w[i][c].y)
-                                     : "l"(r[i].p + piece * 8));
-                }
-            int g = 0;
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c) {
-                if (c >= chunks()) break;
-                if (c == 0 || c == group_end(g - 1)) {
-                    if (!__all_sync(0xffffffffu, wait_free(n, g++))) return false;
+                        for (int k = 0; k < 4; ++k) {
+                            const int piece = (c + k) * 8 + sub;
+                            w[i][k] = r[i].p && c + k < end && piece < pieces
+                                          ? __ldg(reinterpret_cast<const uint2*>(r[i].p) + piece)
+                                          : make_uint2(0, 0);
+                        }
+                    if (c == c0 && !__all_sync(0xffffffffu, wait_free(n, g))) return false;
                     // (the scales of tile n - 2 have been read when its first product is done)
                     if (c == 0 && sub == 0)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) scales(n)[row + 16 * i] = r[i].scale;
-                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sts128(to + line_at<C::CHUNK>(row + 16 * i, c * 8 + sub), codes_to_half2<C::STORE, false>(w[i][c].x),
-                           codes_to_half2<C::STORE, true>(w[i][c].x), codes_to_half2<C::STORE, false>(w[i][c].y),
-                           codes_to_half2<C::STORE, true>(w[i][c].y));
-                if (c + 1 == group_end(g - 1)) {
-                    to_async_proxy();
-                    bar_arrive(&sync->full[n & 1][g - 1]);
+                    for (int k = 0; k < 4; ++k)
+                        if (c + k < end)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                sts128(to + line_at<C::CHUNK>(row + 16 * i, (c + k) * 8 + sub),
+                                       codes_to_half2<C::STORE, false>(w[i][k].x), codes_to_half2<C::STORE, true>(w[i][k].x),
+                                       codes_to_half2<C::STORE, false>(w[i][k].y), codes_to_half2<C::STORE, true>(w[i][k].y));
                 }
+                to_async_proxy();
+                bar_arrive(&sync->full[n & 1][g]);
+                c0 = end;
             }
         }
         return true;
@@ -568,17 +566,14 @@ struct Latent {
                 const uint32_t to = __shfl_sync(0xffffffffu, tmem + C::S_COL + (n & 1) * C::ROWS, 0);
                 const uint32_t k = __shfl_sync(0xffffffffu, stage(n) >> 4, 0), par = (n / 2) & 1;
                 unsigned long long* full = sync->full[n & 1];
+#pragma unroll 1
+                for (int c = 0; c < all; ++c) {
+                    if (c == rest) on = wait(full + groups_of_values, par);
+                    else if (c % 4 == 0 && c < rest) on = wait(full + c / 4, par);
+                    const uint32_t x0 = k + c * (C::CHUNK >> 4), y0 = q + c * (C::Q_CHUNK >> 4);
+                    mma_one(me, to, x0, y0, shape, c > 0);
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    if (c >= all) break;
-                    if (c % 2 == 0) {
-                        if (c == rest) on = wait(full + groups_of_values, par);
-                        else if (c % 4 == 0 && c < rest) on = wait(full + c / 4, par);
-                    }
-                    mma_one(me, to, k + c * (C::CHUNK >> 4), q + c * (C::Q_CHUNK >> 4), shape, c > 0);
-#pragma unroll
-                    for (int i = 1; i < 4; ++i)
-                        mma_one(me, to, k + c * (C::CHUNK >> 4) + i * 2, q + c * (C::Q_CHUNK >> 4) + i * 2, shape, true);
+                    for (int i = 1; i < 4; ++i) mma_one(me, to, x0 + i * 2, y0 + i * 2, shape, true);
                 }
                 on = __all_sync(0xffffffffu, on);  // (given up: the scores are whatever they are)
                 commit_one(me, &sync->s_full[n & 1]);
@@ -605,9 +600,8 @@ struct Latent {
                 tmem_after();
                 const uint32_t v = __shfl_sync(0xffffffffu, (stage(n) >> 4) | lead, 0);
                 const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (t >= tiles) break;
+#pragma unroll 1
+                for (int t = 0; t < tiles; ++t) {
                     mma_one(me, to + t * C::ROWS, v + t * (C::CHUNK >> 3), p, shape, it > 0);
 #pragma unroll
                     for (int i = 1; i < 4; ++i)
@@ -736,7 +730,7 @@ struct Latent {
                 tmem_before();
                 bar_arrive(&sync->s_free[n & 1]);
                 uint32_t seen = 0xffffffffu;
-                if (part) {
+                if (__builtin_expect(part, 0)) {
                     seen = 0;
 #pragma unroll 1
                     for (int i = 0; i < NC; ++i) {
@@ -758,8 +752,8 @@ struct Latent {
                     most[(i >> 1) & 1] = max3(most[(i >> 1) & 1], y.x, y.y);
                 }
                 bool moved = false;
-                if (softmax_any(it == 0 || sync->dead ||
-                                fmaxf(most[0] + lu[0], most[1] + lu[1]) > C::kLag + C::kBias)) {
+                if (__builtin_expect(softmax_any(it == 0 || sync->dead ||
+                                                 fmaxf(most[0] + lu[0], most[1] + lu[1]) > C::kLag + C::kBias), 0)) {
                     if (softmax_any(sync->dead)) return;
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
@@ -796,7 +790,7 @@ struct Latent {
                 // the weights' place is free, and O still, when the tile before is done
                 if (n > 0) wait_product(n - 1);
                 __syncwarp();
-                if (moved) {
+                if (__builtin_expect(moved, 0)) {
                     tmem_after();
                     shrink(lanes);
                 }
@@ -824,7 +818,7 @@ struct Latent {
                                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                                  : "memory");
                 }
-                if (part && C::STORE != ROPE_CACHE_INT8)
+                if (__builtin_expect(part, 0) && C::STORE != ROPE_CACHE_INT8)
                     mend(n, max(prefix - tile * C::TN, 0), x.rq.len - tile * C::TN, run);
                 to_async_proxy();
                 tmem_before();
