@@ -49,6 +49,10 @@ struct LatentCfg {
     static constexpr int STAGE = CHUNKS * CHUNK, STAGES = 2;
     static constexpr int K_AT = Q_BYTES, P_AT = K_AT + STAGES * STAGE, SYNC_AT = P_AT + (ROWS < 64 ? ROWS * 256 : ROWS * 128);  // (P, and results turned over)
     static constexpr int kSmemMax = 232448;
+    // softmax groups of four warps, which share out the columns (query rows): two where the
+    // helpers have little to do
+    static constexpr int SG = ROWS == 64 && BOXES ? 2 : 1, SR = ROWS / SG;
+    static constexpr int HELPERS = SG == 2 ? 128 : 256;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f, kLag = 8.0f;
     static constexpr int MORE = kWide ? 0 : (3 * ROWS + 2 * TN) * 4;  // factors and scales
     static constexpr int kAhead = 3;  // tiles from one that is brought to one that is asked into L2
@@ -74,11 +78,11 @@ struct LatentSync {
     unsigned long long full[2][3], empty[2][2], s_full[2], s_free[2], p_full, q_full[3], q_empty, run_full[3], done;
     uint32_t tmem;
     volatile uint32_t dead;
-    volatile uint32_t patch[3];  // of run r at r % 3: values were taken out
+    volatile uint32_t patch[3];  // of run r at r % 3: r + 1 when values were taken out
     volatile uint32_t taken;     // runs that the softmax has begun
     volatile uint32_t beat;      // tiles done
     RunAt run[3];                // run r at r % 3, when its barrier says so; of no tiles: there is none
-    float red[4][64], fac[64];  // of the softmax
+    float red[256], fac[64];     // of the softmax
 };
 
 template <int ROWS>
@@ -150,18 +154,18 @@ __device__ __forceinline__ void commit_one(uint32_t me, unsigned long long* b) {
                  : "memory");
 }
 
-// Whether any of the softmax's 128 threads says so.
-__device__ __forceinline__ bool softmax_any(bool mine) {
+// Whether any of the 128 threads of softmax group `bar` - 1 says so.
+__device__ __forceinline__ bool softmax_any(int bar, bool mine) {
     uint32_t any;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, 128, p;\n"
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, %2, 128, p;\n"
                  "selp.u32 %0, 1, 0, q;\n}"
                  : "=r"(any)
-                 : "r"(uint32_t(mine))
+                 : "r"(uint32_t(mine)), "r"(bar)
                  : "memory");
     return any != 0;
 }
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync(int bar) { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
 
 template <class C>
 struct Latent {
@@ -355,13 +359,13 @@ struct Latent {
         return uint32_t(piece >> 3) * BYTES + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
     }
 
-    // The queries of a run: eight threads a row, 32 rows a pass.
+    // The queries of a run: eight threads a row.
     __device__ __forceinline__ void queries(const RunAt& x, uint32_t run, int id) const {
         const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
         const uint32_t to = smem_addr(smem);
         const int pieces = a.Dk / 8;
         if constexpr (C::kWide) {
-            for (int row = id >> 3; row < C::ROWS; row += 32) {
+            for (int row = id >> 3; row < C::ROWS; row += C::HELPERS / 8) {
                 const char* src = nullptr;
                 if (row < left) {
                     uint32_t tok, g;
@@ -379,7 +383,7 @@ struct Latent {
             return;
         }
 #pragma unroll 1
-        for (int row = id >> 3; row < C::ROWS; row += 32) {
+        for (int row = id >> 3; row < C::ROWS; row += C::HELPERS / 8) {
             const char* src = nullptr;
             if (row < left) {
                 uint32_t tok, g;
@@ -627,10 +631,10 @@ struct Latent {
     // The last tiles of a request: values of rows that are not there become zeros, and
     // those of drafted rows that are not finite are taken out (see add_not_finite): a
     // weight of 0 times them would reach the tokens that do not see the row.
-    __device__ __noinline__ void mend(uint32_t n, int from, int valid, uint32_t run) const {
+    __device__ __noinline__ void mend(uint32_t n, int from, int valid, uint32_t run, int group) const {
         const int pieces = value_tiles() * 16, lane = int(threadIdx.x) & 31;
         bool found = false;
-        for (int row = from + (int(threadIdx.x) >> 5); row < C::TN; row += 4)
+        for (int row = from + (int(threadIdx.x) >> 5 & 3) * C::SG + group; row < C::TN; row += 4 * C::SG)
             for (int piece = lane; piece < pieces; piece += 32) {
                 const uint32_t at = stage(n) + line_at<C::CHUNK>(row, piece);
                 if (row >= valid) {
@@ -650,15 +654,16 @@ struct Latent {
                     sts128(at, w[0], w[1], w[2], w[3]);
                 }
             }
-        if (found) sync->patch[run % 3] = 1;
+        if (found) sync->patch[run % 3] = run + 1;
         __syncwarp();
     }
 
-    // Columns of O times the factors of their rows.
-    __device__ __forceinline__ void shrink(uint32_t lanes) const {
+    // A group's columns of O times the factors of their rows.
+    __device__ __forceinline__ void shrink(uint32_t lanes, int col0) const {
         const int tiles = value_tiles();
 #pragma unroll 1
-        for (int c = 0; c < tiles * C::ROWS; c += 16) {
+        for (int i = 0; i < tiles * C::SR; i += 16) {
+            const int c = i / C::SR * C::ROWS + col0 + i % C::SR;
             float o[16];
             tmem_ld16(o, lanes + c);
             tmem_wait_ld();
@@ -666,7 +671,7 @@ struct Latent {
             const float* f = sync->fac + c % C::ROWS;
             uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f[i]);
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * f[k]);
             tmem_st16(lanes + c, w);
         }
         tmem_wait_st();
@@ -687,19 +692,20 @@ struct Latent {
         return y;
     }
 
-    __device__ __forceinline__ void softmax() const {
-        constexpr int NC = C::ROWS / 4, J = C::ROWS / 8;  // columns of a thread, blocks of eight
-        const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, k0 = warp * 16 + (lane >> 2),
-                  c0 = (lane & 3) * 2;
+    __device__ __forceinline__ void softmax(int group) const {
+        constexpr int NC = C::SR / 4, J = C::SR / 8;  // columns of a thread, blocks of eight
+        const int tid = int(threadIdx.x) & 127, lane = tid & 31, warp = tid >> 5, k0 = warp * 16 + (lane >> 2),
+                  col0 = group * C::SR, c0 = col0 + (lane & 3) * 2, bar = group + 1;
+        float* red = sync->red + group * 4 * C::SR;  // the warps' maxima of the group's columns
         const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
         // of the four 8 x 8 matrices of a transposing store, this thread names a line
-        const int mat = lane >> 3, qrow = (mat >> 1) * 8 + (lane & 7), chunk = warp * 2 + (mat & 1);
+        const int mat = lane >> 3, qrow = col0 + (mat >> 1) * 8 + (lane & 7), chunk = warp * 2 + (mat & 1);
         const uint32_t p_at = smem_addr(smem + C::P_AT) + qrow * 128 + ((chunk ^ (qrow & 7)) << 4);
         RunAt x;
         uint32_t n = 0;
         for (uint32_t run = 0;; ++run) {
-            if (softmax_any(!take(run, x))) return;
-            if (tid == 0) sync->taken = run + 1;
+            if (softmax_any(bar, !take(run, x))) return;
+            if (threadIdx.x == 0) sync->taken = run + 1;
             const int prefix = x.rq.len - x.rq.n, first = x.m * C::ROWS;
             float ref[NC], l[NC], qf[C::kWide ? 1 : NC];
 #pragma unroll
@@ -707,13 +713,13 @@ struct Latent {
             for (int it = 0; it < x.count; ++it, ++n) {
                 const int tile = x.t0 + it;
                 const bool part = (tile + 1) * C::TN > prefix;  // more than context rows
-                float s[C::ROWS / 2], u[2] = {1.0f, 1.0f}, lu[2] = {0.0f, 0.0f};
+                float s[C::SR / 2], u[2] = {1.0f, 1.0f}, lu[2] = {0.0f, 0.0f};
                 wait(&sync->s_full[n & 1], (n / 2) & 1);
                 if (part || !C::kWide)  // what copies or helpers wrote is seen
                     for (int g = 0; g < value_groups(); ++g) wait(&sync->full[n & 1][g], (n / 2) & 1);
                 __syncwarp();
                 tmem_after();
-                latent_ld<C::ROWS>(s, lanes + C::S_COL + (n & 1) * C::ROWS);
+                latent_ld<C::SR>(s, lanes + C::S_COL + (n & 1) * C::ROWS + col0);
                 if constexpr (!C::kWide) {
                     if (it == 0) wait(&sync->q_full[run % 3], (run / 3) & 1);  // the helpers' factors are seen
                     if (it == 0)
@@ -726,7 +732,7 @@ struct Latent {
                     }
                 }
                 tmem_wait_ld();
-                latent_here<C::ROWS / 2>(s);
+                latent_here<C::SR / 2>(s);
                 tmem_before();
                 bar_arrive(&sync->s_free[n & 1]);
                 uint32_t seen = 0xffffffffu;
@@ -742,19 +748,19 @@ struct Latent {
                     }
                     if constexpr (C::kWide)
 #pragma unroll
-                        for (int i = 0; i < C::ROWS / 2; ++i)
+                        for (int i = 0; i < C::SR / 2; ++i)
                             if (!(seen >> i & 1u)) s[i] = -INFINITY;
                 }
                 float most[2] = {-INFINITY, -INFINITY};  // of the thread's two rows, from the reference
 #pragma unroll
-                for (int i = 0; i < C::ROWS / 2; i += 2) {
+                for (int i = 0; i < C::SR / 2; i += 2) {
                     const float2 y = from_reference(s, ref, qf, u, seen, i);
                     most[(i >> 1) & 1] = max3(most[(i >> 1) & 1], y.x, y.y);
                 }
                 bool moved = false;
-                if (__builtin_expect(softmax_any(it == 0 || sync->dead ||
+                if (__builtin_expect(softmax_any(bar, it == 0 || sync->dead ||
                                                  fmaxf(most[0] + lu[0], most[1] + lu[1]) > C::kLag + C::kBias), 0)) {
-                    if (softmax_any(sync->dead)) return;
+                    if (softmax_any(bar, sync->dead)) return;
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
                         const int j = (i >> 1) * 4 + (i & 1);
@@ -767,14 +773,14 @@ struct Latent {
                                                                 : -INFINITY);
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        if (lane < 4) sync->red[warp][(i >> 1) * 8 + c0 + (i & 1)] = top;
+                        if (lane < 4) red[warp * C::SR + (i >> 1) * 8 + c0 - col0 + (i & 1)] = top;
                     }
-                    softmax_sync();
+                    softmax_sync(bar);
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
                         const int c = (i >> 1) * 8 + c0 + (i & 1);
-                        const float top = fmaxf(fmaxf(sync->red[0][c], sync->red[1][c]),
-                                                fmaxf(sync->red[2][c], sync->red[3][c]));
+                        const float* z = red + c - col0;
+                        const float top = fmaxf(fmaxf(z[0], z[C::SR]), fmaxf(z[2 * C::SR], z[3 * C::SR]));
                         float f = 1.0f;
                         if (top - ref[i] > C::kLag + C::kBias || (it == 0 && top > -3.40282347e+38f)) {
                             const float to = rintf(top - C::kBias);
@@ -784,7 +790,7 @@ struct Latent {
                         }
                         if (tid < 4) sync->fac[c] = f;
                     }
-                    softmax_sync();
+                    softmax_sync(bar);
                     moved = it > 0;
                 }
                 // the weights' place is free, and O still, when the tile before is done
@@ -792,7 +798,7 @@ struct Latent {
                 __syncwarp();
                 if (__builtin_expect(moved, 0)) {
                     tmem_after();
-                    shrink(lanes);
+                    shrink(lanes, col0);
                 }
 #pragma unroll
                 for (int j = 0; j < J; j += 2) {
@@ -819,16 +825,16 @@ struct Latent {
                                  : "memory");
                 }
                 if (__builtin_expect(part, 0) && C::STORE != ROPE_CACHE_INT8)
-                    mend(n, max(prefix - tile * C::TN, 0), x.rq.len - tile * C::TN, run);
+                    mend(n, max(prefix - tile * C::TN, 0), x.rq.len - tile * C::TN, run, group);
                 to_async_proxy();
                 tmem_before();
                 bar_arrive(&sync->p_full);
             }
             // the run's results, when its last product is done
             wait_product(n - 1);
-            if (softmax_any(sync->dead)) return;
+            if (softmax_any(bar, sync->dead)) return;
             tmem_after();
-            finish(x, run, ref, l, lanes);
+            finish(x, run, ref, l, lanes, group);
             tmem_before();
         }
     }
@@ -838,46 +844,49 @@ struct Latent {
     }
 
     __device__ __forceinline__ void finish(const RunAt& x, uint32_t run, const float* ref, float* l,
-                                           uint32_t lanes) const {
-        constexpr int NC = C::ROWS / 4;
-        const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, c0 = (lane & 3) * 2;
+                                           uint32_t lanes, int group) const {
+        constexpr int NC = C::SR / 4;
+        const int tid = int(threadIdx.x) & 127, lane = tid & 31, warp = tid >> 5, col0 = group * C::SR,
+                  c0 = col0 + (lane & 3) * 2, bar = group + 1;
+        float *red = sync->red + group * 4 * C::SR, *fac = sync->fac;
         const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
-        const bool patch = sync->patch[run % 3] != 0;
+        const bool patch = sync->patch[run % 3] == run + 1;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i >> 1) * 8 + c0 + (i & 1);
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-            if (lane < 4) sync->red[warp][c] = l[i];
-            if (tid < 4) sync->fac[c] = ref[i];
+            if (lane < 4) red[warp * C::SR + c - col0] = l[i];
+            if (tid < 4) fac[c] = ref[i];
         }
-        softmax_sync();
-        if (tid == 0) sync->patch[run % 3] = 0;
-        if (tid < C::ROWS) {
-            const float all = sync->red[0][tid] + sync->red[1][tid] + sync->red[2][tid] + sync->red[3][tid];
-            const float m = all == 0.0f ? -INFINITY : sync->fac[tid];
-            sync->fac[tid] = x.slot >= 0 ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
-            if (x.slot >= 0) a.part_ml[x.slot * C::ROWS + tid] = make_float2(m, all);
-            else if (tid < left) {
-                const OutAt y = out_at(a, x.rq.qs, 0, first + tid);
+        softmax_sync(bar);
+        if (tid < C::SR) {
+            const int row = col0 + tid;
+            const float all = red[tid] + red[C::SR + tid] + red[2 * C::SR + tid] + red[3 * C::SR + tid];
+            const float m = all == 0.0f ? -INFINITY : fac[row];
+            fac[row] = x.slot >= 0 ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
+            if (x.slot >= 0) a.part_ml[x.slot * C::ROWS + row] = make_float2(m, all);
+            else if (row < left) {
+                const OutAt y = out_at(a, x.rq.qs, 0, first + row);
                 if (y.lse) *y.lse = latent_lse(m, all);
             }
         }
-        softmax_sync();
+        softmax_sync(bar);
         // where the rows of results lie: in the place of the sums, which have been read
-        int64_t* rows = reinterpret_cast<int64_t*>(sync->red);
+        int64_t* rows = reinterpret_cast<int64_t*>(red);
         if (x.slot < 0) {
-            if (tid < left) rows[tid] = out_at(a, x.rq.qs, 0, first + tid).out - a.out;
-            softmax_sync();
+            if (tid < C::SR && col0 + tid < left) rows[tid] = out_at(a, x.rq.qs, 0, first + col0 + tid).out - a.out;
+            softmax_sync(bar);
         }
-        // Columns (query rows) of a lane by 16 or 32.
-        constexpr int W = C::ROWS < 32 ? C::ROWS : 32;
+        // Columns (query rows) of a lane by 16 or 32, turned over in a group's own part of the
+        // weights' place.
+        constexpr int W = C::SG == 2 || C::ROWS < 32 ? 16 : 32;
         const int tiles = value_tiles();
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int c = t * 128 + tid;
 #pragma unroll 1
-            for (int r0 = 0; r0 < C::ROWS; r0 += W) {
+            for (int r0 = col0; r0 < col0 + C::SR; r0 += W) {
                 if (r0 >= left) break;
                 float o[W];
                 if constexpr (W == 32) tmem_ld32(o, lanes + t * C::ROWS + r0);
@@ -905,29 +914,29 @@ struct Latent {
                     continue;
                 }
                 // turned over in the weights' place, rows of 128 lanes: 16 bytes a thread and store
-                const uint32_t words = smem_addr(smem + C::P_AT);
+                const uint32_t words = smem_addr(smem + C::P_AT) + group * 4096;
 #pragma unroll
                 for (int r = 0; r < W; ++r) {
-                    const uint32_t y = pack_one(o[r] * sync->fac[r0 + r]);
+                    const uint32_t y = pack_one(o[r] * fac[r0 + r]);
                     asm volatile("st.shared.u16 [%0], %1;" ::"r"(words + r * 256 + (((tid >> 3) ^ (r & 7)) << 4) +
                                                                  (tid & 7) * 2),
                                  "h"(static_cast<uint16_t>(y))
                                  : "memory");
                 }
-                softmax_sync();
+                softmax_sync(bar);
 #pragma unroll
                 for (int i = 0; i < W / 8; ++i) {
                     const int r = i * 8 + (tid >> 4), piece = tid & 15, at = t * 128 + piece * 8;
                     if (r0 + r < left && at < a.Dv) {
                         uint32_t w[4];
                         lds128(w, words + r * 256 + ((piece ^ (r & 7)) << 4));
-                        *reinterpret_cast<uint4*>(a.out + rows[r0 + r] + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(a.out + rows[r0 - col0 + r] + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                softmax_sync();
+                softmax_sync(bar);
             }
         }
-        softmax_sync();  // fac and red have been read
+        softmax_sync(bar);  // fac and red have been read
     }
 
     // The block's results, when one of its waits has given up: NaN in all of them, those
@@ -966,16 +975,16 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             for (int g = 0; g < 3; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : 128);
             for (int g = 0; g < 2; ++g) bar_init(&sync->empty[i][g], 1);
             bar_init(&sync->s_full[i], 1);
-            bar_init(&sync->s_free[i], 128);
+            bar_init(&sync->s_free[i], 128 * C::SG);
         }
-        bar_init(&sync->p_full, 128);
+        bar_init(&sync->p_full, 128 * C::SG);
         bar_init(&sync->q_empty, 1);
         bar_init(&sync->done, 2);
         sync->dead = 0;
         for (int i = 0; i < 3; ++i) {
             sync->patch[i] = 0;
             bar_init(&sync->run_full[i], 1);
-            bar_init(&sync->q_full[i], 256);
+            bar_init(&sync->q_full[i], C::HELPERS);
         }
         sync->taken = 0;
         sync->beat = 0;
@@ -992,14 +1001,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     __syncthreads();
     tmem_after();
     const Latent<C> it{a, smem, sync, sync->tmem};
-    if (warp < 4) {
-        it.softmax();
+    if (warp < 4 || (C::SG == 2 && warp >= 8 && warp < 12)) {
+        it.softmax(warp >> 3);
     } else if (warp == 4) {
         it.scores();
     } else if (warp == 5) {
         it.fetches(place, &map, &quads);
     } else if (warp < 14) {
-        it.help(int(threadIdx.x) - 192);
+        it.help(int(threadIdx.x) - (C::SG == 2 && warp >= 12 ? 320 : 192));
     } else {
         it.products();
     }
