@@ -22,7 +22,7 @@
 //         sums l stay in its registers for the whole run.  P^T goes to shared memory by
 //         transposing stores.  O is read and written out when a run ends.
 //   4, 14 issue tcgen05.mma: the scores', the values'.
-//   5     fetches tiles by tensor copies (16-bit rows, pages of a multiple of 8 rows), and
+//   5     fetches tiles by tensor copies (16-bit rows, pages of a multiple of 64 rows), and
 //         walks the division of the work for all.
 //   6-13  helpers: bring the queries of a run, and other tiles: 16-bit rows by
 //         asynchronous copies, 8-bit rows as codes that become fp16 on the way.
@@ -49,10 +49,11 @@ struct LatentCfg {
     static constexpr int STAGE = CHUNKS * CHUNK, STAGES = 2;
     static constexpr int K_AT = Q_BYTES, P_AT = K_AT + STAGES * STAGE, SYNC_AT = P_AT + (ROWS < 64 ? ROWS * 256 : ROWS * 128);  // (P, and results turned over)
     static constexpr int kSmemMax = 232448;
-    // softmax groups of four warps, which share out the columns (query rows): two where the
-    // helpers have little to do
-    static constexpr int SG = ROWS == 64 && BOXES ? 2 : 1, SR = ROWS / SG;
-    static constexpr int HELPERS = SG == 2 ? 128 : 256;
+    // Softmax groups of four warps, which share out the columns (query rows).  64 rows: two, and
+    // four warps of helpers (ragged batch of 16-bit rows 194 us, and 181 so; chunks of prompts
+    // in pages of 16 rows 657 and 569); 8-bit rows need all eight (182 us, with four 236).
+    static constexpr int SG = ROWS == 64 && kWide ? 2 : 1, SR = ROWS / SG;
+    static constexpr int HELPERS = SG == 2 ? 128 : 256, TEAM = HELPERS / 2;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f, kLag = 8.0f;
     static constexpr int MORE = kWide ? 0 : (3 * ROWS + 2 * TN) * 4;  // factors and scales
     static constexpr int kAhead = 3;  // tiles from one that is brought to one that is asked into L2
@@ -242,13 +243,15 @@ struct Latent {
 
     // ---------------------------------------------------------- the walk, and tensor copies
 
-    // Run r for the other roles, whose place the softmax has left: with tensor copies the
-    // tiles' places see to that (a copy is at most two tiles ahead), else it is waited for.
+    // Run r for the other roles, when all of them have taken run r - 3, whose place it gets.  With
+    // tensor copies that is so: the copies before it were made when the products of the tile two
+    // before them, and so of run r - 3, were done.  Else it is waited for: where one softmax group
+    // has taken a run, every role has been through the run before that.
     __device__ __forceinline__ void publish(RunAt& x, uint32_t r, bool there, int lane) const {
         if (lane == 0) {
             if constexpr (!C::BOXES) {
                 uint32_t seen = ~0u, i = 0;
-                while (r >= sync->taken + 3 && !sync->dead) {
+                while (r >= sync->taken + 2 && !sync->dead) {
                     __nanosleep(200);
                     if (++i == kSpins) {
                         i = 0;
@@ -264,14 +267,15 @@ struct Latent {
         __syncwarp();
     }
 
+    // Where a tile's 64 rows lie, all in one page.
     struct Box {
         int page, off;  // page -1: no such rows
     };
 
-    __device__ __forceinline__ Box box_of(const RunAt& x, int tile, int lane, int boxes) const {
+    __device__ __forceinline__ Box box_of(const RunAt& x, int tile) const {
         Box r{-1, 0};
-        const int j = tile * C::TN + lane * a.box;
-        if (lane < boxes && j < x.rq.len) {
+        const int j = tile * C::TN;
+        if (j < x.rq.len) {
             uint32_t p, off;
             a.div_page.divmod(uint32_t(j), p, off);
             r.off = int(off);
@@ -281,7 +285,7 @@ struct Latent {
     }
 
     __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* map, const CUtensorMap* quads) const {
-        const int lane = int(threadIdx.x) & 31, all = groups(), boxes = C::BOXES ? C::TN / a.box : 0;
+        const int lane = int(threadIdx.x) & 31, all = groups();
         Walk walk = walk_from<C::ROWS, C::TN>(a, place);
         RunAt x;
         uint32_t run = 0, n = 0, copies = 0;  // runs, tiles, groups of them asked for
@@ -294,13 +298,12 @@ struct Latent {
             publish(x, run, there, lane);
             if (!there || given_up()) break;
             if constexpr (C::BOXES) {
-                // a lane's box of rows of one page, looked up a tile ahead; rows that are not there
-                // are filled with zeros
-                Box now = box_of(x, x.t0, lane, boxes);
+                // looked up a tile ahead; rows that are not there are filled with zeros
+                Box now = box_of(x, x.t0);
                 bool on = true;
                 for (int it = 0; on && it < x.count; ++it, ++n) {
-                    const Box next = it + 1 < x.count ? box_of(x, x.t0 + it + 1, lane, boxes) : Box{-1, 0};
-                    const uint32_t to = stage(n) + lane * a.box * 128;
+                    const Box next = it + 1 < x.count ? box_of(x, x.t0 + it + 1) : Box{-1, 0};
+                    const uint32_t to = stage(n);
                     for (int g = 0, c = 0; g < all; ++g) {
                         // where a wait has given up, the place may be in use, or its last copy under way
                         on = __all_sync(0xffffffffu, wait_free(n, g));
@@ -321,7 +324,7 @@ struct Latent {
                                     "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + c * C::CHUNK),
                                     "l"(quads), "r"(0), "r"(now.off), "r"(c), "r"(now.page), "r"(bar)
                                     : "memory");
-                        } else if (lane < boxes) {
+                        } else if (lane == 0) {
                             for (int i = c; i < end; ++i)
                                 asm volatile(
                                     "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -333,7 +336,7 @@ struct Latent {
                     }
                     // a later tile is on its way from memory to L2 meanwhile
                     if (a.quads && lane == 0 && it + C::kAhead < x.count) {
-                        const Box far = box_of(x, x.t0 + it + C::kAhead, 0, 1);
+                        const Box far = box_of(x, x.t0 + it + C::kAhead);
                         if (far.page >= 0)
                             for (int c = 0; c < chunks(); c += 4)
                                 asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
@@ -449,31 +452,76 @@ struct Latent {
         return r;
     }
 
-    // A tile without tensor copies, by the 128 threads of a team: eight threads a row, 16 rows
-    // a pass.
+    // A tile without tensor copies, by the threads of a team: eight a row, four rows a thread
+    // at a time.
     __device__ __forceinline__ bool load(const RunAt& x, int it, uint32_t n, int tid) const {
-        const int row = tid >> 3, sub = tid & 7, pieces = a.Dk / 8, all = groups();
+        constexpr int STEP = C::TEAM / 8, PASSES = C::TN / (4 * STEP);
+        const int sub = tid & 7, pieces = a.Dk / 8, all = groups();
         const uint32_t to = stage(n);
-        Row r[4];
+#pragma unroll 1
+        for (int pass = 0; pass < PASSES; ++pass) {
+            const int row = pass * 4 * STEP + (tid >> 3);
+            Row r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = row_of(x, (x.t0 + it) * C::TN + row + 16 * i);
-        if constexpr (C::kWide) {
+            for (int i = 0; i < 4; ++i) r[i] = row_of(x, (x.t0 + it) * C::TN + row + STEP * i);
+#pragma unroll 1
             for (int g = 0, c = 0; g < all; ++g) {
-                if (!__all_sync(0xffffffffu, wait_free(n, g))) {
-                    copies_wait<0>();
-                    return false;
-                }
-                for (const int end = group_end(g); c < end; ++c) {
-                    const int piece = c * 8 + sub;
+                const int end = group_end(g);
+                if constexpr (C::kWide) {
+                    if (pass == 0 && !__all_sync(0xffffffffu, wait_free(n, g))) {
+                        copies_wait<0>();
+                        return false;
+                    }
+#pragma unroll 1
+                    for (; c < end; ++c) {
+                        const int piece = c * 8 + sub;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool ok = r[i].p && piece < pieces;
-                        copy16(to + line_at<C::CHUNK>(row + 16 * i, piece), ok ? r[i].p + piece * 16 : a.k, ok);
+                        for (int i = 0; i < 4; ++i) {
+                            const bool ok = r[i].p && piece < pieces;
+                            copy16(to + line_at<C::CHUNK>(row + STEP * i, piece), ok ? r[i].p + piece * 16 : a.k, ok);
+                        }
+                    }
+                    copies_commit();
+                } else {
+                    // codes are asked for before the place is free, and become fp16 on their way
+                    bool waited = pass > 0;
+#pragma unroll 1
+                    for (; c < end; c = min(c + 4, end)) {
+                        uint2 w[4][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int piece = (c + k) * 8 + sub;
+                                w[i][k] = r[i].p && c + k < end && piece < pieces
+                                              ? __ldg(reinterpret_cast<const uint2*>(r[i].p) + piece)
+                                              : make_uint2(0, 0);
+                            }
+                        if (!waited && !__all_sync(0xffffffffu, wait_free(n, g))) return false;
+                        waited = true;
+                        // (the scales of tile n - 2 have been read when its first product is done)
+                        if (c == 0 && sub == 0)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) scales(n)[row + STEP * i] = r[i].scale;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (c + k < end)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    sts128(to + line_at<C::CHUNK>(row + STEP * i, (c + k) * 8 + sub),
+                                           codes_to_half2<C::STORE, false>(w[i][k].x),
+                                           codes_to_half2<C::STORE, true>(w[i][k].x),
+                                           codes_to_half2<C::STORE, false>(w[i][k].y),
+                                           codes_to_half2<C::STORE, true>(w[i][k].y));
+                    }
+                    if (pass + 1 == PASSES) {
+                        to_async_proxy();
+                        bar_arrive(&sync->full[n & 1][g]);
                     }
                 }
-                copies_commit();
             }
-            // groups as they come
+        }
+        if constexpr (C::kWide)  // groups as they come
             for (int g = 0; g < all; ++g) {
                 if (all - g == 3) copies_wait<2>();
                 else if (all - g == 2) copies_wait<1>();
@@ -481,42 +529,6 @@ struct Latent {
                 to_async_proxy();
                 bar_arrive(&sync->full[n & 1][g]);
             }
-        } else {
-            // codes are asked for before the place is free, and become fp16 on their way
-#pragma unroll 1
-            for (int g = 0, c0 = 0; g < all; ++g) {
-                const int end = group_end(g);
-#pragma unroll 1
-                for (int c = c0; c < end; c += 4) {
-                    uint2 w[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int piece = (c + k) * 8 + sub;
-                            w[i][k] = r[i].p && c + k < end && piece < pieces
-                                          ? __ldg(reinterpret_cast<const uint2*>(r[i].p) + piece)
-                                          : make_uint2(0, 0);
-                        }
-                    if (c == c0 && !__all_sync(0xffffffffu, wait_free(n, g))) return false;
-                    // (the scales of tile n - 2 have been read when its first product is done)
-                    if (c == 0 && sub == 0)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) scales(n)[row + 16 * i] = r[i].scale;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (c + k < end)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                sts128(to + line_at<C::CHUNK>(row + 16 * i, (c + k) * 8 + sub),
-                                       codes_to_half2<C::STORE, false>(w[i][k].x), codes_to_half2<C::STORE, true>(w[i][k].x),
-                                       codes_to_half2<C::STORE, false>(w[i][k].y), codes_to_half2<C::STORE, true>(w[i][k].y));
-                }
-                to_async_proxy();
-                bar_arrive(&sync->full[n & 1][g]);
-                c0 = end;
-            }
-        }
         return true;
     }
 
@@ -524,14 +536,14 @@ struct Latent {
     // either of the tiles' places, so that both are on their way at a time.  A team's first tile
     // of a run comes before the queries, which have to wait for the scores of the run before.
     __device__ __forceinline__ void help(int id) const {
-        const uint32_t team = uint32_t(id) >> 7;
+        const uint32_t team = uint32_t(id) / C::TEAM;
         uint32_t n0 = 0;  // tiles of the runs before
         for (uint32_t run = 0;; ++run) {
             RunAt x;
             if (!__all_sync(0xffffffffu, take(run, x))) return;
             const int first = int((n0 ^ team) & 1);
             if constexpr (!C::BOXES)
-                if (first < x.count && !load(x, first, n0 + first, id & 127)) return;
+                if (first < x.count && !load(x, first, n0 + first, id % C::TEAM)) return;
             if (run > 0) wait_run(&sync->q_empty, (run - 1) & 1);
             if (given_up()) return;
             queries(x, run, id);
@@ -539,7 +551,7 @@ struct Latent {
             bar_arrive(&sync->q_full[run % 3]);
             if constexpr (!C::BOXES)
                 for (int it = first + 2; it < x.count; it += 2)
-                    if (!load(x, it, n0 + it, id & 127)) return;
+                    if (!load(x, it, n0 + it, id % C::TEAM)) return;
             n0 += x.count;
         }
     }
@@ -972,7 +984,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const int warp = int(threadIdx.x) >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            for (int g = 0; g < 3; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : 128);
+            for (int g = 0; g < 3; ++g) bar_init(&sync->full[i][g], C::BOXES ? 1 : C::TEAM);
             for (int g = 0; g < 2; ++g) bar_init(&sync->empty[i][g], 1);
             bar_init(&sync->s_full[i], 1);
             bar_init(&sync->s_free[i], 128 * C::SG);

@@ -15,7 +15,7 @@ constexpr int kLatentJoinThreads = 256;
 struct LatentPlan {
     int store;  // rope_cache_dtype_t
     int rows;   // query rows of a tile: 16, 32 or 64
-    bool boxes; // 16-bit rows fetched by tensor copies: pages of a multiple of 8 rows
+    bool boxes; // 16-bit rows fetched by tensor copies: pages of a multiple of 64 rows
 };
 
 TreeKernel latent_kernel_bf16(const LatentPlan& p);

@@ -19,13 +19,15 @@ TreeKernel kernel_of(const LatentPlan& p) {
 
 }  // namespace
 
-// Tiles as narrow as the query rows allow.  Tensor copies take boxes of at least 8 rows of
-// a page, and a map has no dim of 0; 8-bit rows pass through registers anyway.
+// Tiles as narrow as the query rows allow.  Tensor copies where a tile's 64 rows lie in one
+// page (and there is one: a map has no dim of 0).  A copy takes some 90 cycles whatever its
+// rows, so pages of 16, four times as many, bound chunks of prompts to 724 us, where rows
+// copied by threads took 657.  8-bit rows pass through registers anyway.
 LatentPlan choose_latent(int store, int64_t rows, int64_t pages, int64_t page_size) {
     LatentPlan p{};
     p.store = store;
     p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.boxes = (store == ROPE_CACHE_BF16 || store == ROPE_CACHE_FP16) && pages > 0 && page_size % 64 == 0;
+    p.boxes = (store == ROPE_CACHE_BF16 || store == ROPE_CACHE_FP16) && pages > 0 && page_size % kLatentKeys == 0;
     return p;
 }
 
@@ -53,11 +55,10 @@ rope_status_t launch_latent(const LatentPlan& p, const TreeArgs& args, void* wor
     a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
     CUtensorMap map{}, quads{};
     if (p.boxes) {
-        a.box = 8;
-        while (a.page_size % (2 * a.box) == 0 && 2 * a.box <= kLatentKeys) a.box *= 2;
+        a.box = kLatentKeys;
         const rope_status_t st = tree_map(&map, a.k, a.Dk, a, a.k_st, true, 64, err);
         if (st != ROPE_OK) return st;
-        a.quads = a.box == kLatentKeys && a.Dk % 64 == 0 && a.Dk >= 256;
+        a.quads = a.Dk % 64 == 0 && a.Dk >= 256;
         if (a.quads) {
             const rope_status_t sq = tree_map_quads(&quads, a.k, a.Dk / 64, a, a.k_st, err);
             if (sq != ROPE_OK) return sq;
