@@ -787,83 +787,92 @@ _pack_rows = struct.Struct("=6Q10q").pack  # rope_norm_rows_t
 
 
 def _norm_side(what, x, out, grad, weight, rstd, weight_grad, shape, dtype, device, normed):
-    """One tensor's rope_norm_rows_t; ``shape`` is (B, S, D) of the queries."""
-    B, S, D = shape
-    for t, name in ((x, "" if grad is None else " (x)"), (out, " out"), (grad, " gradient")):
-        if t is None:
-            continue
-        if t.dim() != 4 or t.shape[0] != B or t.shape[1] != S or t.shape[3] != D or t.shape[2] != x.shape[2]:
-            _refuse(f"{what}{name} must be ({B}, {S}, heads, {D})")
-        if t.dtype is not dtype or t.device != device:
-            _refuse(f"{what}{name} must be {dtype} on {device}")
-        if D > 1 and t.stride(3) != 1:
-            _refuse(f"the last dim of {what}{name} must be contiguous")
-    N = x.shape[2]
-    for t, name in ((weight, "weight"), (weight_grad, "weight gradient")):
-        if t is not None and (t.dim() != 1 or t.shape[0] != normed or not t.is_contiguous() or t.device != device):
-            _refuse(f"{what}'s {name} must be a contiguous vector of {normed} on {device}")
-    if weight_grad is not None and weight_grad.dtype is not torch.float32:
-        _refuse(f"{what}'s weight gradient must be fp32")
-    if rstd is not None and (rstd.dtype is not torch.float32 or rstd.shape != (B, S, N) or
-                             not rstd.is_contiguous() or rstd.device != device):
-        _refuse(f"{what}'s rstd must be contiguous fp32 ({B}, {S}, {N}) on {device}")
-
-    def ptr(t):
-        return 0 if t is None else t.data_ptr()
-
-    return _pack_rows(x.data_ptr(), out.data_ptr(), ptr(grad), ptr(weight), ptr(rstd), ptr(weight_grad), N,
-                      *x.stride()[:3], *out.stride()[:3], *((0, 0, 0) if grad is None else grad.stride()[:3]))
+    """One tensor's rope_norm_rows_t; ``shape`` is that of x, (B, S, heads, D)."""
+    st = x.stride()
+    op = xp = x.data_ptr()
+    ost, gst, gp = st, (0, 0, 0, 0), 0
+    if x.dtype is not dtype or x.device != device:
+        _refuse(f"{what} must be {dtype} on {device}")
+    if grad is not None:
+        if grad.shape != shape or grad.dtype is not dtype or grad.device != device:
+            _refuse(f"{what}'s gradient must be {dtype} {tuple(shape)} on {device}")
+        gst, gp = grad.stride(), grad.data_ptr()
+        op, ost = gp, gst
+    if out is not None:
+        if out.shape != shape or out.dtype is not dtype or out.device != device:
+            _refuse(f"{what}'s out must be {dtype} {tuple(shape)} on {device}")
+        op, ost = out.data_ptr(), out.stride()
+    if shape[3] > 1 and (st[3] != 1 or ost[3] != 1 or (grad is not None and gst[3] != 1)):
+        _refuse(f"the last dim of {what}, its out and its gradient must be contiguous")
+    wp = rp = dp = 0
+    if weight is not None:
+        if weight.shape != (normed,) or not weight.is_contiguous() or weight.device != device:
+            _refuse(f"{what}'s weight must be a contiguous vector of {normed} on {device}")
+        wp = weight.data_ptr()
+    if weight_grad is not None:
+        if (weight_grad.shape != (normed,) or not weight_grad.is_contiguous() or weight_grad.device != device or
+                weight_grad.dtype is not torch.float32):
+            _refuse(f"{what}'s weight gradient must be a contiguous fp32 vector of {normed} on {device}")
+        dp = weight_grad.data_ptr()
+    if rstd is not None:
+        if (rstd.dtype is not torch.float32 or rstd.shape != shape[:3] or not rstd.is_contiguous() or
+                rstd.device != device):
+            _refuse(f"{what}'s rstd must be contiguous fp32 {tuple(shape[:3])} on {device}")
+        rp = rstd.data_ptr()
+    return _pack_rows(xp, op, gp, wp, rp, dp, shape[2], st[0], st[1], st[2], ost[0], ost[1], ost[2], gst[0], gst[1],
+                      gst[2])
 
 
 def _norm_call(name, q, k, grads, outs, weights, rstds, weight_grads, cos, sin, start, end, norm, mode, back, extra,
                stream):
     lib = _lib or load_library()
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         _refuse("q must be 4-D (B, S, heads, D)")
-    dtype, device, shape = q.dtype, q.device, q.shape
+    dtype, device = q.dtype, q.device
     code = DTYPE_CODE.get(dtype)
     if code is None:
         _refuse(f"unsupported dtype {dtype}")
     if not q.is_cuda:
         _refuse("q must be a CUDA tensor")
-    B, S, D = shape[0], shape[1], shape[3]
+    B, S, _, D = shape
     n0, n1 = (0, D) if norm is None else norm
     if mode not in MODE_CODE:
         _mode_code(mode)
-    wtype = None
-    for w, x in zip(weights, (q, k)):
-        if w is None:
-            continue
-        if x is None or (wtype is not None and w.dtype is not wtype) or w.dtype not in DTYPE_CODE:
+    wq, wk = weights
+    wcode = code
+    if wq is not None or wk is not None:
+        wtype = (wk if wq is None else wq).dtype
+        wcode = DTYPE_CODE.get(wtype)
+        if wcode is None or (wk is not None and (k is None or wk.dtype is not wtype)):
             _refuse("a weight needs its rows, and both weights one dtype")
-        wtype = w.dtype
-    rows = [None, None]
-    for i, x in enumerate((q, k)):
-        if x is None:
-            if any(t is not None for t in (grads[i], outs[i], rstds[i], weight_grads[i])):
-                _refuse("without k there is nothing else of k's")
-            continue
-        what = "k" if i else "q"
-        if back and (grads[i] is None or rstds[i] is None):
-            _refuse(f"{what}'s gradient and rstd are needed")
-        out = outs[i] if outs[i] is not None else (grads[i] if back else x)
-        rows[i] = _norm_side(what, x, out, grads[i], weights[i], rstds[i], weight_grads[i], (B, S, D), dtype, device,
-                             n1 - n0)
+    if back and (grads[0] is None or rstds[0] is None or (k is not None and (grads[1] is None or rstds[1] is None))):
+        _refuse("the gradients and rstd of q (and k) are needed")
+    rows = _norm_side("q", q, outs[0], grads[0], wq, rstds[0], weight_grads[0], shape, dtype, device, n1 - n0)
+    more = None
+    if k is not None:
+        ks = k.shape
+        if len(ks) != 4 or ks[0] != B or ks[1] != S or ks[3] != D:
+            _refuse(f"k must be ({B}, {S}, heads, {D})")
+        more = _norm_side("k", k, outs[1], grads[1], wk, rstds[1], weight_grads[1], ks, dtype, device, n1 - n0)
+    elif not (grads[1] is outs[1] is rstds[1] is weight_grads[1] is None):
+        _refuse("without k there is nothing else of k's")
     cp = sp = cst = sst = None
     if start != end:
+        got = []
         for t in (cos, sin):
-            if (t is None or t.dim() != 4 or t.dtype is not dtype or t.device != device or
-                    t.shape[0] not in (1, B) or t.shape[1] not in (1, S) or t.shape[2] != 1 or
-                    t.shape[3] != end - start or (t.shape[3] > 1 and t.stride(3) != 1)):
+            ts = None if t is None else t.shape
+            if (t is None or len(ts) != 4 or t.dtype is not dtype or t.device != device or ts[0] not in (1, B) or
+                    ts[1] not in (1, S) or ts[2] != 1 or ts[3] != end - start):
                 _refuse("cos and sin must be (B|1, S|1, 1, end - start) of q's dtype with a contiguous last dim")
-
-        def steps(t):
-            return _pack2(t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
-
-        cp, sp, cst, sst = cos.data_ptr(), sin.data_ptr(), steps(cos), steps(sin)
+            st = t.stride()
+            if ts[3] > 1 and st[3] != 1:
+                _refuse("cos and sin must be (B|1, S|1, 1, end - start) of q's dtype with a contiguous last dim")
+            got.append((t.data_ptr(), _pack2(st[0] if ts[0] > 1 else 0, st[1] if ts[1] > 1 else 0)))
+        (cp, cst), (sp, sst) = got
     _launch(getattr(lib, name),
-            (rows[0], rows[1], code, code if wtype is None else DTYPE_CODE[wtype], B, S, D, n0, n1, *extra[0], cp, sp,
-             cst, sst, start, end, MODE_CODE[mode], *extra[1]), stream, device)
+            (rows, more, code, wcode, B, S, D, n0, n1, *extra[0], cp, sp, cst, sst, start, end, MODE_CODE[mode],
+             *extra[1]), stream, device)
 
 
 def rope_partial_norm_fwd(q, k, q_weight, k_weight, cos, sin, start: int, end: int, eps: float = 1e-6, norm=None,

@@ -37,16 +37,16 @@ struct NormArgs {
     int32_t lanes_log2;  // lanes of a warp that share a row
     bool weight32;       // weights are fp32
     bool wide;           // rows allow 16-byte accesses
-    bool wide_cs;        // cos and sin too, chunk by chunk
-    bool wide_weight;
+    bool pairs_cs;       // cos and sin allow accesses of pairs (kTurnPairs)
     bool interleave;     // pairs are adjacent lanes
     float eps, inv_n;
     FastDiv div_S;
 };
 
-// How pairs lie: within a chunk of 16 bytes; half-split, the partners of a chunk a whole
-// chunk; anything else.
-enum NormTurn : int { kTurnNear = 0, kTurnFar = 1, kTurnAny = 2 };
+// How pairs lie: within a chunk of 16 bytes, which turns as a whole or not at all; within a
+// chunk, each for itself; half-split, the partners of a chunk a whole chunk; anything
+// else.  In all but the last, chunks are normed as a whole or not at all.
+enum NormTurn : int { kTurnNear = 0, kTurnPairs = 1, kTurnFar = 2, kTurnAny = 3 };
 
 struct NormPlan {
     int dtype;   // rope_dtype_t

@@ -233,12 +233,12 @@ rope_status_t norm(const rope_norm_rows_t* q, const rope_norm_rows_t* k, const C
     a.div_S = FastDiv::make(static_cast<uint32_t>(c.S > 0 ? c.S : 1));
     const int ve = 16 / e, half = static_cast<int>(L / 2);
     a.wide = c.D % ve == 0;
-    a.wide_weight = c.n0 % ve == 0;
+    bool wide_weight = true, wide_cs = false;
     for (int i = 0; i < n; ++i) {
         const rope_norm_rows_t* r = sides[i];
         const int64_t shape[3] = {c.B, c.S, r->heads};
         a.wide = a.wide && aligned(r->x, 16) && aligned(r->out, 16) && (!c.back || aligned(r->grad, 16));
-        a.wide_weight = a.wide_weight && aligned(r->weight, 16);
+        wide_weight = wide_weight && aligned(r->weight, 16);
         NormRows& s = a.side[i];
         for (int j = 0; j < 3; ++j) {
             s.x_st[j] = step(shape[j], r->x_stride[j]) * e;
@@ -256,20 +256,30 @@ rope_status_t norm(const rope_norm_rows_t* q, const rope_norm_rows_t* k, const C
     if (L && rows) {
         a.cos = static_cast<const char*>(c.cos);
         a.sin = static_cast<const char*>(c.sin);
-        a.wide_cs = c.start % ve == 0 && L % ve == 0 && aligned(c.cos, 16) && aligned(c.sin, 16);
+        wide_cs = aligned(c.cos, 16) && aligned(c.sin, 16);
+        a.pairs_cs = aligned(c.cos, 2 * e) && aligned(c.sin, 2 * e);
         for (int j = 0; j < 2; ++j) {
             a.cos_st[j] = step(tokens[j], c.cos_stride[j]) * e;
             a.sin_st[j] = step(tokens[j], c.sin_stride[j]) * e;
-            a.wide_cs = a.wide_cs && a.cos_st[j] % 16 == 0 && a.sin_st[j] % 16 == 0;
+            wide_cs = wide_cs && a.cos_st[j] % 16 == 0 && a.sin_st[j] % 16 == 0;
+            a.pairs_cs = a.pairs_cs && a.cos_st[j] % (2 * e) == 0 && a.sin_st[j] % (2 * e) == 0;
         }
     }
     NormPlan p{};
     p.dtype = c.dtype;
     p.back = c.back;
-    // Pairs within a chunk; half-split pairs whose partners are whole chunks; others
-    p.turn = L == 0 || (a.interleave && c.start % 2 == 0)                          ? kTurnNear
-             : !a.interleave && a.wide && c.start % ve == 0 && half % ve == 0 ? kTurnFar
-                                                                                   : kTurnAny;
+    // The fast kernels where chunks are normed as a whole or not at all; pairs within a chunk (of
+    // a slice of whole chunks, or pair by pair), or half-split pairs whose partners are whole
+    // chunks, all normed or none.  Two prompts of 8192 tokens, 32 + 8 heads of 128 bf16:
+    // NORM_FWD_FIGURES.
+    const bool whole = c.start % ve == 0 && wide_cs;
+    const bool chunks_normed = a.wide && wide_weight && c.n0 % ve == 0 && c.n1 % ve == 0;
+    const bool one_kind = (c.start >= c.n0 && c.end <= c.n1) || c.end <= c.n0 || c.start >= c.n1;
+    p.turn = !chunks_normed                                            ? kTurnAny
+             : L == 0 || (a.interleave && whole && L % ve == 0) ? kTurnNear
+             : a.interleave && c.start % 2 == 0                        ? kTurnPairs
+             : !a.interleave && whole && half % ve == 0 && one_kind    ? kTurnFar
+                                                                       : kTurnAny;
     // The lanes of a row and their chunks: as few idle places as can be, then as few
     // chunks a lane as can be (more lanes at work for a row).
     const int chunks = static_cast<int>((c.D + ve - 1) / ve);

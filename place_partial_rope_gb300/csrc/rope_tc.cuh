@@ -1,6 +1,7 @@
 // rope_tc.cuh -- the instructions that the kernels on tcgen05 share: barriers in shared
 // memory, tensor memory, matrix descriptors and products.
 #pragma once
+#include "rope_f32x2.cuh"
 #include "rope_tree_common.cuh"
 
 namespace rope {
@@ -125,38 +126,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(unsigned long long* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(b))
                  : "memory");
-}
-
-// Two fp32 operations in one instruction, each rounded as the single one.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long x, y, z, d;
-    memcpy(&x, &a, 8);
-    memcpy(&y, &b, 8);
-    memcpy(&z, &c, 8);
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-    float2 r;
-    memcpy(&r, &d, 8);
-    return r;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long x, y, d;
-    memcpy(&x, &a, 8);
-    memcpy(&y, &b, 8);
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-    float2 r;
-    memcpy(&r, &d, 8);
-    return r;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long x, y, d;
-    memcpy(&x, &a, 8);
-    memcpy(&y, &b, 8);
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-    float2 r;
-    memcpy(&r, &d, 8);
-    return r;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
