@@ -933,22 +933,21 @@ def rope_partial_norm_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos,
 
 
 def _pages_args(kv_len, n, what, page_table, free_pages, free_count):
-    device = kv_len.device
-    for t, name in ((kv_len, "kv_len"), (n, what), (free_pages, "free_pages"), (free_count, "free_count")):
-        if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
-            _refuse(f"{name} must be a contiguous int32 vector")
-        if not t.is_cuda or t.device != device:
-            _refuse(f"{name} must be a CUDA tensor on kv_len's device")
-    R, pt = kv_len.shape[0], page_table.shape
-    if n.shape[0] != R:
-        _refuse(f"{what} must have a number for each request of kv_len")
-    if free_count.shape[0] != 1:
-        _refuse("free_count must be one int32")
-    if page_table.dtype is not torch.int32 or len(pt) != 2 or pt[0] != R or page_table.device != device:
+    device, i32 = kv_len.device, torch.int32
+    R = kv_len.shape[0]
+    for t, size, name in ((kv_len, R, "kv_len"), (n, R, what), (free_pages, None, "free_pages"),
+                          (free_count, 1, "free_count")):
+        shape = t.shape
+        if (t.dtype is not i32 or len(shape) != 1 or (size is not None and shape[0] != size) or
+                not t.is_contiguous() or t.device != device):
+            _refuse(f"{name} must be a contiguous int32 vector on kv_len's device"
+                    f"{'' if size is None else f' of {size}'}")
+    pt, pst = page_table.shape, page_table.stride()
+    if (page_table.dtype is not i32 or len(pt) != 2 or pt[0] != R or page_table.device != device or
+            (pt[1] > 1 and pst[1] != 1)):
         _refuse("page_table must be int32 (R, pages) on kv_len's device, with a contiguous last dim")
-    pst = page_table.stride()
-    if pt[1] > 1 and pst[1] != 1:
-        _refuse("page_table must be int32 (R, pages) on kv_len's device, with a contiguous last dim")
+    if not kv_len.is_cuda:
+        _refuse("kv_len must be a CUDA tensor")
     return (kv_len.data_ptr(), n.data_ptr(), R, page_table.data_ptr(), pt[1], pst[0] if R > 1 else pt[1],
             free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr())
 

@@ -13,7 +13,9 @@
 // requests after the other, in shared memory; the cluster's barrier stands
 // between the last read of a chunk's lengths and the first block's writing them in
 // place; then the blocks share out the chunk's tokens (pages), four in a row a
-// thread, which looks its first token's request up by halving.
+// thread, which looks its first token's request up by halving.  Where there are places for
+// many tokens, 8 blocks are too few to write them: a grid without clusters fills them in
+// and leaves the lengths, and a launch after it writes those.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -74,7 +76,9 @@ __device__ __forceinline__ int32_t pages_of(const PagesArgs& a, int32_t len) {
 
 __device__ __forceinline__ int32_t length(const PagesArgs& a, int r) { return min(max(a.kv_len[r], 0), a.max_len); }
 
-template <int THREADS>
+// FILL: writes slots, positions and the table; STATE: lengths, offsets and the count.  Both: one
+// cluster; FILL alone: any grid, which only reads what STATE changes.
+template <int THREADS, bool FILL, bool STATE>
 __global__ void __launch_bounds__(THREADS) rope_cache_grow_kernel(const __grid_constant__ PagesArgs a) {
     constexpr int CHUNK = THREADS * kEach;
     __shared__ int64_t start[CHUNK];  // tokens before a request
@@ -83,10 +87,12 @@ __global__ void __launch_bounds__(THREADS) rope_cache_grow_kernel(const __grid_c
     __shared__ int64_t scratch[2 * (THREADS / 32)];
     cg::cluster_group cluster = cg::this_cluster();
     enter_after_predecessor();
-    const int64_t rank = cluster.block_rank(), blocks = cluster.num_blocks();
-    const int64_t me = rank * THREADS + threadIdx.x, threads = blocks * THREADS;
+    const int64_t rank = blockIdx.x;
+    const int64_t me = rank * THREADS + threadIdx.x, threads = int64_t(gridDim.x) * THREADS;
     const int32_t count = min(max(*a.free_count, 0), a.capacity);
-    int64_t tokens = 0, needed = 0, granted = 0;  // of the chunks before; pages that went
+    int64_t tokens = 0, needed = 0;  // of the chunks before
+    __shared__ int32_t went;         // pages that are granted: up to the last request that gets any
+    if (threadIdx.x == 0) went = 0;
     for (int r0 = 0; r0 < a.R; r0 += CHUNK) {
         int32_t len[kEach], grown[kEach], need[kEach];
         int64_t n[kEach];
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__(THREADS) rope_cache_grow_kernel(const __grid_c
         }
         int64_t bn, bp, all_n, all_p;
         block_sums<THREADS>(sum_n, sum_need, scratch, bn, bp, all_n, all_p);
-        int64_t went = 0;
+        int32_t end = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int k = int(threadIdx.x) * kEach + i;
@@ -117,15 +123,16 @@ __global__ void __launch_bounds__(THREADS) rope_cache_grow_kernel(const __grid_c
             start[k] = tokens + bn;
             asked[k] = needed + bp;
             rows[k] = ok[i] ? len[i] : ~len[i];
-            if (ok[i]) went += need[i];
+            if (ok[i] && need[i] > 0) end = int32_t(needed + bp + need[i]);  // <= count
             bn += n[i];
             bp += need[i];
         }
-        int64_t none, all_went, zero, nil;
-        block_sums<THREADS>(went, 0, scratch, none, zero, all_went, nil);
+        end = __reduce_max_sync(0xffffffffu, end);
+        if ((threadIdx.x & 31) == 0 && end > 0) atomicMax(&went, end);
         // all blocks have read the chunk's lengths (and the count), this block's sums are there
-        cluster.sync();
-        if (rank == 0) {
+        if constexpr (FILL && STATE) cluster.sync();
+        else __syncthreads();
+        if (STATE && rank == 0) {
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 const int k = int(threadIdx.x) * kEach + i, r = r0 + k;
@@ -138,7 +145,7 @@ __global__ void __launch_bounds__(THREADS) rope_cache_grow_kernel(const __grid_c
         const int here = min(CHUNK, a.R - r0);
         // slots and positions; tokens past the last place (of a request that is not granted there
         // may be any number) are not looked at
-        const int64_t to = min(tokens + all_n, a.T);
+        const int64_t to = FILL ? min(tokens + all_n, a.T) : 0;
         for (int64_t t0 = tokens + me * 4; t0 < to; t0 += threads * 4) {
             int k = find(start, here, t0), page = -1;
             int32_t p = -1;
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(THREADS) rope_cache_grow_kernel(const __grid_c
         }
         // the table's new entries: granted pages are the first `count` that are asked for, but
         // for those of a request that gets only a part
-        const int64_t last = min(needed + all_p, int64_t(count));
+        const int64_t last = FILL ? min(needed + all_p, int64_t(count)) : 0;
         for (int64_t e = needed + me; e < last; e += threads) {
             const int k = find(asked, here, e);
             if (rows[k] >= 0)
@@ -174,15 +181,14 @@ __global__ void __launch_bounds__(THREADS) rope_cache_grow_kernel(const __grid_c
         }
         tokens += all_n;
         needed += all_p;
-        granted += all_went;
         __syncthreads();  // the chunk's numbers have been read
     }
-    cluster.sync();  // every block has read the count, also where there are no requests
-    if (rank == 0 && threadIdx.x == 0) {
+    if constexpr (FILL && STATE) cluster.sync();  // every block has read the count, also where there are no requests
+    if (STATE && rank == 0 && threadIdx.x == 0) {
         a.q_start[a.R] = int32_t(min(tokens, int64_t(0x7fffffff)));
-        *a.free_count = count - int32_t(granted);
+        *a.free_count = count - went;
     }
-    for (int64_t t = tokens + me; t < a.T; t += threads) {
+    for (int64_t t = tokens + me; FILL && t < a.T; t += threads) {
         a.slots[t] = -1;
         if (a.positions) a.positions[t] = 0;
     }
@@ -253,8 +259,8 @@ __global__ void __launch_bounds__(THREADS) rope_cache_trim_kernel(const __grid_c
         *a.free_count = static_cast<int32_t>(min(int64_t(count) + total, int64_t(a.capacity)));
 }
 
-rope_status_t launch(const void* f, int threads, int blocks, const PagesArgs& args, rope_stream_t stream,
-                     const char** err) {
+rope_status_t launch(const void* f, int threads, int blocks, bool cluster, const PagesArgs& args,
+                     rope_stream_t stream, const char** err) {
     void* params[] = {const_cast<PagesArgs*>(&args)};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -268,7 +274,7 @@ rope_status_t launch(const void* f, int threads, int blocks, const PagesArgs& ar
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cluster ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelExC(&cfg, f, params);
     if (e != cudaSuccess) {
         *err = cudaGetErrorString(e);
@@ -279,9 +285,10 @@ rope_status_t launch(const void* f, int threads, int blocks, const PagesArgs& ar
 }
 
 constexpr int kFew = 256, kMany = 1024;
+constexpr int64_t kWide = 16384;
 
 // Small batches: a block of 256 threads, whose sums take fewer steps.
-bool few(const PagesArgs& a) { return a.R <= kFew * kEach && a.T <= 4 * kFew; }
+bool few(const PagesArgs& a) { return a.R <= kFew * kEach && a.T <= 4 * kFew; }  // to grow
 
 int blocks_for(int64_t work) {
     int b = 1;
@@ -291,19 +298,31 @@ int blocks_for(int64_t work) {
 
 }  // namespace
 
+// From 16384 places on a grid of up to one block an SM and two launches: 500000 tokens of 512
+// requests grown and given back, copies of the table and the lengths between, 172 us with the one
+// cluster and a trim of one block of 256, 50 us so.
 rope_status_t launch_grow(const PagesArgs& args, rope_stream_t stream, const char** err) {
     if (few(args))
-        return launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kFew>), kFew, 1, args, stream, err);
-    return launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kMany>), kMany, blocks_for(args.T), args,
+        return launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kFew, true, true>), kFew, 1, true, args,
+                      stream, err);
+    if (args.T < kWide)
+        return launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kMany, true, true>), kMany,
+                      blocks_for(args.T), true, args, stream, err);
+    const int64_t blocks = (args.T + kMany * 4 - 1) / (kMany * 4);
+    const rope_status_t st = launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kMany, true, false>), kMany,
+                                    static_cast<int>(blocks < 152 ? blocks : 152), false, args, stream, err);
+    if (st != ROPE_OK) return st;
+    return launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kMany, false, true>), kMany, 1, false, args,
                   stream, err);
 }
 
-// (How many pages go is known on the device only: a few a request, more when it ends.)
+// How many pages go is known on the device only: a few of a request that goes on, all of one
+// that has ended (30000 pages of 512 requests: 128 us by one block of 256 threads, 11 us so).
 rope_status_t launch_trim(const PagesArgs& args, rope_stream_t stream, const char** err) {
-    if (few(args))
-        return launch(reinterpret_cast<const void*>(&rope_cache_trim_kernel<kFew>), kFew, 1, args, stream, err);
-    return launch(reinterpret_cast<const void*>(&rope_cache_trim_kernel<kMany>), kMany, blocks_for(int64_t(args.R) * 32),
-                  args, stream, err);
+    if (args.R <= kFew / 8)
+        return launch(reinterpret_cast<const void*>(&rope_cache_trim_kernel<kFew>), kFew, 1, true, args, stream, err);
+    return launch(reinterpret_cast<const void*>(&rope_cache_trim_kernel<kMany>), kMany, blocks_for(int64_t(args.R) * 64),
+                  true, args, stream, err);
 }
 
 }  // namespace rope
