@@ -934,7 +934,7 @@ def rope_partial_norm_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos,
 
 def _pages_args(kv_len, n, what, page_table, free_pages, free_count):
     device, i32 = kv_len.device, torch.int32
-    R = kv_len.shape[0]
+    R = kv_len.numel()
     for t, size, name in ((kv_len, R, "kv_len"), (n, R, what), (free_pages, None, "free_pages"),
                           (free_count, 1, "free_count")):
         shape = t.shape
@@ -966,7 +966,7 @@ def rope_partial_cache_grow(kv_len, new_tokens, page_table, free_pages, free_cou
     pages for, which stays as it is)."""
     lib = _lib or load_library()
     args = _pages_args(kv_len, new_tokens, "new_tokens", page_table, free_pages, free_count)
-    R, T = args[2], slots.shape[0]
+    R, T = args[2], slots.numel()
     for t, size, name, kind in ((q_start, R + 1, "q_start", torch.int32), (slots, T, "slots", torch.int64),
                                 (positions, T, "positions", torch.int32), (granted, R, "granted", torch.int32)):
         if t is not None and (t.dtype is not kind or t.dim() != 1 or t.shape[0] != size or not t.is_contiguous() or

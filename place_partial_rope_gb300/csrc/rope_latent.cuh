@@ -383,42 +383,42 @@ struct Latent {
             }
             copies_commit();
             copies_wait<0>();
-            return;
-        }
+        } else {
 #pragma unroll 1
-        for (int row = id >> 3; row < C::ROWS; row += C::HELPERS / 8) {
-            const char* src = nullptr;
-            if (row < left) {
-                uint32_t tok, g;
-                a.div_group.divmod(uint32_t(first + row), tok, g);
-                src = a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] + int64_t(g) * a.q_st[1];
+            for (int row = id >> 3; row < C::ROWS; row += C::HELPERS / 8) {
+                const char* src = nullptr;
+                if (row < left) {
+                    uint32_t tok, g;
+                    a.div_group.divmod(uint32_t(first + row), tok, g);
+                    src = a.q + int64_t(x.rq.qs + int(tok)) * a.q_st[0] + int64_t(g) * a.q_st[1];
+                }
+                uint4 w[C::CHUNKS];
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    const int piece = c * 8 + (id & 7);
+                    w[c] = src && piece < pieces ? __ldg(reinterpret_cast<const uint4*>(src) + piece)
+                                                 : make_uint4(0, 0, 0, 0);
+                }
+                uint32_t most = 0;
+                float f[8];
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    widen8(w[c], a.bf16, f);
+                    most = max(most, most_of(f));
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+                const float p = row_power(most), by = one_over_power(p);
+                if ((id & 7) == 0) factors(run)[row] = row_factor(p, a.scale_log2);
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+                    widen8(w[c], a.bf16, f);
+                    w[c] = half8(f, by);
+                }
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c)
+                    sts128(to + line_at<C::Q_CHUNK>(row, c * 8 + (id & 7)), w[c].x, w[c].y, w[c].z, w[c].w);
             }
-            uint4 w[C::CHUNKS];
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c) {
-                const int piece = c * 8 + (id & 7);
-                w[c] = src && piece < pieces ? __ldg(reinterpret_cast<const uint4*>(src) + piece)
-                                             : make_uint4(0, 0, 0, 0);
-            }
-            uint32_t most = 0;
-            float f[8];
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c) {
-                widen8(w[c], a.bf16, f);
-                most = max(most, most_of(f));
-            }
-#pragma unroll
-            for (int d = 1; d < 8; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-            const float p = row_power(most), by = one_over_power(p);
-            if ((id & 7) == 0) factors(run)[row] = row_factor(p, a.scale_log2);
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c) {
-                widen8(w[c], a.bf16, f);
-                w[c] = half8(f, by);
-            }
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
-                sts128(to + line_at<C::Q_CHUNK>(row, c * 8 + (id & 7)), w[c].x, w[c].y, w[c].z, w[c].w);
         }
     }
 
@@ -974,10 +974,12 @@ struct Latent {
     }
 };
 
-template <class C>
+// T: Latent, or what a test makes of it.
+template <class T>
 __global__ void __launch_bounds__(kLatentThreads, 1)
     rope_latent_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map,
                        const __grid_constant__ CUtensorMap quads) {
+    using C = typename T::Cfg;
     extern __shared__ __align__(1024) char smem[];
     static_assert(C::SYNC_AT + int(sizeof(LatentSync)) + C::MORE <= C::kSmemMax, "shared memory");
     LatentSync* sync = reinterpret_cast<LatentSync*>(smem + C::SYNC_AT);
@@ -1012,7 +1014,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     tmem_before();
     __syncthreads();
     tmem_after();
-    const Latent<C> it{a, smem, sync, sync->tmem};
+    const T it{a, smem, sync, sync->tmem};
     if (warp < 4 || (C::SG == 2 && warp >= 8 && warp < 12)) {
         it.softmax(warp >> 3);
     } else if (warp == 4) {
@@ -1127,12 +1129,17 @@ __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(co
     }
 }
 
+template <class T>
+TreeKernel latent_of() {
+    using C = typename T::Cfg;
+    return TreeKernel{reinterpret_cast<const void*>(&rope_latent_kernel<T>),
+                      reinterpret_cast<const void*>(&rope_latent_join_kernel<C::ROWS>),
+                      C::SYNC_AT + int(sizeof(LatentSync)) + C::MORE, kLatentThreads, C::TN, 0.0f, 0};
+}
+
 template <int STORE, int ROWS, bool BOXES>
 TreeKernel latent_instance() {
-    using C = LatentCfg<STORE, ROWS, BOXES>;
-    return TreeKernel{reinterpret_cast<const void*>(&rope_latent_kernel<C>),
-                      reinterpret_cast<const void*>(&rope_latent_join_kernel<ROWS>),
-                      C::SYNC_AT + int(sizeof(LatentSync)) + C::MORE, kLatentThreads, C::TN, 0.0f, 0};
+    return latent_of<Latent<LatentCfg<STORE, ROWS, BOXES>>>();
 }
 
 template <int STORE>

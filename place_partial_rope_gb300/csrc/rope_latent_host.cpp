@@ -44,7 +44,7 @@ rope_status_t latent_attention(const rope_kv_cache_t* c, const void* q, int dtyp
     LatentPlan p{};
     st = latent_plan(c, dtype, Hq, v_dim, max_q, &p);
     if (st != ROPE_OK) return st;
-    if (Tq < 0 || Tq > kInt / Hq || R < 0 || R > (1 << 24))
+    if (Tq < 0 || Tq > (kInt - 64) / Hq || R < 0 || R > (1 << 24))
         return fail(ROPE_ERR_INVALID, "Tq=%lld query tokens, R=%lld requests", (long long)Tq, (long long)R);
     if (max_pages < 0 || max_pages > kInt || max_pages * c->page_size > kInt - 1024)
         return fail(ROPE_ERR_INVALID, "%lld pages of %lld tokens a request exceed 2^31 rows", (long long)max_pages,
