@@ -601,10 +601,11 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_fast_fwd_kernel(const 
 }
 
 // (16-bit rows of one chunk a lane: three blocks an SM, at 80 registers, 59 us for 16384 tokens
-// of 16 + 4 heads of 128, where 118 registers and two took 70 and 64 and four 71; others best
-// without a bound)
+// of 16 + 4 heads of 128, where 118 registers and two took 70 and 64 and four 71.  0 is no bound:
+// rows of 96 fp32 lanes take 36.5 us at 62 registers so, 41 with a bound of three and 45 of one)
 template <typename T, int C, int U, int TURN>
-__global__ void __launch_bounds__(kNormThreads, C == 1 && sizeof(T) == 2 ? 3 : 1) rope_norm_fast_bwd_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, C == 1 && sizeof(T) == 2 ? 3 : 0)
+    rope_norm_fast_bwd_kernel(const __grid_constant__ NormArgs a) {
     using N = NormPairs<T>;
     constexpr int VE = N::VE, H = N::N, WARPS = kNormThreads / 32;
     constexpr bool FAR = TURN == kTurnFar, PARTS = TURN == kTurnPairs;
