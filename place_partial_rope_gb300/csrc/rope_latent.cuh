@@ -22,7 +22,7 @@
 //         sums l stay in its registers for the whole run.  P^T goes to shared memory by
 //         transposing stores.  O is read and written out when a run ends.
 //   4, 14 issue tcgen05.mma: the scores', the values'.
-//   5     fetches tiles by tensor copies (16-bit rows, pages of a multiple of 64 rows), and
+//   5     fetches tiles by tensor copies (16-bit rows, pages of a multiple of 8 rows), and
 //         walks the division of the work for all.
 //   6-13  helpers: bring the queries of a run, and other tiles: 16-bit rows by
 //         asynchronous copies, 8-bit rows as codes that become fp16 on the way.
@@ -30,8 +30,6 @@
 //   Every wait is bounded; one that gives up sets `dead`, the threads of a role leave
 // together, and every result that the block has a share in becomes NaN.
 #pragma once
-#include <cuda.h>
-
 #include "rope_latent.h"
 #include "rope_tc.cuh"
 
@@ -45,18 +43,25 @@ struct LatentCfg {
     static constexpr bool BF16 = STORE == ROPE_CACHE_BF16;
     static constexpr int CHUNK = TN * 128;  // 64 lanes of a tile, in bytes
     static constexpr int CHUNKS = kLatentLanes / 64;
+    // A tile in shared memory.  With tensor copies: its groups of chunks, one behind the other; of
+    // four chunks the rows by eight, and of those the matrices of 8 x 64 lanes side by side; the
+    // last group chunk by chunk.  So a copy can bring any number of eights of its lanes.
+    // Without: all rows by eight.
+    static constexpr int MATRIX = 1024;
+    static constexpr uint32_t EIGHT = (BOXES ? 4 : CHUNKS) * MATRIX, EIGHT_LAST = BOXES ? MATRIX : EIGHT;
     static constexpr int Q_CHUNK = ROWS * 128, Q_BYTES = CHUNKS * Q_CHUNK;
     static constexpr int STAGE = CHUNKS * CHUNK, STAGES = 2;
     static constexpr int K_AT = Q_BYTES, P_AT = K_AT + STAGES * STAGE, SYNC_AT = P_AT + (ROWS < 64 ? ROWS * 256 : ROWS * 128);  // (P, and results turned over)
     static constexpr int kSmemMax = 232448;
     // Softmax groups of four warps, which share out the columns (query rows).  64 rows: two, and
-    // four warps of helpers (ragged batch of 16-bit rows 194 us, and 181 so; chunks of prompts
-    // in pages of 16 rows 657 and 569); 8-bit rows need all eight (182 us, with four 236).
+    // four warps of helpers (ragged batch of 16-bit rows 194 us, and 181 so; chunks of prompts,
+    // rows copied by threads, 657 and 569); 8-bit rows need all eight (182 us, with four 236).
     static constexpr int SG = ROWS == 64 && kWide ? 2 : 1, SR = ROWS / SG;
     static constexpr int HELPERS = SG == 2 ? 128 : 256, TEAM = HELPERS / 2;
     static constexpr float kBias = BF16 ? 0.0f : 7.0f, kLag = 8.0f;
     static constexpr int MORE = kWide ? 0 : (3 * ROWS + 2 * TN) * 4;  // factors and scales
-    static constexpr int kAhead = 3;  // tiles from one that is brought to one that is asked into L2
+    // tiles from one that is brought to one that is asked into L2 (3: 2 % slower, 5: 10 %)
+    static constexpr int kAhead = 2;
     // tensor memory: O^T in tiles of 128 value lanes, then two S^T
     static constexpr uint32_t S_COL = 4 * ROWS;
 };
@@ -139,12 +144,15 @@ __device__ __forceinline__ uint32_t elected() {
 }
 
 // A product, and a commit, by the lane of the warp that has `me`.  a and b: the low words of
-// the descriptors (see smem_matrix), whose high words are one constant.
+// the descriptors (see smem_matrix); EIGHT: bytes between a's groups of eight rows (b's are
+// 1024), in the high words, which are constants.
+template <uint32_t EIGHT>
 __device__ __forceinline__ void mma_one(uint32_t me, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
-    constexpr uint64_t HIGH = (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+    constexpr uint64_t KIND = (uint64_t(1) << 46) | (uint64_t(2) << 61), A = KIND | (uint64_t(EIGHT >> 4) << 32),
+                       B = KIND | (uint64_t(1024 >> 4) << 32);
     asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %5, 0;\nsetp.ne.b32 q, %4, 0;\n"
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-                 "l"(HIGH | a), "l"(HIGH | b), "r"(shape), "r"(me), "r"(uint32_t(add))
+                 "l"(A | a), "l"(B | b), "r"(shape), "r"(me), "r"(uint32_t(add))
                  : "memory");
 }
 
@@ -176,15 +184,16 @@ struct Latent {
     LatentSync* sync;
     uint32_t tmem;
 
-    __device__ __forceinline__ int chunks() const { return (a.Dk + 63) / 64; }
-    __device__ __forceinline__ int value_tiles() const { return (a.Dv + 127) / 128; }
-    // Groups of a tile's chunks that come and go together: the 256 lanes of two value tiles,
-    // then the lanes that are no value's.  (Groups of 128 lanes: a wait more for each, of some
-    // 100 cycles, for products that take 256.)
-    __device__ __forceinline__ int value_groups() const { return (a.Dv + 255) / 256; }
-    __device__ __forceinline__ int groups() const { return value_groups() + (chunks() > 2 * value_tiles() ? 1 : 0); }
+    __device__ __forceinline__ int chunks() const { return latent_chunks(a); }
+    __device__ __forceinline__ int value_tiles() const { return latent_value_tiles(a); }
+    __device__ __forceinline__ int value_groups() const { return latent_value_groups(a); }
+    __device__ __forceinline__ int groups() const { return latent_groups(a); }
     __device__ __forceinline__ int group_end(int g) const {
-        return g < value_groups() ? min(min(4 * g + 4, 2 * value_tiles()), chunks()) : chunks();
+        return g < value_groups() ? min(4 * g + 4, chunks()) : chunks();
+    }
+    // Bytes of a tile before the group that begins with chunk c0 (or a later chunk of the last).
+    static __device__ __forceinline__ uint32_t group_at(int c0) {
+        return uint32_t(c0) * (C::BOXES ? C::CHUNK : C::MATRIX);
     }
     __device__ __forceinline__ uint32_t stage(uint32_t n) const { return smem_addr(smem + C::K_AT) + (n & 1) * C::STAGE; }
 
@@ -267,14 +276,14 @@ struct Latent {
         __syncwarp();
     }
 
-    // Where a tile's 64 rows lie, all in one page.
+    // Where a.box rows of a tile lie, all in one page.
     struct Box {
         int page, off;  // page -1: no such rows
     };
 
-    __device__ __forceinline__ Box box_of(const RunAt& x, int tile) const {
+    __device__ __forceinline__ Box box_of(const RunAt& x, int tile, int lane) const {
         Box r{-1, 0};
-        const int j = tile * C::TN;
+        const int j = tile * C::TN + lane * a.box;
         if (j < x.rq.len) {
             uint32_t p, off;
             a.div_page.divmod(uint32_t(j), p, off);
@@ -284,7 +293,7 @@ struct Latent {
         return r;
     }
 
-    __device__ __forceinline__ void fetches(const Place& place, const CUtensorMap* map, const CUtensorMap* quads) const {
+    __device__ __forceinline__ void fetches(const Place& place, const LatentMaps& maps) const {
         const int lane = int(threadIdx.x) & 31, all = groups();
         Walk walk = walk_from<C::ROWS, C::TN>(a, place);
         RunAt x;
@@ -298,49 +307,47 @@ struct Latent {
             publish(x, run, there, lane);
             if (!there || given_up()) break;
             if constexpr (C::BOXES) {
-                // looked up a tile ahead; rows that are not there are filled with zeros
-                Box now = box_of(x, x.t0);
+                // a lane a box, looked up a tile ahead; rows that are not there are filled with zeros
+                const int boxes = C::TN / a.box;
+                Box now{-1, 0};
+                if (lane < boxes) now = box_of(x, x.t0, lane);
                 bool on = true;
                 for (int it = 0; on && it < x.count; ++it, ++n) {
-                    const Box next = it + 1 < x.count ? box_of(x, x.t0 + it + 1) : Box{-1, 0};
+                    Box next{-1, 0};
+                    if (it + 1 < x.count && lane < boxes) next = box_of(x, x.t0 + it + 1, lane);
                     const uint32_t to = stage(n);
                     for (int g = 0, c = 0; g < all; ++g) {
                         // where a wait has given up, the place may be in use, or its last copy under way
                         on = __all_sync(0xffffffffu, wait_free(n, g));
                         if (!on) break;
                         const uint32_t bar = smem_addr(&sync->full[n & 1][g]);
-                        const int end = group_end(g);
+                        const bool values = g < value_groups();
+                        const int end = values ? c + 4 : chunks(), each = values ? 4 : 1;  // (chunks past a row: zeros)
                         if (lane == 0)
                             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                                          "r"((end - c) * C::CHUNK)
                                          : "memory");
                         __syncwarp();
                         ++copies;
-                        if (a.quads && end - c == 4) {
-                            // a page's 64 rows of 256 lanes in one copy
-                            if (lane == 0)
+                        if (lane < boxes)
+                            for (int i = c; i < end; i += each)
                                 asm volatile(
-                                    "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                                    "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + c * C::CHUNK),
-                                    "l"(quads), "r"(0), "r"(now.off), "r"(c), "r"(now.page), "r"(bar)
+                                    "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                    "[%0], [%1, {%2, %2, %3, %4, %5}], [%6];" ::"r"(
+                                        to + i * C::CHUNK + lane * (a.box >> 3) * each * C::MATRIX),
+                                    "l"(values ? &maps.four : &maps.one), "r"(0), "r"(i), "r"(now.off >> 3),
+                                    "r"(now.page), "r"(bar)
                                     : "memory");
-                        } else if (lane == 0) {
-                            for (int i = c; i < end; ++i)
-                                asm volatile(
-                                    "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                                    "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + i * C::CHUNK),
-                                    "l"(map), "r"(i * 64), "r"(0), "r"(now.off), "r"(now.page), "r"(bar)
-                                    : "memory");
-                        }
                         c = end;
                     }
-                    // a later tile is on its way from memory to L2 meanwhile
-                    if (a.quads && lane == 0 && it + C::kAhead < x.count) {
-                        const Box far = box_of(x, x.t0 + it + C::kAhead);
+                    // a later tile is on its way from memory to L2 meanwhile (in small boxes that costs
+                    // more than it gives: ragged batch in boxes of 8 rows 187 us, and 251 so)
+                    if (boxes == 1 && lane == 0 && it + C::kAhead < x.count) {
+                        const Box far = box_of(x, x.t0 + it + C::kAhead, 0);
                         if (far.page >= 0)
                             for (int c = 0; c < chunks(); c += 4)
-                                asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                                                 quads), "r"(0), "r"(far.off), "r"(c), "r"(far.page)
+                                asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %1, %2, %3, %4}];" ::"l"(
+                                                 &maps.four), "r"(0), "r"(c), "r"(far.off >> 3), "r"(far.page)
                                              : "memory");
                     }
                     now = next;
@@ -356,10 +363,9 @@ struct Latent {
 
     // ---------------------------------------------------------- helpers
 
-    // Where 16 bytes (8 lanes from 8 piece) of line `row` lie.
-    template <int BYTES>
+    // Where 16 bytes (8 lanes from 8 piece) of query row `row` lie.
     static __device__ __forceinline__ uint32_t line_at(int row, int piece) {
-        return uint32_t(piece >> 3) * BYTES + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+        return uint32_t(piece >> 3) * C::Q_CHUNK + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
     }
 
     // The queries of a run: eight threads a row.
@@ -378,7 +384,7 @@ struct Latent {
                 for (int c = 0; c < chunks(); ++c) {
                     const int piece = c * 8 + (id & 7);
                     const bool ok = src && piece < pieces;
-                    copy16(to + line_at<C::Q_CHUNK>(row, piece), ok ? src + piece * 16 : a.q, ok);
+                    copy16(to + line_at(row, piece), ok ? src + piece * 16 : a.q, ok);
                 }
             }
             copies_commit();
@@ -417,7 +423,7 @@ struct Latent {
                 }
 #pragma unroll
                 for (int c = 0; c < C::CHUNKS; ++c)
-                    sts128(to + line_at<C::Q_CHUNK>(row, c * 8 + (id & 7)), w[c].x, w[c].y, w[c].z, w[c].w);
+                    sts128(to + line_at(row, c * 8 + (id & 7)), w[c].x, w[c].y, w[c].z, w[c].w);
             }
         }
     }
@@ -461,6 +467,8 @@ struct Latent {
 #pragma unroll 1
         for (int pass = 0; pass < PASSES; ++pass) {
             const int row = pass * 4 * STEP + (tid >> 3);
+            const uint32_t at = to + (row >> 3) * C::EIGHT + (row & 7) * 128 + ((sub ^ (row & 7)) << 4),
+                           step = STEP / 8 * C::EIGHT;
             Row r[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = row_of(x, (x.t0 + it) * C::TN + row + STEP * i);
@@ -478,7 +486,7 @@ struct Latent {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const bool ok = r[i].p && piece < pieces;
-                            copy16(to + line_at<C::CHUNK>(row + STEP * i, piece), ok ? r[i].p + piece * 16 : a.k, ok);
+                            copy16(at + c * C::MATRIX + i * step, ok ? r[i].p + piece * 16 : a.k, ok);
                         }
                     }
                     copies_commit();
@@ -508,7 +516,7 @@ struct Latent {
                             if (c + k < end)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    sts128(to + line_at<C::CHUNK>(row + STEP * i, (c + k) * 8 + sub),
+                                    sts128(at + (c + k) * C::MATRIX + i * step,
                                            codes_to_half2<C::STORE, false>(w[i][k].x),
                                            codes_to_half2<C::STORE, true>(w[i][k].x),
                                            codes_to_half2<C::STORE, false>(w[i][k].y),
@@ -567,7 +575,7 @@ struct Latent {
     __device__ __forceinline__ void scores() const {
         constexpr uint32_t shape = latent_shape<C::BF16, C::TN, C::ROWS, false>();
         const uint32_t me = elected(), q = __shfl_sync(0xffffffffu, smem_addr(smem) >> 4, 0);
-        const int all = chunks(), rest = 2 * value_tiles(), groups_of_values = value_groups();
+        const int all = chunks(), last = min(4 * value_groups(), all), groups_of_values = value_groups();
         uint32_t n = 0;
         for (uint32_t run = 0;; ++run) {
             RunAt x;
@@ -582,14 +590,22 @@ struct Latent {
                 const uint32_t to = __shfl_sync(0xffffffffu, tmem + C::S_COL + (n & 1) * C::ROWS, 0);
                 const uint32_t k = __shfl_sync(0xffffffffu, stage(n) >> 4, 0), par = (n / 2) & 1;
                 unsigned long long* full = sync->full[n & 1];
+                int c = 0;
 #pragma unroll 1
-                for (int c = 0; c < all; ++c) {
-                    if (c == rest) on = wait(full + groups_of_values, par);
-                    else if (c % 4 == 0 && c < rest) on = wait(full + c / 4, par);
-                    const uint32_t x0 = k + c * (C::CHUNK >> 4), y0 = q + c * (C::Q_CHUNK >> 4);
-                    mma_one(me, to, x0, y0, shape, c > 0);
+                for (; c < last; ++c) {
+                    if (c % 4 == 0) on = wait(full + c / 4, par);
+                    const uint32_t x0 = k + (group_at(c & ~3) >> 4) + (c & 3) * (C::MATRIX >> 4),
+                                   y0 = q + c * (C::Q_CHUNK >> 4);
+                    mma_one<C::EIGHT>(me, to, x0, y0, shape, c > 0);
 #pragma unroll
-                    for (int i = 1; i < 4; ++i) mma_one(me, to, x0 + i * 2, y0 + i * 2, shape, true);
+                    for (int i = 1; i < 4; ++i) mma_one<C::EIGHT>(me, to, x0 + i * 2, y0 + i * 2, shape, true);
+                }
+                if (c < all) on = wait(full + groups_of_values, par);
+#pragma unroll 1
+                for (; c < all; ++c) {
+                    const uint32_t x0 = k + (group_at(c) >> 4), y0 = q + c * (C::Q_CHUNK >> 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_one<C::EIGHT_LAST>(me, to, x0 + i * 2, y0 + i * 2, shape, true);
                 }
                 on = __all_sync(0xffffffffu, on);  // (given up: the scores are whatever they are)
                 commit_one(me, &sync->s_full[n & 1]);
@@ -602,7 +618,7 @@ struct Latent {
 
     __device__ __forceinline__ void products() const {
         constexpr uint32_t shape = latent_shape<C::BF16, 128, C::ROWS, true>();
-        constexpr uint32_t lead = uint32_t(C::CHUNK >> 4) << 16;
+        constexpr uint32_t lead = uint32_t(C::MATRIX >> 4) << 16;  // from 64 value lanes to the next
         const uint32_t me = elected(), p = __shfl_sync(0xffffffffu, smem_addr(smem + C::P_AT) >> 4, 0);
         const int tiles = value_tiles();
         uint32_t n = 0;
@@ -618,10 +634,11 @@ struct Latent {
                 const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
                 for (int t = 0; t < tiles; ++t) {
-                    mma_one(me, to + t * C::ROWS, v + t * (C::CHUNK >> 3), p, shape, it > 0);
+                    const uint32_t v0 = v + (group_at(t >> 1 << 2) >> 4) + (t & 1) * (C::MATRIX >> 3);
+                    mma_one<C::EIGHT>(me, to + t * C::ROWS, v0, p, shape, it > 0);
 #pragma unroll
                     for (int i = 1; i < 4; ++i)
-                        mma_one(me, to + t * C::ROWS, v + t * (C::CHUNK >> 3) + i * 128, p + i * 2, shape, true);
+                        mma_one<C::EIGHT>(me, to + t * C::ROWS, v0 + i * (C::EIGHT >> 3), p + i * 2, shape, true);
                     if (t % 2 == 1 || t + 1 == tiles) commit_one(me, &sync->empty[n & 1][t / 2]);
                 }
                 if (me) sync->beat = n + 1;
@@ -644,11 +661,13 @@ struct Latent {
     // those of drafted rows that are not finite are taken out (see add_not_finite): a
     // weight of 0 times them would reach the tokens that do not see the row.
     __device__ __noinline__ void mend(uint32_t n, int from, int valid, uint32_t run, int group) const {
-        const int pieces = value_tiles() * 16, lane = int(threadIdx.x) & 31;
+        const int pieces = min(value_tiles() * 16, chunks() * 8), lane = int(threadIdx.x) & 31;
         bool found = false;
         for (int row = from + (int(threadIdx.x) >> 5 & 3) * C::SG + group; row < C::TN; row += 4 * C::SG)
             for (int piece = lane; piece < pieces; piece += 32) {
-                const uint32_t at = stage(n) + line_at<C::CHUNK>(row, piece);
+                const int c0 = piece >> 5 << 2;  // its group's first chunk
+                const uint32_t at = stage(n) + group_at(c0) + (row >> 3) * C::EIGHT + ((piece >> 3) - c0) * C::MATRIX +
+                                    (row & 7) * 128 + (((piece & 7) ^ (row & 7)) << 4);
                 if (row >= valid) {
                     sts128(at, 0, 0, 0, 0);
                     continue;
@@ -977,8 +996,7 @@ struct Latent {
 // T: Latent, or what a test makes of it.
 template <class T>
 __global__ void __launch_bounds__(kLatentThreads, 1)
-    rope_latent_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map,
-                       const __grid_constant__ CUtensorMap quads) {
+    rope_latent_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ LatentMaps maps) {
     using C = typename T::Cfg;
     extern __shared__ __align__(1024) char smem[];
     static_assert(C::SYNC_AT + int(sizeof(LatentSync)) + C::MORE <= C::kSmemMax, "shared memory");
@@ -1020,7 +1038,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     } else if (warp == 4) {
         it.scores();
     } else if (warp == 5) {
-        it.fetches(place, &map, &quads);
+        it.fetches(place, maps);
     } else if (warp < 14) {
         it.help(int(threadIdx.x) - (C::SG == 2 && warp >= 12 ? 320 : 192));
     } else {

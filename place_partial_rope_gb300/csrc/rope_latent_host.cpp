@@ -27,7 +27,7 @@ rope_status_t latent_plan(const rope_kv_cache_t* c, int dtype, int64_t Hq, int64
                     "%d and v_dim <= %d", (long long)c->k_dim, (long long)v_dim, kLatentLanes, kLatentValues);
     if (Hq < 1 || Hq > (1 << 20)) return fail(ROPE_ERR_INVALID, "Hq=%lld must be positive", (long long)Hq);
     if (max_q < 1 || max_q > kInt) return fail(ROPE_ERR_INVALID, "max_q=%lld must be positive", (long long)max_q);
-    *p = choose_latent(c->dtype, max_q * Hq, c->pages, c->page_size);
+    *p = choose_latent(c->dtype, max_q * Hq, c->k_dim, c->pages, c->page_size);
     return ROPE_OK;
 }
 

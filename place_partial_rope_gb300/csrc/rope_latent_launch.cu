@@ -19,15 +19,16 @@ TreeKernel kernel_of(const LatentPlan& p) {
 
 }  // namespace
 
-// Tiles as narrow as the query rows allow.  Tensor copies where a tile's 64 rows lie in one
-// page (and there is one: a map has no dim of 0).  A copy takes some 90 cycles whatever its
-// rows, so pages of 16, four times as many, bound chunks of prompts to 724 us, where rows
-// copied by threads took 657.  8-bit rows pass through registers anyway.
-LatentPlan choose_latent(int store, int64_t rows, int64_t pages, int64_t page_size) {
+// Tiles as narrow as the query rows allow.  Tensor copies where eights of rows lie in one
+// page (and there is one: a map has no dim of 0) and rows are whole chunks: chunks of prompts in
+// pages of 16 rows 463 us, and 568 copied by threads.
+// 8-bit rows pass through registers anyway.
+LatentPlan choose_latent(int store, int64_t rows, int64_t k_dim, int64_t pages, int64_t page_size) {
     LatentPlan p{};
     p.store = store;
     p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.boxes = (store == ROPE_CACHE_BF16 || store == ROPE_CACHE_FP16) && pages > 0 && page_size % kLatentKeys == 0;
+    p.boxes = (store == ROPE_CACHE_BF16 || store == ROPE_CACHE_FP16) && pages > 0 && page_size % 8 == 0 &&
+              k_dim % 64 == 0;
     return p;
 }
 
@@ -53,18 +54,15 @@ rope_status_t launch_latent(const LatentPlan& p, const TreeArgs& args, void* wor
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * kLatentValues);
     a.meta = reinterpret_cast<TreeMeta*>(a.part_ml + rows);
-    CUtensorMap map{}, quads{};
+    LatentMaps maps{};
     if (p.boxes) {
-        a.box = kLatentKeys;
-        const rope_status_t st = tree_map(&map, a.k, a.Dk, a, a.k_st, true, 64, err);
+        a.box = 8;
+        while (a.box < kLatentKeys && a.page_size % (2 * a.box) == 0) a.box *= 2;
+        rope_status_t st = tree_map_eights(&maps.four, a, 4, err);
+        if (st == ROPE_OK && latent_groups(a) > latent_value_groups(a)) st = tree_map_eights(&maps.one, a, 1, err);
         if (st != ROPE_OK) return st;
-        a.quads = a.Dk % 64 == 0 && a.Dk >= 256;
-        if (a.quads) {
-            const rope_status_t sq = tree_map_quads(&quads, a.k, a.Dk / 64, a, a.k_st, err);
-            if (sq != ROPE_OK) return sq;
-        }
     }
-    void* params[] = {&a, &map, &quads};
+    void* params[] = {&a, &maps};
     const rope_status_t st = tree_launch(k.main, blocks, 1, k.threads, k.smem, params, stream, err);
     if (st != ROPE_OK || blocks < 2) return st;
     void* join[] = {&a};

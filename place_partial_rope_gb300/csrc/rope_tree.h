@@ -39,7 +39,6 @@ struct TreeArgs {
     FastDiv div_page, div_group;
     float scale_log2;            // scale * log2(e)
     bool bf16;                   // type of q and out (the cache's own for 16 bits)
-    bool quads;                  // latent rows: 256 lanes of 64 rows of a page are one copy
 };
 
 // The group of row tiles that a block's first unit lies in, when it began in
@@ -81,13 +80,11 @@ struct TreeKernel {
 };
 
 // For the kernels of rope_latent.h, too: a kernel's blocks on the current device (allowing
-// its shared memory), the map of a cache tensor, and a launch.
+// its shared memory), the map of a cache's keys, and a launch.
 rope_status_t tree_resident(const TreeKernel& k, int* blocks, const char** err);
-rope_status_t tree_map(struct CUtensorMap_st* map, const void* base, int dim, const TreeArgs& a, const int64_t* st,
-                       bool wide, int lanes, const char** err);
-// (the same in pieces of 64 lanes: (lane, token of the page, piece, page), four pieces a fetch)
-rope_status_t tree_map_quads(struct CUtensorMap_st* map, const void* base, int pieces, const TreeArgs& a,
-                             const int64_t* st, const char** err);
+// (of a cache with one head: lanes of a piece of 64, eight rows, pieces, eights of a page, pages;
+// a copy has `pieces` of them and a.box rows)
+rope_status_t tree_map_eights(struct CUtensorMap_st* map, const TreeArgs& a, int pieces, const char** err);
 rope_status_t tree_launch(const void* f, int blocks, int per, int threads, int smem, void** params,
                           rope_stream_t stream, const char** err);
 

@@ -201,22 +201,17 @@ rope_status_t tree_resident(const TreeKernel& k, int* blocks, const char** err) 
     return st;
 }
 
-rope_status_t tree_map(CUtensorMap* map, const void* base, int dim, const TreeArgs& a, const int64_t* st, bool wide,
-                       int lanes, const char** err) {
-    return map_of(map, base, dim, a, st, wide, lanes, err);
-}
-
-rope_status_t tree_map_quads(CUtensorMap* map, const void* base, int pieces, const TreeArgs& a, const int64_t* st,
-                             const char** err) {
+rope_status_t tree_map_eights(CUtensorMap* map, const TreeArgs& a, int pieces, const char** err) {
     const Encode encode = encoder();
     if (!encode) {
         *err = "the driver has no cuTensorMapEncodeTiled";
         return ROPE_ERR_CUDA;
     }
-    const cuuint64_t sizes[4] = {64, cuuint64_t(a.page_size), cuuint64_t(pieces), cuuint64_t(a.pages)};
-    const cuuint64_t strides[3] = {a.page_size > 1 ? cuuint64_t(st[1]) : 16, 128, a.pages > 1 ? cuuint64_t(st[0]) : 16};
-    const cuuint32_t box[4] = {64, cuuint32_t(a.box), 4, 1}, steps[4] = {1, 1, 1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), sizes, strides, box,
+    const cuuint64_t row = cuuint64_t(a.k_st[1]);
+    const cuuint64_t sizes[5] = {64, 8, cuuint64_t(a.Dk / 64), cuuint64_t(a.page_size / 8), cuuint64_t(a.pages)};
+    const cuuint64_t strides[4] = {row, 128, row * 8, a.pages > 1 ? cuuint64_t(a.k_st[0]) : 16};
+    const cuuint32_t box[5] = {64, 8, cuuint32_t(pieces), cuuint32_t(a.box / 8), 1}, steps[5] = {1, 1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<char*>(a.k), sizes, strides, box,
                               steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
