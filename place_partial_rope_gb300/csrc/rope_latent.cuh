@@ -27,6 +27,14 @@
 //   6-13  helpers: bring the queries of a run, and other tiles: 16-bit rows by
 //         asynchronous copies, 8-bit rows as codes that become fp16 on the way.
 // Two tiles of 64 rows x 576 lanes beside 64 query rows fill shared memory.
+//   What bounds it: shared memory, which both products read at its full rate (1150 cycles for
+// the scores of 64 query rows and 770 for the values of a tile of 64 rows, 570 more to bring it),
+// and the chain of fetch, scores, softmax and values over two tiles in flight: 64 requests
+// of 128 heads over 90 to 12000 bf16 rows take 177 us (2.6 TB/s; 68 by the cache's bytes), 3
+// chunks of 200 to 256 tokens of 64 heads over 1031 to 4099 fp16 rows 463 us (519 TFLOP/s).  8-bit
+// rows: threads that turn codes into fp16, and instruction fetch: 32 requests of 1 to 7 tokens
+// of 32 heads over 8000 fp8 rows 182 us (347 TFLOP/s), 2 of 131072 int8 rows and 16 heads 76 us
+// (2.0 TB/s).  One token of 16 heads over 4097 rows: 16.8 us, a tile a block and the join.
 //   Every wait is bounded; one that gives up sets `dead`, the threads of a role leave
 // together, and every result that the block has a share in becomes NaN.
 #pragma once
