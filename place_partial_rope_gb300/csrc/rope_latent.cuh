@@ -30,7 +30,7 @@
 //   What bounds it: shared memory, which both products read at its full rate (1150 cycles for
 // the scores of 64 query rows and 770 for the values of a tile of 64 rows, 570 more to bring it),
 // and the chain of fetch, scores, softmax and values over two tiles in flight: 64 requests
-// of 128 heads over 90 to 12000 bf16 rows take 177 us (2.6 TB/s; 68 by the cache's bytes), 3
+// of 128 heads over 90 to 12000 bf16 rows take 161 us (2.9 TB/s; 68 by the cache's bytes), 3
 // chunks of 200 to 256 tokens of 64 heads over 1031 to 4099 fp16 rows 463 us (519 TFLOP/s).  8-bit
 // rows: threads that turn codes into fp16, and instruction fetch: 32 requests of 1 to 7 tokens
 // of 32 heads over 8000 fp8 rows 182 us (347 TFLOP/s), 2 of 131072 int8 rows and 16 heads 76 us
@@ -260,6 +260,14 @@ struct Latent {
 
     // ---------------------------------------------------------- the walk, and tensor copies
 
+    // The block's next run.  Of two blocks that walk a pair of row tiles (blockIdx.y) each has one.
+    __device__ __forceinline__ bool run_after(Walk& walk, RunAt& x) const {
+        if (!next_run<C::ROWS, C::TN>(a, walk, x)) return false;
+        x.m = x.m * int(gridDim.y) + int(blockIdx.y);
+        if (x.slot >= 0) x.slot += int64_t(blockIdx.y) * 2 * gridDim.x;
+        return true;
+    }
+
     // Run r for the other roles, when all of them have taken run r - 3, whose place it gets.  With
     // tensor copies that is so: the copies before it were made when the products of the tile two
     // before them, and so of run r - 3, were done.  Else it is waited for: where one softmax group
@@ -308,8 +316,8 @@ struct Latent {
         uint32_t run = 0, n = 0, copies = 0;  // runs, tiles, groups of them asked for
         bool first = true;
         for (;; ++run) {
-            const bool there = next_run<C::ROWS, C::TN>(a, walk, x);
-            if (first && lane == 0)
+            const bool there = run_after(walk, x);
+            if (first && lane == 0 && blockIdx.y == 0)
                 a.meta[blockIdx.x] = there ? meta_of(place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, place.lead};
             first = false;
             publish(x, run, there, lane);
@@ -984,7 +992,7 @@ struct Latent {
         const int tid = int(threadIdx.x);
         Walk walk = walk_from<C::ROWS, C::TN>(a, place);
         RunAt x;
-        while (next_run<C::ROWS, C::TN>(a, walk, x)) {
+        while (run_after(walk, x)) {
             const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
             if (x.slot >= 0) {
                 for (int r = tid; r < C::ROWS; r += kLatentThreads)
@@ -1064,9 +1072,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 
 // Puts the parts of each split (request, row tile) together: out = sum_p O_p 2^(m_p - m) /
 // sum_p l_p 2^(m_p - m).  A group cut by s block borders has s blocks here (times
-// gridDim.y), which share out its pieces of 128 lanes of a row.  Up to 8 parts: a warp takes
-// a piece, four lanes a thread, with its parts' loads in flight together; more: a block
-// does, whose warps take the parts in turn and are added up in one order.
+// gridDim.y; of a pair of row tiles each has half of those), which share out its pieces of 128
+// lanes of a row.  Up to 8 parts: a warp takes a piece, four lanes a thread, with its parts'
+// loads in flight together; more: a block does, whose warps take the parts in turn and are
+// added up in one order.
 template <int ROWS>
 __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int WARPS = kLatentJoinThreads / 32;
@@ -1080,16 +1089,19 @@ __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(co
     const int parts = static_cast<int>(to - from + 1);
     const int qs = min(max(__ldg(a.q_start + w.r), 0), a.Tq);
     const int n = min(max(__ldg(a.q_start + w.r + 1), qs), a.Tq) - qs;
-    const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(w.m) * ROWS));
+    // of a pair of row tiles this block joins one
+    const int pair = a.share != a.G ? 1 : 0, odd = int(blockIdx.y) & pair, m = w.m + odd, shares = int(gridDim.y) >> pair;
+    const int left = static_cast<int>(min(int64_t(ROWS), int64_t(n) * a.G - int64_t(m) * ROWS));
     const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5, quarters = (a.Dv + 127) / 128;
-    const int own = static_cast<int>(b - from - 1) * int(gridDim.y) + int(blockIdx.y);
-    const int all = (parts - 1) * int(gridDim.y);
+    const int own = static_cast<int>(b - from - 1) * shares + (int(blockIdx.y) >> pair);
+    const int all = (parts - 1) * shares;
     // part p: block `from` holds it second unless the group begins with the block's run
     const int64_t second = from * w.chunk < w.u0 - w.lead ? 1 : 0;
-    auto slot = [&](int p) { return ((from + p) * 2 + (p == 0 ? second : 0)) * ROWS; };
+    const int64_t before = int64_t(odd) * 2 * (gridDim.x + 1);  // parts of the pair's other
+    auto slot = [&](int p) { return (before + (from + p) * 2 + (p == 0 ? second : 0)) * ROWS; };
     auto write = [&](int row, int c, float4 o, float top, float l) {
         const float norm = l == 0.0f ? 0.0f : 1.0f / l;
-        const OutAt z = out_at(a, qs, 0, w.m * ROWS + row);
+        const OutAt z = out_at(a, qs, 0, m * ROWS + row);
         if (c < a.Dv)
             *reinterpret_cast<uint2*>(z.out + c * 2) =
                 a.bf16 ? make_uint2(pack2<true>(o.x * norm, o.y * norm), pack2<true>(o.z * norm, o.w * norm))

@@ -207,7 +207,7 @@ __device__ __forceinline__ Request request(const TreeArgs& a, int r) {
     q.qs = lo;
     q.n = hi - lo;
     q.len = min(max(__ldg(a.kv_len + r), 0), a.max_len);
-    q.mt = static_cast<int>((int64_t(q.n) * a.G + ROWS - 1) / ROWS);
+    q.mt = static_cast<int>((int64_t(q.n) * a.share + ROWS - 1) / ROWS);
     q.nt = max(1, (q.len + TN - 1) / TN);
     q.groups = q.n == 0 ? 0 : int64_t(a.Hk) * q.mt;
     return q;
