@@ -31,7 +31,7 @@
 // the scores of 64 query rows and 770 for the values of a tile of 64 rows, 570 more to bring it),
 // and the chain of fetch, scores, softmax and values over two tiles in flight: 64 requests
 // of 128 heads over 90 to 12000 bf16 rows take 161 us (2.9 TB/s; 68 by the cache's bytes), 3
-// chunks of 200 to 256 tokens of 64 heads over 1031 to 4099 fp16 rows 463 us (519 TFLOP/s).  8-bit
+// chunks of 200 to 256 tokens of 64 heads over 1031 to 4099 fp16 rows 395 us (609 TFLOP/s).  8-bit
 // rows: threads that turn codes into fp16, and instruction fetch: 32 requests of 1 to 7 tokens
 // of 32 heads over 8000 fp8 rows 182 us (347 TFLOP/s), 2 of 131072 int8 rows and 16 heads 76 us
 // (2.0 TB/s).  One token of 16 heads over 4097 rows: 16.8 us, a tile a block and the join.
@@ -319,7 +319,7 @@ struct Latent {
         for (;; ++run) {
             const bool there = run_after(walk, x);
             if (first && lane == 0 && blockIdx.y == 0)
-                a.meta[blockIdx.x] = there ? meta_of(place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, place.lead};
+                a.meta[blockIdx.x] = there ? meta_of(place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, 0};
             first = false;
             publish(x, run, there, lane);
             if (!there || given_up()) break;

@@ -37,6 +37,7 @@ struct TreeArgs {
     int32_t share;               // of the G query heads of a key head, those in a block's row tiles: all, or half
                                  // where blocks go in pairs (set by the launch)
     int32_t pages, page_size, max_len;
+    int32_t masked;              // units that a tile with masks counts beyond its own (set by the launch)
     int32_t box;                 // tile kernels: rows of a fetch, a power of two that divides page_size
     FastDiv div_page, div_group;
     float scale_log2;            // scale * log2(e)

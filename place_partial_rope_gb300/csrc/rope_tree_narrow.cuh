@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kNarrowThreads) rope_tree_narrow_kernel(const 
     after_predecessor();
     const Place p = find_place<C::ROWS, C::TN, kNarrowThreads>(a, reinterpret_cast<int64_t*>(smem));
     Walk walk = walk_from<C::ROWS, C::TN>(a, p);
-    TreeMeta meta{0, p.chunk, 0, 0, 0, 0, p.lead};
+    TreeMeta meta{0, p.chunk, 0, 0, 0, 0, 0};
     RunAt step;
     bool first = true;
     __syncthreads();  // the place's scratch is done with
