@@ -203,6 +203,8 @@ rope_status_t rope_partial_cache_trim(int32_t* kv_len, const int32_t* new_len, i
  *                are written by rope_partial_cache_write and read by
  *                rope_partial_cache_read as any keys are.
  *   v_dim        the lanes of the value, and of a row of out
+ *   scale        the model's own: with matrices multiplied into q, that of the heads' query
+ *                rows before the product (1 / sqrt(192) for heads of 128 + 64 lanes), not of k_dim
  *   other arguments, requests, trees, lengths, masks and the workspace
  *                as for rope_partial_tree_attention: chains without a tree, tokens that
  *                see no row (0 and -inf), tokens outside every request (left as

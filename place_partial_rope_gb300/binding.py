@@ -40,6 +40,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import warnings
 
 import torch
 
@@ -1010,8 +1011,16 @@ def rope_partial_latent_attention(q, cache: KVCache, q_start, kv_len, page_table
                                   scale=None, max_q=None, workspace=None, stream=None) -> None:
     """rope_partial_tree_attention over a cache of latent rows (one head, keys only):
     one row a token for all heads of ``q`` (Tq, Hq, k_dim), whose first v_dim lanes
-    are its value, v_dim being the last size of ``out`` (Tq, Hq, v_dim)."""
+    are its value, v_dim being the last size of ``out`` (Tq, Hq, v_dim).
+
+    ``scale`` is the model's: for heads whose matrices were multiplied into q it is that of
+    their own query rows before that product (1 / sqrt(192) for heads of 128 + 64 lanes over
+    rows of 576), which no argument tells.  A call without one takes 1 / sqrt(k_dim), that of
+    the rows as they lie in the cache, and warns."""
     lib = _lib or load_library()
+    if scale is None:
+        warnings.warn(f"rope_partial_latent_attention: no scale was given, and 1 / sqrt({cache.k_dim}) is taken, which "
+                      "is not the scale of heads whose matrices were multiplied into q", stacklevel=2)
     if out.dim() != 3:
         _refuse("out must be (tokens, heads, v_dim)")
     vd = out.shape[2]
