@@ -428,7 +428,8 @@ def run(s):
         binding.rope_partial_cache_trim(s["kv_len"], s["back"], s["table"], s["free"], s["count"], c["page"])
         return {**got, "kv_len": s["kv_len"], "table": s["table"], "free": s["free"], "count": s["count"]}
     binding.rope_partial_latent_attention(s["q"], s["cache"], s["q_start"], s["kv_len"], s["table"], s["out"],
-                                          lse=s["lse"], tree=s["tree"], max_q=c["n_hi"], workspace=s["workspace"])
+                                          lse=s["lse"], tree=s["tree"], scale=1.0 / math.sqrt(c["dk"]),
+                                          max_q=c["n_hi"], workspace=s["workspace"])
     return {"out": s["out"], "lse": s["lse"]}
 
 
