@@ -263,7 +263,7 @@ struct Latent {
 
     // The block's next run.  Of two blocks that walk a pair of row tiles (blockIdx.y) each has one.
     __device__ __forceinline__ bool run_after(Walk& walk, RunAt& x) const {
-        if (!next_run<C::ROWS, C::TN>(a, walk, x)) return false;
+        if (!next_run<C::ROWS, C::TN, true>(a, walk, x)) return false;
         x.m = x.m * int(gridDim.y) + int(blockIdx.y);
         if (x.slot >= 0) x.slot += int64_t(blockIdx.y) * 2 * gridDim.x;
         return true;
@@ -312,14 +312,14 @@ struct Latent {
 
     __device__ __forceinline__ void fetches(const Place& place, const LatentMaps& maps) const {
         const int lane = int(threadIdx.x) & 31, all = groups();
-        Walk walk = walk_from<C::ROWS, C::TN>(a, place);
+        Walk walk = walk_from<C::ROWS, C::TN, true>(a, place);
         RunAt x;
         uint32_t run = 0, n = 0, copies = 0;  // runs, tiles, groups of them asked for
         bool first = true;
         for (;; ++run) {
             const bool there = run_after(walk, x);
             if (first && lane == 0 && blockIdx.y == 0)
-                a.meta[blockIdx.x] = there ? meta_of(place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, 0};
+                a.meta[blockIdx.x] = there ? meta_of<C::TN, true>(a, place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, 0};
             first = false;
             publish(x, run, there, lane);
             if (!there || given_up()) break;
@@ -991,7 +991,7 @@ struct Latent {
     // of the block's other runs too, and in its parts, whose joined results then are NaN.
     __device__ __noinline__ void give_up(const Place& place) const {
         const int tid = int(threadIdx.x);
-        Walk walk = walk_from<C::ROWS, C::TN>(a, place);
+        Walk walk = walk_from<C::ROWS, C::TN, true>(a, place);
         RunAt x;
         while (run_after(walk, x)) {
             const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
@@ -1045,7 +1045,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     after_predecessor();
-    const Place place = find_place<C::ROWS, C::TN, kLatentThreads>(a, reinterpret_cast<int64_t*>(smem));
+    const Place place = find_place<C::ROWS, C::TN, kLatentThreads, true>(a, reinterpret_cast<int64_t*>(smem));
     tmem_before();
     __syncthreads();
     tmem_after();

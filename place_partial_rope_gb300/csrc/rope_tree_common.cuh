@@ -185,10 +185,10 @@ __device__ __forceinline__ uint4 half8(const float* f, float by) {
 // Request r: groups (key heads x row tiles) of nt cache tiles (a request with no
 // cache rows still has a tile, so that its results are written).
 struct Request {
-    int qs, n, len, mt, nt, lead;
+    int qs, n, len, mt, nt;
     int64_t groups;
 
-    __device__ __forceinline__ int64_t units(bool leads) const { return groups * (nt + (leads ? lead : 0)); }
+    __device__ __forceinline__ int64_t units(int lead) const { return groups * (nt + lead); }
 };
 
 // A run of tiles costs its block its tiles and, once, what takes about as long as
@@ -196,11 +196,20 @@ struct Request {
 // So a group counts kLead units before those of its tiles, where a block has
 // several tiles.  48 requests of 90 to 12000 fp8 rows, of which some blocks had
 // four runs and some forty: 0 264 us, 2 252, 3 240, 4 232, 6 233; 12 requests of
-// 6000 to 8200 bf16 rows: 112.9, 110.7, 110.6, 108.6, 112.2.  Tiles that drafted rows fill may
-// count more (`masked`).
+// 6000 to 8200 bf16 rows: 112.9, 110.7, 110.6, 108.6, 112.2.
 constexpr int kLead = 4;
 
-template <int ROWS, int TN>
+// LATENT, here and below: row tiles hold a.share of the heads, and a request's groups count
+// a.masked units more for each tile that drafted rows fill.  (The other kernels' lead is one
+// number for all: worked out and carried for each request, it cost the first batch above 7 %.)
+template <int TN, bool LATENT>
+__device__ __forceinline__ int lead_of(const TreeArgs& a, const Request& q, int lead) {
+    if constexpr (LATENT)
+        if (lead) lead += static_cast<int>(min(int64_t(q.n) * a.masked / TN, int64_t(1) << 20));
+    return lead;
+}
+
+template <int ROWS, int TN, bool LATENT>
 __device__ __forceinline__ Request request(const TreeArgs& a, int r) {
     Request q;
     const int lo = min(max(__ldg(a.q_start + r), 0), a.Tq);
@@ -208,56 +217,54 @@ __device__ __forceinline__ Request request(const TreeArgs& a, int r) {
     q.qs = lo;
     q.n = hi - lo;
     q.len = min(max(__ldg(a.kv_len + r), 0), a.max_len);
-    q.mt = static_cast<int>((int64_t(q.n) * a.share + ROWS - 1) / ROWS);
+    q.mt = static_cast<int>((int64_t(q.n) * (LATENT ? a.share : a.G) + ROWS - 1) / ROWS);
     q.nt = max(1, (q.len + TN - 1) / TN);
     q.groups = q.n == 0 ? 0 : int64_t(a.Hk) * q.mt;
-    q.lead = kLead + static_cast<int>(min(int64_t(q.n) * a.masked / TN, int64_t(1) << 20));
     return q;
 }
 
 // A block's units, and the request that holds the first of them.
 struct Place {
-    int r;
-    bool leads;                       // groups count their leads
+    int r, lead;
     int64_t base, start, end, chunk;  // base: units before request r
 };
 
 // Sum the requests' units, cut them into equal runs, and find this block's.
 // All THREADS threads of the block take part; `scratch` holds THREADS / 16 + 2
 // numbers of shared memory.
-template <int ROWS, int TN, int THREADS>
+template <int ROWS, int TN, int THREADS, bool LATENT = false>
 __device__ __forceinline__ Place find_place(const TreeArgs& a, int64_t* scratch) {
     constexpr int WARPS = THREADS / 32;
     int64_t* warp_sum = scratch;
-    int64_t* warp_leads = scratch + WARPS;
+    int64_t* warp_groups = scratch + WARPS;
     int64_t* found = scratch + 2 * WARPS;
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    int64_t mine = 0, leads = 0;
+    int64_t mine = 0, groups = 0;
     for (int r = tid; r < a.R; r += THREADS) {
-        const Request q = request<ROWS, TN>(a, r);
-        mine += q.units(false);
-        leads += q.groups * q.lead;
+        const Request q = request<ROWS, TN, LATENT>(a, r);
+        mine += q.units(0);
+        groups += q.groups * (LATENT ? lead_of<TN, LATENT>(a, q, kLead) : 1);
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         mine += __shfl_xor_sync(0xffffffffu, mine, d);
-        leads += __shfl_xor_sync(0xffffffffu, leads, d);
+        groups += __shfl_xor_sync(0xffffffffu, groups, d);
     }
     if (lane == 0) {
         warp_sum[warp] = mine;
-        warp_leads[warp] = leads;
+        warp_groups[warp] = groups;
     }
     if (tid == 0) found[0] = a.R;
     __syncthreads();
     int64_t total = 0;
-    leads = 0;
+    groups = 0;
     for (int w = 0; w < WARPS; ++w) {
         total += warp_sum[w];
-        leads += warp_leads[w];
+        groups += warp_groups[w];
     }
     Place p;
-    p.leads = total >= int64_t(gridDim.x) * 8;
-    if (p.leads) total += leads;
+    p.lead = total >= int64_t(gridDim.x) * 8 ? kLead : 0;
+    total += LATENT ? (p.lead ? groups : 0) : groups * p.lead;
     p.chunk = (total + gridDim.x - 1) / gridDim.x;
     if (p.chunk < 1) p.chunk = 1;
     p.start = int64_t(blockIdx.x) * p.chunk;
@@ -268,7 +275,11 @@ __device__ __forceinline__ Place find_place(const TreeArgs& a, int64_t* scratch)
     int64_t before = 0;
     for (int r0 = 0; r0 < a.R; r0 += THREADS) {
         const int r = r0 + tid;
-        const int64_t u = r < a.R ? request<ROWS, TN>(a, r).units(p.leads) : 0;
+        int64_t u = 0;
+        if (r < a.R) {
+            const Request q = request<ROWS, TN, LATENT>(a, r);
+            u = q.units(lead_of<TN, LATENT>(a, q, p.lead));
+        }
         int64_t sum = u;  // inclusive over the warp
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -308,20 +319,20 @@ struct Walk {
     Request q;
     int64_t u, end, g0;  // g0: the group's first unit (of its lead)
     int r, h, m, lead;
-    bool leads, first;
+    bool first;
 };
 
-template <int ROWS, int TN>
+template <int ROWS, int TN, bool LATENT = false>
 __device__ __forceinline__ Walk walk_from(const TreeArgs& a, const Place& p) {
     Walk w{};
     w.u = p.start;
     w.end = p.end;
-    w.leads = p.leads;
+    w.lead = p.lead;
     w.first = true;
     if (w.u < w.end) {
         w.r = p.r;
-        w.q = request<ROWS, TN>(a, w.r);
-        w.lead = w.leads ? w.q.lead : 0;
+        w.q = request<ROWS, TN, LATENT>(a, w.r);
+        w.lead = lead_of<TN, LATENT>(a, w.q, p.lead);
         const int each = w.q.nt + w.lead;
         const int64_t group = (w.u - p.base) / each;
         w.h = static_cast<int>(group / w.q.mt);
@@ -331,7 +342,7 @@ __device__ __forceinline__ Walk walk_from(const TreeArgs& a, const Place& p) {
     return w;
 }
 
-template <int ROWS, int TN>
+template <int ROWS, int TN, bool LATENT = false>
 __device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out) {
     if (w.u >= w.end) return false;
     if (w.u >= w.g0 + w.lead + w.q.nt) {  // the next group; there is one, as units are left
@@ -342,9 +353,9 @@ __device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out)
                 w.h = 0;
                 do {
                     if (++w.r >= a.R) return false;
-                    w.q = request<ROWS, TN>(a, w.r);
+                    w.q = request<ROWS, TN, LATENT>(a, w.r);
                 } while (w.q.groups == 0);
-                w.lead = w.leads ? w.q.lead : 0;
+                w.lead = lead_of<TN, LATENT>(a, w.q, w.lead ? kLead : 0);
             }
         }
     }
@@ -366,9 +377,10 @@ __device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out)
 
 // What the join kernel needs to know of a block: the group that its first run
 // belongs to, when that began in an earlier block.
-__device__ __forceinline__ TreeMeta meta_of(const Place& p, const RunAt& x) {
-    if (x.t0 == 0) return TreeMeta{0, p.chunk, 0, 0, 0, 0, 0};
-    return TreeMeta{p.start - x.t0, p.chunk, x.r, x.h, x.m, x.rq.nt, p.leads ? x.rq.lead : 0};
+template <int TN = 1, bool LATENT = false>
+__device__ __forceinline__ TreeMeta meta_of(const TreeArgs& a, const Place& p, const RunAt& x) {
+    if (x.t0 == 0) return TreeMeta{0, p.chunk, 0, 0, 0, 0, p.lead};
+    return TreeMeta{p.start - x.t0, p.chunk, x.r, x.h, x.m, x.rq.nt, lead_of<TN, LATENT>(a, x.rq, p.lead)};
 }
 
 // Which of the 32 rows from j drafted token i of a request sees.

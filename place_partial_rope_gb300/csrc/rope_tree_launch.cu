@@ -236,8 +236,6 @@ rope_status_t launch_tree(const TreePlan& p, const TreeArgs& args, void* workspa
                           rope_stream_t stream, const char** err) {
     const TreeKernel k = kernel_of(p);
     TreeArgs a = args;
-    a.share = a.G;
-    a.masked = 0;
     const int64_t rows = int64_t(2) * blocks * p.rows;
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * p.dv);
