@@ -262,8 +262,8 @@ struct Latent {
     // ---------------------------------------------------------- the walk, and tensor copies
 
     // The block's next run.  Of two blocks that walk a pair of row tiles (blockIdx.y) each has one.
-    __device__ __forceinline__ bool run_after(Walk& walk, RunAt& x) const {
-        if (!next_run<C::ROWS, C::TN, true>(a, walk, x)) return false;
+    __device__ __forceinline__ bool run_after(LatentWalk& walk, RunAt& x) const {
+        if (!next_run<C::ROWS, C::TN>(a, walk, x)) return false;
         x.m = x.m * int(gridDim.y) + int(blockIdx.y);
         if (x.slot >= 0) x.slot += int64_t(blockIdx.y) * 2 * gridDim.x;
         return true;
@@ -312,14 +312,14 @@ struct Latent {
 
     __device__ __forceinline__ void fetches(const Place& place, const LatentMaps& maps) const {
         const int lane = int(threadIdx.x) & 31, all = groups();
-        Walk walk = walk_from<C::ROWS, C::TN, true>(a, place);
+        LatentWalk walk = latent_walk_from<C::ROWS, C::TN>(a, place);
         RunAt x;
         uint32_t run = 0, n = 0, copies = 0;  // runs, tiles, groups of them asked for
         bool first = true;
         for (;; ++run) {
             const bool there = run_after(walk, x);
             if (first && lane == 0 && blockIdx.y == 0)
-                a.meta[blockIdx.x] = there ? meta_of<C::TN, true>(a, place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, 0};
+                a.meta[blockIdx.x] = there ? meta_of(place, walk, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, 0};
             first = false;
             publish(x, run, there, lane);
             if (!there || given_up()) break;
@@ -991,7 +991,7 @@ struct Latent {
     // of the block's other runs too, and in its parts, whose joined results then are NaN.
     __device__ __noinline__ void give_up(const Place& place) const {
         const int tid = int(threadIdx.x);
-        Walk walk = walk_from<C::ROWS, C::TN, true>(a, place);
+        LatentWalk walk = latent_walk_from<C::ROWS, C::TN>(a, place);
         RunAt x;
         while (run_after(walk, x)) {
             const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
@@ -1096,10 +1096,9 @@ __global__ void __launch_bounds__(kLatentJoinThreads) rope_latent_join_kernel(co
     const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5, quarters = (a.Dv + 127) / 128;
     const int own = static_cast<int>(b - from - 1) * shares + (int(blockIdx.y) >> pair);
     const int all = (parts - 1) * shares;
-    // part p: block `from` holds it second unless the group begins with the block's run
-    const int64_t second = from * w.chunk < w.u0 - w.lead ? 1 : 0;
     const int64_t before = int64_t(odd) * 2 * (gridDim.x + 1);  // parts of the pair's other
-    auto slot = [&](int p) { return (before + (from + p) * 2 + (p == 0 ? second : 0)) * ROWS; };
+    // the part that begins the group has its block's second place
+    auto slot = [&](int p) { return (before + (from + p) * 2 + (p == 0 ? 1 : 0)) * ROWS; };
     auto write = [&](int row, int c, float4 o, float top, float l) {
         const float norm = l == 0.0f ? 0.0f : 1.0f / l;
         const OutAt z = out_at(a, qs, 0, m * ROWS + row);

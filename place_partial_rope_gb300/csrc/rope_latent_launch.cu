@@ -55,9 +55,6 @@ rope_status_t launch_latent(const LatentPlan& p, const TreeArgs& args, void* wor
     // 64 requests of 128 heads over 90 to 12000 bf16 rows 161 us, and 177 without.
     const int per = a.G % (2 * p.rows) == 0 && blocks % 2 == 0 ? 2 : 1;
     a.share = a.G / per;
-    // A masked tile takes as long as four: 3 chunks of 200 to 256 tokens of 64 heads over 1031 to
-    // 4099 rows, 0 463 us, 2 415, 3 395, 5 416.
-    a.masked = 3;
     const int64_t rows = int64_t(2) * blocks * p.rows;
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * kLatentValues);

@@ -34,14 +34,13 @@ struct TreeArgs {
     struct TreeMeta* meta;       // one per block
     int32_t words;
     int32_t R, Tq, Hk, G, Hq, Dk, Dv;
-    int32_t share;               // of the G query heads of a key head, those in a block's row tiles: all, or half
-                                 // where blocks go in pairs (set by the launch)
     int32_t pages, page_size, max_len;
-    int32_t masked;              // units that a tile with masks counts beyond its own (set by the launch)
     int32_t box;                 // tile kernels: rows of a fetch, a power of two that divides page_size
     FastDiv div_page, div_group;
     float scale_log2;            // scale * log2(e)
     bool bf16;                   // type of q and out (the cache's own for 16 bits)
+    int32_t share;               // latent rows: of the G query heads, those in a block's row tiles: all, or half
+                                 // where blocks go in pairs (set by the launch)
 };
 
 // The group of row tiles that a block's first unit lies in, when it began in

@@ -199,14 +199,20 @@ struct Request {
 // 6000 to 8200 bf16 rows: 112.9, 110.7, 110.6, 108.6, 112.2.
 constexpr int kLead = 4;
 
-// LATENT, here and below: row tiles hold a.share of the heads, and a request's groups count
-// a.masked units more for each tile that drafted rows fill.  (The other kernels' lead is one
-// number for all: worked out and carried for each request, it cost the first batch above 7 %.)
+// LATENT, here and below: row tiles hold a.share of the heads, and where groups count leads, the
+// tiles that drafted rows fill (a request's last) count kMasked units more each, at their own
+// place, so that a border between blocks may fall among them.
+// Masks make such a tile that much slower: 3 chunks of 200 to 256 fp16 tokens of 64 heads over
+// 1031 to 4099 rows 463 us with none, 394 so.  Counted before a group's first tile, the same, but
+// 4096 tokens of one head over their own rows 310 us, where they take 152 so, and 1024 of 4 heads
+// over 5120 rows 153 and 103.
+// (The other kernels' groups are alike, and their walk has nothing of this: a lead worked out and
+// carried for each request cost the first batch above 7 %.)
+constexpr int kMasked = 3;
+
 template <int TN, bool LATENT>
-__device__ __forceinline__ int lead_of(const TreeArgs& a, const Request& q, int lead) {
-    if constexpr (LATENT)
-        if (lead) lead += static_cast<int>(min(int64_t(q.n) * a.masked / TN, int64_t(1) << 20));
-    return lead;
+__device__ __forceinline__ int masked_tiles(const Request& q, int lead) {
+    return LATENT && lead ? min(q.n / TN, q.nt) : 0;
 }
 
 template <int ROWS, int TN, bool LATENT>
@@ -243,7 +249,7 @@ __device__ __forceinline__ Place find_place(const TreeArgs& a, int64_t* scratch)
     for (int r = tid; r < a.R; r += THREADS) {
         const Request q = request<ROWS, TN, LATENT>(a, r);
         mine += q.units(0);
-        groups += q.groups * (LATENT ? lead_of<TN, LATENT>(a, q, kLead) : 1);
+        groups += q.groups * (LATENT ? kLead + kMasked * masked_tiles<TN, LATENT>(q, kLead) : 1);
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) {
@@ -278,7 +284,7 @@ __device__ __forceinline__ Place find_place(const TreeArgs& a, int64_t* scratch)
         int64_t u = 0;
         if (r < a.R) {
             const Request q = request<ROWS, TN, LATENT>(a, r);
-            u = q.units(lead_of<TN, LATENT>(a, q, p.lead));
+            u = q.units(p.lead + kMasked * masked_tiles<TN, LATENT>(q, p.lead));
         }
         int64_t sum = u;  // inclusive over the warp
 #pragma unroll
@@ -322,7 +328,7 @@ struct Walk {
     bool first;
 };
 
-template <int ROWS, int TN, bool LATENT = false>
+template <int ROWS, int TN>
 __device__ __forceinline__ Walk walk_from(const TreeArgs& a, const Place& p) {
     Walk w{};
     w.u = p.start;
@@ -331,8 +337,7 @@ __device__ __forceinline__ Walk walk_from(const TreeArgs& a, const Place& p) {
     w.first = true;
     if (w.u < w.end) {
         w.r = p.r;
-        w.q = request<ROWS, TN, LATENT>(a, w.r);
-        w.lead = lead_of<TN, LATENT>(a, w.q, p.lead);
+        w.q = request<ROWS, TN, false>(a, w.r);
         const int each = w.q.nt + w.lead;
         const int64_t group = (w.u - p.base) / each;
         w.h = static_cast<int>(group / w.q.mt);
@@ -342,7 +347,7 @@ __device__ __forceinline__ Walk walk_from(const TreeArgs& a, const Place& p) {
     return w;
 }
 
-template <int ROWS, int TN, bool LATENT = false>
+template <int ROWS, int TN>
 __device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out) {
     if (w.u >= w.end) return false;
     if (w.u >= w.g0 + w.lead + w.q.nt) {  // the next group; there is one, as units are left
@@ -353,9 +358,8 @@ __device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out)
                 w.h = 0;
                 do {
                     if (++w.r >= a.R) return false;
-                    w.q = request<ROWS, TN, LATENT>(a, w.r);
+                    w.q = request<ROWS, TN, false>(a, w.r);
                 } while (w.q.groups == 0);
-                w.lead = lead_of<TN, LATENT>(a, w.q, w.lead ? kLead : 0);
             }
         }
     }
@@ -375,12 +379,84 @@ __device__ __forceinline__ bool next_run(const TreeArgs& a, Walk& w, RunAt& out)
     return true;
 }
 
+// The same for LATENT.  A tile belongs to the block that its first unit lies in, so a block may begin
+// (or end) with units of a group and none of its tiles.  A part that begins its group has the
+// block's second place, one that goes on has the first.
+struct LatentWalk {
+    Request q;
+    int64_t u, end, g0;
+    int r, m, lead;
+    int masked;  // tiles of the request that count kMasked units more
+
+    __device__ __forceinline__ int each() const { return lead + q.nt + kMasked * masked; }
+
+    // The group's tiles whose units begin before unit p of it.
+    __device__ __forceinline__ int tiles_before(int p) const {
+        const int at = max(p - lead, 0), over = at - (q.nt - masked);
+        return over <= 0 ? at : at - over + int(uint32_t(over + kMasked) / (1 + kMasked));
+    }
+};
+
+template <int ROWS, int TN>
+__device__ __forceinline__ LatentWalk latent_walk_from(const TreeArgs& a, const Place& p) {
+    LatentWalk w{};
+    w.u = p.start;
+    w.end = p.end;
+    w.lead = p.lead;
+    if (w.u < w.end) {
+        w.r = p.r;
+        w.q = request<ROWS, TN, true>(a, w.r);
+        w.masked = masked_tiles<TN, true>(w.q, w.lead);
+        w.m = static_cast<int>((w.u - p.base) / w.each());
+        w.g0 = p.base + int64_t(w.m) * w.each();
+    }
+    return w;
+}
+
+template <int ROWS, int TN>
+__device__ __forceinline__ bool next_run(const TreeArgs& a, LatentWalk& w, RunAt& out) {
+    RunAt x;
+    int to;
+    do {
+        if (w.u >= w.end) return false;
+        if (w.u >= w.g0 + w.each()) {  // the next group; there is one, as units are left
+            w.g0 = w.u;
+            if (++w.m == w.q.mt) {
+                w.m = 0;
+                do {
+                    if (++w.r >= a.R) return false;
+                    w.q = request<ROWS, TN, true>(a, w.r);
+                } while (w.q.groups == 0);
+                w.masked = masked_tiles<TN, true>(w.q, w.lead);
+            }
+        }
+        const int off = static_cast<int>(w.u - w.g0), stop = static_cast<int>(min(w.end - w.g0, int64_t(w.each())));
+        x.t0 = w.tiles_before(off);
+        to = w.tiles_before(stop);
+        w.u += stop - off;
+    } while (to == x.t0);
+    x.rq = w.q;
+    x.r = w.r;
+    x.h = 0;
+    x.m = w.m;
+    x.count = to - x.t0;
+    x.slot = x.count == w.q.nt ? int64_t(-1) : int64_t(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
+    out = x;
+    return true;
+}
+
 // What the join kernel needs to know of a block: the group that its first run
 // belongs to, when that began in an earlier block.
-template <int TN = 1, bool LATENT = false>
-__device__ __forceinline__ TreeMeta meta_of(const TreeArgs& a, const Place& p, const RunAt& x) {
+__device__ __forceinline__ TreeMeta meta_of(const Place& p, const RunAt& x) {
     if (x.t0 == 0) return TreeMeta{0, p.chunk, 0, 0, 0, 0, p.lead};
-    return TreeMeta{p.start - x.t0, p.chunk, x.r, x.h, x.m, x.rq.nt, lead_of<TN, LATENT>(a, x.rq, p.lead)};
+    return TreeMeta{p.start - x.t0, p.chunk, x.r, x.h, x.m, x.rq.nt, p.lead};
+}
+
+// The same for LATENT, from the walk that has found the run: nt counts units, from the first tile's
+// to the last's.
+__device__ __forceinline__ TreeMeta meta_of(const Place& p, const LatentWalk& w, const RunAt& x) {
+    if (x.t0 == 0) return TreeMeta{0, p.chunk, 0, 0, 0, 0, 0};
+    return TreeMeta{w.g0 + w.lead, p.chunk, x.r, x.h, x.m, x.rq.nt + kMasked * max(w.masked - 1, 0), w.lead};
 }
 
 // Which of the 32 rows from j drafted token i of a request sees.

@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kNarrowThreads) rope_tree_narrow_kernel(const 
     __syncthreads();  // the place's scratch is done with
     while (next_run<C::ROWS, C::TN>(a, walk, step)) {
         const RunAt x = step;
-        if (first) meta = meta_of(a, p, x);
+        if (first) meta = meta_of(p, x);
         first = false;
         Narrow<C>{a, smem, x}.go();
     }

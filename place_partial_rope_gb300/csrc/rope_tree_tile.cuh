@@ -273,7 +273,7 @@ struct Tile {
         uint32_t runs = 0;
         publish(x, runs++, more, lane);
         if (lane == 0)
-            a.meta[blockIdx.x] = more ? meta_of(a, place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, 0};
+            a.meta[blockIdx.x] = more ? meta_of(place, x) : TreeMeta{0, place.chunk, 0, 0, 0, 0, 0};
         Look now{-1, 0};
         if (more) now = look(x, x.t0 * C::TN + lane * a.box);
         int it = 0;
