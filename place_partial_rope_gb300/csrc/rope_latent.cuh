@@ -93,7 +93,7 @@ struct LatentSync {
     unsigned long long full[2][3], empty[2][2], s_full[2], s_free[2], p_full, q_full[3], q_empty, run_full[3], done;
     uint32_t tmem;
     volatile uint32_t dead;
-    volatile uint32_t patch[3];  // of run r at r % 3: r + 1 when values were taken out
+    volatile uint32_t patch[3][4];  // of run r at r % 3, by 128 value lanes: r + 1 when infinities were taken out
     volatile uint32_t taken;     // runs that the softmax has begun
     volatile uint32_t beat;      // tiles done
     RunAt run[3];                // run r at r % 3, when its barrier says so; of no tiles: there is none
@@ -675,11 +675,13 @@ struct Latent {
     // ---------------------------------------------------------- softmax
 
     // The last tiles of a request: values of rows that are not there become zeros, and
-    // those of drafted rows that are not finite are taken out (see add_not_finite): a
-    // weight of 0 times them would reach the tokens that do not see the row.
+    // those of drafted rows that are not finite are taken out: a weight of 0 times them
+    // would reach the tokens that do not see the row.  Of those that do see it, a NaN (the row is
+    // their key, too) has made the score and all results NaN, but infinities may have
+    // made a score of -inf, and are put back (see finish).
     __device__ __noinline__ void mend(uint32_t n, int from, int valid, uint32_t run, int group) const {
         const int pieces = min(value_tiles() * 16, chunks() * 8), lane = int(threadIdx.x) & 31;
-        bool found = false;
+        uint32_t found = 0;  // infinities, by 128 lanes
         for (int row = from + (int(threadIdx.x) >> 5 & 3) * C::SG + group; row < C::TN; row += 4 * C::SG)
             for (int piece = lane; piece < pieces; piece += 32) {
                 const int c0 = piece >> 5 << 2;  // its group's first chunk
@@ -698,11 +700,20 @@ struct Latent {
                     if (not_finite<KIND>(w[j] >> 16)) w[j] &= 0xffffu, bad = 1;
                 }
                 if (bad) {
-                    found = true;
+                    if constexpr (C::kWide) {
+                        constexpr uint32_t INF = C::BF16 ? 0x7f80u : 0x7c00u;
+                        uint32_t was[4];
+                        lds128(was, at);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if ((was[j] & 0x7fffu) == INF || (was[j] >> 16 & 0x7fffu) == INF) found |= 1u << (piece >> 4);
+                    }
                     sts128(at, w[0], w[1], w[2], w[3]);
                 }
             }
-        if (found) sync->patch[run % 3] = run + 1;
+        if (found)
+            for (int t = 0; t < 4; ++t)
+                if (found >> t & 1u) sync->patch[run % 3][t] = run + 1;
         __syncwarp();
     }
 
@@ -887,6 +898,21 @@ struct Latent {
         }
     }
 
+    // 16-bit rows of a chain: the first drafted row of the run's tiles whose value lane c is not
+    // finite, and that value.  (Looked up once for all query rows: those of a chunk of 16000 tokens,
+    // each looking at every row it sees, would take a second and more for a tile.)
+    __device__ __noinline__ int first_not_finite(const RunAt x, int c, float* value) const {
+        const int to = static_cast<int>(min(int64_t(x.rq.len), int64_t(x.t0 + x.count) * C::TN));
+        for (int j = max(max(x.rq.len - x.rq.n, 0), x.t0 * C::TN); c < a.Dv && j < to; ++j) {
+            const Row row = row_of(x, j);
+            const uint32_t y = row.p ? __ldg(reinterpret_cast<const uint16_t*>(row.p) + c) : 0;
+            if (!not_finite<C::STORE>(y)) continue;
+            *value = value16<C::STORE>(y);
+            return j;
+        }
+        return to;
+    }
+
     __device__ __forceinline__ uint32_t pack_one(float y) const {
         return a.bf16 ? pack2<true>(y, 0.0f) : pack2<false>(y, 0.0f);
     }
@@ -898,7 +924,6 @@ struct Latent {
                   c0 = col0 + (lane & 3) * 2, bar = group + 1;
         float *red = sync->red + group * 4 * C::SR, *fac = sync->fac;
         const int first = x.m * C::ROWS, left = min(C::ROWS, x.rq.n * a.G - first);
-        const bool patch = sync->patch[run % 3] == run + 1;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i >> 1) * 8 + c0 + (i & 1);
@@ -933,6 +958,11 @@ struct Latent {
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const int c = t * 128 + tid;
+            const bool patch = C::kWide && sync->patch[run % 3][t] == run + 1;
+            int spoilt = 0;
+            float spoils = 0.0f;
+            if constexpr (C::kWide)
+                if (patch && !a.tree) spoilt = first_not_finite(x, c, &spoils);
 #pragma unroll 1
             for (int r0 = col0; r0 < col0 + C::SR; r0 += W) {
                 if (r0 >= left) break;
@@ -945,7 +975,11 @@ struct Latent {
 #pragma unroll 1
                     for (int r = 0; r < W && r0 + r < left; ++r) {
                         float add = 0.0f;
-                        add_not_finite<C::STORE, C::TN, 1>(a, x, first + r0 + r, c, &add);
+                        if (a.tree) {
+                            if constexpr (C::kWide) add_not_finite<C::STORE, C::TN, 1>(a, x, first + r0 + r, c, &add);
+                        } else if (int(a.div_group.div(uint32_t(first + r0 + r))) >= spoilt - (x.rq.len - x.rq.n)) {
+                            add = spoils;
+                        }
 #pragma unroll
                         for (int k = 0; k < W; ++k) o[k] += k == r ? add : 0.0f;
                     }
@@ -1031,7 +1065,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         bar_init(&sync->done, 2);
         sync->dead = 0;
         for (int i = 0; i < 3; ++i) {
-            sync->patch[i] = 0;
+            for (int t = 0; t < 4; ++t) sync->patch[i][t] = 0;
             bar_init(&sync->run_full[i], 1);
             bar_init(&sync->q_full[i], C::HELPERS);
         }
