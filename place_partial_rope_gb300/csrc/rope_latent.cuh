@@ -226,6 +226,10 @@ struct Latent {
     // For those that may rightly wait for a whole run: gives up when no tile has been
     // done between two such stretches.
     __device__ __forceinline__ void wait_run(unsigned long long* b, uint32_t parity) const {
+        if (!bar_nap(b, parity)) wait_run_on(b, parity);
+    }
+
+    __device__ __noinline__ void wait_run_on(unsigned long long* b, uint32_t parity) const {
         for (uint32_t seen = ~0u;;) {
             for (uint32_t i = 0; i < kNaps; ++i) {
                 if (bar_nap(b, parity)) return;
