@@ -259,6 +259,12 @@ __global__ void __launch_bounds__(THREADS) rope_cache_trim_kernel(const __grid_c
         *a.free_count = static_cast<int32_t>(min(int64_t(count) + total, int64_t(a.capacity)));
 }
 
+rope_status_t failed(cudaError_t e, const char** err) {
+    *err = cudaGetErrorString(e);
+    (void)cudaGetLastError();
+    return ROPE_ERR_CUDA;
+}
+
 rope_status_t launch(const void* f, int threads, int blocks, bool cluster, const PagesArgs& args,
                      rope_stream_t stream, const char** err) {
     void* params[] = {const_cast<PagesArgs*>(&args)};
@@ -276,12 +282,7 @@ rope_status_t launch(const void* f, int threads, int blocks, bool cluster, const
     cfg.attrs = attr;
     cfg.numAttrs = cluster ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelExC(&cfg, f, params);
-    if (e != cudaSuccess) {
-        *err = cudaGetErrorString(e);
-        (void)cudaGetLastError();
-        return ROPE_ERR_CUDA;
-    }
-    return ROPE_OK;
+    return e == cudaSuccess ? ROPE_OK : failed(e, err);
 }
 
 constexpr int kFew = 256, kMany = 1024;
@@ -308,9 +309,13 @@ rope_status_t launch_grow(const PagesArgs& args, rope_stream_t stream, const cha
     if (args.T < kWide)
         return launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kMany, true, true>), kMany,
                       blocks_for(args.T), true, args, stream, err);
+    int device = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (e != cudaSuccess) return failed(e, err);
     const int64_t blocks = (args.T + kMany * 4 - 1) / (kMany * 4);
     const rope_status_t st = launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kMany, true, false>), kMany,
-                                    static_cast<int>(blocks < 152 ? blocks : 152), false, args, stream, err);
+                                    static_cast<int>(blocks < sms ? blocks : sms), false, args, stream, err);
     if (st != ROPE_OK) return st;
     return launch(reinterpret_cast<const void*>(&rope_cache_grow_kernel<kMany, false, true>), kMany, 1, false, args,
                   stream, err);
