@@ -105,6 +105,9 @@ rope_status_t check_side(const rope_norm_rows_t* r, const char* name, const Call
         return fail(ROPE_ERR_INVALID, "%s: heads=%lld must be positive", name, (long long)r->heads);
     if (c.B * c.S > kMaxRows / r->heads)  // (both below 2^31 by now)
         return fail(ROPE_ERR_INVALID, "%s: 2^31 rows or more", name);
+    // (written also where there are no rows)
+    if (c.back && !aligned(r->weight_grad, 4))
+        return fail(ROPE_ERR_INVALID, "%s: weight_grad must be aligned to its elements", name);
     if (c.B * c.S == 0) return ROPE_OK;
     if (!r->x || !r->out || (c.back && (!r->grad || !r->rstd)))
         return fail(ROPE_ERR_NULLPTR, "%s: x, out%s is null", name, c.back ? ", grad or rstd" : "");
@@ -115,7 +118,7 @@ rope_status_t check_side(const rope_norm_rows_t* r, const char* name, const Call
         return fail(ROPE_ERR_INVALID, "%s: strides must be >= 0 and in range", name);
     if (!rows_apart(out)) return fail(ROPE_ERR_INVALID, "%s: strides of out must keep its rows apart", name);
     if (!aligned(r->x, e) || !aligned(r->out, e) || (c.back && !aligned(r->grad, e)) || !aligned(r->rstd, 4) ||
-        !aligned(r->weight, size_of(c.weight_dtype)) || (c.back && !aligned(r->weight_grad, 4)))
+        !aligned(r->weight, size_of(c.weight_dtype)))
         return fail(ROPE_ERR_INVALID, "%s: pointers must be aligned to their elements", name);
     return ROPE_OK;
 }
