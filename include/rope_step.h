@@ -220,7 +220,8 @@ rope_status_t rope_partial_cache_trim(int32_t* kv_len, const int32_t* new_len, i
  * once; in fp16 what is below 2^-21 of the token's largest loses bits and below 2^-31
  * vanishes (scales below 2^-80 are as small there as they are).  For 8-bit caches q is
  * rounded to fp16 after a power of two that brings the row's largest lane to [1, 2).
- * 16-bit rows of a multiple of 64 lanes in pages of a multiple of 16 rows are the fast case.
+ * 16-bit rows of a multiple of 64 lanes in pages of a multiple of 8 rows are the fast case
+ * (the larger the power of two that divides the page, to 64, the larger the copies).
  */
 rope_status_t rope_partial_latent_attention(const rope_kv_cache_t* cache, const void* q,
                                             rope_dtype_t dtype, int64_t Tq, int64_t Hq, int64_t v_dim,
