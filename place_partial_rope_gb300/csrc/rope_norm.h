@@ -11,7 +11,6 @@ namespace rope {
 constexpr int kNormThreads = 256;
 constexpr int kNormBlocksPerSm = 8;   // no backward has more resident blocks an SM
 constexpr int kNormJoinLanes = 32;    // lanes of the weights that a joining block adds up
-constexpr uint32_t kMaxNormItems = 1u << 30;  // of one launch: indexes fit 32 bits
 
 // The queries' or the keys' rows of a launch.
 struct NormRows {

@@ -70,6 +70,13 @@ NormKernel norm_kernel(const NormPlan& p) {
 rope_status_t launch_norm_fwd(const NormKernel& k, const NormArgs& args, rope_stream_t stream, const char** err) {
     const uint64_t items = uint64_t(args.side[0].items) + (args.sides == 2 ? args.side[1].items : 0);
     const uint64_t per = uint64_t(kNormThreads >> args.lanes_log2);
+    // The kernel numbers items in 32 bits, those of both sides and the rest of the last block:
+    // a side has less than 2^31, so all are at most 2^32, which `per`, a power of two, divides.
+    static_assert((kNormThreads & (kNormThreads - 1)) == 0, "a block's items are a power of two");
+    if ((items + per - 1) / per * per > uint64_t(1) << 32) {
+        *err = "internal error: more rows than a launch can number";
+        return ROPE_ERR_CUDA;
+    }
     void* params[] = {const_cast<NormArgs*>(&args)};
     return launch(k.f, dim3(static_cast<unsigned>((items + per - 1) / per)), dim3(kNormThreads), params, stream, err);
 }
