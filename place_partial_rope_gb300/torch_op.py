@@ -144,48 +144,50 @@ def _like(x, shape=None, dtype=None):
     return torch.empty(x.shape if shape is None else shape, dtype=dtype or x.dtype, device=x.device)
 
 
-def _norm_outputs(q, k):
-    return (_like(q), _like(k), _like(q, q.shape[:3], torch.float32),
-            _like(k, None if k is None else k.shape[:3], torch.float32))
+def _norm_outputs(q, k, keep_rstd):
+    return (_like(q), _like(k), *(_like(x if keep_rstd else None, None if x is None else x.shape[:3], torch.float32)
+                                  for x in (q, k)))
 
 
-def _norm_grads(q, k, q_weight, k_weight):
-    return (_like(q), _like(k), _like(q_weight, None, torch.float32), _like(k_weight, None, torch.float32))
+def _norm_grads(q, k, q_weight, k_weight, weight_grads):
+    return (_like(q), _like(k), *(_like(w if wanted else None, None, torch.float32)
+                                  for w, wanted in zip((q_weight, k_weight), weight_grads)))
 
 
 def _norm_cuda(q, k, q_weight, k_weight, cos, sin, rotary_mode="interleave", partial_slice=(0, 0),
-               norm_slice=(0, 0), eps=1e-6):
+               norm_slice=(0, 0), eps=1e-6, keep_rstd=True):
     _check_norm(q, k, rotary_mode, partial_slice, norm_slice)
     q, k = _rows(q), _rows(k)
-    got = _norm_outputs(q, k)
+    got = _norm_outputs(q, k, keep_rstd)
     binding.rope_partial_norm_fwd(q, k, q_weight, k_weight, cos, sin, *partial_slice, eps=eps, norm=tuple(norm_slice),
-                                  mode=rotary_mode, q_out=got[0], k_out=None if k is None else got[1], q_rstd=got[2],
-                                  k_rstd=None if k is None else got[3])
+                                  mode=rotary_mode, q_out=got[0], k_out=None if k is None else got[1],
+                                  q_rstd=got[2] if keep_rstd else None,
+                                  k_rstd=got[3] if keep_rstd and k is not None else None)
     return got
 
 
 def _norm_cuda_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, rotary_mode="interleave",
-                   partial_slice=(0, 0), norm_slice=(0, 0)):
+                   partial_slice=(0, 0), norm_slice=(0, 0), weight_grads=(True, True)):
     _check_norm(q, k, rotary_mode, partial_slice, norm_slice)
     q, k = _rows(q), _rows(k)
-    got = _norm_grads(q, k, q_weight, k_weight)
+    got = _norm_grads(q, k, q_weight, k_weight, weight_grads)
     binding.rope_partial_norm_bwd(_rows(dq), _rows(dk), q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin,
                                   *partial_slice, norm=tuple(norm_slice), mode=rotary_mode, dq_out=got[0],
                                   dk_out=None if k is None else got[1],
-                                  dq_weight=None if q_weight is None else got[2],
-                                  dk_weight=None if k_weight is None else got[3])
+                                  dq_weight=got[2] if q_weight is not None and weight_grads[0] else None,
+                                  dk_weight=got[3] if k_weight is not None and weight_grads[1] else None)
     return got
 
 
 def _norm_meta(q, k, q_weight, k_weight, cos, sin, rotary_mode="interleave", partial_slice=(0, 0),
-               norm_slice=(0, 0), eps=1e-6):
+               norm_slice=(0, 0), eps=1e-6, keep_rstd=True):
     _check_norm(q, k, rotary_mode, partial_slice, norm_slice)
-    return _norm_outputs(q, k)
+    return _norm_outputs(q, k, keep_rstd)
 
 
 def _norm_meta_bwd(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, rotary_mode="interleave",
-                   partial_slice=(0, 0), norm_slice=(0, 0)):
-    return _norm_grads(q, k, q_weight, k_weight)
+                   partial_slice=(0, 0), norm_slice=(0, 0), weight_grads=(True, True)):
+    return _norm_grads(q, k, q_weight, k_weight, weight_grads)
 
 
 def register() -> None:
@@ -211,9 +213,10 @@ def register() -> None:
         lib.impl(name, _axes_meta, "Meta")
     rest = "*, str rotary_mode='interleave', int[2] partial_slice=[0, 0], int[2] norm_slice=[0, 0]"
     lib.define(f"{_NORM_FWD}(Tensor q, Tensor? k, Tensor? q_weight, Tensor? k_weight, Tensor? cos, Tensor? sin, "
-               f"{rest}, float eps=1e-06) -> (Tensor, Tensor, Tensor, Tensor)")
+               f"{rest}, float eps=1e-06, bool keep_rstd=True) -> (Tensor, Tensor, Tensor, Tensor)")
     lib.define(f"{_NORM_BWD}(Tensor dq, Tensor? dk, Tensor q, Tensor? k, Tensor? q_weight, Tensor? k_weight, "
-               f"Tensor q_rstd, Tensor? k_rstd, Tensor? cos, Tensor? sin, {rest}) -> (Tensor, Tensor, Tensor, Tensor)")
+               f"Tensor q_rstd, Tensor? k_rstd, Tensor? cos, Tensor? sin, {rest}, "
+               "bool[2] weight_grads=[True, True]) -> (Tensor, Tensor, Tensor, Tensor)")
     lib.impl(_NORM_FWD, _norm_cuda, "CUDA")
     lib.impl(_NORM_FWD, _norm_meta, "Meta")
     lib.impl(_NORM_BWD, _norm_cuda_bwd, "CUDA")
@@ -323,9 +326,9 @@ class NormRotaryFn(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk=None):
         q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin = ctx.saved_tensors
-        # (a weight whose gradient nobody wants takes part all the same)
-        got = _op(_NORM_FWD, True)(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, **ctx.kwargs)
         need = ctx.needs_input_grad
+        got = _op(_NORM_FWD, True)(dq, dk, q, k, q_weight, k_weight, q_rstd, k_rstd, cos, sin, **ctx.kwargs,
+                                   weight_grads=[need[2], need[3]])
         return (got[0] if need[0] else None, got[1] if need[1] else None,
                 got[2].to(q_weight.dtype) if need[2] else None, got[3].to(k_weight.dtype) if need[3] else None,
                 None, None, None, None)
@@ -347,5 +350,5 @@ def norm_rotary(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[t
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight)):
         got = NormRotaryFn.apply(q, k, q_weight, k_weight, cos, sin, kwargs, float(eps))
         return got if k is not None else (got, None)
-    got = _op(_NORM_FWD, False)(q, k, q_weight, k_weight, cos, sin, **kwargs, eps=float(eps))
+    got = _op(_NORM_FWD, False)(q, k, q_weight, k_weight, cos, sin, **kwargs, eps=float(eps), keep_rstd=False)
     return got[0], got[1] if k is not None else None
