@@ -365,7 +365,7 @@ struct Latent {
                     // more than it gives: ragged batch in boxes of 8 rows 187 us, and 251 so)
                     if (boxes == 1 && lane == 0 && it + C::kAhead < x.count) {
                         const Box far = box_of(x, x.t0 + it + C::kAhead, 0);
-                        if (far.page >= 0)
+                        if (far.page >= 0 && far.page < a.pages)
                             for (int c = 0; c < chunks(); c += 4)
                                 asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %1, %2, %3, %4}];" ::"l"(
                                                  &maps.four), "r"(0), "r"(c), "r"(far.off >> 3), "r"(far.page)
