@@ -31,10 +31,10 @@
 // the scores of 64 query rows and 770 for the values of a tile of 64 rows, 570 more to bring it),
 // and the chain of fetch, scores, softmax and values over two tiles in flight: 64 requests
 // of 128 heads over 90 to 12000 bf16 rows take 161 us (2.9 TB/s; 68 by the cache's bytes), 3
-// chunks of 200 to 256 tokens of 64 heads over 1031 to 4099 fp16 rows 395 us (609 TFLOP/s).  8-bit
+// chunks of 200 to 256 tokens of 64 heads over 1031 to 4099 fp16 rows 396 us (606 TFLOP/s).  8-bit
 // rows: threads that turn codes into fp16, and instruction fetch: 32 requests of 1 to 7 tokens
-// of 32 heads over 8000 fp8 rows 182 us (347 TFLOP/s), 2 of 131072 int8 rows and 16 heads 76 us
-// (2.0 TB/s).  One token of 16 heads over 4097 rows: 16.8 us, a tile a block and the join.
+// of 32 heads over 8000 fp8 rows 179 us (352 TFLOP/s), 2 of 131072 int8 rows and 16 heads 74 us
+// (2.0 TB/s).  One token of 16 heads over 4097 rows: 16 to 17 us, a tile a block and the join.
 //   Every wait is bounded; one that gives up sets `dead`, the threads of a role leave
 // together, and every result that the block has a share in becomes NaN.
 #pragma once

@@ -203,8 +203,8 @@ constexpr int kLead = 4;
 // tiles that drafted rows fill (a request's last) count kMasked units more each, at their own
 // place, so that a border between blocks may fall among them.
 // Masks make such a tile that much slower: 3 chunks of 200 to 256 fp16 tokens of 64 heads over
-// 1031 to 4099 rows 463 us with none, 394 so.  Counted before a group's first tile, the same, but
-// 4096 tokens of one head over their own rows 310 us, where they take 152 so, and 1024 of 4 heads
+// 1031 to 4099 rows 463 us with none, 396 so.  Counted before a group's first tile, the same, but
+// 4096 tokens of one head over their own rows 310 us, where they take 154 so, and 1024 of 4 heads
 // over 5120 rows 153 and 103.
 // (The other kernels' groups are alike, and their walk has nothing of this: a lead worked out and
 // carried for each request cost the first batch above 7 %.)
