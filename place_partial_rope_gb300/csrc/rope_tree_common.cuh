@@ -202,10 +202,11 @@ constexpr int kLead = 4;
 // LATENT, here and below: row tiles hold a.share of the heads, and where groups count leads, the
 // tiles that drafted rows fill (a request's last) count kMasked units more each, at their own
 // place, so that a border between blocks may fall among them.
-// Masks make such a tile that much slower: 3 chunks of 200 to 256 fp16 tokens of 64 heads over
-// 1031 to 4099 rows 463 us with none, 396 so.  Counted before a group's first tile, the same, but
-// 4096 tokens of one head over their own rows 310 us, where they take 154 so, and 1024 of 4 heads
-// over 5120 rows 153 and 103.
+// Masks make such a tile that much slower.  With 0, 1, 2, 3 and 4: chunks of 200, 228 and 256 fp16
+// tokens of 64 heads over 1031, 2565 and 4099 rows 459, 435, 408, 403 and 406 us; 1024 tokens of 4
+// heads over 5120 rows 125, 114, 102, 103 and 116; of 16 heads over 8192 441, 434, 427, 434 and 442.
+// (Counted before a group's first tile: 408, 153 and 485; 4096 tokens of one head over their own
+// rows 310, where they take 153 here with any of these.)
 // (The other kernels' groups are alike, and their walk has nothing of this: a lead worked out and
 // carried for each request cost the first batch above 7 %.)
 constexpr int kMasked = 3;
